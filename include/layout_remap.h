@@ -56,7 +56,9 @@ typedef enum {
   LR_ERR_HIP = -9,               /* a HIP call failed; lr_last_hip_error() gives its text */
   LR_ERR_PATH = -10,             /* a forced copy path does not apply to these layouts */
   LR_ERR_OVERLAP = -11,          /* source and destination storage overlap */
-  LR_ERR_CAPACITY = -12          /* text buffer too small (lr_layout_format) */
+  LR_ERR_CAPACITY = -12,         /* text buffer (lr_layout_format) or workspace too small */
+  LR_ERR_TYPE = -13              /* an element type the operator does not take, or a pair of types it
+                                    does not combine */
 } lr_status;
 
 /*
@@ -492,6 +494,163 @@ int lr_layout_copy_count_writes(const void* src, const lr_layout* Ls, int64_t sr
                                 void* dst, const lr_layout* Ld, int64_t dst_capacity_elems,
                                 size_t elem_bytes, uint32_t flags, const lr_copy_tuning* tuning,
                                 int32_t* counts, void* stream);
+
+/* ------------------------------------------- attention: positions, cache, tokens */
+
+/* The operators below read and write numbers (not opaque bytes).  Every tensor is a
+ * buffer with an unswizzled layout whose top-level modes have the meaning stated;
+ * a mode may have several leaves where "leaves" is said (a token index that runs over
+ * (sequence, batch), say), otherwise it has to coalesce to one leaf.  Extents are
+ * those of the layout; token counts are arguments, so one layout serves every step.
+ * Sums, softmax statistics and rotations are computed in 32 bits and rounded once,
+ * to nearest even, where they are stored.
+ *
+ * Errors of every entry point, before anything is launched: LR_ERR_INVALID (NULL,
+ * a negative count, wrong number of modes, a mode of several leaves where one is
+ * needed, a parameter out of range), LR_ERR_SWIZZLE, LR_ERR_TYPE,
+ * LR_ERR_SIZE_MISMATCH (extents that have to agree), LR_ERR_BOUNDS (a layout beyond
+ * its buffer), LR_ERR_ALIAS (an output layout that is not injective),
+ * LR_ERR_OVERLAP (an output that overlaps an input), LR_ERR_OVERFLOW (a count or an
+ * extent of 2^31 or more), LR_ERR_HIP. */
+
+/* Element types. */
+typedef enum {
+  LR_F32 = 0,
+  LR_F16 = 1,
+  LR_BF16 = 2,
+  LR_E4M3 = 3, /* OCP 8-bit float, 4 exponent and 3 mantissa bits, largest 448, no infinities */
+  LR_INT8 = 4  /* -127 .. 127 */
+} lr_dtype;
+
+/* How the pairs of a rotation lie in the first rot_dim elements of a head. */
+typedef enum {
+  LR_PAIRS_HALF = 0,       /* pair i is elements i and i + rot_dim/2: the mode (2, rot_dim/2):(rot_dim/2, 1) */
+  LR_PAIRS_INTERLEAVED = 1 /* pair i is elements 2i and 2i + 1: the mode (2, rot_dim/2):(1, 2) */
+} lr_pairs;
+
+/* Frequencies of a rotation: pair i of rot_dim/2 turns by w_i = base^(-2i/rot_dim) radians a
+ * position, changed for contexts longer than original_len by factor: */
+typedef enum {
+  LR_ROPE_PLAIN = 0,
+  LR_ROPE_LINEAR = 1, /* w_i / factor */
+  LR_ROPE_BASE = 2,   /* base * factor^(rot_dim/(rot_dim-2)) in base's place */
+  LR_ROPE_PARTS = 3,  /* w_i/factor * (1-k_i) + w_i * k_i, k_i falling linearly in i from 1 to 0 between the
+                         pairs (rounded outwards, within [0, rot_dim-1]) that turn `high` and `low` times over
+                         original_len; magnitude 0.1 ln(factor) + 1 (factor > 1; Peng et al., "YaRN: Efficient
+                         Context Window Extension of Large Language Models", 2023) */
+  LR_ROPE_BANDS = 4   /* the same blend with k_i = clamp((t_i - low)/(high - low), 0, 1), t_i = original_len *
+                         w_i / 2pi the pair's turns over original_len; magnitude 1 */
+} lr_rope_scaling;
+
+typedef struct {
+  int32_t rot_dim;      /* even, 2 .. 1024 */
+  int32_t scaling;      /* lr_rope_scaling */
+  double base;          /* > 1 */
+  double factor;        /* > 0; unused by LR_ROPE_PLAIN */
+  double original_len;  /* > 0, LR_ROPE_PARTS and LR_ROPE_BANDS */
+  double low, high;     /* 0 < low < high, LR_ROPE_PARTS and LR_ROPE_BANDS */
+} lr_rope_params;
+
+/* The table a rotation needs (host only): turns[i], i < rot_dim/2, is w_i / 2pi as the 64 bits of a
+ * fraction of one turn, so that position * turns[i] modulo 2^64 is the exact angle modulo one turn of
+ * the rounded frequency (off by under |position| * 2^-61 turns).  The caller keeps it in device
+ * memory.  *magnitude: the factor that scales the rotated elements. */
+int lr_rope_table(const lr_rope_params* p, int64_t* turns, double* magnitude);
+
+/* One rotation: the device table, its shape and the positions. */
+typedef struct {
+  const int64_t* turns;     /* device, rot_dim/2 entries (lr_rope_table) */
+  const int64_t* positions; /* device, any int64 values */
+  int32_t rot_dim;
+  int32_t pairs;            /* lr_pairs */
+  float magnitude;
+} lr_rotation;
+
+#define LR_ROPE_BACKWARD 0x1u /* the gradient: the transposed rotation of dy, written to dx */
+
+/* Rotary positions, regrouped on the way: with x of layout Lx and y of layout Ly, both (head_dim,
+ * heads (leaves), tokens (leaves)), for the first n tokens t, every head h and every pair (a, b) of
+ * the first rot_dim elements
+ *   y[a] = m (x[a] cos A - x[b] sin A),  y[b] = m (x[b] cos A + x[a] sin A),
+ * A = positions[Lp(t)] * w, and the elements past rot_dim are copied.  Lp: layout of the position of
+ * each token (stride 0 shares them over a batch), NULL for t itself; p_capacity entries.  With
+ * LR_ROPE_BACKWARD the sign of A is changed: x is then dL/dy and y dL/dx.  dtype: LR_F32, LR_F16 or
+ * LR_BF16.  y may be x itself when Lx and Ly are the same. */
+int lr_rope(const void* x, const lr_layout* Lx, int64_t x_capacity, void* y, const lr_layout* Ly,
+            int64_t y_capacity, int32_t dtype, const lr_rotation* r, const lr_layout* Lp, int64_t p_capacity,
+            int64_t n, uint32_t flags, void* stream);
+
+/* A paged cache of keys and values: tensors of layout (head_dim, heads, slots of a page, pages), so any
+ * order of heads and slots inside a page, and any padding, is a layout.  Token slot s of a cache is
+ * slot s % page_size of page s / page_size.  An LR_E4M3 or LR_INT8 cache holds codes and, for each slot
+ * and head, the 32-bit scale they are multiplied by, in two arrays of layout scale_layout
+ * (heads, slots of a page, pages).  k and v may differ in head_dim (up to 512 each). */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale; /* LR_E4M3 and LR_INT8 only, else NULL */
+  float* v_scale;
+  lr_layout k_layout, v_layout;
+  lr_layout scale_layout; /* not looked at for the other types */
+  int64_t k_capacity, v_capacity, scale_capacity;
+  int32_t dtype;
+} lr_cache;
+
+/* Check a cache's description (host only). */
+int lr_cache_validate(const lr_cache* c);
+
+/* Write the keys and values of n tokens into the slots slots[0..n) (device; distinct).  A slot outside
+ * [0, pages * page_size) writes nothing (padding).  k, v: layout (head_dim, heads, tokens), at least n
+ * tokens.  r (NULL: none) rotates the keys first, by positions[t]; nothing is rounded in between.
+ * dtype LR_F32, LR_F16 or LR_BF16; the cache has the same type, or LR_E4M3 or LR_INT8, for which a row x
+ * of head_dim elements is stored as
+ *   scale = max(amax / Q, 2^-126),  code = x / scale rounded to nearest even, within [-Q, Q],
+ * Q = 448 or 127 and amax the largest finite |x| of the row.  Infinities become +-Q, NaN stays NaN in
+ * LR_E4M3 and becomes 0 in LR_INT8. */
+int lr_cache_write(const lr_cache* c, const void* k, const lr_layout* Lk, int64_t k_capacity, const void* v,
+                   const lr_layout* Lv, int64_t v_capacity, int32_t dtype, const int64_t* slots, int64_t n,
+                   const lr_rotation* r, void* stream);
+
+/* Read the slots slots[0..n) back: k and v (layouts as lr_cache_write) receive code * scale, or the
+ * stored elements; a slot outside the cache gives zeros. */
+int lr_cache_read(const lr_cache* c, const int64_t* slots, int64_t n, void* k, const lr_layout* Lk,
+                  int64_t k_capacity, void* v, const lr_layout* Lv, int64_t v_capacity, int32_t dtype,
+                  void* stream);
+
+/* How lr_paged_attention runs (host only). */
+typedef enum {
+  LR_ATTENTION_ELEMENT = 0, /* any types, strides and alignment: one key per lane */
+  LR_ATTENTION_MATRIX = 1   /* matrix instructions over 16-byte aligned rows */
+} lr_attention_path;
+
+typedef struct {
+  int32_t path;            /* lr_attention_path, for 16-byte aligned buffers */
+  int32_t head_tiles;      /* workgroups that share the keys of one cache head */
+  int64_t chunk;           /* tokens of one workgroup */
+  int64_t splits;          /* chunks of the longest sequence */
+  int64_t workspace_bytes; /* device memory lr_paged_attention needs; 0 when splits is 1 */
+} lr_attention_plan;
+
+/* Attention of one new token a sequence over a paged cache:
+ *   out[b, h] = sum_t softmax_t(scale * q[b, h] . k[t, g]) v[t, g],   g = h / (heads / cache heads),
+ * over the tokens t of sequence b with max(0, n_b - window) <= t < n_b (window 0: all), n_b = lens[b]
+ * limited to [0, max_pages * page_size].  Token t is slot t % page_size of page table[b * table_stride +
+ * t / page_size]; the tokens of a page outside [0, pages) are left out.  A sequence with no token gives
+ * zeros.  What the cache holds in other slots does not matter, NaN included.
+ * q, out: layouts (head_dim, heads, sequences), the first batch sequences used; heads a multiple of the
+ * cache's; q's head_dim is the keys', out's the values', each at most 256.  dtype (of q and out): LR_F32,
+ * LR_F16 or LR_BF16; the cache has the same type, or LR_E4M3 or LR_INT8.  lse (NULL: not wanted): device
+ * float[batch][heads], log sum_t exp(scale * q . k), -inf with no token.
+ * A sequence's tokens are split into chunks that are joined by a second launch; workspace: device memory
+ * of at least the plan's workspace_bytes (LR_ERR_CAPACITY), 16-byte aligned, its contents don't matter.
+ * The result does not depend on timing: every sum has a fixed order. */
+int lr_paged_attention_plan(const lr_layout* Lq, const lr_cache* c, const lr_layout* Lo, int64_t max_pages,
+                            int32_t dtype, int64_t window, lr_attention_plan* out);
+int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, const lr_cache* c,
+                       const int32_t* table, int64_t table_stride, int64_t max_pages, const int32_t* lens,
+                       int64_t batch, void* out, const lr_layout* Lo, int64_t out_capacity, float* lse,
+                       int32_t dtype, float scale, int64_t window, void* workspace, int64_t workspace_bytes,
+                       void* stream);
 
 /* ------------------------------------------------------------------ misc */
 

@@ -32,6 +32,7 @@ ERR_HIP = -9
 ERR_PATH = -10
 ERR_OVERLAP = -11
 ERR_CAPACITY = -12
+ERR_TYPE = -13
 
 # lr_path
 PATH_GENERIC = 0
@@ -165,6 +166,68 @@ class lr_access_report(ctypes.Structure):
     ]
 
 
+# lr_dtype
+F32 = 0
+F16 = 1
+BF16 = 2
+E4M3 = 3
+INT8 = 4
+
+# lr_pairs, lr_rope_scaling, lr_attention_path
+PAIRS = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3, "bands": 4}
+ATTENTION_PATH_NAMES = {0: "element", 1: "matrix"}
+ROPE_BACKWARD = 0x1
+
+
+class lr_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_len", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+    ]
+
+
+class lr_rotation(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int32),
+        ("pairs", ctypes.c_int32),
+        ("magnitude", ctypes.c_float),
+    ]
+
+
+class lr_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("k_layout", lr_layout),
+        ("v_layout", lr_layout),
+        ("scale_layout", lr_layout),
+        ("k_capacity", ctypes.c_int64),
+        ("v_capacity", ctypes.c_int64),
+        ("scale_capacity", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class lr_attention_plan(ctypes.Structure):
+    _fields_ = [
+        ("path", ctypes.c_int32),
+        ("head_tiles", ctypes.c_int32),
+        ("chunk", ctypes.c_int64),
+        ("splits", ctypes.c_int64),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 class LibraryNotBuilt(RuntimeError):
     pass
 
@@ -215,6 +278,24 @@ _SIGS = {
     "lr_layout_copy_count_writes": (ctypes.c_int, [ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, _L,
                                                    ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint32,
                                                    _P(lr_copy_tuning), ctypes.c_void_p, ctypes.c_void_p]),
+    "lr_rope_table": (ctypes.c_int, [_P(lr_rope_params), _P(ctypes.c_int64), _P(ctypes.c_double)]),
+    "lr_rope": (ctypes.c_int, [ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, _L, ctypes.c_int64,
+                               ctypes.c_int32, _P(lr_rotation), _L, ctypes.c_int64, ctypes.c_int64, ctypes.c_uint32,
+                               ctypes.c_void_p]),
+    "lr_cache_validate": (ctypes.c_int, [_P(lr_cache)]),
+    "lr_cache_write": (ctypes.c_int, [_P(lr_cache), ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, _L,
+                                      ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                      _P(lr_rotation), ctypes.c_void_p]),
+    "lr_cache_read": (ctypes.c_int, [_P(lr_cache), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, _L,
+                                     ctypes.c_int64, ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_int32,
+                                     ctypes.c_void_p]),
+    "lr_paged_attention_plan": (ctypes.c_int, [_L, _P(lr_cache), _L, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64,
+                                               _P(lr_attention_plan)]),
+    "lr_paged_attention": (ctypes.c_int, [ctypes.c_void_p, _L, ctypes.c_int64, _P(lr_cache), ctypes.c_void_p,
+                                          ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
+                                          ctypes.c_float, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p]),
     "lr_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "lr_last_hip_error": (ctypes.c_char_p, []),
     "lr_version": (ctypes.c_char_p, []),
@@ -626,3 +707,222 @@ def layout_copy_count_writes(src, Ls, dst, Ld, counts, elem_bytes: Optional[int]
                                              ctypes.byref(Ld.c), db // eb, eb, flags, _tuning(tuning),
                                              counts.data_ptr(), _stream_ptr(stream)), "layout_copy_count_writes")
     return counts
+
+
+# ---------------------------------------------------------------------------
+# Attention: rotary positions, the paged cache, the attention that reads it
+# ---------------------------------------------------------------------------
+_DTYPES = None
+
+
+def _dtype_code(dtype) -> int:
+    """lr_dtype of a torch type (torch.uint8 holds LR_E4M3 codes); ValueError for another."""
+    global _DTYPES
+    if _DTYPES is None:
+        torch = _torch()
+        _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3,
+                   torch.uint8: E4M3, torch.int8: INT8}
+    if dtype not in _DTYPES:
+        raise ValueError(f"no operator takes elements of {dtype}")
+    return _DTYPES[dtype]
+
+
+def _device_tensors(device, **tensors):
+    """Every tensor contiguous and on `device` (None: any one GPU)."""
+    for what, t in tensors.items():
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a GPU tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{what} is on {t.device}, not on {device}")
+
+
+class RopeTable:
+    """The frequencies of a rotation in device memory (lr_rope_table), kept by the caller."""
+
+    __slots__ = ("turns", "rot_dim", "magnitude")
+
+    def __init__(self, turns, rot_dim: int, magnitude: float):
+        self.turns, self.rot_dim, self.magnitude = turns, rot_dim, magnitude
+
+
+def rope_table(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               original_len: float = 0.0, low: float = 1.0, high: float = 32.0, device="cuda") -> RopeTable:
+    """lr_rope_table: the table for rotations of the first ``rot_dim`` elements of a head.
+    ``scaling``: "none", "linear", "base", "parts" or "bands" (lr_rope_scaling)."""
+    torch = _torch()
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling {scaling!r} is none of {sorted(ROPE_SCALING)}")
+    p = lr_rope_params(rot_dim, ROPE_SCALING[scaling], base, factor, original_len, low, high)
+    buf = (ctypes.c_int64 * max(1, min(rot_dim, 1024) // 2))()
+    m = ctypes.c_double()
+    _check(lib().lr_rope_table(ctypes.byref(p), buf, ctypes.byref(m)), "rope_table")
+    return RopeTable(torch.tensor(list(buf), dtype=torch.int64).to(device), rot_dim, m.value)
+
+
+def _rotation(table: RopeTable, positions, pairs: str) -> lr_rotation:
+    if pairs not in PAIRS:
+        raise ValueError(f"pairs {pairs!r} is neither 'half' nor 'interleaved'")
+    if positions.dtype != table.turns.dtype:
+        raise TypeError("positions must be int64")
+    return lr_rotation(table.turns.data_ptr(), positions.data_ptr(), table.rot_dim, PAIRS[pairs], table.magnitude)
+
+
+def rope(x, Lx, y, Ly, positions, table: RopeTable, pairs: str = "half", backward: bool = False, Lp=None,
+         n: Optional[int] = None, stream=None):
+    """lr_rope: y = the rotation of x, from layout Lx to layout Ly, both (head_dim, heads, tokens).
+    ``positions``: int64, one per token, or one per offset of the layout ``Lp``; ``n``: the first n
+    tokens only.  ``backward``: x is dL/dy and y becomes dL/dx.  Returns y."""
+    _device_tensors(None, x=x, y=y, positions=positions, table=table.turns)
+    if x.dtype != y.dtype:
+        raise TypeError("x and y must have the same type")
+    Lx, Ly = _as_layout(Lx), _as_layout(Ly)
+    count = positions.numel()
+    if n is None:
+        n = count if Lp is None else size(Lp)
+    _check(lib().lr_rope(x.data_ptr(), Lx.c, x.numel(), y.data_ptr(), Ly.c, y.numel(), _dtype_code(x.dtype),
+                         _rotation(table, positions, pairs), _as_layout(Lp).c if Lp is not None else None, count, n,
+                         ROPE_BACKWARD if backward else 0, _stream_ptr(stream)), "rope")
+    return y
+
+
+class PagedCache:
+    """lr_cache over torch tensors: keys ``k`` of layout ``Lk`` and values ``v`` of layout ``Lv``, both
+    (head_dim, heads, slots of a page, pages).  A float8_e4m3fn (or uint8) or int8 cache has float32
+    scales ``k_scale`` and ``v_scale`` of layout ``Ls`` (heads, slots of a page, pages).  Holds the
+    tensors; checked once, here."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "c")
+
+    def __init__(self, k, Lk, v, Lv, k_scale=None, v_scale=None, Ls=None):
+        torch = _torch()
+        _device_tensors(None, k=k)
+        _device_tensors(k.device, v=v)
+        if k.dtype != v.dtype:
+            raise TypeError("k and v must have the same type")
+        c = lr_cache()
+        c.k, c.v, c.dtype = k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype)
+        c.k_layout, c.v_layout = _as_layout(Lk).c, _as_layout(Lv).c
+        c.k_capacity, c.v_capacity = k.numel(), v.numel()
+        if k_scale is not None or v_scale is not None:
+            if k_scale is None or v_scale is None or Ls is None:
+                raise ValueError("k_scale, v_scale and Ls go together")
+            _device_tensors(k.device, k_scale=k_scale, v_scale=v_scale)
+            if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+                raise TypeError("scales must be float32")
+            c.k_scale, c.v_scale, c.scale_layout = k_scale.data_ptr(), v_scale.data_ptr(), _as_layout(Ls).c
+            c.scale_capacity = min(k_scale.numel(), v_scale.numel())
+        self.k, self.v, self.k_scale, self.v_scale, self.c = k, v, k_scale, v_scale, c
+        cache_validate(self)
+
+
+def cache_validate(cache: PagedCache) -> None:
+    """lr_cache_validate: raises LayoutRemapError for a bad description."""
+    _check(lib().lr_cache_validate(cache.c), "cache_validate")
+
+
+def cache_write(cache: PagedCache, k, Lk, v, Lv, slots, table: Optional[RopeTable] = None, positions=None,
+                pairs: str = "half", stream=None):
+    """lr_cache_write: the keys and values of len(slots) tokens, layouts (head_dim, heads, tokens), into
+    the cache's int64 ``slots`` (one outside the cache writes nothing), quantised as its type asks.  With
+    ``table`` and ``positions`` the keys are rotated first.  Returns the cache."""
+    _device_tensors(cache.k.device, k=k, v=v, slots=slots)
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must have the same type")
+    if slots.dtype != _torch().int64:
+        raise TypeError("slots must be int64")
+    n = slots.numel()
+    r = None
+    if table is not None:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _device_tensors(cache.k.device, positions=positions, table=table.turns)
+        if positions.numel() < n:
+            raise ValueError("positions needs one entry per slot")
+        r = _rotation(table, positions, pairs)
+    Lk, Lv = _as_layout(Lk), _as_layout(Lv)
+    _check(lib().lr_cache_write(cache.c, k.data_ptr(), Lk.c, k.numel(), v.data_ptr(), Lv.c, v.numel(),
+                                _dtype_code(k.dtype), slots.data_ptr(), n, r, _stream_ptr(stream)), "cache_write")
+    return cache
+
+
+def cache_read(cache: PagedCache, slots, k, Lk, v, Lv, stream=None):
+    """lr_cache_read: the cache's ``slots`` back into k and v, layouts (head_dim, heads, tokens); zeros
+    for a slot outside the cache.  Returns (k, v)."""
+    _device_tensors(cache.k.device, k=k, v=v, slots=slots)
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must have the same type")
+    if slots.dtype != _torch().int64:
+        raise TypeError("slots must be int64")
+    Lk, Lv = _as_layout(Lk), _as_layout(Lv)
+    _check(lib().lr_cache_read(cache.c, slots.data_ptr(), slots.numel(), k.data_ptr(), Lk.c, k.numel(), v.data_ptr(),
+                               Lv.c, v.numel(), _dtype_code(k.dtype), _stream_ptr(stream)), "cache_read")
+    return k, v
+
+
+def _mode_size(c: lr_layout, mode: int) -> int:
+    """Extent of a top-level mode (1 when the layout has fewer)."""
+    n = 1
+    if mode < c.nmodes:
+        for i in range(c.mode_end[mode - 1] if mode else 0, c.mode_end[mode]):
+            n *= c.shape[i]
+    return n
+
+
+def paged_attention_plan(Lq, cache: PagedCache, Lo, max_pages: int, dtype, window: int = 0) -> dict:
+    """lr_paged_attention_plan: the path, split and workspace of paged_attention (host only)."""
+    p = lr_attention_plan()
+    _check(lib().lr_paged_attention_plan(_as_layout(Lq).c, cache.c, _as_layout(Lo).c, max_pages, _dtype_code(dtype),
+                                         window, p), "paged_attention_plan")
+    return {"path": ATTENTION_PATH_NAMES[p.path], "head_tiles": p.head_tiles, "chunk": p.chunk, "splits": p.splits,
+            "workspace_bytes": p.workspace_bytes}
+
+
+def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: Optional[float] = None,
+                    window: int = 0, lse=None, workspace=None, stream=None):
+    """lr_paged_attention: attention of one token a sequence over the cache.  q, out: layouts (head_dim,
+    heads, sequences); ``page_table``: int32 (sequences, pages of the longest), rows contiguous; ``lens``:
+    int32, the tokens of each of the first len(lens) sequences.  ``scale``: 1/sqrt(head_dim) by default;
+    ``window``: the last tokens seen, 0 for all; ``lse``: float32 (sequences, heads) to fill;
+    ``workspace``: a byte tensor of the plan's size, allocated on the stream if not given.  Returns out."""
+    torch = _torch()
+    dev = cache.k.device
+    _device_tensors(dev, q=q, out=out, lens=lens)
+    if q.dtype != out.dtype:
+        raise TypeError("q and out must have the same type")
+    if page_table.dtype != torch.int32 or lens.dtype != torch.int32:
+        raise TypeError("page_table and lens must be int32")
+    if page_table.device != dev or page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise ValueError("page_table must be a 2-D GPU tensor with contiguous rows")
+    batch, max_pages = lens.numel(), page_table.shape[1]
+    if page_table.shape[0] < batch:
+        raise ValueError("page_table needs a row per sequence")
+    Lq, Lo = _as_layout(Lq), _as_layout(Lo)
+    code = _dtype_code(q.dtype)
+    lse_ptr = None
+    if lse is not None:
+        _device_tensors(dev, lse=lse)
+        if lse.dtype != torch.float32:
+            raise TypeError("lse must be float32")
+        if lse.numel() < batch * _mode_size(Lq.c, 1):
+            raise ValueError("lse needs one entry per sequence and head")
+        lse_ptr = lse.data_ptr()
+    if workspace is None:
+        need = paged_attention_plan(Lq, cache, Lo, max_pages, q.dtype, window)["workspace_bytes"]
+        if need:  # from the stream the kernels run on, so that its reuse waits for them
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.numel():
+        _device_tensors(dev, workspace=workspace)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    if scale is None:
+        scale = _mode_size(Lq.c, 0) ** -0.5
+    _check(lib().lr_paged_attention(q.data_ptr(), Lq.c, q.numel(), cache.c, page_table.data_ptr(),
+                                    page_table.stride(0), max_pages, lens.data_ptr(), batch, out.data_ptr(), Lo.c,
+                                    out.numel(), lse_ptr, code, scale, window,
+                                    workspace.data_ptr() if ws_bytes else None, ws_bytes, _stream_ptr(stream)),
+           "paged_attention")
+    return out

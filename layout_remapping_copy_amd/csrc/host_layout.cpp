@@ -747,6 +747,7 @@ const char* lr_strerror(int code) {
     case LR_ERR_PATH: return "forced copy path does not apply";
     case LR_ERR_OVERLAP: return "source and destination storage overlap";
     case LR_ERR_CAPACITY: return "output buffer too small";
+    case LR_ERR_TYPE: return "element type not supported here";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,277 @@
+// The paged cache of keys and values: lr_cache_validate, lr_cache_write, lr_cache_read.
+#include "op_common.h"
+
+namespace lr {
+
+int check_rotation(const lr_rotation* r, int64_t dim);
+
+constexpr int kCacheDim = 512;  // head_dim at most
+
+struct CacheSide {  // keys or values
+  void* cache;
+  float* scale;
+  void* rows;                 // the tensor written from or read to
+  ModeArg rh, rt;             // its heads and tokens
+  int64_t rd;                 // its head-dimension stride
+  int64_t cd, ch, cs, cp;     // cache strides: head dimension, heads, slots, pages
+  int32_t dim, rot;           // rot: rotated elements, 0 for none
+};
+
+struct CacheArgs {
+  CacheSide side[2];
+  int64_t sh, ss, sp;  // scale strides
+  const int64_t* slots;
+  const int64_t* turns;
+  const int64_t* positions;
+  float magnitude;
+  int32_t pairs;
+  int64_t cache_slots;
+  uint32_t page_size, heads, n;
+};
+
+// The code nearest x / scale, exactly: the fp32 quotient's remainder says which side of
+// the quotient the true value lies on, and a quotient that could be a tie (an even last
+// bit) is moved one step towards it.
+template <int DT>
+__device__ __forceinline__ typename ElemOf<DT>::T code_of(float x, float scale) {
+  constexpr float top = DT == LR_E4M3 ? 448.f : 127.f;
+  if (DT == LR_INT8 && x != x) return 0;
+  const float inv = 1.f / scale;  // scale >= 2^-126: finite
+  const float q0 = x * inv;
+  float q = __builtin_fmaf(__builtin_fmaf(-q0, scale, x), inv, q0);
+  const float rest = __builtin_fmaf(-q, scale, x);
+  const uint32_t bits = __float_as_uint(q);
+  if (!(bits & 1) && q != 0 && rest != 0 && __builtin_fabsf(q) < 2 * top)
+    q = __uint_as_float((rest > 0) == (q > 0) ? bits + 1 : bits - 1);
+  if (__builtin_fabsf(x) == __builtin_inff()) q = x;
+  if constexpr (DT == LR_E4M3) {
+    if (q == q) q = __builtin_fminf(__builtin_fmaxf(q, -top), top);
+    return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false) & 0xff);
+  } else {
+    return (int8_t)(int)__builtin_rintf(__builtin_fminf(__builtin_fmaxf(q, -top), top));
+  }
+}
+
+// One wave per row (token, head) of one side; a lane holds pairs lane, lane + 64, ...
+template <int DT, int CT>
+__global__ void __launch_bounds__(256) k_cache_write(CacheArgs a) {
+  using T = typename ElemOf<DT>::T;
+  using C = typename ElemOf<CT>::T;
+  const uint32_t lane = threadIdx.x & 63;
+  const uint64_t rows = 2ull * a.n * a.heads;
+  for (uint64_t row = (uint64_t)blockIdx.x * 4 + threadIdx.x / 64; row < rows; row += (uint64_t)gridDim.x * 4) {
+    const CacheSide& s = a.side[row & 1];
+    const uint32_t t = (uint32_t)((row >> 1) / a.heads), h = (uint32_t)((row >> 1) % a.heads);
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.cache_slots) continue;
+    const uint32_t page = (uint32_t)slot / a.page_size, in = (uint32_t)slot % a.page_size;
+    const T* x = (const T*)s.rows + mode_offset(s.rh, h) + mode_offset(s.rt, t);
+    C* y = (C*)s.cache + (int64_t)page * s.cp + (int64_t)in * s.cs + (int64_t)h * s.ch;
+    const uint32_t half = (uint32_t)s.rot / 2, units = half + (uint32_t)(s.dim - s.rot + 1) / 2;
+    float v[kCacheDim / 64];
+    float amax = 0;
+#pragma unroll
+    for (int k = 0; k < kCacheDim / 128; ++k) {
+      const uint32_t u = lane + 64 * k;
+      v[2 * k] = v[2 * k + 1] = 0;
+      if (u >= units) continue;
+      const bool turned = u < half;
+      const uint32_t i = !turned ? s.rot + 2 * (u - half) : a.pairs == LR_PAIRS_HALF ? u : 2 * u;
+      const uint32_t j = turned && a.pairs == LR_PAIRS_HALF ? u + half : i + 1;
+      float p = value_of<DT>(x[(int64_t)i * s.rd]), q = j < (uint32_t)s.dim ? value_of<DT>(x[(int64_t)j * s.rd]) : 0.f;
+      if (turned) {
+        float sn, cs;
+        sincos_turn((uint64_t)a.positions[t] * (uint64_t)a.turns[u], &sn, &cs);
+        sn *= a.magnitude;
+        cs *= a.magnitude;
+        const float w = p * cs - q * sn;
+        q = q * cs + p * sn;
+        p = w;
+      }
+      v[2 * k] = p;
+      v[2 * k + 1] = q;
+      if (__builtin_fabsf(p) < __builtin_inff()) amax = fmaxf(amax, __builtin_fabsf(p));
+      if (__builtin_fabsf(q) < __builtin_inff()) amax = fmaxf(amax, __builtin_fabsf(q));
+    }
+    float scale = 1;
+    if constexpr (CT == LR_E4M3 || CT == LR_INT8) {
+      for (int m = 32; m; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
+      scale = fmaxf(amax / (CT == LR_E4M3 ? 448.f : 127.f), 0x1p-126f);
+      if (lane == 0) s.scale[(int64_t)page * a.sp + (int64_t)in * a.ss + (int64_t)h * a.sh] = scale;
+    }
+#pragma unroll
+    for (int k = 0; k < kCacheDim / 128; ++k) {
+      const uint32_t u = lane + 64 * k;
+      if (u >= units) continue;
+      const bool turned = u < half;
+      const uint32_t i = !turned ? s.rot + 2 * (u - half) : a.pairs == LR_PAIRS_HALF ? u : 2 * u;
+      const uint32_t j = turned && a.pairs == LR_PAIRS_HALF ? u + half : i + 1;
+      if constexpr (CT == LR_E4M3 || CT == LR_INT8) {
+        y[(int64_t)i * s.cd] = code_of<CT>(v[2 * k], scale);
+        if (j < (uint32_t)s.dim) y[(int64_t)j * s.cd] = code_of<CT>(v[2 * k + 1], scale);
+      } else {
+        y[(int64_t)i * s.cd] = (C)v[2 * k];
+        if (j < (uint32_t)s.dim) y[(int64_t)j * s.cd] = (C)v[2 * k + 1];
+      }
+    }
+  }
+}
+
+template <int DT, int CT>
+__global__ void __launch_bounds__(256) k_cache_read(CacheArgs a) {
+  using T = typename ElemOf<DT>::T;
+  using C = typename ElemOf<CT>::T;
+  const uint32_t lane = threadIdx.x & 63;
+  const uint64_t rows = 2ull * a.n * a.heads;
+  for (uint64_t row = (uint64_t)blockIdx.x * 4 + threadIdx.x / 64; row < rows; row += (uint64_t)gridDim.x * 4) {
+    const CacheSide& s = a.side[row & 1];
+    const uint32_t t = (uint32_t)((row >> 1) / a.heads), h = (uint32_t)((row >> 1) % a.heads);
+    const int64_t slot = a.slots[t];
+    T* y = (T*)s.rows + mode_offset(s.rh, h) + mode_offset(s.rt, t);
+    const bool held = slot >= 0 && slot < a.cache_slots;
+    const uint32_t page = held ? (uint32_t)slot / a.page_size : 0, in = held ? (uint32_t)slot % a.page_size : 0;
+    const C* x = (const C*)s.cache + (int64_t)page * s.cp + (int64_t)in * s.cs + (int64_t)h * s.ch;
+    float scale = 1;
+    if constexpr (CT == LR_E4M3 || CT == LR_INT8) scale = s.scale[(int64_t)page * a.sp + (int64_t)in * a.ss + (int64_t)h * a.sh];
+    for (uint32_t e = lane; e < (uint32_t)s.dim; e += 64)
+      y[(int64_t)e * s.rd] = held ? (T)(value_of<CT>(x[(int64_t)e * s.cd]) * scale) : (T)0.f;
+  }
+}
+
+// The cache's own checks, and the part of the kernel arguments that comes from it.
+static int fill_cache(const lr_cache* c, CacheArgs* a) {
+  if (!c || !c->k || !c->v) return LR_ERR_INVALID;
+  const bool quant = is_quantised(c->dtype);
+  if (!quant && !is_model_type(c->dtype)) return LR_ERR_TYPE;
+  if (quant ? !c->k_scale || !c->v_scale : c->k_scale || c->v_scale) return LR_ERR_INVALID;
+  std::memset(a, 0, sizeof(*a));
+  const lr_layout* L[2] = {&c->k_layout, &c->v_layout};
+  const int64_t cap[2] = {c->k_capacity, c->v_capacity};
+  int64_t heads = 0, slots = 0, pages = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (int rc = check_tensor(L[i], 4, cap[i], true)) return rc;
+    CacheSide& s = a->side[i];
+    const Mode d = mode_of(*L[i], 0), h = mode_of(*L[i], 1), p = mode_of(*L[i], 2), g = mode_of(*L[i], 3);
+    if (one_leaf(d, &s.cd) || one_leaf(h, &s.ch) || one_leaf(p, &s.cs) || one_leaf(g, &s.cp)) return LR_ERR_INVALID;
+    if (d.size > kCacheDim) return LR_ERR_INVALID;
+    if (i && (h.size != heads || p.size != slots || g.size != pages)) return LR_ERR_SIZE_MISMATCH;
+    heads = h.size;
+    slots = p.size;
+    pages = g.size;
+    s.dim = (int32_t)d.size;
+    s.cache = i ? c->v : c->k;
+    s.scale = i ? c->v_scale : c->k_scale;
+  }
+  if (pages > kMaxCount / slots) return LR_ERR_OVERFLOW;
+  const int64_t e = dtype_bytes(c->dtype);
+  if (overlap(c->k, c->k_capacity * e, c->v, c->v_capacity * e)) return LR_ERR_OVERLAP;
+  if (quant) {
+    if (int rc = check_tensor(&c->scale_layout, 3, c->scale_capacity, true)) return rc;
+    const Mode h = mode_of(c->scale_layout, 0), p = mode_of(c->scale_layout, 1), g = mode_of(c->scale_layout, 2);
+    if (h.size != heads || p.size != slots || g.size != pages) return LR_ERR_SIZE_MISMATCH;
+    if (one_leaf(h, &a->sh) || one_leaf(p, &a->ss) || one_leaf(g, &a->sp)) return LR_ERR_INVALID;
+    if (overlap(c->k_scale, c->scale_capacity * 4, c->v_scale, c->scale_capacity * 4)) return LR_ERR_OVERLAP;
+  }
+  a->heads = (uint32_t)heads;
+  a->page_size = (uint32_t)slots;
+  a->cache_slots = pages * slots;
+  return LR_OK;
+}
+
+// The rows written from or read to.
+static int fill_rows(const lr_cache* c, CacheArgs* a, const void* k, const lr_layout* Lk, int64_t k_capacity,
+                     const void* v, const lr_layout* Lv, int64_t v_capacity, int32_t dtype, const int64_t* slots,
+                     int64_t n, bool output) {
+  if (!k || !v || n < 0 || (n > 0 && !slots)) return LR_ERR_INVALID;
+  if (!is_model_type(dtype) || (!is_quantised(c->dtype) && c->dtype != dtype)) return LR_ERR_TYPE;
+  const lr_layout* L[2] = {Lk, Lv};
+  const void* p[2] = {k, v};
+  const int64_t cap[2] = {k_capacity, v_capacity};
+  const int64_t e = dtype_bytes(dtype), ce = dtype_bytes(c->dtype);
+  for (int i = 0; i < 2; ++i) {
+    if (int rc = check_tensor(L[i], 3, cap[i], output)) return rc;
+    CacheSide& s = a->side[i];
+    const Mode d = mode_of(*L[i], 0), h = mode_of(*L[i], 1), t = mode_of(*L[i], 2);
+    if (one_leaf(d, &s.rd)) return LR_ERR_INVALID;
+    if (d.size != s.dim || h.size != (int64_t)a->heads) return LR_ERR_SIZE_MISMATCH;
+    if (n > t.size) return LR_ERR_BOUNDS;
+    s.rh = mode_arg(h);
+    s.rt = mode_arg(t);
+    s.rows = const_cast<void*>(p[i]);
+    if (overlap(p[i], cap[i] * e, c->k, c->k_capacity * ce) || overlap(p[i], cap[i] * e, c->v, c->v_capacity * ce))
+      return LR_ERR_OVERLAP;
+    if (is_quantised(c->dtype) && (overlap(p[i], cap[i] * e, c->k_scale, c->scale_capacity * 4) ||
+                                   overlap(p[i], cap[i] * e, c->v_scale, c->scale_capacity * 4)))
+      return LR_ERR_OVERLAP;
+  }
+  if (output && overlap(k, k_capacity * e, v, v_capacity * e)) return LR_ERR_OVERLAP;
+  a->slots = slots;
+  a->n = (uint32_t)n;
+  return LR_OK;
+}
+
+// Calls f<dtype, cache type>() for the pairs of types the cache takes.
+template <class F>
+static int with_types(int32_t dtype, int32_t ctype, F&& f) {
+#define LR_CACHE_CASE(D)                                                                  \
+  if (dtype == D) {                                                                       \
+    if (ctype == D) return f(std::integral_constant<int, D>{}, std::integral_constant<int, D>{});             \
+    if (ctype == LR_E4M3) return f(std::integral_constant<int, D>{}, std::integral_constant<int, LR_E4M3>{}); \
+    if (ctype == LR_INT8) return f(std::integral_constant<int, D>{}, std::integral_constant<int, LR_INT8>{}); \
+  }
+  LR_CACHE_CASE(LR_F32)
+  LR_CACHE_CASE(LR_F16)
+  LR_CACHE_CASE(LR_BF16)
+#undef LR_CACHE_CASE
+  return LR_ERR_TYPE;
+}
+
+}  // namespace lr
+
+using namespace lr;
+
+extern "C" {
+
+int lr_cache_validate(const lr_cache* c) {
+  CacheArgs a;
+  return fill_cache(c, &a);
+}
+
+int lr_cache_write(const lr_cache* c, const void* k, const lr_layout* Lk, int64_t k_capacity, const void* v,
+                   const lr_layout* Lv, int64_t v_capacity, int32_t dtype, const int64_t* slots, int64_t n,
+                   const lr_rotation* r, void* stream) {
+  CacheArgs a;
+  int rc = fill_cache(c, &a);
+  if (rc || (rc = fill_rows(c, &a, k, Lk, k_capacity, v, Lv, v_capacity, dtype, slots, n, false))) return rc;
+  if (r) {
+    if ((rc = check_rotation(r, a.side[0].dim))) return rc;
+    a.side[0].rot = r->rot_dim;
+    a.turns = r->turns;
+    a.positions = r->positions;
+    a.pairs = r->pairs;
+    a.magnitude = r->magnitude;
+  }
+  if (n == 0) return LR_OK;
+  const int64_t rows = 2 * n * (int64_t)a.heads, groups = std::min<int64_t>((rows + 3) / 4, 1 << 22);
+  return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
+    hipLaunchKernelGGL((k_cache_write<decltype(dt)::value, decltype(ct)::value>), dim3((unsigned)groups), dim3(256), 0,
+                       (hipStream_t)stream, a);
+    return check_op_launch();
+  });
+}
+
+int lr_cache_read(const lr_cache* c, const int64_t* slots, int64_t n, void* k, const lr_layout* Lk, int64_t k_capacity,
+                  void* v, const lr_layout* Lv, int64_t v_capacity, int32_t dtype, void* stream) {
+  CacheArgs a;
+  int rc = fill_cache(c, &a);
+  if (rc || (rc = fill_rows(c, &a, k, Lk, k_capacity, v, Lv, v_capacity, dtype, slots, n, true))) return rc;
+  if (n == 0) return LR_OK;
+  const int64_t rows = 2 * n * (int64_t)a.heads, groups = std::min<int64_t>((rows + 3) / 4, 1 << 22);
+  return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
+    hipLaunchKernelGGL((k_cache_read<decltype(dt)::value, decltype(ct)::value>), dim3((unsigned)groups), dim3(256), 0,
+                       (hipStream_t)stream, a);
+    return check_op_launch();
+  });
+}
+
+}  // extern "C"
