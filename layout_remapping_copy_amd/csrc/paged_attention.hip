@@ -28,6 +28,7 @@ struct AttentionArgs {
   uint32_t chunk, splits;
   int64_t window;
   float scale2;  // scale * log2 e
+  int32_t path, wide, tiles;  // host only: lr_attention_path and the matrix kernel's variant
 };
 
 // The tokens [first, n) a sequence sees; chunks start at `base`, first rounded down so
@@ -150,6 +151,412 @@ __global__ void __launch_bounds__(256) k_attention_element(AttentionArgs a) {
   }
 }
 
+// ------------------------------------------------------------------ matrix instructions
+
+typedef float F4 __attribute__((ext_vector_type(4)));
+typedef __bf16 B2 __attribute__((ext_vector_type(2)));
+typedef __bf16 B8 __attribute__((ext_vector_type(8)));
+typedef _Float16 H2 __attribute__((ext_vector_type(2)));
+typedef _Float16 H8 __attribute__((ext_vector_type(8)));
+typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+
+template <int BYTES> struct Raw { typedef uint32_t T __attribute__((ext_vector_type(BYTES / 4))); };
+template <> struct Raw<4> { typedef uint32_t T; };
+
+__device__ __forceinline__ F4 mfma(B8 a, B8 b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ F4 mfma(H8 a, H8 b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ F4 mfma(F4 a, F4 b, F4 c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+  return c;
+}
+
+template <int DT> struct MatrixOf { typedef F4 T; };
+template <> struct MatrixOf<LR_BF16> { typedef B8 T; };
+template <> struct MatrixOf<LR_F16> { typedef H8 T; };
+
+// Eight codes (8 bytes) as matrix elements of the model's type: both 8-bit types are exact in it.
+template <int DT, int CT>
+__device__ __forceinline__ typename MatrixOf<DT>::T decode(typename Raw<8>::T x) {
+  typename MatrixOf<DT>::T y;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    if constexpr (CT == LR_E4M3 && DT == LR_BF16) {
+      const B2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[d], 1.f, false);
+      const B2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[d], 1.f, true);
+      y[4 * d] = a[0], y[4 * d + 1] = a[1], y[4 * d + 2] = b[0], y[4 * d + 3] = b[1];
+    } else if constexpr (CT == LR_E4M3) {
+      const H2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[d], 1.f, false);
+      const H2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[d], 1.f, true);
+      y[4 * d] = a[0], y[4 * d + 1] = a[1], y[4 * d + 2] = b[0], y[4 * d + 3] = b[1];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[4 * d + e] = (typename ElemOf<DT>::T)(float)(int8_t)(x[d] >> (8 * e));
+    }
+  }
+  return y;
+}
+
+// Two codes (the low or the high half of x) as bf16.
+template <int CT, bool HIGH>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t x) {
+  if constexpr (CT == LR_E4M3) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.f, HIGH));
+  } else {
+    const B2 y = {(__bf16)(float)(int8_t)(x >> (HIGH ? 16 : 0)), (__bf16)(float)(int8_t)(x >> (HIGH ? 24 : 8))};
+    return __builtin_bit_cast(uint32_t, y);
+  }
+}
+
+__device__ __forceinline__ float across_groups_max(float x) {  // over lanes l, l ^ 16, l ^ 32
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float across_groups_sum(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+// Orders this wave's accesses to shared memory; one wave's are done in their order, so no wait is needed.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Keys and values up to DC wide; HT tiles of 16 query heads of one cache head.
+template <int DT, int CT, int DC, int HT>
+struct MatrixShape {
+  static constexpr bool kF32 = DT == LR_F32;
+  static constexpr int kElem = CT == LR_F32 ? 4 : CT == LR_E4M3 || CT == LR_INT8 ? 1 : 2;
+  static constexpr int kTiles = kF32 ? 1 : 2;                  // 16-token tiles of a wave's step
+  static constexpr int kTokens = 16 * kTiles;
+  static constexpr int kKeyChunk = kF32 ? 4 : 8;               // key elements a lane loads at a time
+  static constexpr int kKeySteps = DC / (4 * kKeyChunk);
+  static constexpr int kValChunk = kF32 || DC == 64 ? 4 : 8;   // value elements a lane loads at a time
+  static constexpr int kValSteps = DC / (16 * kValChunk);
+  static constexpr int kVals = 4 * kTiles;                     // value rows a lane loads in a step
+};
+
+// A workgroup has one chunk of one sequence and HT * 16 query heads that share a cache head; its four
+// waves take steps of 32 tokens (16 in fp32) in turn and join at the end.
+//
+// The scores of 16 tokens x 16 heads are a product of keys (rows) and queries (columns), so that a lane
+// (head = lane % 16, j = lane / 16) gets tokens 4j .. 4j + 3 of each tile: exactly the operand that the
+// second product, values transposed x weights, wants from it when its inner index runs over the tokens
+// in that order.  Weights never leave their lane.  Keys come from memory as the operand itself (16 rows,
+// each lane a chunk).  Values come as whole rows (a row a group of 16 lanes), eight rows a lane, and are
+// transposed within the lane by byte permutes; the output's column 8 r + m is then row r of product m.
+template <int DT, int CT, int DC, int HT>
+__global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
+  using S = MatrixShape<DT, CT, DC, HT>;
+  using T = typename ElemOf<DT>::T;
+  using M = typename MatrixOf<DT>::T;
+  using KR = typename Raw<S::kKeyChunk * S::kElem>::T;
+  using VR = typename Raw<S::kValChunk * S::kElem>::T;
+  constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
+  constexpr int kRow = 16 * S::kValChunk + 4;  // floats; the 4 keep 16 heads' accesses off one bank
+  __shared__ int64_t offs_all[4][64];
+  __shared__ __attribute__((aligned(16))) float scale_all[4][64];
+  __shared__ float ms[4][16 * HT], ls[4][16 * HT];
+  __shared__ __attribute__((aligned(16))) float os[4][16 * kRow];
+  const uint32_t lane = threadIdx.x & 63, w = threadIdx.x / 64, r = lane & 15, j = lane >> 4;
+  int64_t* offs = offs_all[w];
+  float* scales = scale_all[w];
+
+  const uint32_t split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
+  const uint32_t tiles = (a.group + 16 * HT - 1) / (16 * HT);
+  const uint32_t b = unit / (a.kv_heads * tiles), gt = unit % (a.kv_heads * tiles), g = gt / tiles;
+  const uint32_t in_group = (gt % tiles) * 16 * HT;  // first query head of this workgroup within its group
+  const Span sp = span_of(a, b);
+  const uint64_t lo = (uint64_t)sp.base + (uint64_t)split * a.chunk;
+  if (split && lo >= sp.n) return;
+  const uint32_t hi = (uint32_t)(lo + a.chunk < sp.n ? lo + a.chunk : sp.n);
+
+  // queries: lane r's head, dimensions chunk kk * 4 + j
+  M q[HT][S::kKeySteps];
+#pragma unroll
+  for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+    for (int kk = 0; kk < S::kKeySteps; ++kk) {
+      const uint32_t h = in_group + 16 * ht + r, e0 = (kk * 4 + j) * S::kKeyChunk;
+      const T* x = (const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group + h) * a.qh;
+#pragma unroll
+      for (int e = 0; e < S::kKeyChunk; ++e)
+        q[ht][kk][e] = h < a.group && e0 + e < (uint32_t)a.dk ? x[(int64_t)(e0 + e) * a.qd] : (T)0.f;
+    }
+
+  // Page lookup: lanes 0 .. and 32 .. find the pages of a step's tokens, the first for keys, the second
+  // for values; -1 for a token that is not seen.
+  const uint32_t li = lane & 31;
+  const bool for_v = lane >= 32;
+  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+  auto page_of = [&](uint64_t t0) -> int32_t {
+    const uint64_t t = t0 + li;
+    if (li >= (uint32_t)S::kTokens || t < sp.first || t >= hi) return -1;
+    return table[op_div((uint32_t)t, a.fd_page)];
+  };
+  const int64_t page_step = (for_v ? a.vp : a.kp) * S::kElem, slot_step = (for_v ? a.vsl : a.ksl) * S::kElem;
+  const float* scale_base = nullptr;
+  if constexpr (kQuant) scale_base = (for_v ? a.vs : a.ks) + (int64_t)g * a.sh;
+  const char* kbase = (const char*)a.k + (int64_t)g * a.kh * S::kElem;
+  const char* vbase = (const char*)a.v + (int64_t)g * a.vh * S::kElem;
+
+  // The step's row offsets to shared memory (0, the cache's first row, for a token that is not seen);
+  // returns the mask of its seen tokens.
+  auto place = [&](uint64_t t0, int32_t page, float* scale) -> uint32_t {
+    const uint32_t t = (uint32_t)(t0 + li), in = t - op_div(t, a.fd_page) * a.page_size;
+    const bool ok = page >= 0 && (uint32_t)page < a.pages;
+    wave_fence();
+    offs[lane] = ok ? page * page_step + in * slot_step : 0;
+    wave_fence();
+    if constexpr (kQuant) *scale = ok ? scale_base[page * a.sp + (int64_t)in * a.ssl] : 0.f;
+    return (uint32_t)__ballot(ok);
+  };
+
+  KR kr[S::kTiles][S::kKeySteps];
+  VR vr[S::kVals][S::kValSteps];
+  auto load_keys = [&]() {
+#pragma unroll
+    for (int t = 0; t < S::kTiles; ++t) {
+      const char* row = kbase + offs[16 * t + r];
+#pragma unroll
+      for (int kk = 0; kk < S::kKeySteps; ++kk) {
+        const uint32_t e0 = (kk * 4 + j) * S::kKeyChunk;
+        kr[t][kk] = KR{};
+        if (e0 < (uint32_t)a.dk) kr[t][kk] = *(const KR*)(row + e0 * S::kElem);
+      }
+    }
+  };
+  auto load_values = [&]() {
+#pragma unroll
+    for (int x = 0; x < S::kVals; ++x) {
+      const char* row = vbase + offs[32 + 16 * (x / 4) + 4 * j + x % 4];
+#pragma unroll
+      for (int p = 0; p < S::kValSteps; ++p) {
+        const uint32_t e0 = (p * 16 + r) * S::kValChunk;
+        vr[x][p] = *(const VR*)(row + (e0 < (uint32_t)a.dv ? e0 : 0) * S::kElem);  // past dv: rows of no output
+      }
+    }
+  };
+
+  F4 o[HT][S::kValSteps][S::kValChunk] = {};
+  float base[HT], l[HT];  // scores are taken off `base`, at most 8 below the running maximum
+#pragma unroll
+  for (int ht = 0; ht < HT; ++ht) base[ht] = -__FLT_MAX__, l[ht] = 0;
+  constexpr uint32_t kAll = S::kTokens == 32 ? 0xffffffffu : 0xffffu;
+
+  constexpr uint32_t kStep = 4 * S::kTokens;
+  uint64_t t0 = lo + w * S::kTokens;
+  if (t0 < hi) {
+    float sc = 0, sc_next = 0;
+    uint32_t seen = place(t0, page_of(t0), &sc);
+    int32_t page = page_of(t0 + kStep);
+    load_keys();
+    load_values();
+    for (;;) {
+      const bool more = t0 + kStep < hi;
+      // scores
+      F4 s[HT][S::kTiles];
+#pragma unroll
+      for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+          s[ht][t] = F4{};
+#pragma unroll
+          for (int kk = 0; kk < S::kKeySteps; ++kk) {
+            M k;
+            if constexpr (kQuant)
+              k = decode<DT, CT>(kr[t][kk]);
+            else
+              k = __builtin_bit_cast(M, kr[t][kk]);
+            s[ht][t] = mfma(k, q[ht][kk], s[ht][t]);
+          }
+        }
+      F4 ksc[S::kTiles], vsc[S::kTiles];
+      if constexpr (kQuant) {
+        wave_fence();
+        scales[lane] = sc;
+        wave_fence();
+#pragma unroll
+        for (int t = 0; t < S::kTiles; ++t) {
+          ksc[t] = *(const F4*)&scales[16 * t + 4 * j] * a.scale2;
+          vsc[t] = *(const F4*)&scales[32 + 16 * t + 4 * j];
+        }
+      }
+      uint32_t seen_next = 0;
+      if (more) {
+        seen_next = place(t0 + kStep, page, &sc_next);
+        page = page_of(t0 + 2 * kStep);
+        load_keys();
+      }
+      // weights
+      M pw[HT];
+      B8 phi[HT], plo[HT];
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int t = 0; t < S::kTiles; ++t) {
+          if constexpr (kQuant)
+            s[ht][t] *= ksc[t];
+          else
+            s[ht][t] *= a.scale2;
+          if (seen != kAll)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              s[ht][t][i] = (seen >> (16 * t + 4 * j + i)) & 1 ? s[ht][t][i] : -__builtin_inff();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, s[ht][t][i]);
+        }
+        if (__any(top > base[ht] + 8.f)) {
+          top = fmaxf(base[ht], across_groups_max(top));
+          const float keep = __builtin_amdgcn_exp2f(base[ht] - top);
+          base[ht] = top;
+          l[ht] *= keep;
+#pragma unroll
+          for (int p = 0; p < S::kValSteps; ++p)
+#pragma unroll
+            for (int m = 0; m < S::kValChunk; ++m) o[ht][p][m] *= keep;
+        }
+#pragma unroll
+        for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = __builtin_amdgcn_exp2f(s[ht][t][i] - base[ht]);
+            l[ht] += x;
+            if constexpr (kQuant) {
+              // two bf16 parts hold 16 bits of weight * scale: a bf16 alone would cost an fp16 model
+              // its last three bits
+              x *= vsc[t][i];
+              phi[ht][4 * t + i] = (__bf16)x;
+              plo[ht][4 * t + i] = (__bf16)(x - (float)phi[ht][4 * t + i]);
+            } else {
+              pw[ht][4 * t + i] = (T)x;
+            }
+          }
+      }
+      if (seen != kAll)  // what is not seen may hold NaN
+#pragma unroll
+        for (int x = 0; x < S::kVals; ++x)
+          if (!((seen >> (16 * (x / 4) + 4 * j + x % 4)) & 1))
+#pragma unroll
+            for (int p = 0; p < S::kValSteps; ++p) vr[x][p] = VR{};
+      // values
+#pragma unroll
+      for (int p = 0; p < S::kValSteps; ++p) {
+        if constexpr (S::kF32) {
+#pragma unroll
+          for (int m = 0; m < S::kValChunk; ++m)
+#pragma unroll
+            for (int ht = 0; ht < HT; ++ht)
+              o[ht][p][m] = mfma(F4{__uint_as_float(vr[0][p][m]), __uint_as_float(vr[1][p][m]),
+                                    __uint_as_float(vr[2][p][m]), __uint_as_float(vr[3][p][m])}, pw[ht], o[ht][p][m]);
+        } else if constexpr (kQuant) {
+#pragma unroll
+          for (int d = 0; d < S::kValChunk / 4; ++d) {
+            auto word = [&](int x) { if constexpr (S::kValChunk == 4) return vr[x][p]; else return vr[x][p][d]; };
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // columns 4 d + 2 half and the next
+              U4 v0, v1;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t y = __builtin_amdgcn_perm(word(2 * x + 1), word(2 * x), half ? 0x07030602 : 0x05010400);
+                v0[x] = decode_pair<CT, false>(y);
+                v1[x] = decode_pair<CT, true>(y);
+              }
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht) {
+                F4& oa = o[ht][p][4 * d + 2 * half];
+                F4& ob = o[ht][p][4 * d + 2 * half + 1];
+                oa = mfma(__builtin_bit_cast(B8, v0), phi[ht], oa);
+                ob = mfma(__builtin_bit_cast(B8, v1), phi[ht], ob);
+                oa = mfma(__builtin_bit_cast(B8, v0), plo[ht], oa);
+                ob = mfma(__builtin_bit_cast(B8, v1), plo[ht], ob);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int d = 0; d < S::kValChunk / 2; ++d) {  // columns 2 d and the next
+            U4 v0, v1;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              v0[x] = __builtin_amdgcn_perm(vr[2 * x + 1][p][d], vr[2 * x][p][d], 0x05040100);
+              v1[x] = __builtin_amdgcn_perm(vr[2 * x + 1][p][d], vr[2 * x][p][d], 0x07060302);
+            }
+#pragma unroll
+            for (int ht = 0; ht < HT; ++ht) {
+              o[ht][p][2 * d] = mfma(__builtin_bit_cast(M, v0), pw[ht], o[ht][p][2 * d]);
+              o[ht][p][2 * d + 1] = mfma(__builtin_bit_cast(M, v1), pw[ht], o[ht][p][2 * d + 1]);
+            }
+          }
+        }
+      }
+      if (!more) break;
+      load_values();
+      seen = seen_next;
+      sc = sc_next;
+      t0 += kStep;
+    }
+  }
+
+  // join the waves: maxima and sums, then 16 heads x 16 chunks of columns at a time
+#pragma unroll
+  for (int ht = 0; ht < HT; ++ht) {
+    const float sum = across_groups_sum(l[ht]);
+    if (j == 0) {
+      ms[w][16 * ht + r] = base[ht] == -__FLT_MAX__ ? -__builtin_inff() : base[ht];
+      ls[w][16 * ht + r] = sum;
+    }
+  }
+#pragma unroll
+  for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+    for (int p = 0; p < S::kValSteps; ++p) {
+      if (ht || p) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < S::kValChunk; m += 4)
+          *(F4*)&os[w][r * kRow + (4 * j + i) * S::kValChunk + m] =
+              F4{o[ht][p][m][i], o[ht][p][m + 1][i], o[ht][p][m + 2][i], o[ht][p][m + 3][i]};
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < S::kValChunk / 4; ++x) {
+        const uint32_t at = threadIdx.x + 256 * x, hd = at / (4 * S::kValChunk), c4 = at % (4 * S::kValChunk) * 4;
+        const uint32_t h = in_group + 16 * ht + hd, e = p * 16 * S::kValChunk + c4;
+        if (h >= a.group || e >= (uint32_t)a.dv) continue;
+        float m4[4], top = -__builtin_inff(), total = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, m4[i] = ms[i][16 * ht + hd]);
+        F4 acc = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float wt = weight_of(m4[i], top);
+          total += ls[i][16 * ht + hd] * wt;
+          acc += *(const F4*)&os[i][hd * kRow + c4] * wt;
+        }
+        const uint32_t bh = b * a.heads + g * a.group + h;
+        if (a.splits == 1) {
+          T* out = (T*)a.out + (int64_t)b * a.ob + (int64_t)(g * a.group + h) * a.oh;
+          const float inv = total > 0 ? 1.f / total : 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[(int64_t)(e + i) * a.od] = (T)(total != total ? total : acc[i] * inv);
+        } else {
+          *(F4*)&a.part_o[((uint64_t)bh * a.splits + split) * a.dv + e] = acc;
+        }
+        if (e == 0) {
+          if (a.splits > 1) {
+            a.part_ml[2 * ((uint64_t)bh * a.splits + split)] = top;
+            a.part_ml[2 * ((uint64_t)bh * a.splits + split) + 1] = total;
+          } else if (a.lse) {
+            a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
+          }
+        }
+      }
+    }
+}
+
 // Joins the chunks of one query head in their order.
 template <int DT>
 __global__ void __launch_bounds__(256) k_attention_join(AttentionArgs a) {
@@ -216,8 +623,16 @@ static int plan_attention(const lr_layout* Lq, const lr_cache* c, const lr_layou
   a->v = c->v;
   a->ks = c->k_scale;
   a->vs = c->v_scale;
-  out->path = LR_ATTENTION_ELEMENT;
-  out->head_tiles = (int32_t)a->group;
+  // The matrix kernel wants rows of whole chunks: a multiple of 8 elements (4 in fp32), contiguous and
+  // that much aligned.  Rows of an 8-bit cache under an fp32 model have no matrix form.
+  const int64_t v = c->dtype == LR_F32 ? 4 : 8;
+  const bool matrix = !(dtype == LR_F32 && is_quantised(c->dtype)) && kd.size % v == 0 && vd.size % v == 0 &&
+                      rows_aligned(c->k_layout, nullptr, dtype_bytes(c->dtype), v) &&
+                      rows_aligned(c->v_layout, nullptr, dtype_bytes(c->dtype), v);
+  out->path = matrix ? LR_ATTENTION_MATRIX : LR_ATTENTION_ELEMENT;
+  a->wide = std::max(kd.size, vd.size) <= 64 ? 64 : std::max(kd.size, vd.size) <= 128 ? 128 : 256;
+  a->tiles = a->group > 16 && a->wide < 256 ? 2 : 1;
+  out->head_tiles = (int32_t)(matrix ? (a->group + 16 * a->tiles - 1) / (16 * a->tiles) : a->group);
   int64_t span = max_pages * ks.size;
   if (window > 0) span = std::min(span, window + 31);
   const double work = (double)span * (double)qb.size * a->kv_heads * out->head_tiles;
@@ -236,7 +651,21 @@ static int plan_attention(const lr_layout* Lq, const lr_cache* c, const lr_layou
 template <int DT, int CT>
 static int launch_attention(const AttentionArgs& a, hipStream_t st) {
   const uint32_t rows = a.batch * a.heads;
-  hipLaunchKernelGGL((k_attention_element<DT, CT>), dim3(rows * a.splits), dim3(256), 0, st, a);
+  if (a.path == LR_ATTENTION_ELEMENT) {
+    hipLaunchKernelGGL((k_attention_element<DT, CT>), dim3(rows * a.splits), dim3(256), 0, st, a);
+  } else if constexpr (!(DT == LR_F32 && CT != LR_F32)) {
+    const dim3 grid(a.batch * a.kv_heads * ((a.group + 16 * a.tiles - 1) / (16 * a.tiles)) * a.splits);
+    if (a.wide == 64 && a.tiles == 1)
+      hipLaunchKernelGGL((k_attention_matrix<DT, CT, 64, 1>), grid, dim3(256), 0, st, a);
+    else if (a.wide == 64)
+      hipLaunchKernelGGL((k_attention_matrix<DT, CT, 64, 2>), grid, dim3(256), 0, st, a);
+    else if (a.wide == 128 && a.tiles == 1)
+      hipLaunchKernelGGL((k_attention_matrix<DT, CT, 128, 1>), grid, dim3(256), 0, st, a);
+    else if (a.wide == 128)
+      hipLaunchKernelGGL((k_attention_matrix<DT, CT, 128, 2>), grid, dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((k_attention_matrix<DT, CT, 256, 1>), grid, dim3(256), 0, st, a);
+  }
   if (int rc = check_op_launch()) return rc;
   if (a.splits == 1) return LR_OK;
   hipLaunchKernelGGL((k_attention_join<DT>), dim3(rows), dim3(256), 0, st, a);
@@ -299,6 +728,9 @@ int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, c
   a.scale2 = scale * kLog2e;
   a.part_o = (float*)workspace;
   a.part_ml = (float*)workspace + (p.workspace_bytes / 4 - 2 * (int64_t)mode_of(*Lq, 2).size * a.heads * p.splits);
+  const uintptr_t align = c->dtype == LR_F32 || !is_quantised(c->dtype) ? 16 : 8;  // bytes of a chunk
+  a.path = p.path == LR_ATTENTION_MATRIX && (uintptr_t)c->k % align == 0 && (uintptr_t)c->v % align == 0
+               ? LR_ATTENTION_MATRIX : LR_ATTENTION_ELEMENT;
   const hipStream_t st = (hipStream_t)stream;
   if (dtype == LR_F32) return launch_attention_of<LR_F32>(a, c->dtype, st);
   if (dtype == LR_F16) return launch_attention_of<LR_F16>(a, c->dtype, st);
