@@ -25,23 +25,149 @@ struct AttentionArgs {
   int32_t dk, dv;
   uint32_t heads, kv_heads, group, page_size, pages, max_pages, batch;
   FastDiv fd_page;
-  uint32_t chunk, splits;
+  uint32_t unit_heads, tiles, units;  // query heads of a unit, units of a cache head, units of a sequence
+  uint32_t splits, min_share;         // parts of a unit at most; blocks of a workgroup at least
+  uint32_t grid;                      // workgroups (splits > 1; else one a unit)
   int64_t window;
+  bool q_wide;   // query rows are contiguous and 16-byte aligned
   float scale2;  // scale * log2 e
-  int32_t path, wide, tiles;  // host only: lr_attention_path and the matrix kernel's variant
+  int32_t path, wide;         // host only: lr_attention_path and the matrix kernel's variant
 };
 
-// The tokens [first, n) a sequence sees; chunks start at `base`, first rounded down so
-// that their tiles stay aligned to 32 tokens.
+// The work is split evenly however uneven the sequences are.  A unit is one sequence's tokens for the
+// query heads that one workgroup takes together (unit_heads of one cache head); its tokens are cut into
+// blocks of kBlock.  All blocks of all units, in order, are dealt out to `used` workgroups in equal runs:
+// workgroup w has the blocks [w T / used, (w + 1) T / used) of T.  A run that starts or ends inside a unit
+// leaves a part of it, joined by a second launch.  A unit of n blocks meets at most
+// 1 + ceil((n - 1) / min_share) runs, as none is shorter than min_share.
+constexpr uint32_t kBlock = 128;
+
+// The tokens [first, n) a sequence sees; blocks start at `base`, first rounded down so that steps of 32
+// tokens stay aligned.  A sequence without tokens has one (empty) block, so that it is written too.
 struct Span {
-  uint32_t base, first, n;
+  uint32_t base, first, n, blocks;
 };
 __device__ __forceinline__ Span span_of(const AttentionArgs& a, uint32_t b) {
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
   int64_t n = a.lens[b];
   n = n < 0 ? 0 : n > cap ? cap : n;
   const int64_t first = a.window > 0 && n > a.window ? n - a.window : 0;
-  return Span{(uint32_t)first & ~31u, (uint32_t)first, (uint32_t)n};
+  const uint32_t base = (uint32_t)first & ~31u;
+  const uint32_t blocks = ((uint32_t)n - base + kBlock - 1) / kBlock;
+  return Span{base, (uint32_t)first, (uint32_t)n, blocks ? blocks : 1};
+}
+
+struct Deal {
+  uint64_t total;
+  uint32_t used;
+};
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint64_t uniform64(uint64_t x) {
+  return uniform((uint32_t)x) | (uint64_t)uniform((uint32_t)(x >> 32)) << 32;
+}
+__device__ __forceinline__ Deal deal_of(const AttentionArgs& a, uint64_t blocks) {  // blocks of one unit each, all sequences
+  const uint64_t total = uniform64(blocks) * a.units, most = total / a.min_share;
+  return Deal{total, (uint32_t)(most < 1 ? 1 : most < a.grid ? most : a.grid)};
+}
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v, uint32_t lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t u = __shfl_up((unsigned long long)v, d);
+    if (lane >= (uint32_t)d) v += u;
+  }
+  return v;
+}
+// Where the blocks of sequence b start, with the deal.  Every wave computes it for itself.
+__device__ __forceinline__ uint64_t blocks_before(const AttentionArgs& a, uint32_t b, Deal* deal) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint64_t all = 0, before = 0;
+  for (uint32_t i = lane; i < a.batch; i += 64) {
+    const uint64_t n = span_of(a, i).blocks;
+    all += n;
+    before += i < b ? n : 0;
+  }
+  for (int x = 32; x; x >>= 1) {
+    all += __shfl_xor((unsigned long long)all, x);
+    before += __shfl_xor((unsigned long long)before, x);
+  }
+  *deal = deal_of(a, all);
+  return uniform64(before) * a.units;
+}
+__device__ __forceinline__ uint64_t run_start(const Deal& d, uint64_t w) { return w * d.total / d.used; }
+__device__ __forceinline__ uint32_t run_of(const Deal& d, uint64_t block) {
+  return (uint32_t)(((block + 1) * d.used - 1) / d.total);
+}
+
+// One workgroup's way through its run, a unit at a time.
+struct Run {
+  Deal deal;
+  uint64_t at, end;  // blocks
+  uint64_t start;    // of the current unit
+  uint32_t b, u;     // the current unit: sequence, and its number there
+  uint32_t split;    // the part of it that this run has
+  bool whole;        // all of it
+  Span sp;
+  uint32_t lo, hi;   // its tokens
+};
+__device__ __forceinline__ void run_unit(const AttentionArgs& a, uint32_t w, Run* r) {
+  const uint64_t left = r->start + r->sp.blocks, stop = r->end < left ? r->end : left;
+  r->whole = r->at == r->start && stop == left;
+  r->split = r->whole ? 0 : w - run_of(r->deal, r->start);
+  r->lo = r->sp.base + (uint32_t)(r->at - r->start) * kBlock;
+  const uint64_t hi = (uint64_t)r->sp.base + (stop - r->start) * kBlock;
+  r->hi = hi < r->sp.n ? (uint32_t)hi : r->sp.n;
+}
+__device__ __forceinline__ bool run_begin(const AttentionArgs& a, Run* r) {
+  const uint32_t lane = threadIdx.x & 63;
+  if (a.splits == 1) {  // one unit a workgroup
+    r->b = blockIdx.x / a.units;
+    r->u = blockIdx.x % a.units;
+    r->sp = span_of(a, r->b);
+    r->deal = Deal{1, 1};
+    r->at = r->start = 0;
+    r->end = r->sp.blocks;
+  } else {
+    uint64_t v = lane < a.batch ? span_of(a, lane).blocks : 0;
+    uint64_t upto = wave_scan(v, lane);  // the first 64 sequences
+    if (a.batch <= 64) {
+      r->deal = deal_of(a, __shfl((unsigned long long)upto, 63));
+    } else {
+      blocks_before(a, 0, &r->deal);
+    }
+    if (blockIdx.x >= r->deal.used) return false;
+    r->at = run_start(r->deal, blockIdx.x);
+    r->end = run_start(r->deal, blockIdx.x + 1);
+    uint64_t past = 0;  // blocks of the sequences before the 64 looked at
+    for (uint32_t i = 0;; i += 64) {
+      const uint64_t hit = __ballot((past + upto) * a.units > r->at);
+      if (hit) {
+        const int f = __ffsll((unsigned long long)hit) - 1;
+        r->b = i + f;
+        r->start = (past + uniform64(__shfl((unsigned long long)(upto - v), f))) * a.units;
+        break;
+      }
+      past += uniform64(__shfl((unsigned long long)upto, 63));
+      v = i + 64 + lane < a.batch ? span_of(a, i + 64 + lane).blocks : 0;
+      upto = wave_scan(v, lane);
+    }
+    r->sp = span_of(a, r->b);
+    r->u = (uint32_t)((r->at - r->start) / r->sp.blocks);
+    r->start += (uint64_t)r->u * r->sp.blocks;
+  }
+  run_unit(a, blockIdx.x, r);
+  return true;
+}
+__device__ __forceinline__ bool run_next(const AttentionArgs& a, Run* r) {
+  r->start += r->sp.blocks;
+  r->at = r->start;
+  if (r->at >= r->end) return false;
+  if (++r->u == a.units) {
+    r->u = 0;
+    r->sp = span_of(a, ++r->b);
+  }
+  run_unit(a, blockIdx.x, r);
+  return true;
 }
 
 // Weight 2^(m - top) of a part with maximum m among parts with maximum top; 0 for a part
@@ -50,8 +176,8 @@ __device__ __forceinline__ float weight_of(float m, float top) {
   return m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - top);
 }
 
-// Any types, strides and alignment.  A workgroup has one chunk of one query head; its
-// waves take tiles of 64 tokens in turn, a lane a token for the scores and every 64th
+// Any types, strides and alignment.  A unit is one query head; a workgroup's
+// waves take tiles of 64 tokens of its run in turn, a lane a token for the scores and every 64th
 // value column for the sums.
 template <int DT, int CT>
 __global__ void __launch_bounds__(256) k_attention_element(AttentionArgs a) {
@@ -62,13 +188,14 @@ __global__ void __launch_bounds__(256) k_attention_element(AttentionArgs a) {
   __shared__ int64_t at[4][64];
   __shared__ float os[4][kAttentionDim];
   __shared__ float ms[4], ls[4];
-  const uint32_t lane = threadIdx.x & 63, w = threadIdx.x / 64;
-  const uint32_t split = blockIdx.x % a.splits, bh = blockIdx.x / a.splits, b = bh / a.heads, h = bh % a.heads;
-  const uint32_t g = h / a.group;
-  const Span sp = span_of(a, b);
-  const uint64_t lo = (uint64_t)sp.base + (uint64_t)split * a.chunk;
-  if (split && lo >= sp.n) return;
-  const uint32_t hi = (uint32_t)(lo + a.chunk < sp.n ? lo + a.chunk : sp.n);
+  const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
+  Run run;
+  if (!run_begin(a, &run)) return;
+  do {
+  const uint32_t b = run.b, h = run.u, g = h / a.group, bh = b * a.heads + h, split = run.split, hi = run.hi;
+  const uint64_t lo = run.lo;
+  const Span sp = run.sp;
+  __syncthreads();
   for (uint32_t e = threadIdx.x; e < (uint32_t)a.dk; e += 256)
     qs[e] = value_of<DT>(((const T*)a.q)[(int64_t)b * a.qb + (int64_t)h * a.qh + (int64_t)e * a.qd]) * a.scale2;
   __syncthreads();
@@ -136,19 +263,20 @@ __global__ void __launch_bounds__(256) k_attention_element(AttentionArgs a) {
   if (e < (uint32_t)a.dv) {
     float acc = 0;
     for (int i = 0; i < 4; ++i) acc += os[i][e] * wt[i];
-    if (a.splits == 1)
+    if (run.whole)
       ((T*)a.out)[(int64_t)b * a.ob + (int64_t)h * a.oh + (int64_t)e * a.od] = (T)(total > 0 ? acc / total : 0.f * acc);
     else
       a.part_o[((uint64_t)bh * a.splits + split) * a.dv + e] = acc;
   }
   if (threadIdx.x == 0) {
-    if (a.splits > 1) {
+    if (!run.whole) {
       a.part_ml[2 * ((uint64_t)bh * a.splits + split)] = top;
       a.part_ml[2 * ((uint64_t)bh * a.splits + split) + 1] = total;
     } else if (a.lse) {
       a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
     }
   }
+  } while (run_next(a, &run));
 }
 
 // ------------------------------------------------------------------ matrix instructions
@@ -208,6 +336,12 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t x) {
   }
 }
 
+// x itself, unknown to the compiler: what is computed from it is not kept in registers over the loop around.
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 __device__ __forceinline__ float across_groups_max(float x) {  // over lanes l, l ^ 16, l ^ 32
   x = fmaxf(x, __shfl_xor(x, 16));
   return fmaxf(x, __shfl_xor(x, 32));
@@ -230,7 +364,9 @@ struct MatrixShape {
   static constexpr int kElem = CT == LR_F32 ? 4 : CT == LR_E4M3 || CT == LR_INT8 ? 1 : 2;
   static constexpr int kTiles = kF32 ? 1 : 2;                  // 16-token tiles of a wave's step
   static constexpr int kTokens = 16 * kTiles;
-  static constexpr int kKeyChunk = kF32 ? 4 : 8;               // key elements a lane loads at a time
+  static constexpr int kPart = kF32 ? 4 : 8;                   // inner elements a lane gives one product
+  static constexpr int kKeyChunk = 16 / kElem;                 // key elements a lane loads at a time
+  static constexpr int kKeyParts = kKeyChunk / kPart;
   static constexpr int kKeySteps = DC / (4 * kKeyChunk);
   static constexpr int kValChunk = kF32 || DC == 64 ? 4 : 8;   // value elements a lane loads at a time
   static constexpr int kValSteps = DC / (16 * kValChunk);
@@ -251,7 +387,8 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
   using S = MatrixShape<DT, CT, DC, HT>;
   using T = typename ElemOf<DT>::T;
   using M = typename MatrixOf<DT>::T;
-  using KR = typename Raw<S::kKeyChunk * S::kElem>::T;
+  typedef U4 KR __attribute__((aligned(8)));  // rows of 8-bit caches are aligned to 8 elements
+  typedef typename Raw<8>::T KHalf;
   using VR = typename Raw<S::kValChunk * S::kElem>::T;
   constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
   constexpr int kRow = 16 * S::kValChunk + 4;  // floats; the 4 keep 16 heads' accesses off one bank
@@ -259,41 +396,51 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
   __shared__ __attribute__((aligned(16))) float scale_all[4][64];
   __shared__ float ms[4][16 * HT], ls[4][16 * HT];
   __shared__ __attribute__((aligned(16))) float os[4][16 * kRow];
-  const uint32_t lane = threadIdx.x & 63, w = threadIdx.x / 64, r = lane & 15, j = lane >> 4;
+  const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64), r = lane & 15, j = lane >> 4;
   int64_t* offs = offs_all[w];
   float* scales = scale_all[w];
 
-  const uint32_t split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
-  const uint32_t tiles = (a.group + 16 * HT - 1) / (16 * HT);
-  const uint32_t b = unit / (a.kv_heads * tiles), gt = unit % (a.kv_heads * tiles), g = gt / tiles;
-  const uint32_t in_group = (gt % tiles) * 16 * HT;  // first query head of this workgroup within its group
-  const Span sp = span_of(a, b);
-  const uint64_t lo = (uint64_t)sp.base + (uint64_t)split * a.chunk;
-  if (split && lo >= sp.n) return;
-  const uint32_t hi = (uint32_t)(lo + a.chunk < sp.n ? lo + a.chunk : sp.n);
+  Run run;
+  if (!run_begin(a, &run)) return;
+  for (bool again = false;; again = true) {
+  const uint32_t b = run.b, g = run.u / a.tiles, split = run.split, hi = run.hi;
+  const uint32_t in_group = run.u % a.tiles * 16 * HT;  // first query head of this unit within its group
+  const Span sp = run.sp;
+  const uint32_t lo = run.lo;
 
   // queries: lane r's head, dimensions chunk kk * 4 + j
-  M q[HT][S::kKeySteps];
+  const uint32_t rq = here(r), jq = here(j);
+  M q[HT][S::kKeySteps * S::kKeyParts];
 #pragma unroll
-  for (int ht = 0; ht < HT; ++ht)
+  for (int ht = 0; ht < HT; ++ht) {
+    const uint32_t h = in_group + 16 * ht + rq;
+    const T* x = (const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group + h) * a.qh;
 #pragma unroll
-    for (int kk = 0; kk < S::kKeySteps; ++kk) {
-      const uint32_t h = in_group + 16 * ht + r, e0 = (kk * 4 + j) * S::kKeyChunk;
-      const T* x = (const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group + h) * a.qh;
+    for (int kk = 0; kk < S::kKeySteps * S::kKeyParts; ++kk) {
+      const uint32_t e0 = ((kk / S::kKeyParts * 4 + jq) * S::kKeyParts + kk % S::kKeyParts) * S::kPart;
+      q[ht][kk] = M{};
+      if (h < a.group && e0 < (uint32_t)a.dk) {
+        if (a.q_wide) {
+          q[ht][kk] = *(const M*)(x + e0);
+        } else {
 #pragma unroll
-      for (int e = 0; e < S::kKeyChunk; ++e)
-        q[ht][kk][e] = h < a.group && e0 + e < (uint32_t)a.dk ? x[(int64_t)(e0 + e) * a.qd] : (T)0.f;
+          for (int e = 0; e < S::kPart; ++e) q[ht][kk][e] = x[(int64_t)(e0 + e) * a.qd];
+        }
+      }
     }
+  }
 
   // Page lookup: lanes 0 .. and 32 .. find the pages of a step's tokens, the first for keys, the second
-  // for values; -1 for a token that is not seen.
-  const uint32_t li = lane & 31;
+  // for values.  All loads of the loop below are unconditional, so that each wait is for the loads it
+  // needs and no younger ones: what is not there is read from a place that is, and left out after.
+  const uint32_t li = lane & (S::kTokens - 1);
   const bool for_v = lane >= 32;
   const int32_t* table = a.table + (int64_t)b * a.table_stride;
-  auto page_of = [&](uint64_t t0) -> int32_t {
-    const uint64_t t = t0 + li;
-    if (li >= (uint32_t)S::kTokens || t < sp.first || t >= hi) return -1;
-    return table[op_div((uint32_t)t, a.fd_page)];
+  const uint32_t one = a.fd_page.m ? 0 : ~0u;  // pages of one slot: the quotient is the dividend
+  auto page_index = [&](uint32_t t) -> uint32_t { return (__umulhi(t, a.fd_page.m) >> a.fd_page.s) + (t & one); };
+  auto page_of = [&](uint32_t t0) -> int32_t {
+    const uint32_t t = t0 + li;
+    return table[page_index(t < hi ? t : hi - 1)];
   };
   const int64_t page_step = (for_v ? a.vp : a.kp) * S::kElem, slot_step = (for_v ? a.vsl : a.ksl) * S::kElem;
   const float* scale_base = nullptr;
@@ -303,27 +450,33 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
 
   // The step's row offsets to shared memory (0, the cache's first row, for a token that is not seen);
   // returns the mask of its seen tokens.
-  auto place = [&](uint64_t t0, int32_t page, float* scale) -> uint32_t {
-    const uint32_t t = (uint32_t)(t0 + li), in = t - op_div(t, a.fd_page) * a.page_size;
-    const bool ok = page >= 0 && (uint32_t)page < a.pages;
+  auto place = [&](uint32_t t0, int32_t page, float* scale) -> uint32_t {
+    const uint32_t t = t0 + li;
+    const bool ok = (t >= sp.first) & (t < hi) & ((uint32_t)page < a.pages);
+    const uint32_t in = ok ? t - page_index(t) * a.page_size : 0, pg = ok ? page : 0;
     wave_fence();
-    offs[lane] = ok ? page * page_step + in * slot_step : 0;
+    offs[lane] = (int64_t)(pg * (uint64_t)page_step + in * (uint64_t)slot_step);
     wave_fence();
-    if constexpr (kQuant) *scale = ok ? scale_base[page * a.sp + (int64_t)in * a.ssl] : 0.f;
+    if constexpr (kQuant) *scale = __builtin_nontemporal_load(scale_base + (pg * (uint64_t)a.sp + in * (uint64_t)a.ssl));
     return (uint32_t)__ballot(ok);
   };
 
   KR kr[S::kTiles][S::kKeySteps];
   VR vr[S::kVals][S::kValSteps];
+  // Where a lane's chunk kk of a row is read: past the row's end the first one's place, and half past it (8
+  // elements of 16 are left) 8 before, whose upper half they are.
+  auto key_at = [&](int kk) -> uint32_t {
+    const uint32_t e0 = (kk * 4 + j) * S::kKeyChunk;
+    return e0 >= (uint32_t)a.dk ? 0 : e0 + S::kKeyChunk > (uint32_t)a.dk ? e0 - 8 : e0;
+  };
+  const bool ragged = a.dk != DC;
   auto load_keys = [&]() {
 #pragma unroll
     for (int t = 0; t < S::kTiles; ++t) {
       const char* row = kbase + offs[16 * t + r];
 #pragma unroll
       for (int kk = 0; kk < S::kKeySteps; ++kk) {
-        const uint32_t e0 = (kk * 4 + j) * S::kKeyChunk;
-        kr[t][kk] = KR{};
-        if (e0 < (uint32_t)a.dk) kr[t][kk] = *(const KR*)(row + e0 * S::kElem);
+        kr[t][kk] = __builtin_nontemporal_load((const KR*)(row + key_at(kk) * S::kElem));
       }
     }
   };
@@ -334,7 +487,7 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
 #pragma unroll
       for (int p = 0; p < S::kValSteps; ++p) {
         const uint32_t e0 = (p * 16 + r) * S::kValChunk;
-        vr[x][p] = *(const VR*)(row + (e0 < (uint32_t)a.dv ? e0 : 0) * S::kElem);  // past dv: rows of no output
+        vr[x][p] = __builtin_nontemporal_load((const VR*)(row + (e0 < (uint32_t)a.dv ? e0 : 0) * S::kElem));
       }
     }
   };
@@ -346,16 +499,25 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
   constexpr uint32_t kAll = S::kTokens == 32 ? 0xffffffffu : 0xffffu;
 
   constexpr uint32_t kStep = 4 * S::kTokens;
-  uint64_t t0 = lo + w * S::kTokens;
+  uint32_t t0 = lo + w * S::kTokens;
   if (t0 < hi) {
-    float sc = 0, sc_next = 0;
+    float sc = 0;
     uint32_t seen = place(t0, page_of(t0), &sc);
     int32_t page = page_of(t0 + kStep);
     load_keys();
     load_values();
-    for (;;) {
-      const bool more = t0 + kStep < hi;
+    // The last round's loads are of the cache's first row, so that they need no branch either.
+    do {
       // scores
+      if (ragged)
+#pragma unroll
+        for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+          for (int kk = 0; kk < S::kKeySteps; ++kk) {
+            const uint32_t e0 = (kk * 4 + j) * S::kKeyChunk;
+            if (S::kKeyParts == 2 && e0 + 8 == (uint32_t)a.dk) kr[t][kk] = KR{kr[t][kk][2], kr[t][kk][3], 0, 0};
+            if (e0 >= (uint32_t)a.dk) kr[t][kk] = KR{};
+          }
       F4 s[HT][S::kTiles];
 #pragma unroll
       for (int t = 0; t < S::kTiles; ++t)
@@ -364,18 +526,18 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
           s[ht][t] = F4{};
 #pragma unroll
           for (int kk = 0; kk < S::kKeySteps; ++kk) {
-            M k;
-            if constexpr (kQuant)
-              k = decode<DT, CT>(kr[t][kk]);
-            else
-              k = __builtin_bit_cast(M, kr[t][kk]);
-            s[ht][t] = mfma(k, q[ht][kk], s[ht][t]);
+            if constexpr (kQuant) {
+              s[ht][t] = mfma(decode<DT, CT>(KHalf{kr[t][kk][0], kr[t][kk][1]}), q[ht][2 * kk], s[ht][t]);
+              s[ht][t] = mfma(decode<DT, CT>(KHalf{kr[t][kk][2], kr[t][kk][3]}), q[ht][2 * kk + 1], s[ht][t]);
+            } else {
+              s[ht][t] = mfma(__builtin_bit_cast(M, kr[t][kk]), q[ht][kk], s[ht][t]);
+            }
           }
         }
       F4 ksc[S::kTiles], vsc[S::kTiles];
       if constexpr (kQuant) {
         wave_fence();
-        scales[lane] = sc;
+        scales[lane] = (seen >> li) & 1 ? sc : 0.f;
         wave_fence();
 #pragma unroll
         for (int t = 0; t < S::kTiles; ++t) {
@@ -383,12 +545,9 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
           vsc[t] = *(const F4*)&scales[32 + 16 * t + 4 * j];
         }
       }
-      uint32_t seen_next = 0;
-      if (more) {
-        seen_next = place(t0 + kStep, page, &sc_next);
-        page = page_of(t0 + 2 * kStep);
-        load_keys();
-      }
+      const uint32_t seen_next = place(t0 + kStep, page, &sc);
+      page = page_of(t0 + 2 * kStep);
+      load_keys();
       // weights
       M pw[HT];
       B8 phi[HT], plo[HT];
@@ -492,21 +651,21 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
           }
         }
       }
-      if (!more) break;
       load_values();
       seen = seen_next;
-      sc = sc_next;
       t0 += kStep;
-    }
+    } while (t0 < hi);
   }
 
   // join the waves: maxima and sums, then 16 heads x 16 chunks of columns at a time
+  const uint32_t re = here(r), je = here(j), lane256 = here(threadIdx.x);
+  if (again) __syncthreads();
 #pragma unroll
   for (int ht = 0; ht < HT; ++ht) {
     const float sum = across_groups_sum(l[ht]);
-    if (j == 0) {
-      ms[w][16 * ht + r] = base[ht] == -__FLT_MAX__ ? -__builtin_inff() : base[ht];
-      ls[w][16 * ht + r] = sum;
+    if (je == 0) {
+      ms[w][16 * ht + re] = base[ht] == -__FLT_MAX__ ? -__builtin_inff() : base[ht];
+      ls[w][16 * ht + re] = sum;
     }
   }
 #pragma unroll
@@ -518,12 +677,12 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int m = 0; m < S::kValChunk; m += 4)
-          *(F4*)&os[w][r * kRow + (4 * j + i) * S::kValChunk + m] =
+          *(F4*)&os[w][re * kRow + (4 * je + i) * S::kValChunk + m] =
               F4{o[ht][p][m][i], o[ht][p][m + 1][i], o[ht][p][m + 2][i], o[ht][p][m + 3][i]};
       __syncthreads();
 #pragma unroll
       for (int x = 0; x < S::kValChunk / 4; ++x) {
-        const uint32_t at = threadIdx.x + 256 * x, hd = at / (4 * S::kValChunk), c4 = at % (4 * S::kValChunk) * 4;
+        const uint32_t at = lane256 + 256 * x, hd = at / (4 * S::kValChunk), c4 = at % (4 * S::kValChunk) * 4;
         const uint32_t h = in_group + 16 * ht + hd, e = p * 16 * S::kValChunk + c4;
         if (h >= a.group || e >= (uint32_t)a.dv) continue;
         float m4[4], top = -__builtin_inff(), total = 0;
@@ -537,7 +696,7 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
           acc += *(const F4*)&os[i][hd * kRow + c4] * wt;
         }
         const uint32_t bh = b * a.heads + g * a.group + h;
-        if (a.splits == 1) {
+        if (run.whole) {
           T* out = (T*)a.out + (int64_t)b * a.ob + (int64_t)(g * a.group + h) * a.oh;
           const float inv = total > 0 ? 1.f / total : 0.f;
 #pragma unroll
@@ -546,7 +705,7 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
           *(F4*)&a.part_o[((uint64_t)bh * a.splits + split) * a.dv + e] = acc;
         }
         if (e == 0) {
-          if (a.splits > 1) {
+          if (!run.whole) {
             a.part_ml[2 * ((uint64_t)bh * a.splits + split)] = top;
             a.part_ml[2 * ((uint64_t)bh * a.splits + split) + 1] = total;
           } else if (a.lse) {
@@ -555,28 +714,60 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
         }
       }
     }
+  if (!run_next(a, &run)) break;
+  }
 }
 
-// Joins the chunks of one query head in their order.
+// Joins the parts of one query head: 256 lanes are groups of lanes with four columns each, a group takes
+// every next part, and the groups' sums are added in their order.
 template <int DT>
 __global__ void __launch_bounds__(256) k_attention_join(AttentionArgs a) {
   using T = typename ElemOf<DT>::T;
-  const uint32_t bh = blockIdx.x, b = bh / a.heads, h = bh % a.heads;
-  const Span sp = span_of(a, b);
-  const uint32_t used = sp.n > sp.base ? (sp.n - sp.base + a.chunk - 1) / a.chunk : 1;  // chunk 0 always writes
+  __shared__ __attribute__((aligned(16))) float os[256 * 4];
+  __shared__ float ms[256], ls[256];
+  const uint32_t bh = blockIdx.x, b = bh / a.heads, h = bh % a.heads, g = h / a.group;
+  Deal deal;
+  const uint32_t blocks = span_of(a, b).blocks;
+  const uint64_t start = blocks_before(a, b, &deal) + (uint64_t)(g * a.tiles + h % a.group / a.unit_heads) * blocks;
+  const uint32_t from = run_of(deal, start), parts = run_of(deal, start + blocks - 1) - from + 1;
+  if (parts == 1) return;  // whole: written already
+  const uint32_t wide = ((uint32_t)a.dv + 3) / 4, groups = 256 / wide, grp = threadIdx.x / wide, c = threadIdx.x % wide;
   const float* ml = a.part_ml + 2 * (uint64_t)bh * a.splits;
-  float top = -__builtin_inff();
-  for (uint32_t s = 0; s < used; ++s) top = fmaxf(top, ml[2 * s]);
-  float total = 0, acc = 0;
-  const uint32_t e = threadIdx.x;
-  for (uint32_t s = 0; s < used; ++s) {
-    const float wt = weight_of(ml[2 * s], top);
-    total += ml[2 * s + 1] * wt;
-    if (e < (uint32_t)a.dv) acc += a.part_o[((uint64_t)bh * a.splits + s) * a.dv + e] * wt;
+  const float* po = a.part_o + (uint64_t)bh * a.splits * a.dv;
+  float m = -__builtin_inff(), l = 0;
+  F4 acc = {};
+  if (grp < groups)
+    for (uint32_t s = grp; s < parts; s += groups) {
+      const float top = fmaxf(m, ml[2 * s]), keep = weight_of(m, top), wt = weight_of(ml[2 * s], top);
+      F4 x;
+      if (a.dv % 4 == 0) {
+        x = *(const F4*)&po[(uint64_t)s * a.dv + 4 * c];
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) x[i] = 4 * c + i < (uint32_t)a.dv ? po[(uint64_t)s * a.dv + 4 * c + i] : 0.f;
+      }
+      acc = acc * keep + x * wt;
+      l = l * keep + ml[2 * s + 1] * wt;
+      m = top;
+    }
+  *(F4*)&os[4 * threadIdx.x] = acc;
+  ms[threadIdx.x] = m;
+  ls[threadIdx.x] = l;
+  __syncthreads();
+  if (grp) return;
+  for (uint32_t i = 1; i < groups; ++i) {
+    const uint32_t at = i * wide + c;
+    const float top = fmaxf(m, ms[at]), keep = weight_of(m, top), wt = weight_of(ms[at], top);
+    acc = acc * keep + *(const F4*)&os[4 * at] * wt;
+    l = l * keep + ls[at] * wt;
+    m = top;
   }
-  if (e < (uint32_t)a.dv)
-    ((T*)a.out)[(int64_t)b * a.ob + (int64_t)h * a.oh + (int64_t)e * a.od] = (T)(total > 0 ? acc / total : 0.f * acc);
-  if (e == 0 && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
+  T* out = (T*)a.out + (int64_t)b * a.ob + (int64_t)h * a.oh;
+  const float inv = l > 0 ? 1.f / l : 0.f;
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i)
+    if (4 * c + i < (uint32_t)a.dv) out[(int64_t)(4 * c + i) * a.od] = (T)(l != l ? l : acc[i] * inv);
+  if (c == 0 && a.lse) a.lse[bh] = m == -__builtin_inff() ? m : (m + __log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
@@ -626,40 +817,44 @@ static int plan_attention(const lr_layout* Lq, const lr_cache* c, const lr_layou
   // The matrix kernel wants rows of whole chunks: a multiple of 8 elements (4 in fp32), contiguous and
   // that much aligned.  Rows of an 8-bit cache under an fp32 model have no matrix form.
   const int64_t v = c->dtype == LR_F32 ? 4 : 8;
-  const bool matrix = !(dtype == LR_F32 && is_quantised(c->dtype)) && kd.size % v == 0 && vd.size % v == 0 &&
+  const bool matrix = !(dtype == LR_F32 && is_quantised(c->dtype)) &&
+                      kd.size >= 16 && kd.size % v == 0 && vd.size % v == 0 &&
                       rows_aligned(c->k_layout, nullptr, dtype_bytes(c->dtype), v) &&
                       rows_aligned(c->v_layout, nullptr, dtype_bytes(c->dtype), v);
   out->path = matrix ? LR_ATTENTION_MATRIX : LR_ATTENTION_ELEMENT;
   a->wide = std::max(kd.size, vd.size) <= 64 ? 64 : std::max(kd.size, vd.size) <= 128 ? 128 : 256;
-  a->tiles = a->group > 16 && a->wide < 256 ? 2 : 1;
-  out->head_tiles = (int32_t)(matrix ? (a->group + 16 * a->tiles - 1) / (16 * a->tiles) : a->group);
+  a->unit_heads = !matrix ? 1 : a->group > 16 && a->wide < 256 ? 32 : 16;
+  a->tiles = (a->group + a->unit_heads - 1) / a->unit_heads;
+  a->units = a->kv_heads * a->tiles;
+  out->head_tiles = (int32_t)a->tiles;
+  // Parts of a sequence: short ones stay whole, which saves the second launch; otherwise as many as there
+  // are blocks, up to 8192 parts in all (their sums are some 66 MB for 16 heads of 128), or 8 a unit.
   int64_t span = max_pages * ks.size;
   if (window > 0) span = std::min(span, window + 31);
-  const double work = (double)span * (double)qb.size * a->kv_heads * out->head_tiles;
-  int64_t chunk = (int64_t)(work / 1024 / 128 + 1) * 128;
-  chunk = std::min<int64_t>(std::max<int64_t>(chunk, 128), 2048);
-  out->chunk = chunk;
-  out->splits = (span + chunk - 1) / chunk;
+  const int64_t blocks = (span + kBlock - 1) / kBlock;
+  const double units = (double)qb.size * a->units;
+  int64_t most = blocks <= 4 ? 1 : std::min(blocks, std::max<int64_t>((int64_t)(8192 / units), 8));
+  out->chunk = (span + most - 1) / most;
+  out->splits = (span + out->chunk - 1) / out->chunk;
   const double parts = (double)qb.size * a->heads * (double)out->splits;
-  if (parts > (double)kMaxCount / 256) return LR_ERR_OVERFLOW;
+  if (parts > (double)kMaxCount / 256 || units > (double)kMaxCount || units * blocks > 0x1p50) return LR_ERR_OVERFLOW;
+  a->min_share = out->splits > 1 ? (uint32_t)((blocks - 2) / (out->splits - 1) + 1) : 1;
   out->workspace_bytes = out->splits == 1 ? 0 : (int64_t)parts * (a->dv + 2) * 4;
-  a->chunk = (uint32_t)chunk;
   a->splits = (uint32_t)out->splits;
   return LR_OK;
 }
 
 template <int DT, int CT>
 static int launch_attention(const AttentionArgs& a, hipStream_t st) {
-  const uint32_t rows = a.batch * a.heads;
+  const dim3 grid(a.splits == 1 ? a.batch * a.units : a.grid);
   if (a.path == LR_ATTENTION_ELEMENT) {
-    hipLaunchKernelGGL((k_attention_element<DT, CT>), dim3(rows * a.splits), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_attention_element<DT, CT>), grid, dim3(256), 0, st, a);
   } else if constexpr (!(DT == LR_F32 && CT != LR_F32)) {
-    const dim3 grid(a.batch * a.kv_heads * ((a.group + 16 * a.tiles - 1) / (16 * a.tiles)) * a.splits);
-    if (a.wide == 64 && a.tiles == 1)
+    if (a.wide == 64 && a.unit_heads == 16)
       hipLaunchKernelGGL((k_attention_matrix<DT, CT, 64, 1>), grid, dim3(256), 0, st, a);
     else if (a.wide == 64)
       hipLaunchKernelGGL((k_attention_matrix<DT, CT, 64, 2>), grid, dim3(256), 0, st, a);
-    else if (a.wide == 128 && a.tiles == 1)
+    else if (a.wide == 128 && a.unit_heads == 16)
       hipLaunchKernelGGL((k_attention_matrix<DT, CT, 128, 1>), grid, dim3(256), 0, st, a);
     else if (a.wide == 128)
       hipLaunchKernelGGL((k_attention_matrix<DT, CT, 128, 2>), grid, dim3(256), 0, st, a);
@@ -668,7 +863,7 @@ static int launch_attention(const AttentionArgs& a, hipStream_t st) {
   }
   if (int rc = check_op_launch()) return rc;
   if (a.splits == 1) return LR_OK;
-  hipLaunchKernelGGL((k_attention_join<DT>), dim3(rows), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((k_attention_join<DT>), dim3(a.batch * a.heads), dim3(256), 0, st, a);
   return check_op_launch();
 }
 
@@ -728,9 +923,16 @@ int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, c
   a.scale2 = scale * kLog2e;
   a.part_o = (float*)workspace;
   a.part_ml = (float*)workspace + (p.workspace_bytes / 4 - 2 * (int64_t)mode_of(*Lq, 2).size * a.heads * p.splits);
-  const uintptr_t align = c->dtype == LR_F32 || !is_quantised(c->dtype) ? 16 : 8;  // bytes of a chunk
-  a.path = p.path == LR_ATTENTION_MATRIX && (uintptr_t)c->k % align == 0 && (uintptr_t)c->v % align == 0
-               ? LR_ATTENTION_MATRIX : LR_ATTENTION_ELEMENT;
+  const uintptr_t align = is_quantised(c->dtype) ? 8 : 16;
+  a.path = p.path;
+  if (a.path == LR_ATTENTION_MATRIX && ((uintptr_t)c->k % align || (uintptr_t)c->v % align)) {
+    a.path = LR_ATTENTION_ELEMENT;
+    a.unit_heads = 1;
+    a.tiles = a.group;
+    a.units = a.heads;
+  }
+  a.q_wide = rows_aligned(*Lq, q, e, 16 / e);
+  a.grid = a.path == LR_ATTENTION_ELEMENT ? 2048 : 256;
   const hipStream_t st = (hipStream_t)stream;
   if (dtype == LR_F32) return launch_attention_of<LR_F32>(a, c->dtype, st);
   if (dtype == LR_F16) return launch_attention_of<LR_F16>(a, c->dtype, st);
