@@ -127,6 +127,26 @@ __device__ __forceinline__ int64_t mode_offset(const ModeArg& m, uint32_t i) {
   return m.n ? off + (int64_t)i * m.stride[m.n - 1] : 0;
 }
 
+// A mode of at most two leaves, without loops and in few bytes: arguments come from host memory, and a kernel
+// of a few microseconds waits for each line of them that it reads on its way.
+struct ModePair {
+  FastDiv fd;  // by the first leaf's extent, at least 2
+  uint32_t ext;
+  int64_t stride[2];
+};
+inline bool mode_pair(const Mode& m, ModePair* a) {
+  if (m.n > 2) return false;
+  a->ext = m.n == 2 ? (uint32_t)m.leaf[0].n : (uint32_t)kMaxCount;  // one leaf: never reached by an index
+  a->fd = make_fastdiv(a->ext);
+  a->stride[0] = m.n ? m.leaf[0].d : 0;
+  a->stride[1] = m.n == 2 ? m.leaf[1].d : 0;
+  return true;
+}
+__device__ __forceinline__ int64_t mode_offset(const ModePair& m, uint32_t i) {
+  const uint32_t q = __umulhi(i, m.fd.m) >> m.fd.s;
+  return (int64_t)(i - q * m.ext) * m.stride[0] + (int64_t)q * m.stride[1];
+}
+
 // ------------------------------------------------------------------ element types
 
 template <int DT> struct ElemOf;
@@ -160,6 +180,116 @@ __device__ __forceinline__ void sincos_turn(uint64_t t, float* sin_out, float* c
   const float a = q & 1 ? c : s, b = q & 1 ? s : c;
   *sin_out = q & 2 ? -a : a;
   *cos_out = (q + 1) & 2 ? -b : b;
+}
+
+// ------------------------------------------------------------------ rows in chunks
+
+// A row of `dim` elements, the first `rot` of them rotated, as units of two chunks of V elements each: a
+// rotated unit has the chunks that pairs of the half layout lie in (i and i + rot/2), a unit past them two
+// chunks that are as far apart, so that neighbouring lanes' chunks are neighbours in memory.
+struct Units {
+  int32_t rot, dim, turned, rest;  // turned: rotated units; rest: distance of the two chunks past them
+  int32_t count;
+};
+inline Units units_of(int32_t rot, int32_t dim, int32_t V) {
+  Units u{rot, dim, rot / (2 * V), 0, 0};
+  const int32_t chunks = (dim - rot) / V;
+  u.rest = (chunks + 1) / 2 * V;
+  u.count = u.turned + (chunks + 1) / 2;
+  return u;
+}
+// First elements of unit u's chunks; the second is past the row's end when there is none.
+__device__ __forceinline__ void chunks_of(const Units& n, uint32_t u, uint32_t V, uint32_t* i, uint32_t* j) {
+  const bool turned = u < (uint32_t)n.turned;
+  *i = turned ? u * V : n.rot + (u - n.turned) * V;
+  *j = *i + (turned ? n.rot / 2 : n.rest);
+}
+
+// V elements of type T, moved at once.
+template <class T, int V> struct Chunk {
+  typedef T Vec __attribute__((ext_vector_type(V)));
+};
+template <bool NT, class Vec> __device__ __forceinline__ Vec load_chunk(const void* p) {
+  return NT ? __builtin_nontemporal_load((const Vec*)p) : *(const Vec*)p;
+}
+template <bool NT, class Vec> __device__ __forceinline__ void store_chunk(void* p, Vec x) {
+  if (NT)
+    __builtin_nontemporal_store(x, (Vec*)p);
+  else
+    *(Vec*)p = x;
+}
+
+// Work beyond the 256 MiB of the memory-side cache streams past the caches: reads reach 7.2 TB/s instead
+// of 6.3, and what is written would not be found there anyway.
+constexpr double kStreamBytes = 256.0 * (1 << 20);
+
+// cos and sin of the angles of one unit's V pairs: pair k of a half layout is element k of both chunks, pairs
+// of an interleaved one lie inside the first chunk, then the second.
+template <int V>
+__device__ __forceinline__ void angles_of(const int64_t* turns, int64_t position, uint32_t u, int32_t rot, bool half,
+                                          float magnitude, float sign, float* c, float* s) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const uint32_t pair = half ? u * V + k : u * (V / 2) + (k < V / 2 ? k : rot / 4 + k - V / 2);
+    sincos_turn((uint64_t)position * (uint64_t)turns[pair], &s[k], &c[k]);
+    s[k] *= magnitude * sign;
+    c[k] *= magnitude;
+  }
+}
+template <int V>
+__device__ __forceinline__ void rotate_unit(float* a, float* b, const float* c, const float* s, bool half) {
+  if (half) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float v = a[k], w = b[k];
+      a[k] = v * c[k] - w * s[k];
+      b[k] = w * c[k] + v * s[k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float* x = k < V / 2 ? a + 2 * k : b + 2 * (k - V / 2);
+      const float v = x[0], w = x[1];
+      x[0] = v * c[k] - w * s[k];
+      x[1] = w * c[k] + v * s[k];
+    }
+  }
+}
+
+// How a workgroup of 256 lanes covers rows: `lanes` a row (2^row_shift where lanes of a row reduce among each
+// other), 2^head_shift heads next to each other, the rest tokens; a lane then takes `per_lane` heads,
+// 2^head_shift apart, so that what depends on the token alone is computed once for them.
+struct RowGrid {
+  uint32_t lanes, head_shift, tokens, per_lane;
+  FastDiv fd_lanes;
+  uint32_t blocks_x, blocks_y;  // token blocks, head blocks
+};
+inline RowGrid row_grid(uint32_t lanes, uint32_t heads, uint32_t n, uint32_t sides) {
+  RowGrid g;
+  g.lanes = lanes;
+  g.fd_lanes = make_fastdiv(lanes);
+  // up to 4 heads side by side: runs of 4 rows on the side where heads are neighbours, while the other
+  // lanes are neighbouring tokens for the side where those are
+  g.head_shift = heads >= 4 && lanes <= 16 ? 2 : heads >= 2 && lanes <= 32 ? 1 : 0;
+  g.tokens = (256 / lanes) >> g.head_shift;
+  if (!g.tokens) g.tokens = 1, g.head_shift = 0;
+  g.blocks_x = (n + g.tokens - 1) / g.tokens;
+  const uint32_t steps = (heads + (1u << g.head_shift) - 1) >> g.head_shift;
+  // several heads a lane once there are 8 workgroups a CU without
+  const uint64_t all = (uint64_t)g.blocks_x * steps * sides;
+  g.per_lane = (uint32_t)std::min<uint64_t>({steps, 8, std::max<uint64_t>(all / 2048, 1)});
+  g.blocks_y = (steps + g.per_lane - 1) / g.per_lane;
+  return g;
+}
+// Within the launch's limits: 2^32 lanes along x, 65535 workgroups along y.
+inline bool row_grid_fits(const RowGrid& g) { return g.blocks_x < 1u << 24 && g.blocks_y <= 65535; }
+// Lane's unit, first head and token; false for a lane without work.
+__device__ __forceinline__ bool row_lane(const RowGrid& g, uint32_t lane, uint32_t* u, uint32_t* h, uint32_t* t) {
+  const uint32_t row = op_div(lane, g.fd_lanes);
+  *u = lane - row * g.lanes;
+  *h = row & ((1u << g.head_shift) - 1);
+  *t = row >> g.head_shift;
+  return *t < g.tokens;
 }
 
 }  // namespace lr

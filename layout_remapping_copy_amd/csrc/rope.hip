@@ -16,7 +16,71 @@ struct RopeArgs {
   float magnitude, sign;
 };
 
-// One pair of a head (or two elements past the rotated part) per lane.
+struct RopeChunkArgs {
+  const void* x;
+  void* y;
+  const int64_t* turns;
+  const int64_t* positions;
+  ModePair xh, yh, xt, yt, p;
+  Units un;
+  RowGrid grid;
+  uint32_t heads, n;
+  int32_t pairs;
+  float magnitude, sign;
+};
+
+// Rows in chunks of V elements: a lane has one unit of a token's rows, computes its V angles once and turns
+// `per_lane` heads with them, their loads two at a time ahead of the arithmetic.
+template <int DT, int V, bool NT>
+__global__ void __launch_bounds__(256) k_rope_chunks(RopeChunkArgs a) {
+  using T = typename ElemOf<DT>::T;
+  using Vec = typename Chunk<T, V>::Vec;
+  uint32_t u, h, t;
+  if (!row_lane(a.grid, threadIdx.x, &u, &h, &t)) return;
+  const uint64_t token = (uint64_t)blockIdx.x * a.grid.tokens + t;
+  if (token >= a.n) return;
+  t = (uint32_t)token;
+  h += blockIdx.y * a.grid.per_lane << a.grid.head_shift;
+  uint32_t i, j;
+  chunks_of(a.un, u, V, &i, &j);
+  const bool turned = u < (uint32_t)a.un.turned, two = j < (uint32_t)a.un.dim, half = a.pairs == LR_PAIRS_HALF;
+  const T* x = (const T*)a.x + mode_offset(a.xt, t);
+  T* y = (T*)a.y + mode_offset(a.yt, t);
+  float c[V], s[V];
+  if (turned) angles_of<V>(a.turns, a.positions[mode_offset(a.p, t)], u, a.un.rot, half, a.magnitude, a.sign, c, s);
+  const uint32_t end = min(a.heads, h + (a.grid.per_lane << a.grid.head_shift)), step = 1u << a.grid.head_shift;
+  for (; h < end; h += 2 * step) {
+    const uint32_t h2 = h + step < end ? h + step : h;  // an odd last head is done twice
+    const T *p = x + mode_offset(a.xh, h), *p2 = x + mode_offset(a.xh, h2);
+    Vec v[2], w[2] = {};
+    v[0] = load_chunk<NT, Vec>(p + i);
+    v[1] = load_chunk<NT, Vec>(p2 + i);
+    if (two) {
+      w[0] = load_chunk<NT, Vec>(p + j);
+      w[1] = load_chunk<NT, Vec>(p2 + j);
+    }
+    if (turned) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        float f[V], g[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = value_of<DT>(v[z][k]), g[k] = value_of<DT>(w[z][k]);
+        rotate_unit<V>(f, g, c, s, half);
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[z][k] = (T)f[k], w[z][k] = (T)g[k];
+      }
+    }
+    T *q = y + mode_offset(a.yh, h), *q2 = y + mode_offset(a.yh, h2);
+    store_chunk<NT>(q + i, v[0]);
+    if (two) store_chunk<NT>(q + j, w[0]);
+    if (h2 != h) {
+      store_chunk<NT>(q2 + i, v[1]);
+      if (two) store_chunk<NT>(q2 + j, w[1]);
+    }
+  }
+}
+
+// Any strides and sizes: one pair of a head (or two elements past the rotated part) per lane.
 template <int DT>
 __global__ void __launch_bounds__(256) k_rope(RopeArgs a) {
   using T = typename ElemOf<DT>::T;
@@ -41,6 +105,15 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a) {
   y[(int64_t)i * a.yd] = (T)(v * c - w * s);
   y[(int64_t)j * a.yd] = (T)(w * c + v * s);
   }
+}
+
+template <int DT, int V>
+static void launch_chunks(const RopeChunkArgs& a, double bytes, hipStream_t st) {
+  const dim3 grid(a.grid.blocks_x, a.grid.blocks_y);
+  if (bytes > kStreamBytes)
+    hipLaunchKernelGGL((k_rope_chunks<DT, V, true>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_rope_chunks<DT, V, false>), grid, dim3(256), 0, st, a);
 }
 
 static bool same_leaves(const Mode& a, const Mode& b) {
@@ -154,18 +227,50 @@ int lr_rope(const void* x, const lr_layout* Lx, int64_t x_capacity, void* y, con
   a.pairs = r->pairs;
   a.heads = (uint32_t)xh.size;
   a.n = (uint32_t)n;
-  a.units = (uint32_t)(a.rot / 2 + (a.dim - a.rot + 1) / 2);
   a.magnitude = r->magnitude;
   a.sign = flags & LR_ROPE_BACKWARD ? -1.f : 1.f;
-  const double lanes = (double)a.heads * (double)n * a.units;
-  const int64_t groups = lanes > 1e9 ? 1 << 22 : ((int64_t)lanes + 255) / 256;
   const hipStream_t st = (hipStream_t)stream;
-  if (dtype == LR_F32)
-    hipLaunchKernelGGL(k_rope<LR_F32>, dim3((unsigned)groups), dim3(256), 0, st, a);
-  else if (dtype == LR_F16)
-    hipLaunchKernelGGL(k_rope<LR_F16>, dim3((unsigned)groups), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(k_rope<LR_BF16>, dim3((unsigned)groups), dim3(256), 0, st, a);
+  // the widest chunks that halves, rest and rows are whole numbers of
+  int64_t v = 16 / e;
+  while (v > 1 && (a.rot / 2 % v || (a.dim - a.rot) % v || !rows_aligned(*Lx, x, e, v) || !rows_aligned(*Ly, y, e, v))) v /= 2;
+  const double bytes = 2.0 * (double)a.heads * (double)n * a.dim * (double)e;
+  RopeChunkArgs k;
+  bool chunked = v > 1 && mode_pair(xh, &k.xh) && mode_pair(yh, &k.yh) && mode_pair(xt, &k.xt) && mode_pair(yt, &k.yt) &&
+                 mode_pair(p, &k.p);
+  if (chunked) {
+    k.un = units_of(a.rot, a.dim, (int32_t)v);
+    chunked = k.un.count <= 256;
+  }
+  if (chunked) {
+    k.grid = row_grid((uint32_t)k.un.count, a.heads, a.n, 1);
+    chunked = row_grid_fits(k.grid);
+    k.x = x;
+    k.y = y;
+    k.turns = r->turns;
+    k.positions = r->positions;
+    k.heads = a.heads;
+    k.n = a.n;
+    k.pairs = r->pairs;
+    k.magnitude = a.magnitude;
+    k.sign = a.sign;
+  }
+  if (chunked && dtype == LR_F32) {
+    v == 4 ? launch_chunks<LR_F32, 4>(k, bytes, st) : launch_chunks<LR_F32, 2>(k, bytes, st);
+  } else if (chunked && dtype == LR_F16) {
+    v == 8 ? launch_chunks<LR_F16, 8>(k, bytes, st) : v == 4 ? launch_chunks<LR_F16, 4>(k, bytes, st) : launch_chunks<LR_F16, 2>(k, bytes, st);
+  } else if (chunked) {
+    v == 8 ? launch_chunks<LR_BF16, 8>(k, bytes, st) : v == 4 ? launch_chunks<LR_BF16, 4>(k, bytes, st) : launch_chunks<LR_BF16, 2>(k, bytes, st);
+  } else {
+    a.units = (uint32_t)(a.rot / 2 + (a.dim - a.rot + 1) / 2);
+    const double lanes = (double)a.heads * (double)n * a.units;
+    const int64_t groups = lanes > 1e9 ? 1 << 22 : ((int64_t)lanes + 255) / 256;
+    if (dtype == LR_F32)
+      hipLaunchKernelGGL(k_rope<LR_F32>, dim3((unsigned)groups), dim3(256), 0, st, a);
+    else if (dtype == LR_F16)
+      hipLaunchKernelGGL(k_rope<LR_F16>, dim3((unsigned)groups), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL(k_rope<LR_BF16>, dim3((unsigned)groups), dim3(256), 0, st, a);
+  }
   return check_op_launch();
 }
 
