@@ -52,7 +52,227 @@ __device__ __forceinline__ typename ElemOf<DT>::T code_of(float x, float scale) 
   }
 }
 
-// One wave per row (token, head) of one side; a lane holds pairs lane, lane + 64, ...
+// The chunked kernels' arguments: both sides' rows in chunks of V elements.
+struct ChunkSide {
+  void* cache;
+  float* scale;
+  void* rows;
+  ModePair rh, rt;
+  int64_t ch, cs, cp;
+  Units un;
+};
+struct ChunkArgs {
+  ChunkSide side[2];
+  RowGrid grid;
+  const int64_t* slots;
+  const int64_t* turns;
+  const int64_t* positions;
+  int64_t sh, ss, sp;
+  int64_t cache_slots;
+  FastDiv fd_page;
+  uint32_t page_size, heads, n;
+  float magnitude;
+  int32_t pairs;
+};
+
+// Page and slot of a token's place; false for none.
+__device__ __forceinline__ bool place_of(const ChunkArgs& a, int64_t slot, uint32_t* page, uint32_t* in) {
+  const bool held = (uint64_t)slot < (uint64_t)a.cache_slots;
+  const uint32_t s = held ? (uint32_t)slot : 0;
+  *page = op_div(s, a.fd_page);
+  *in = s - *page * a.page_size;
+  return held;
+}
+
+// V finite numbers as codes, without a remainder each: x * (1 / scale) is within 2 steps of the quotient, and
+// two numbers round to the same code unless a tie lies between them.  `near` gathers how near the products
+// come to ties; below 8 (of the steps of fp32, 4 either way) the caller takes code_of instead.
+template <int CT, int V>
+__device__ __forceinline__ void fast_codes(const float* v, float inv, uint32_t* code, uint32_t* near) {
+  if constexpr (CT == LR_E4M3) {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      float q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        q[e] = v[k + e] * inv;
+        // ties are half steps of a 3-bit mantissa; codes below 2^-6 are spaced as those just above it
+        float m = __builtin_fabsf(q[e]);
+        m = m < 0x1p-6f ? m + 0x1p-6f : m;
+        *near = min(*near, (__float_as_uint(m) + 0x80004u) & 0xfffffu);
+      }
+      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+      code[k / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      code[k / 4] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float q = v[k + e] * inv, r = __builtin_rintf(q);
+        if (__builtin_fabsf(q - r) > 0.5f - 0x1p-15f) *near = 0;
+        code[k / 4] |= ((uint32_t)(int32_t)r & 0xff) << (8 * e);
+      }
+    }
+  }
+}
+template <int CT, int V>
+__device__ __forceinline__ void exact_codes(const float* v, float scale, uint32_t* code) {
+#pragma unroll
+  for (int k = 0; k < V; k += 4) {
+    code[k / 4] = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) code[k / 4] |= (uint32_t)(uint8_t)code_of<CT>(v[k + e], scale) << (8 * e);
+  }
+}
+
+// Rows in chunks: a lane has one unit of a token's rows, its angles in registers for `per_lane` heads; the
+// lanes of a row (a power of two next to each other) find its largest value by exchange.  Absolute values
+// are compared as integers, in which order infinity and NaN come last: a row that holds one is told by its
+// maximum alone, and is done again with the care that it needs.
+template <int DT, int CT, int V, bool NT>
+__global__ void __launch_bounds__(256) k_cache_write_chunks(ChunkArgs a) {
+  using T = typename ElemOf<DT>::T;
+  using C = typename ElemOf<CT>::T;
+  using Vec = typename Chunk<T, V>::Vec;
+  constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
+  constexpr float kTop = CT == LR_E4M3 ? 448.f : 127.f;
+  const ChunkSide& sd = a.side[blockIdx.z];
+  uint32_t u, h, t;
+  row_lane(a.grid, threadIdx.x, &u, &h, &t);  // lanes of a row are all there, for the exchange
+  const uint64_t token = (uint64_t)blockIdx.x * a.grid.tokens + t;
+  const bool there = token < a.n;
+  t = there ? (uint32_t)token : a.n - 1;
+  h += blockIdx.y * a.grid.per_lane << a.grid.head_shift;
+  uint32_t i, j, page, in;
+  chunks_of(sd.un, u, V, &i, &j);
+  const bool one = u < (uint32_t)sd.un.count, two = one && j < (uint32_t)sd.un.dim, turned = u < (uint32_t)sd.un.turned;
+  const bool half = a.pairs == LR_PAIRS_HALF;
+  const bool held = place_of(a, a.slots[t], &page, &in) && there;
+  const T* x = (const T*)sd.rows + mode_offset(sd.rt, t);
+  C* y = (C*)sd.cache + (int64_t)page * sd.cp + (int64_t)in * sd.cs;
+  float* scales = sd.scale + (int64_t)page * a.sp + (int64_t)in * a.ss;
+  float c[V], s[V];
+  if (turned) angles_of<V>(a.turns, a.positions[t], u, sd.un.rot, half, a.magnitude, 1.f, c, s);
+  const uint32_t step = 1u << a.grid.head_shift;
+  const uint32_t first = blockIdx.y * a.grid.per_lane << a.grid.head_shift;  // the same for every lane of the group
+  for (uint32_t n = 0; n < a.grid.per_lane && first + n * step < a.heads; ++n, h += step) {
+    const bool mine = held && h < a.heads;
+    const T* p = x + mode_offset(sd.rh, h < a.heads ? h : 0);
+    Vec v = {}, w = {};
+    if (one) v = load_chunk<NT, Vec>(p + i);
+    if (two) w = load_chunk<NT, Vec>(p + j);
+    C* q = y + (int64_t)h * sd.ch;
+    if constexpr (!kQuant) {
+      if (turned) {
+        float f[V], g[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = value_of<DT>(v[k]), g[k] = value_of<DT>(w[k]);
+        rotate_unit<V>(f, g, c, s, half);
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = (T)f[k], w[k] = (T)g[k];
+      }
+      if (mine && one) store_chunk<NT>(q + i, v);
+      if (mine && two) store_chunk<NT>(q + j, w);
+    } else {
+      float f[V], g[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] = value_of<DT>(v[k]), g[k] = value_of<DT>(w[k]);
+      if (turned) rotate_unit<V>(f, g, c, s, half);
+      uint32_t bits = 0;
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        bits = max(bits, max(__float_as_uint(f[k]) & 0x7fffffffu, __float_as_uint(g[k]) & 0x7fffffffu));
+      for (uint32_t m = a.grid.lanes / 2; m; m >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, m));
+      const bool special = bits >= 0x7f800000u;
+      float amax = __uint_as_float(bits);
+      if (__any(special)) {  // the largest finite value instead
+        float z = 0;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          if (__builtin_fabsf(f[k]) < __builtin_inff()) z = fmaxf(z, __builtin_fabsf(f[k]));
+          if (__builtin_fabsf(g[k]) < __builtin_inff()) z = fmaxf(z, __builtin_fabsf(g[k]));
+        }
+        for (uint32_t m = a.grid.lanes / 2; m; m >>= 1) z = fmaxf(z, __shfl_xor(z, m));
+        if (special) amax = z;
+      }
+      const float scale = fmaxf(amax / kTop, 0x1p-126f), inv = 1.f / scale;
+      uint32_t cv[V / 4], cw[V / 4], near = special ? 0 : ~0u;
+      fast_codes<CT, V>(f, inv, cv, &near);
+      fast_codes<CT, V>(g, inv, cw, &near);
+      if (__any(near < 8)) {
+        exact_codes<CT, V>(f, scale, cv);
+        exact_codes<CT, V>(g, scale, cw);
+      }
+      using CVec = typename Chunk<uint32_t, V / 4>::Vec;
+      if (mine && one) store_chunk<NT>(q + i, *(const CVec*)cv);
+      if (mine && two) store_chunk<NT>(q + j, *(const CVec*)cw);
+      if (mine && u == 0) scales[(int64_t)h * a.sh] = scale;
+    }
+  }
+}
+
+// Rows in chunks, the other way: codes times their scale, or the elements as they are.
+template <int DT, int CT, int V, bool NT>
+__global__ void __launch_bounds__(256) k_cache_read_chunks(ChunkArgs a) {
+  using T = typename ElemOf<DT>::T;
+  using C = typename ElemOf<CT>::T;
+  using Vec = typename Chunk<T, V>::Vec;
+  constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
+  using CVec = typename Chunk<C, V>::Vec;
+  const ChunkSide& sd = a.side[blockIdx.z];
+  uint32_t u, h, t, page, in, i, j;
+  if (!row_lane(a.grid, threadIdx.x, &u, &h, &t) || u >= (uint32_t)sd.un.count) return;
+  const uint64_t token = (uint64_t)blockIdx.x * a.grid.tokens + t;
+  if (token >= a.n) return;
+  t = (uint32_t)token;
+  h += blockIdx.y * a.grid.per_lane << a.grid.head_shift;
+  chunks_of(sd.un, u, V, &i, &j);
+  const bool two = j < (uint32_t)sd.un.dim, held = place_of(a, a.slots[t], &page, &in);
+  const C* x = (const C*)sd.cache + (int64_t)page * sd.cp + (int64_t)in * sd.cs;
+  const float* scales = sd.scale + (int64_t)page * a.sp + (int64_t)in * a.ss;
+  T* y = (T*)sd.rows + mode_offset(sd.rt, t);
+  const uint32_t end = min(a.heads, h + (a.grid.per_lane << a.grid.head_shift)), step = 1u << a.grid.head_shift;
+  auto made = [&](CVec v, float scale) -> Vec {
+    Vec r;
+    if constexpr (CT == LR_E4M3) {
+      const uint32_t* d = (const uint32_t*)&v;
+      typedef float F2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const F2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(d[k / 4], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(d[k / 4], true);
+        r[k] = (T)(lo[0] * scale), r[k + 1] = (T)(lo[1] * scale), r[k + 2] = (T)(hi[0] * scale), r[k + 3] = (T)(hi[1] * scale);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if constexpr (kQuant)
+          r[k] = (T)(value_of<CT>(v[k]) * scale);
+        else
+          r[k] = v[k];
+    }
+    return held ? r : Vec{};
+  };
+  for (; h < end; h += 2 * step) {
+    const uint32_t h2 = h + step < end ? h + step : h;  // an odd last head is done twice
+    const C *p = x + (int64_t)h * sd.ch, *p2 = x + (int64_t)h2 * sd.ch;
+    float s = 1, s2 = 1;
+    if constexpr (kQuant) s = scales[(int64_t)h * a.sh], s2 = scales[(int64_t)h2 * a.sh];
+    const CVec v = load_chunk<NT, CVec>(p + i), v2 = load_chunk<NT, CVec>(p2 + i);
+    CVec w = {}, w2 = {};
+    if (two) w = load_chunk<NT, CVec>(p + j), w2 = load_chunk<NT, CVec>(p2 + j);
+    T *q = y + mode_offset(sd.rh, h), *q2 = y + mode_offset(sd.rh, h2);
+    store_chunk<NT>(q + i, made(v, s));
+    if (two) store_chunk<NT>(q + j, made(w, s));
+    if (h2 != h) {
+      store_chunk<NT>(q2 + i, made(v2, s2));
+      if (two) store_chunk<NT>(q2 + j, made(w2, s2));
+    }
+  }
+}
+
+// Any strides and sizes: one wave per row (token, head) of one side; a lane holds pairs lane, lane + 64, ...
 template <int DT, int CT>
 __global__ void __launch_bounds__(256) k_cache_write(CacheArgs a) {
   using T = typename ElemOf<DT>::T;
@@ -117,6 +337,7 @@ __global__ void __launch_bounds__(256) k_cache_write(CacheArgs a) {
   }
 }
 
+// Any strides and sizes.
 template <int DT, int CT>
 __global__ void __launch_bounds__(256) k_cache_read(CacheArgs a) {
   using T = typename ElemOf<DT>::T;
@@ -226,6 +447,54 @@ static int with_types(int32_t dtype, int32_t ctype, F&& f) {
   return LR_ERR_TYPE;
 }
 
+// The chunked kernels' arguments; the elements of a chunk, or 0 where rows are no whole chunks: 16 bytes of
+// the rows' type, or 8.  `reduce`: the lanes of a row are a power of two within a wave.
+static int fill_chunks(const lr_cache* c, const CacheArgs& a, const lr_layout* Lk, const lr_layout* Lv, int32_t dtype,
+                       bool reduce, ChunkArgs* k, double* bytes) {
+  const int64_t e = dtype_bytes(dtype), ce = dtype_bytes(c->dtype);
+  const lr_layout *L[2] = {Lk, Lv}, *cl[2] = {&c->k_layout, &c->v_layout};
+  *bytes = 0;
+  int v = (int)(16 / e);
+  for (int i = 0; i < 2; ++i) {
+    const CacheSide& s = a.side[i];
+    if (!mode_pair(mode_of(*L[i], 1), &k->side[i].rh) || !mode_pair(mode_of(*L[i], 2), &k->side[i].rt)) return 0;
+    while (v > 1 && (s.rot / 2 % v || (s.dim - s.rot) % v || !rows_aligned(*L[i], s.rows, e, v) || !rows_aligned(*cl[i], s.cache, ce, v))) v /= 2;
+  }
+  if (v < 4) return 0;
+  uint32_t lanes = 1;
+  for (int i = 0; i < 2; ++i) {
+    const CacheSide& s = a.side[i];
+    ChunkSide& d = k->side[i];
+    d.cache = s.cache;
+    d.scale = s.scale;
+    d.rows = s.rows;
+    d.ch = s.ch;
+    d.cs = s.cs;
+    d.cp = s.cp;
+    d.un = units_of(s.rot, s.dim, v);
+    lanes = std::max(lanes, (uint32_t)d.un.count);
+    *bytes += (double)a.n * a.heads * (double)(s.dim * (e + ce));
+  }
+  if (reduce)
+    while (lanes & (lanes - 1)) lanes += lanes & -lanes;
+  if (lanes > 64) return 0;
+  k->grid = row_grid(lanes, a.heads, a.n, 2);
+  k->slots = a.slots;
+  k->turns = a.turns;
+  k->positions = a.positions;
+  k->sh = a.sh;
+  k->ss = a.ss;
+  k->sp = a.sp;
+  k->cache_slots = a.cache_slots;
+  k->fd_page = make_fastdiv(a.page_size);
+  k->page_size = a.page_size;
+  k->heads = a.heads;
+  k->n = a.n;
+  k->magnitude = a.magnitude;
+  k->pairs = a.pairs;
+  return row_grid_fits(k->grid) ? v : 0;
+}
+
 }  // namespace lr
 
 using namespace lr;
@@ -252,10 +521,34 @@ int lr_cache_write(const lr_cache* c, const void* k, const lr_layout* Lk, int64_
     a.magnitude = r->magnitude;
   }
   if (n == 0) return LR_OK;
+  const hipStream_t st = (hipStream_t)stream;
+  ChunkArgs chunks;
+  double bytes;
+  const int wide = fill_chunks(c, a, Lk, Lv, dtype, true, &chunks, &bytes);
+  const bool nt = bytes > kStreamBytes;
+  if (wide)
+    return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
+      constexpr int D = decltype(dt)::value, C = decltype(ct)::value;
+      const dim3 grid(chunks.grid.blocks_x, chunks.grid.blocks_y, 2);
+      if constexpr (D != LR_F32) {
+        if (wide == 8) {
+          if (nt)
+            hipLaunchKernelGGL((k_cache_write_chunks<D, C, 8, true>), grid, dim3(256), 0, st, chunks);
+          else
+            hipLaunchKernelGGL((k_cache_write_chunks<D, C, 8, false>), grid, dim3(256), 0, st, chunks);
+          return check_op_launch();
+        }
+      }
+      if (nt)
+        hipLaunchKernelGGL((k_cache_write_chunks<D, C, 4, true>), grid, dim3(256), 0, st, chunks);
+      else
+        hipLaunchKernelGGL((k_cache_write_chunks<D, C, 4, false>), grid, dim3(256), 0, st, chunks);
+      return check_op_launch();
+    });
   const int64_t rows = 2 * n * (int64_t)a.heads, groups = std::min<int64_t>((rows + 3) / 4, 1 << 22);
   return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
     hipLaunchKernelGGL((k_cache_write<decltype(dt)::value, decltype(ct)::value>), dim3((unsigned)groups), dim3(256), 0,
-                       (hipStream_t)stream, a);
+                       st, a);
     return check_op_launch();
   });
 }
@@ -266,10 +559,34 @@ int lr_cache_read(const lr_cache* c, const int64_t* slots, int64_t n, void* k, c
   int rc = fill_cache(c, &a);
   if (rc || (rc = fill_rows(c, &a, k, Lk, k_capacity, v, Lv, v_capacity, dtype, slots, n, true))) return rc;
   if (n == 0) return LR_OK;
+  const hipStream_t st = (hipStream_t)stream;
+  ChunkArgs chunks;
+  double bytes;
+  const int wide = fill_chunks(c, a, Lk, Lv, dtype, false, &chunks, &bytes);
+  const bool nt = bytes > kStreamBytes;
+  if (wide)
+    return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
+      constexpr int D = decltype(dt)::value, C = decltype(ct)::value;
+      const dim3 grid(chunks.grid.blocks_x, chunks.grid.blocks_y, 2);
+      if constexpr (D != LR_F32) {
+        if (wide == 8) {
+          if (nt)
+            hipLaunchKernelGGL((k_cache_read_chunks<D, C, 8, true>), grid, dim3(256), 0, st, chunks);
+          else
+            hipLaunchKernelGGL((k_cache_read_chunks<D, C, 8, false>), grid, dim3(256), 0, st, chunks);
+          return check_op_launch();
+        }
+      }
+      if (nt)
+        hipLaunchKernelGGL((k_cache_read_chunks<D, C, 4, true>), grid, dim3(256), 0, st, chunks);
+      else
+        hipLaunchKernelGGL((k_cache_read_chunks<D, C, 4, false>), grid, dim3(256), 0, st, chunks);
+      return check_op_launch();
+    });
   const int64_t rows = 2 * n * (int64_t)a.heads, groups = std::min<int64_t>((rows + 3) / 4, 1 << 22);
   return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
     hipLaunchKernelGGL((k_cache_read<decltype(dt)::value, decltype(ct)::value>), dim3((unsigned)groups), dim3(256), 0,
-                       (hipStream_t)stream, a);
+                       st, a);
     return check_op_launch();
   });
 }
