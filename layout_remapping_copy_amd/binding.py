@@ -593,9 +593,15 @@ def _torch():
 
 
 def _stream_ptr(stream) -> int:
+    """The hipStream_t of a torch stream, or of the current one.  The current one is asked for its handle
+    alone: building the torch.cuda.Stream object takes 3 us, most of what a call of a few takes here."""
+    if stream is not None:
+        return int(stream.cuda_stream)
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return int(torch.cuda.current_stream().cuda_stream)
+    return raw(torch.cuda.current_device())
 
 
 def _device_tensor(t, what: str):

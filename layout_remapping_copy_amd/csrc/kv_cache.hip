@@ -57,8 +57,8 @@ struct ChunkSide {
   void* cache;
   float* scale;
   void* rows;
-  ModePair rh, rt;
-  int64_t ch, cs, cp;
+  ModePair rt;
+  int64_t rh, ch, cs, cp;
   Units un;
 };
 struct ChunkArgs {
@@ -84,60 +84,117 @@ __device__ __forceinline__ bool place_of(const ChunkArgs& a, int64_t slot, uint3
   return held;
 }
 
-// V finite numbers as codes, without a remainder each: x * (1 / scale) is within 2 steps of the quotient, and
-// two numbers round to the same code unless a tie lies between them.  `near` gathers how near the products
-// come to ties; below 8 (of the steps of fp32, 4 either way) the caller takes code_of instead.
+// V numbers as codes, without a remainder each: x * (1 / scale), the reciprocal off by a step at most, is
+// within 3 steps of fp32 of the quotient, so the two round to the same code unless a tie is that near.  Returns whether one may be (4 steps either way);
+// the caller then takes exact_codes.  NaN gives what code_of gives, infinities do not come here.
 template <int CT, int V>
-__device__ __forceinline__ void fast_codes(const float* v, float inv, uint32_t* code, uint32_t* near) {
+__device__ __forceinline__ bool fast_codes(const float* v, float inv, uint32_t* code) {
   if constexpr (CT == LR_E4M3) {
+    // Ties are the numbers between two codes.  They, and the codes themselves, have the last 19 bits zero.
+    // A row's largest value comes to 448, a code: all above the last tie, 432, is taken as 433.1, and all
+    // below the first, 2^-10, as 0.0009, which have other bits there.
+    uint32_t near = ~0u;
 #pragma unroll
     for (int k = 0; k < V; k += 4) {
       float q[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         q[e] = v[k + e] * inv;
-        // ties are half steps of a 3-bit mantissa; codes below 2^-6 are spaced as those just above it
-        float m = __builtin_fabsf(q[e]);
-        m = m < 0x1p-6f ? m + 0x1p-6f : m;
-        *near = min(*near, (__float_as_uint(m) + 0x80004u) & 0xfffffu);
+        near = min(near, (__float_as_uint(__builtin_amdgcn_fmed3f(__builtin_fabsf(q[e]), 0.0009f, 433.1f)) << 13) + (4u << 13));
       }
       const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
       code[k / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
     }
+    return near < 8u << 13;
   } else {
+    float far = 0;  // from the nearest whole number
 #pragma unroll
     for (int k = 0; k < V; k += 4) {
-      code[k / 4] = 0;
+      uint32_t c[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float q = v[k + e] * inv, r = __builtin_rintf(q);
-        if (__builtin_fabsf(q - r) > 0.5f - 0x1p-15f) *near = 0;
-        code[k / 4] |= ((uint32_t)(int32_t)r & 0xff) << (8 * e);
+        far = fmaxf(far, __builtin_fabsf(q - r));
+        c[e] = (uint32_t)(int32_t)r;
       }
+      const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400), hi = __builtin_amdgcn_perm(c[3], c[2], 0x04000c0c);
+      code[k / 4] = lo | hi;
     }
+    return far > 0.5f - 0x1p-15f;
   }
 }
+
+// max(x, |y|, |z|) in one instruction, of which fmaxf would make four: a NaN is passed over.
+__device__ __forceinline__ float max_abs(float x, float y, float z) {
+  float r;
+  asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  return r;
+}
+
+// The largest x >= 0 (as its bits, which have the same order) over the `lanes` lanes, a power of two, of a row:
+// within 16 lanes by exchanges that are part of the instruction (neighbours, pairs, mirrors of 8 and 16).
+__device__ __forceinline__ float row_max(float value, uint32_t lanes) {
+  uint32_t x = __float_as_uint(value);
+  if (lanes > 1) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xb1, 0xf, 0xf, true));
+  if (lanes > 2) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4e, 0xf, 0xf, true));
+  if (lanes > 4) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xf, 0xf, true));
+  if (lanes > 8) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xf, 0xf, true));
+  if (lanes > 16) x = max(x, (uint32_t)__shfl_xor((int)x, 16));
+  if (lanes > 32) x = max(x, (uint32_t)__shfl_xor((int)x, 32));
+  return __uint_as_float(x);
+}
+
+// amax / Q, rounded to nearest: with the rounded reciprocal of Q, one step on the remainder is exact (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
+template <int CT> __device__ __forceinline__ float scale_of(float amax) {
+  constexpr float kTop = CT == LR_E4M3 ? 448.f : 127.f, kInv = 1.f / kTop;
+  const float q = amax * kInv;
+  return fmaxf(__builtin_fmaf(__builtin_fmaf(-kTop, q, amax), kInv, q), 0x1p-126f);
+}
+// The same with the side of the nearest tie T decided by the sign of x - T scale, which one fma has right (T has
+// 8 bits at most): the quotient is moved a little to that side of T, or to T itself.  Values that repeat a simple
+// part of their row's largest, as 16-bit inputs often do, come here.  Takes infinities too.
 template <int CT, int V>
-__device__ __forceinline__ void exact_codes(const float* v, float scale, uint32_t* code) {
+__device__ __forceinline__ void exact_codes(const float* v, float scale, float inv, uint32_t* code) {
+  constexpr float kTop = CT == LR_E4M3 ? 448.f : 127.f;
+  float q[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const float x = v[k], p = x * inv;
+    if constexpr (CT == LR_E4M3) {
+      const uint32_t n = (__float_as_uint(p) + 4) & ~7u;
+      const float r = __builtin_fmaf(-__uint_as_float(n), scale, x);
+      const uint32_t moved = r == 0 ? n : (r > 0) == (x > 0) ? n + 1 : n - 1;
+      q[k] = n << 13 ? p : __uint_as_float(moved);
+    } else {
+      const float two = __builtin_rintf(2 * p), t = 0.5f * two;
+      const float r = __builtin_fmaf(-t, scale, x);
+      q[k] = __builtin_fabsf(p - t) < 0x1p-14f ? t + (r > 0 ? 0.25f : r < 0 ? -0.25f : 0.f) : p;
+    }
+    q[k] = x == x ? __builtin_amdgcn_fmed3f(__builtin_fabsf(x) < __builtin_inff() ? q[k] : x, -kTop, kTop) : CT == LR_E4M3 ? x : 0.f;
+  }
 #pragma unroll
   for (int k = 0; k < V; k += 4) {
-    code[k / 4] = 0;
+    if constexpr (CT == LR_E4M3) {
+      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[k], q[k + 1], 0, false);
+      code[k / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[k + 2], q[k + 3], lo, true);
+    } else {
+      code[k / 4] = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) code[k / 4] |= (uint32_t)(uint8_t)code_of<CT>(v[k + e], scale) << (8 * e);
+      for (int e = 0; e < 4; ++e) code[k / 4] |= ((uint32_t)(int32_t)__builtin_rintf(q[k + e]) & 0xff) << (8 * e);
+    }
   }
 }
 
 // Rows in chunks: a lane has one unit of a token's rows, its angles in registers for `per_lane` heads; the
-// lanes of a row (a power of two next to each other) find its largest value by exchange.  Absolute values
-// are compared as integers, in which order infinity and NaN come last: a row that holds one is told by its
-// maximum alone, and is done again with the care that it needs.
+// lanes of a row (a power of two next to each other) find its largest value by exchange.  A row that holds an
+// infinity is told by that value, and is done again with the care that it needs.
 template <int DT, int CT, int V, bool NT>
 __global__ void __launch_bounds__(256) k_cache_write_chunks(ChunkArgs a) {
   using T = typename ElemOf<DT>::T;
   using C = typename ElemOf<CT>::T;
   using Vec = typename Chunk<T, V>::Vec;
   constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
-  constexpr float kTop = CT == LR_E4M3 ? 448.f : 127.f;
   const ChunkSide& sd = a.side[blockIdx.z];
   uint32_t u, h, t;
   row_lane(a.grid, threadIdx.x, &u, &h, &t);  // lanes of a row are all there, for the exchange
@@ -149,20 +206,27 @@ __global__ void __launch_bounds__(256) k_cache_write_chunks(ChunkArgs a) {
   chunks_of(sd.un, u, V, &i, &j);
   const bool one = u < (uint32_t)sd.un.count, two = one && j < (uint32_t)sd.un.dim, turned = u < (uint32_t)sd.un.turned;
   const bool half = a.pairs == LR_PAIRS_HALF;
+  const bool ragged = sd.un.count * 2 * V != sd.un.dim || (uint32_t)sd.un.count != a.grid.lanes;
   const bool held = place_of(a, a.slots[t], &page, &in) && there;
   const T* x = (const T*)sd.rows + mode_offset(sd.rt, t);
   C* y = (C*)sd.cache + (int64_t)page * sd.cp + (int64_t)in * sd.cs;
   float* scales = sd.scale + (int64_t)page * a.sp + (int64_t)in * a.ss;
+  const uint32_t step = 1u << a.grid.head_shift, last = a.heads - 1;
+  const uint32_t left = (a.heads - (blockIdx.y * a.grid.per_lane << a.grid.head_shift) + step - 1) >> a.grid.head_shift;
+  const uint32_t count = min(a.grid.per_lane, left);  // the same for all lanes
+  Vec v, w, vn, wn;
+  auto load = [&](uint32_t head) {  // a lane past its row's end reads the row's first chunk, and stores nothing
+    const T* p = x + (int64_t)min(head, last) * sd.rh;
+    vn = load_chunk<NT, Vec>(p + (one ? i : 0));
+    wn = load_chunk<NT, Vec>(p + (two ? j : 0));
+  };
+  load(h);
   float c[V], s[V];
   if (turned) angles_of<V>(a.turns, a.positions[t], u, sd.un.rot, half, a.magnitude, 1.f, c, s);
-  const uint32_t step = 1u << a.grid.head_shift;
-  const uint32_t first = blockIdx.y * a.grid.per_lane << a.grid.head_shift;  // the same for every lane of the group
-  for (uint32_t n = 0; n < a.grid.per_lane && first + n * step < a.heads; ++n, h += step) {
+  for (uint32_t n = 0; n < count; ++n, h += step) {
     const bool mine = held && h < a.heads;
-    const T* p = x + mode_offset(sd.rh, h < a.heads ? h : 0);
-    Vec v = {}, w = {};
-    if (one) v = load_chunk<NT, Vec>(p + i);
-    if (two) w = load_chunk<NT, Vec>(p + j);
+    v = vn, w = wn;
+    if (n + 1 < count) load(h + step);
     C* q = y + (int64_t)h * sd.ch;
     if constexpr (!kQuant) {
       if (turned) {
@@ -180,30 +244,34 @@ __global__ void __launch_bounds__(256) k_cache_write_chunks(ChunkArgs a) {
 #pragma unroll
       for (int k = 0; k < V; ++k) f[k] = value_of<DT>(v[k]), g[k] = value_of<DT>(w[k]);
       if (turned) rotate_unit<V>(f, g, c, s, half);
-      uint32_t bits = 0;
+      if (ragged) {  // lanes past their row's end read something else
 #pragma unroll
-      for (int k = 0; k < V; ++k)
-        bits = max(bits, max(__float_as_uint(f[k]) & 0x7fffffffu, __float_as_uint(g[k]) & 0x7fffffffu));
-      for (uint32_t m = a.grid.lanes / 2; m; m >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, m));
-      const bool special = bits >= 0x7f800000u;
-      float amax = __uint_as_float(bits);
-      if (__any(special)) {  // the largest finite value instead
+        for (int k = 0; k < V; ++k) f[k] = one ? f[k] : 0.f, g[k] = two ? g[k] : 0.f;
+      }
+      auto largest = [&](float bound) {
         float z = 0;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-          if (__builtin_fabsf(f[k]) < __builtin_inff()) z = fmaxf(z, __builtin_fabsf(f[k]));
-          if (__builtin_fabsf(g[k]) < __builtin_inff()) z = fmaxf(z, __builtin_fabsf(g[k]));
+          const float x = __builtin_fabsf(f[k]), y = __builtin_fabsf(g[k]);
+          z = fmaxf(z, x < bound ? x : 0.f);
+          z = fmaxf(z, y < bound ? y : 0.f);
         }
-        for (uint32_t m = a.grid.lanes / 2; m; m >>= 1) z = fmaxf(z, __shfl_xor(z, m));
-        if (special) amax = z;
-      }
-      const float scale = fmaxf(amax / kTop, 0x1p-126f), inv = 1.f / scale;
-      uint32_t cv[V / 4], cw[V / 4], near = special ? 0 : ~0u;
-      fast_codes<CT, V>(f, inv, cv, &near);
-      fast_codes<CT, V>(g, inv, cw, &near);
-      if (__any(near < 8)) {
-        exact_codes<CT, V>(f, scale, cv);
-        exact_codes<CT, V>(g, scale, cw);
+        return row_max(z, a.grid.lanes);
+      };
+      float amax = 0;
+#pragma unroll
+      for (int k = 0; k < V; ++k) amax = max_abs(amax, f[k], g[k]);
+      amax = row_max(amax, a.grid.lanes);
+      const bool special = amax == __builtin_inff();
+      if (__any(special)) amax = largest(__builtin_inff());
+      const float scale = scale_of<CT>(amax), inv = __builtin_amdgcn_rcpf(scale);
+      uint32_t cv[V / 4], cw[V / 4];
+      bool near = special;
+      near |= fast_codes<CT, V>(f, inv, cv);
+      near |= fast_codes<CT, V>(g, inv, cw);
+      if (__any(near)) {
+        exact_codes<CT, V>(f, scale, inv, cv);
+        exact_codes<CT, V>(g, scale, inv, cw);
       }
       using CVec = typename Chunk<uint32_t, V / 4>::Vec;
       if (mine && one) store_chunk<NT>(q + i, *(const CVec*)cv);
@@ -233,7 +301,9 @@ __global__ void __launch_bounds__(256) k_cache_read_chunks(ChunkArgs a) {
   const C* x = (const C*)sd.cache + (int64_t)page * sd.cp + (int64_t)in * sd.cs;
   const float* scales = sd.scale + (int64_t)page * a.sp + (int64_t)in * a.ss;
   T* y = (T*)sd.rows + mode_offset(sd.rt, t);
-  const uint32_t end = min(a.heads, h + (a.grid.per_lane << a.grid.head_shift)), step = 1u << a.grid.head_shift;
+  const uint32_t step = 1u << a.grid.head_shift, last = a.heads - 1;
+  const uint32_t left = (a.heads - (blockIdx.y * a.grid.per_lane << a.grid.head_shift) + step - 1) >> a.grid.head_shift;
+  const uint32_t count = min(a.grid.per_lane, left);  // the same for all lanes
   auto made = [&](CVec v, float scale) -> Vec {
     Vec r;
     if constexpr (CT == LR_E4M3) {
@@ -254,20 +324,31 @@ __global__ void __launch_bounds__(256) k_cache_read_chunks(ChunkArgs a) {
     }
     return held ? r : Vec{};
   };
-  for (; h < end; h += 2 * step) {
-    const uint32_t h2 = h + step < end ? h + step : h;  // an odd last head is done twice
-    const C *p = x + (int64_t)h * sd.ch, *p2 = x + (int64_t)h2 * sd.ch;
-    float s = 1, s2 = 1;
-    if constexpr (kQuant) s = scales[(int64_t)h * a.sh], s2 = scales[(int64_t)h2 * a.sh];
-    const CVec v = load_chunk<NT, CVec>(p + i), v2 = load_chunk<NT, CVec>(p2 + i);
-    CVec w = {}, w2 = {};
-    if (two) w = load_chunk<NT, CVec>(p + j), w2 = load_chunk<NT, CVec>(p2 + j);
-    T *q = y + mode_offset(sd.rh, h), *q2 = y + mode_offset(sd.rh, h2);
-    store_chunk<NT>(q + i, made(v, s));
-    if (two) store_chunk<NT>(q + j, made(w, s));
-    if (h2 != h) {
-      store_chunk<NT>(q2 + i, made(v2, s2));
-      if (two) store_chunk<NT>(q2 + j, made(w2, s2));
+  CVec v[2], w[2];
+  float sc[2] = {1, 1};
+  auto load = [&](uint32_t n) {  // heads h + n step and the next
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const uint32_t hd = min(h + (n + z) * step, last);
+      const C* p = x + (int64_t)hd * sd.ch;
+      if constexpr (kQuant) sc[z] = load_chunk<NT, float>(scales + (int64_t)hd * a.sh);
+      v[z] = load_chunk<NT, CVec>(p + i);
+      w[z] = load_chunk<NT, CVec>(p + (two ? j : i));
+    }
+  };
+  load(0);
+  for (uint32_t n = 0; n < count; n += 2) {
+    CVec f[2], g[2];
+    float m[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) f[z] = v[z], g[z] = w[z], m[z] = sc[z];
+    if (n + 2 < count) load(n + 2);
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      if (n + z >= count || h + (n + z) * step > last) continue;
+      T* q = y + (int64_t)(h + (n + z) * step) * sd.rh;
+      store_chunk<NT>(q + i, made(f[z], m[z]));
+      if (two) store_chunk<NT>(q + j, made(g[z], m[z]));
     }
   }
 }
@@ -457,7 +538,7 @@ static int fill_chunks(const lr_cache* c, const CacheArgs& a, const lr_layout* L
   int v = (int)(16 / e);
   for (int i = 0; i < 2; ++i) {
     const CacheSide& s = a.side[i];
-    if (!mode_pair(mode_of(*L[i], 1), &k->side[i].rh) || !mode_pair(mode_of(*L[i], 2), &k->side[i].rt)) return 0;
+    if (one_leaf(mode_of(*L[i], 1), &k->side[i].rh) || !mode_pair(mode_of(*L[i], 2), &k->side[i].rt)) return 0;
     while (v > 1 && (s.rot / 2 % v || (s.dim - s.rot) % v || !rows_aligned(*L[i], s.rows, e, v) || !rows_aligned(*cl[i], s.cache, ce, v))) v /= 2;
   }
   if (v < 4) return 0;
@@ -478,7 +559,7 @@ static int fill_chunks(const lr_cache* c, const CacheArgs& a, const lr_layout* L
   if (reduce)
     while (lanes & (lanes - 1)) lanes += lanes & -lanes;
   if (lanes > 64) return 0;
-  k->grid = row_grid(lanes, a.heads, a.n, 2);
+  k->grid = row_grid(lanes, a.heads, a.n, 2, reduce ? 2 : 4);
   k->slots = a.slots;
   k->turns = a.turns;
   k->positions = a.positions;

@@ -264,13 +264,12 @@ struct RowGrid {
   FastDiv fd_lanes;
   uint32_t blocks_x, blocks_y;  // token blocks, head blocks
 };
-inline RowGrid row_grid(uint32_t lanes, uint32_t heads, uint32_t n, uint32_t sides) {
+inline RowGrid row_grid(uint32_t lanes, uint32_t heads, uint32_t n, uint32_t sides, uint32_t side_by_side) {
   RowGrid g;
   g.lanes = lanes;
   g.fd_lanes = make_fastdiv(lanes);
-  // up to 4 heads side by side: runs of 4 rows on the side where heads are neighbours, while the other
-  // lanes are neighbouring tokens for the side where those are
-  g.head_shift = heads >= 4 && lanes <= 16 ? 2 : heads >= 2 && lanes <= 32 ? 1 : 0;
+  g.head_shift = 0;
+  while (2u << g.head_shift <= std::min(heads, side_by_side) && lanes << g.head_shift <= 64) ++g.head_shift;
   g.tokens = (256 / lanes) >> g.head_shift;
   if (!g.tokens) g.tokens = 1, g.head_shift = 0;
   g.blocks_x = (n + g.tokens - 1) / g.tokens;

@@ -46,36 +46,43 @@ __global__ void __launch_bounds__(256) k_rope_chunks(RopeChunkArgs a) {
   const bool turned = u < (uint32_t)a.un.turned, two = j < (uint32_t)a.un.dim, half = a.pairs == LR_PAIRS_HALF;
   const T* x = (const T*)a.x + mode_offset(a.xt, t);
   T* y = (T*)a.y + mode_offset(a.yt, t);
+  const uint32_t step = 1u << a.grid.head_shift, last = a.heads - 1;
+  Vec v[2], w[2];
+  auto load = [&](uint32_t n) {  // heads h + n step and the next
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const T* p = x + mode_offset(a.xh, min(h + (n + z) * step, last));
+      v[z] = load_chunk<NT, Vec>(p + i);
+      w[z] = load_chunk<NT, Vec>(p + (two ? j : i));
+    }
+  };
+  load(0);
   float c[V], s[V];
   if (turned) angles_of<V>(a.turns, a.positions[mode_offset(a.p, t)], u, a.un.rot, half, a.magnitude, a.sign, c, s);
-  const uint32_t end = min(a.heads, h + (a.grid.per_lane << a.grid.head_shift)), step = 1u << a.grid.head_shift;
-  for (; h < end; h += 2 * step) {
-    const uint32_t h2 = h + step < end ? h + step : h;  // an odd last head is done twice
-    const T *p = x + mode_offset(a.xh, h), *p2 = x + mode_offset(a.xh, h2);
-    Vec v[2], w[2] = {};
-    v[0] = load_chunk<NT, Vec>(p + i);
-    v[1] = load_chunk<NT, Vec>(p2 + i);
-    if (two) {
-      w[0] = load_chunk<NT, Vec>(p + j);
-      w[1] = load_chunk<NT, Vec>(p2 + j);
-    }
+  const uint32_t left = (a.heads - (blockIdx.y * a.grid.per_lane << a.grid.head_shift) + step - 1) >> a.grid.head_shift;
+  const uint32_t count = min(a.grid.per_lane, left);  // the same for all lanes
+  for (uint32_t n = 0; n < count; n += 2) {
+    Vec f2[2], g2[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) f2[z] = v[z], g2[z] = w[z];
+    if (n + 2 < count) load(n + 2);
     if (turned) {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         float f[V], g[V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) f[k] = value_of<DT>(v[z][k]), g[k] = value_of<DT>(w[z][k]);
+        for (int k = 0; k < V; ++k) f[k] = value_of<DT>(f2[z][k]), g[k] = value_of<DT>(g2[z][k]);
         rotate_unit<V>(f, g, c, s, half);
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[z][k] = (T)f[k], w[z][k] = (T)g[k];
+        for (int k = 0; k < V; ++k) f2[z][k] = (T)f[k], g2[z][k] = (T)g[k];
       }
     }
-    T *q = y + mode_offset(a.yh, h), *q2 = y + mode_offset(a.yh, h2);
-    store_chunk<NT>(q + i, v[0]);
-    if (two) store_chunk<NT>(q + j, w[0]);
-    if (h2 != h) {
-      store_chunk<NT>(q2 + i, v[1]);
-      if (two) store_chunk<NT>(q2 + j, w[1]);
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      if (n + z >= count || h + (n + z) * step > last) continue;
+      T* q = y + mode_offset(a.yh, h + (n + z) * step);
+      store_chunk<NT>(q + i, f2[z]);
+      if (two) store_chunk<NT>(q + j, g2[z]);
     }
   }
 }
@@ -242,7 +249,10 @@ int lr_rope(const void* x, const lr_layout* Lx, int64_t x_capacity, void* y, con
     chunked = k.un.count <= 256;
   }
   if (chunked) {
-    k.grid = row_grid((uint32_t)k.un.count, a.heads, a.n, 1);
+    // four heads side by side: runs of four rows on the side where heads are neighbours, while the other lanes
+    // are neighbouring tokens for the side where those are (1, 2, 4, 8, 32 took 213, 194, 185, 197, 272 us for a
+    // head split of 512 MiB)
+    k.grid = row_grid((uint32_t)k.un.count, a.heads, a.n, 1, 4);
     chunked = row_grid_fits(k.grid);
     k.x = x;
     k.y = y;
