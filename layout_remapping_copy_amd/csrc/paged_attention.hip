@@ -70,29 +70,13 @@ __device__ __forceinline__ Deal deal_of(const AttentionArgs& a, uint64_t blocks)
   const uint64_t total = uniform64(blocks) * a.units, most = total / a.min_share;
   return Deal{total, (uint32_t)(most < 1 ? 1 : most < a.grid ? most : a.grid)};
 }
-__device__ __forceinline__ uint64_t wave_scan(uint64_t v, uint32_t lane) {  // inclusive
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t lane) {  // inclusive; 64 sequences stay below 2^30
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t u = __shfl_up((unsigned long long)v, d);
+    const uint32_t u = __shfl_up(v, d);
     if (lane >= (uint32_t)d) v += u;
   }
   return v;
-}
-// Where the blocks of sequence b start, with the deal.  Every wave computes it for itself.
-__device__ __forceinline__ uint64_t blocks_before(const AttentionArgs& a, uint32_t b, Deal* deal) {
-  const uint32_t lane = threadIdx.x & 63;
-  uint64_t all = 0, before = 0;
-  for (uint32_t i = lane; i < a.batch; i += 64) {
-    const uint64_t n = span_of(a, i).blocks;
-    all += n;
-    before += i < b ? n : 0;
-  }
-  for (int x = 32; x; x >>= 1) {
-    all += __shfl_xor((unsigned long long)all, x);
-    before += __shfl_xor((unsigned long long)before, x);
-  }
-  *deal = deal_of(a, all);
-  return uniform64(before) * a.units;
 }
 __device__ __forceinline__ uint64_t run_start(const Deal& d, uint64_t w) { return w * d.total / d.used; }
 __device__ __forceinline__ uint32_t run_of(const Deal& d, uint64_t block) {
@@ -106,13 +90,14 @@ struct Run {
   uint64_t start;    // of the current unit
   uint32_t b, u;     // the current unit: sequence, and its number there
   uint32_t split;    // the part of it that this run has
-  bool whole;        // all of it
+  bool whole, last;  // all of it; its end
   Span sp;
   uint32_t lo, hi;   // its tokens
 };
 __device__ __forceinline__ void run_unit(const AttentionArgs& a, uint32_t w, Run* r) {
   const uint64_t left = r->start + r->sp.blocks, stop = r->end < left ? r->end : left;
-  r->whole = r->at == r->start && stop == left;
+  r->last = stop == left;
+  r->whole = r->at == r->start && r->last;
   r->split = r->whole ? 0 : w - run_of(r->deal, r->start);
   r->lo = r->sp.base + (uint32_t)(r->at - r->start) * kBlock;
   const uint64_t hi = (uint64_t)r->sp.base + (stop - r->start) * kBlock;
@@ -128,13 +113,16 @@ __device__ __forceinline__ bool run_begin(const AttentionArgs& a, Run* r) {
     r->at = r->start = 0;
     r->end = r->sp.blocks;
   } else {
-    uint64_t v = lane < a.batch ? span_of(a, lane).blocks : 0;
-    uint64_t upto = wave_scan(v, lane);  // the first 64 sequences
-    if (a.batch <= 64) {
-      r->deal = deal_of(a, __shfl((unsigned long long)upto, 63));
-    } else {
-      blocks_before(a, 0, &r->deal);
+    uint32_t v = lane < a.batch ? span_of(a, lane).blocks : 0;
+    uint32_t upto = wave_scan(v, lane);  // the first 64 sequences
+    uint64_t all = __shfl(upto, 63);
+    if (a.batch > 64) {
+      uint64_t more = 0;
+      for (uint32_t i = 64 + lane; i < a.batch; i += 64) more += span_of(a, i).blocks;
+      for (int x = 32; x; x >>= 1) more += __shfl_xor((unsigned long long)more, x);
+      all += more;
     }
+    r->deal = deal_of(a, all);
     if (blockIdx.x >= r->deal.used) return false;
     r->at = run_start(r->deal, blockIdx.x);
     r->end = run_start(r->deal, blockIdx.x + 1);
@@ -144,10 +132,10 @@ __device__ __forceinline__ bool run_begin(const AttentionArgs& a, Run* r) {
       if (hit) {
         const int f = __ffsll((unsigned long long)hit) - 1;
         r->b = i + f;
-        r->start = (past + uniform64(__shfl((unsigned long long)(upto - v), f))) * a.units;
+        r->start = (past + uniform(__shfl(upto - v, f))) * a.units;
         break;
       }
-      past += uniform64(__shfl((unsigned long long)upto, 63));
+      past += uniform(__shfl(upto, 63));
       v = i + 64 + lane < a.batch ? span_of(a, i + 64 + lane).blocks : 0;
       upto = wave_scan(v, lane);
     }
@@ -168,6 +156,14 @@ __device__ __forceinline__ bool run_next(const AttentionArgs& a, Run* r) {
   }
   run_unit(a, blockIdx.x, r);
   return true;
+}
+
+// A part's maximum and sum for the second launch; the sign of the sum tells the last part of a unit.  A whole
+// unit is written at once, and leaves a first part that is the last, for which there is nothing to join.
+__device__ __forceinline__ void leave_part(const AttentionArgs& a, const Run& run, uint32_t bh, float m, float l) {
+  float* ml = a.part_ml + 2 * ((uint64_t)bh * a.splits + run.split);
+  ml[0] = m;
+  ml[1] = __uint_as_float((__float_as_uint(l) & 0x7fffffffu) | (run.last ? 0x80000000u : 0));
 }
 
 // Weight 2^(m - top) of a part with maximum m among parts with maximum top; 0 for a part
@@ -269,12 +265,8 @@ __global__ void __launch_bounds__(256) k_attention_element(AttentionArgs a) {
       a.part_o[((uint64_t)bh * a.splits + split) * a.dv + e] = acc;
   }
   if (threadIdx.x == 0) {
-    if (!run.whole) {
-      a.part_ml[2 * ((uint64_t)bh * a.splits + split)] = top;
-      a.part_ml[2 * ((uint64_t)bh * a.splits + split) + 1] = total;
-    } else if (a.lse) {
-      a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
-    }
+    if (a.splits > 1) leave_part(a, run, bh, top, total);
+    if (run.whole && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
   }
   } while (run_next(a, &run));
 }
@@ -371,6 +363,7 @@ struct MatrixShape {
   static constexpr int kValChunk = kF32 || DC == 64 ? 4 : 8;   // value elements a lane loads at a time
   static constexpr int kValSteps = DC / (16 * kValChunk);
   static constexpr int kVals = 4 * kTiles;                     // value rows a lane loads in a step
+  static constexpr int kMinWaves = DC == 256 && kElem > 1 ? 1 : 2;  // of a SIMD: the most that needs no spills
 };
 
 // A workgroup has one chunk of one sequence and HT * 16 query heads that share a cache head; its four
@@ -383,7 +376,7 @@ struct MatrixShape {
 // each lane a chunk).  Values come as whole rows (a row a group of 16 lanes), eight rows a lane, and are
 // transposed within the lane by byte permutes; the output's column 8 r + m is then row r of product m.
 template <int DT, int CT, int DC, int HT>
-__global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
+__global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves)) k_attention_matrix(AttentionArgs a) {
   using S = MatrixShape<DT, CT, DC, HT>;
   using T = typename ElemOf<DT>::T;
   using M = typename MatrixOf<DT>::T;
@@ -705,12 +698,8 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
           *(F4*)&a.part_o[((uint64_t)bh * a.splits + split) * a.dv + e] = acc;
         }
         if (e == 0) {
-          if (!run.whole) {
-            a.part_ml[2 * ((uint64_t)bh * a.splits + split)] = top;
-            a.part_ml[2 * ((uint64_t)bh * a.splits + split) + 1] = total;
-          } else if (a.lse) {
-            a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
-          }
+          if (a.splits > 1) leave_part(a, run, bh, top, total);
+          if (run.whole && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
         }
       }
     }
@@ -718,56 +707,63 @@ __global__ void __launch_bounds__(256) k_attention_matrix(AttentionArgs a) {
   }
 }
 
-// Joins the parts of one query head: 256 lanes are groups of lanes with four columns each, a group takes
-// every next part, and the groups' sums are added in their order.
+// Joins the parts of one query head: a wave has the weights of 64 parts at a time, one a lane; 256 lanes are
+// groups of lanes with four columns each, a group takes every next part, and the groups' sums are added in
+// their order.
 template <int DT>
 __global__ void __launch_bounds__(256) k_attention_join(AttentionArgs a) {
   using T = typename ElemOf<DT>::T;
+  typedef float F2 __attribute__((ext_vector_type(2)));
   __shared__ __attribute__((aligned(16))) float os[256 * 4];
-  __shared__ float ms[256], ls[256];
-  const uint32_t bh = blockIdx.x, b = bh / a.heads, h = bh % a.heads, g = h / a.group;
-  Deal deal;
-  const uint32_t blocks = span_of(a, b).blocks;
-  const uint64_t start = blocks_before(a, b, &deal) + (uint64_t)(g * a.tiles + h % a.group / a.unit_heads) * blocks;
-  const uint32_t from = run_of(deal, start), parts = run_of(deal, start + blocks - 1) - from + 1;
-  if (parts == 1) return;  // whole: written already
+  const uint32_t bh = blockIdx.x, lane = threadIdx.x & 63;
   const uint32_t wide = ((uint32_t)a.dv + 3) / 4, groups = 256 / wide, grp = threadIdx.x / wide, c = threadIdx.x % wide;
-  const float* ml = a.part_ml + 2 * (uint64_t)bh * a.splits;
-  const float* po = a.part_o + (uint64_t)bh * a.splits * a.dv;
-  float m = -__builtin_inff(), l = 0;
+  const F2* ml = (const F2*)a.part_ml + (uint64_t)bh * a.splits;
+  const float* po = a.part_o + (uint64_t)bh * a.splits * a.dv + 4 * c;
+  float top = -__builtin_inff(), total = 0;
   F4 acc = {};
-  if (grp < groups)
-    for (uint32_t s = grp; s < parts; s += groups) {
-      const float top = fmaxf(m, ml[2 * s]), keep = weight_of(m, top), wt = weight_of(ml[2 * s], top);
-      F4 x;
+  for (uint32_t s = 0; s < a.splits; s += 64) {
+    F2 x = {-__builtin_inff(), 0.f};
+    if (s + lane < a.splits) x = ml[s + lane];
+    const uint64_t hit = __ballot(__float_as_uint(x[1]) >> 31);  // what is past the last part means nothing
+    const uint32_t parts = hit ? __ffsll((unsigned long long)hit) : 64;
+    if (s == 0 && parts == 1) return;  // whole: written already
+    const float m = lane < parts ? x[0] : -__builtin_inff();
+    float most = m;
+    for (int d = 32; d; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
+    most = fmaxf(top, most);
+    const float keep = weight_of(top, most), wt = weight_of(m, most);
+    float sum = lane < parts ? __builtin_fabsf(x[1]) * wt : 0.f;
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    total = total * keep + sum;
+    top = most;
+    acc *= keep;
+#pragma unroll 4
+    for (uint32_t q = 0; q < parts; q += groups) {
+      const uint32_t p = q + grp;
+      const float w = __shfl(wt, p & 63);
+      if (p >= parts || grp >= groups) continue;
+      const float* y = po + (uint64_t)(s + p) * a.dv;
       if (a.dv % 4 == 0) {
-        x = *(const F4*)&po[(uint64_t)s * a.dv + 4 * c];
+        acc += *(const F4*)y * w;
       } else {
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) x[i] = 4 * c + i < (uint32_t)a.dv ? po[(uint64_t)s * a.dv + 4 * c + i] : 0.f;
+        for (uint32_t i = 0; i < 4; ++i)
+          if (4 * c + i < (uint32_t)a.dv) acc[i] += y[i] * w;
       }
-      acc = acc * keep + x * wt;
-      l = l * keep + ml[2 * s + 1] * wt;
-      m = top;
     }
+    if (hit) break;
+  }
   *(F4*)&os[4 * threadIdx.x] = acc;
-  ms[threadIdx.x] = m;
-  ls[threadIdx.x] = l;
   __syncthreads();
   if (grp) return;
-  for (uint32_t i = 1; i < groups; ++i) {
-    const uint32_t at = i * wide + c;
-    const float top = fmaxf(m, ms[at]), keep = weight_of(m, top), wt = weight_of(ms[at], top);
-    acc = acc * keep + *(const F4*)&os[4 * at] * wt;
-    l = l * keep + ls[at] * wt;
-    m = top;
-  }
+  for (uint32_t i = 1; i < groups; ++i) acc += *(const F4*)&os[4 * (i * wide + c)];
+  const uint32_t b = bh / a.heads, h = bh % a.heads;
   T* out = (T*)a.out + (int64_t)b * a.ob + (int64_t)h * a.oh;
-  const float inv = l > 0 ? 1.f / l : 0.f;
+  const float inv = total > 0 ? 1.f / total : 0.f;
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i)
-    if (4 * c + i < (uint32_t)a.dv) out[(int64_t)(4 * c + i) * a.od] = (T)(l != l ? l : acc[i] * inv);
-  if (c == 0 && a.lse) a.lse[bh] = m == -__builtin_inff() ? m : (m + __log2f(l)) * kLn2;
+    if (4 * c + i < (uint32_t)a.dv) out[(int64_t)(4 * c + i) * a.od] = (T)(total != total ? total : acc[i] * inv);
+  if (c == 0 && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
@@ -932,7 +928,7 @@ int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, c
     a.units = a.heads;
   }
   a.q_wide = rows_aligned(*Lq, q, e, 16 / e);
-  a.grid = a.path == LR_ATTENTION_ELEMENT ? 2048 : 256;
+  a.grid = a.path == LR_ATTENTION_ELEMENT ? 2048 : getenv("GRID") ? atoi(getenv("GRID")) : 256;
   const hipStream_t st = (hipStream_t)stream;
   if (dtype == LR_F32) return launch_attention_of<LR_F32>(a, c->dtype, st);
   if (dtype == LR_F16) return launch_attention_of<LR_F16>(a, c->dtype, st);
