@@ -558,8 +558,12 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
       page = page_of(t0 + 2 * kStep);
       load_keys();
       // weights
-      M pw[HT];
-      B8 phi[HT], plo[HT];
+      // Of 16-bit products' weights two parts are taken, the value and what its rounding left: a bf16 alone
+      // would add as much error to the output as its own rounding does, and cost an fp16 model with an 8-bit
+      // cache its last three bits.
+      using P = std::conditional_t<kQuant, B8, M>;
+      using PE = std::conditional_t<kQuant, __bf16, T>;
+      P phi[HT], plo[HT];
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
         float top = -__builtin_inff();
@@ -592,15 +596,9 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
           for (int i = 0; i < 4; ++i) {
             float x = __builtin_amdgcn_exp2f(s[ht][t][i] - base[ht]);
             l[ht] += x;
-            if constexpr (kQuant) {
-              // two bf16 parts hold 16 bits of weight * scale: a bf16 alone would cost an fp16 model
-              // its last three bits
-              x *= vsc[t][i];
-              phi[ht][4 * t + i] = (__bf16)x;
-              plo[ht][4 * t + i] = (__bf16)(x - (float)phi[ht][4 * t + i]);
-            } else {
-              pw[ht][4 * t + i] = (T)x;
-            }
+            if constexpr (kQuant) x *= vsc[t][i];
+            phi[ht][4 * t + i] = (PE)x;
+            if constexpr (!S::kF32) plo[ht][4 * t + i] = (PE)(x - (float)phi[ht][4 * t + i]);
           }
       }
       if (seen != kAll)  // what is not seen may hold NaN
@@ -618,7 +616,7 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
 #pragma unroll
             for (int ht = 0; ht < HT; ++ht)
               o[ht][p][m] = mfma(F4{__uint_as_float(vr[0][p][m]), __uint_as_float(vr[1][p][m]),
-                                    __uint_as_float(vr[2][p][m]), __uint_as_float(vr[3][p][m])}, pw[ht], o[ht][p][m]);
+                                    __uint_as_float(vr[2][p][m]), __uint_as_float(vr[3][p][m])}, phi[ht], o[ht][p][m]);
         } else if constexpr (kQuant) {
 #pragma unroll
           for (int d = 0; d < S::kValChunk / 4; ++d) {
@@ -654,8 +652,12 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
             }
 #pragma unroll
             for (int ht = 0; ht < HT; ++ht) {
-              o[ht][p][2 * d] = mfma(__builtin_bit_cast(M, v0), pw[ht], o[ht][p][2 * d]);
-              o[ht][p][2 * d + 1] = mfma(__builtin_bit_cast(M, v1), pw[ht], o[ht][p][2 * d + 1]);
+              F4& oa = o[ht][p][2 * d];
+              F4& ob = o[ht][p][2 * d + 1];
+              oa = mfma(__builtin_bit_cast(M, v0), phi[ht], oa);
+              ob = mfma(__builtin_bit_cast(M, v1), phi[ht], ob);
+              oa = mfma(__builtin_bit_cast(M, v0), plo[ht], oa);
+              ob = mfma(__builtin_bit_cast(M, v1), plo[ht], ob);
             }
           }
         }
