@@ -84,9 +84,10 @@ __device__ __forceinline__ bool place_of(const ChunkArgs& a, int64_t slot, uint3
   return held;
 }
 
-// V numbers as codes, without a remainder each: x * (1 / scale), the reciprocal off by a step at most, is
-// within 3 steps of fp32 of the quotient, so the two round to the same code unless a tie is that near.  Returns whether one may be (4 steps either way);
-// the caller then takes exact_codes.  NaN gives what code_of gives, infinities do not come here.
+// V numbers as codes, without a remainder each: x * (1 / scale), the reciprocal off by a step at most, is within
+// 3 steps of fp32 of the quotient, so the two round to the same code unless a tie is that near.  Returns whether
+// one may be (4 steps either way); the caller then takes exact_codes.  NaN gives what code_of gives, infinities
+// do not come here.
 template <int CT, int V>
 __device__ __forceinline__ bool fast_codes(const float* v, float inv, uint32_t* code) {
   if constexpr (CT == LR_E4M3) {
@@ -100,7 +101,8 @@ __device__ __forceinline__ bool fast_codes(const float* v, float inv, uint32_t* 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         q[e] = v[k + e] * inv;
-        near = min(near, (__float_as_uint(__builtin_amdgcn_fmed3f(__builtin_fabsf(q[e]), 0.0009f, 433.1f)) << 13) + (4u << 13));
+        const float m = __builtin_amdgcn_fmed3f(__builtin_fabsf(q[e]), 0.0009f, 433.1f);
+        near = min(near, (__float_as_uint(m) << 13) + (4u << 13));
       }
       const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
       code[k / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
@@ -117,8 +119,8 @@ __device__ __forceinline__ bool fast_codes(const float* v, float inv, uint32_t* 
         far = fmaxf(far, __builtin_fabsf(q - r));
         c[e] = (uint32_t)(int32_t)r;
       }
-      const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400), hi = __builtin_amdgcn_perm(c[3], c[2], 0x04000c0c);
-      code[k / 4] = lo | hi;
+      const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400);
+      code[k / 4] = lo | __builtin_amdgcn_perm(c[3], c[2], 0x04000c0c);
     }
     return far > 0.5f - 0x1p-15f;
   }
@@ -171,7 +173,8 @@ __device__ __forceinline__ void exact_codes(const float* v, float scale, float i
       const float r = __builtin_fmaf(-t, scale, x);
       q[k] = __builtin_fabsf(p - t) < 0x1p-14f ? t + (r > 0 ? 0.25f : r < 0 ? -0.25f : 0.f) : p;
     }
-    q[k] = x == x ? __builtin_amdgcn_fmed3f(__builtin_fabsf(x) < __builtin_inff() ? q[k] : x, -kTop, kTop) : CT == LR_E4M3 ? x : 0.f;
+    const float within = __builtin_amdgcn_fmed3f(__builtin_fabsf(x) < __builtin_inff() ? q[k] : x, -kTop, kTop);
+    q[k] = x == x ? within : CT == LR_E4M3 ? x : 0.f;
   }
 #pragma unroll
   for (int k = 0; k < V; k += 4) {
@@ -311,8 +314,10 @@ __global__ void __launch_bounds__(256) k_cache_read_chunks(ChunkArgs a) {
       typedef float F2 __attribute__((ext_vector_type(2)));
 #pragma unroll
       for (int k = 0; k < V; k += 4) {
-        const F2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(d[k / 4], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(d[k / 4], true);
-        r[k] = (T)(lo[0] * scale), r[k + 1] = (T)(lo[1] * scale), r[k + 2] = (T)(hi[0] * scale), r[k + 3] = (T)(hi[1] * scale);
+        const F2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(d[k / 4], false);
+        const F2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(d[k / 4], true);
+        r[k] = (T)(lo[0] * scale), r[k + 1] = (T)(lo[1] * scale);
+        r[k + 2] = (T)(hi[0] * scale), r[k + 3] = (T)(hi[1] * scale);
       }
     } else {
 #pragma unroll
@@ -434,7 +439,8 @@ __global__ void __launch_bounds__(256) k_cache_read(CacheArgs a) {
     const uint32_t page = held ? (uint32_t)slot / a.page_size : 0, in = held ? (uint32_t)slot % a.page_size : 0;
     const C* x = (const C*)s.cache + (int64_t)page * s.cp + (int64_t)in * s.cs + (int64_t)h * s.ch;
     float scale = 1;
-    if constexpr (CT == LR_E4M3 || CT == LR_INT8) scale = s.scale[(int64_t)page * a.sp + (int64_t)in * a.ss + (int64_t)h * a.sh];
+    if constexpr (CT == LR_E4M3 || CT == LR_INT8)
+      scale = s.scale[(int64_t)page * a.sp + (int64_t)in * a.ss + (int64_t)h * a.sh];
     for (uint32_t e = lane; e < (uint32_t)s.dim; e += 64)
       y[(int64_t)e * s.rd] = held ? (T)(value_of<CT>(x[(int64_t)e * s.cd]) * scale) : (T)0.f;
   }
@@ -539,7 +545,9 @@ static int fill_chunks(const lr_cache* c, const CacheArgs& a, const lr_layout* L
   for (int i = 0; i < 2; ++i) {
     const CacheSide& s = a.side[i];
     if (one_leaf(mode_of(*L[i], 1), &k->side[i].rh) || !mode_pair(mode_of(*L[i], 2), &k->side[i].rt)) return 0;
-    while (v > 1 && (s.rot / 2 % v || (s.dim - s.rot) % v || !rows_aligned(*L[i], s.rows, e, v) || !rows_aligned(*cl[i], s.cache, ce, v))) v /= 2;
+    while (v > 1 && (s.rot / 2 % v || (s.dim - s.rot) % v || !rows_aligned(*L[i], s.rows, e, v) ||
+                     !rows_aligned(*cl[i], s.cache, ce, v)))
+      v /= 2;
   }
   if (v < 4) return 0;
   uint32_t lanes = 1;

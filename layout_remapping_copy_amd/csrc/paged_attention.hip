@@ -66,7 +66,8 @@ __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgc
 __device__ __forceinline__ uint64_t uniform64(uint64_t x) {
   return uniform((uint32_t)x) | (uint64_t)uniform((uint32_t)(x >> 32)) << 32;
 }
-__device__ __forceinline__ Deal deal_of(const AttentionArgs& a, uint64_t blocks) {  // blocks of one unit each, all sequences
+// blocks: of all sequences, one unit each.
+__device__ __forceinline__ Deal deal_of(const AttentionArgs& a, uint64_t blocks) {
   const uint64_t total = uniform64(blocks) * a.units, most = total / a.min_share;
   return Deal{total, (uint32_t)(most < 1 ? 1 : most < a.grid ? most : a.grid)};
 }
@@ -178,6 +179,13 @@ __device__ __forceinline__ float weight_of(float m, float top) {
   return m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - top);
 }
 
+// Orders this wave's accesses to shared memory; one wave's are done in their order, so no wait is needed.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Any types, strides and alignment.  A unit is one query head; a workgroup's
 // waves take tiles of 64 tokens of its run in turn, a lane a token for the scores and every 64th
 // value column for the sums.
@@ -194,86 +202,87 @@ __global__ void __launch_bounds__(256) k_attention_element(AttentionArgs a) {
   Run run;
   if (!run_begin(a, &run)) return;
   do {
-  const uint32_t b = run.b, h = run.u, g = h / a.group, bh = b * a.heads + h, split = run.split, hi = run.hi;
-  const uint64_t lo = run.lo;
-  const Span sp = run.sp;
-  __syncthreads();
-  for (uint32_t e = threadIdx.x; e < (uint32_t)a.dk; e += 256)
-    qs[e] = value_of<DT>(((const T*)a.q)[(int64_t)b * a.qb + (int64_t)h * a.qh + (int64_t)e * a.qd]) * a.scale2;
-  __syncthreads();
-  float m = -__builtin_inff(), l = 0, o[kAttentionDim / 64] = {};
-  for (uint64_t t0 = lo + 64 * w; t0 < hi; t0 += 256) {
-    const uint32_t t = (uint32_t)t0 + lane;
-    bool seen = t < hi && t >= sp.first;
-    int64_t page = 0;
-    const uint32_t pg = op_div(t, a.fd_page), in = t - pg * a.page_size;
-    if (seen) {
-      page = a.table[(int64_t)b * a.table_stride + pg];
-      seen = page >= 0 && page < (int64_t)a.pages;
-    }
-    float s = -__builtin_inff(), vscale = 1;
-    if (seen) {
-      const C* k = (const C*)a.k + page * a.kp + (int64_t)in * a.ksl + (int64_t)g * a.kh;
-      float dot = 0;
-      for (int e = 0; e < a.dk; ++e) dot += qs[e] * value_of<CT>(k[(int64_t)e * a.kd]);
-      if constexpr (CT == LR_E4M3 || CT == LR_INT8) {
-        const int64_t so = page * a.sp + (int64_t)in * a.ssl + (int64_t)g * a.sh;
-        dot *= a.ks[so];
-        vscale = a.vs[so];
+    const uint32_t b = run.b, h = run.u, g = h / a.group, bh = b * a.heads + h, split = run.split, hi = run.hi;
+    const uint64_t lo = run.lo;
+    const Span sp = run.sp;
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < (uint32_t)a.dk; e += 256)
+      qs[e] = value_of<DT>(((const T*)a.q)[(int64_t)b * a.qb + (int64_t)h * a.qh + (int64_t)e * a.qd]) * a.scale2;
+    __syncthreads();
+    float m = -__builtin_inff(), l = 0, o[kAttentionDim / 64] = {};
+    for (uint64_t t0 = lo + 64 * w; t0 < hi; t0 += 256) {
+      const uint32_t t = (uint32_t)t0 + lane;
+      bool seen = t < hi && t >= sp.first;
+      int64_t page = 0;
+      const uint32_t pg = op_div(t, a.fd_page), in = t - pg * a.page_size;
+      if (seen) {
+        page = a.table[(int64_t)b * a.table_stride + pg];
+        seen = page >= 0 && page < (int64_t)a.pages;
       }
-      s = dot;
-    }
-    float top = s;
-    for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-    top = fmaxf(m, top);
-    const float keep = weight_of(m, top);
-    const float p = seen ? __builtin_amdgcn_exp2f(s - (top == -__builtin_inff() ? 0.f : top)) : 0.f;
-    float sum = p;
-    for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
-    l = l * keep + sum;
-    m = top;
-    ps[w][lane] = p * vscale;
-    at[w][lane] = seen ? page * a.vp + (int64_t)in * a.vsl + (int64_t)g * a.vh : -1;
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int i = 0; i < kAttentionDim / 64; ++i) {
-      const int e = (int)lane + 64 * i;
-      if (64 * i >= a.dv) break;
-      float acc = o[i] * keep;
-      for (int j = 0; j < 64; ++j) {
-        const int64_t off = at[w][j];
-        if (off >= 0 && e < a.dv) acc += ps[w][j] * value_of<CT>(((const C*)a.v)[off + (int64_t)e * a.vd]);
+      float s = -__builtin_inff(), vscale = 1;
+      if (seen) {
+        const C* k = (const C*)a.k + page * a.kp + (int64_t)in * a.ksl + (int64_t)g * a.kh;
+        float dot = 0;
+        for (int e = 0; e < a.dk; ++e) dot += qs[e] * value_of<CT>(k[(int64_t)e * a.kd]);
+        if constexpr (CT == LR_E4M3 || CT == LR_INT8) {
+          const int64_t so = page * a.sp + (int64_t)in * a.ssl + (int64_t)g * a.sh;
+          dot *= a.ks[so];
+          vscale = a.vs[so];
+        }
+        s = dot;
       }
-      o[i] = acc;
-    }
-    __builtin_amdgcn_wave_barrier();
-  }
-  if (lane == 0) {
-    ms[w] = m;
-    ls[w] = l;
-  }
+      float top = s;
+      for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+      top = fmaxf(m, top);
+      const float keep = weight_of(m, top);
+      const float p = seen ? __builtin_amdgcn_exp2f(s - (top == -__builtin_inff() ? 0.f : top)) : 0.f;
+      float sum = p;
+      for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
+      l = l * keep + sum;
+      m = top;
+      ps[w][lane] = p * vscale;
+      at[w][lane] = seen ? page * a.vp + (int64_t)in * a.vsl + (int64_t)g * a.vh : -1;
+      wave_fence();
 #pragma unroll
-  for (int i = 0; i < kAttentionDim / 64; ++i) os[w][lane + 64 * i] = o[i];
-  __syncthreads();
-  const float top = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
-  float total = 0, wt[4];
-  for (int i = 0; i < 4; ++i) {
-    wt[i] = weight_of(ms[i], top);
-    total += ls[i] * wt[i];
-  }
-  const uint32_t e = threadIdx.x;
-  if (e < (uint32_t)a.dv) {
-    float acc = 0;
-    for (int i = 0; i < 4; ++i) acc += os[i][e] * wt[i];
-    if (run.whole)
-      ((T*)a.out)[(int64_t)b * a.ob + (int64_t)h * a.oh + (int64_t)e * a.od] = (T)(total > 0 ? acc / total : 0.f * acc);
-    else
-      a.part_o[((uint64_t)bh * a.splits + split) * a.dv + e] = acc;
-  }
-  if (threadIdx.x == 0) {
-    if (a.splits > 1) leave_part(a, run, bh, top, total);
-    if (run.whole && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
-  }
+      for (int i = 0; i < kAttentionDim / 64; ++i) {
+        const int e = (int)lane + 64 * i;
+        if (64 * i >= a.dv) break;
+        float acc = o[i] * keep;
+        for (int j = 0; j < 64; ++j) {
+          const int64_t off = at[w][j];
+          if (off >= 0 && e < a.dv) acc += ps[w][j] * value_of<CT>(((const C*)a.v)[off + (int64_t)e * a.vd]);
+        }
+        o[i] = acc;
+      }
+      wave_fence();
+    }
+    if (lane == 0) {
+      ms[w] = m;
+      ls[w] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < kAttentionDim / 64; ++i) os[w][lane + 64 * i] = o[i];
+    __syncthreads();
+    const float top = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+    float total = 0, wt[4];
+    for (int i = 0; i < 4; ++i) {
+      wt[i] = weight_of(ms[i], top);
+      total += ls[i] * wt[i];
+    }
+    const uint32_t e = threadIdx.x;
+    if (e < (uint32_t)a.dv) {
+      float acc = 0;
+      for (int i = 0; i < 4; ++i) acc += os[i][e] * wt[i];
+      if (run.whole)
+        ((T*)a.out)[(int64_t)b * a.ob + (int64_t)h * a.oh + (int64_t)e * a.od] =
+            (T)(total > 0 ? acc / total : 0.f * acc);
+      else
+        a.part_o[((uint64_t)bh * a.splits + split) * a.dv + e] = acc;
+    }
+    if (threadIdx.x == 0) {
+      if (a.splits > 1) leave_part(a, run, bh, top, total);
+      if (run.whole && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
+    }
   } while (run_next(a, &run));
 }
 
@@ -289,8 +298,12 @@ typedef uint32_t U4 __attribute__((ext_vector_type(4)));
 template <int BYTES> struct Raw { typedef uint32_t T __attribute__((ext_vector_type(BYTES / 4))); };
 template <> struct Raw<4> { typedef uint32_t T; };
 
-__device__ __forceinline__ F4 mfma(B8 a, B8 b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-__device__ __forceinline__ F4 mfma(H8 a, H8 b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ F4 mfma(B8 a, B8 b, F4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ F4 mfma(H8 a, H8 b, F4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
 __device__ __forceinline__ F4 mfma(F4 a, F4 b, F4 c) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
@@ -323,6 +336,20 @@ __device__ __forceinline__ typename MatrixOf<DT>::T decode(typename Raw<8>::T x)
   return y;
 }
 
+// Four codes as fp32.
+template <int CT> __device__ __forceinline__ F4 decode4(uint32_t x) {
+  F4 y;
+  if constexpr (CT == LR_E4M3) {
+    typedef float F2 __attribute__((ext_vector_type(2)));
+    const F2 a = __builtin_amdgcn_cvt_pk_f32_fp8(x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(x, true);
+    y = F4{a[0], a[1], b[0], b[1]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = (float)(int8_t)(x >> (8 * e));
+  }
+  return y;
+}
+
 // Two codes (the low or the high half of x) as bf16.
 template <int CT, bool HIGH>
 __device__ __forceinline__ uint32_t decode_pair(uint32_t x) {
@@ -348,13 +375,6 @@ __device__ __forceinline__ float across_groups_sum(float x) {
   x += __shfl_xor(x, 16);
   return x + __shfl_xor(x, 32);
 }
-// Orders this wave's accesses to shared memory; one wave's are done in their order, so no wait is needed.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // Keys and values up to DC wide; HT tiles of 16 query heads of one cache head.
 template <int DT, int CT, int DC, int HT>
 struct MatrixShape {
@@ -369,7 +389,8 @@ struct MatrixShape {
   static constexpr int kValChunk = kF32 || DC == 64 ? 4 : 8;   // value elements a lane loads at a time
   static constexpr int kValSteps = DC / (16 * kValChunk);
   static constexpr int kVals = 4 * kTiles;                     // value rows a lane loads in a step
-  static constexpr int kMinWaves = (DC == 256 && kElem > 1) || (kF32 && DC * HT > 128) ? 1 : 2;  // of a SIMD: the most that needs no spills
+  // waves of a SIMD, the most that needs no spills
+  static constexpr int kMinWaves = (DC == 256 && kElem > 1) || (kF32 && DC * HT > 128) ? 1 : 2;
 };
 
 // A workgroup has one chunk of one sequence and HT * 16 query heads that share a cache head; its four
@@ -402,326 +423,338 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
   Run run;
   if (!run_begin(a, &run)) return;
   for (bool again = false;; again = true) {
-  const uint32_t b = run.b, g = run.u / a.tiles, split = run.split, hi = run.hi;
-  const uint32_t in_group = run.u % a.tiles * 16 * HT;  // first query head of this unit within its group
-  const Span sp = run.sp;
-  const uint32_t lo = run.lo;
+    const uint32_t b = run.b, g = run.u / a.tiles, split = run.split, hi = run.hi;
+    const uint32_t in_group = run.u % a.tiles * 16 * HT;  // first query head of this unit within its group
+    const Span sp = run.sp;
+    const uint32_t lo = run.lo;
 
-  // queries: lane r's head, dimensions chunk kk * 4 + j
-  const uint32_t rq = here(r), jq = here(j);
-  M q[HT][S::kKeySteps * S::kKeyParts];
-  auto dim_at = [&](int kk) -> uint32_t { return ((kk / S::kKeyParts * 4 + jq) * S::kKeyParts + kk % S::kKeyParts) * S::kPart; };
-  const T* qb = (const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group) * a.qh;
-  auto load_queries = [&](auto wide) {
-#pragma unroll
-    for (int ht = 0; ht < HT; ++ht) {
-      const uint32_t h = in_group + 16 * ht + rq;
-      const T* x = qb + (int64_t)(h < a.group ? h : 0) * a.qh;
-#pragma unroll
-      for (int kk = 0; kk < S::kKeySteps * S::kKeyParts; ++kk) {
-        const uint32_t e0 = dim_at(kk) < (uint32_t)a.dk ? dim_at(kk) : 0;
-        if constexpr (decltype(wide)::value) {
-          q[ht][kk] = *(const M*)(x + e0);
-        } else {
-#pragma unroll
-          for (int e = 0; e < S::kPart; ++e) q[ht][kk][e] = x[(int64_t)(e0 + e) * a.qd];
-        }
-      }
-    }
-  };
-  if (a.q_wide)
-    load_queries(std::true_type{});
-  else
-    load_queries(std::false_type{});
-#pragma unroll
-  for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-    for (int kk = 0; kk < S::kKeySteps * S::kKeyParts; ++kk)
-      if (in_group + 16 * ht + rq >= a.group || dim_at(kk) >= (uint32_t)a.dk) q[ht][kk] = M{};
-
-  // Page lookup: lanes 0 .. and 32 .. find the pages of a step's tokens, the first for keys, the second
-  // for values.  All loads of the loop below are unconditional, so that each wait is for the loads it
-  // needs and no younger ones: what is not there is read from a place that is, and left out after.
-  const uint32_t li = lane & (S::kTokens - 1);
-  const bool for_v = lane >= 32;
-  const int32_t* table = a.table + (int64_t)b * a.table_stride;
-  const uint32_t one = a.fd_page.m ? 0 : ~0u;  // pages of one slot: the quotient is the dividend
-  auto page_index = [&](uint32_t t) -> uint32_t { return (__umulhi(t, a.fd_page.m) >> a.fd_page.s) + (t & one); };
-  auto page_of = [&](uint32_t t0) -> int32_t {
-    const uint32_t t = t0 + li;
-    return table[page_index(t < hi ? t : hi - 1)];
-  };
-  const int64_t page_step = (for_v ? a.vp : a.kp) * S::kElem, slot_step = (for_v ? a.vsl : a.ksl) * S::kElem;
-  const float* scale_base = nullptr;
-  if constexpr (kQuant) scale_base = (for_v ? a.vs : a.ks) + (int64_t)g * a.sh;
-  const char* kbase = (const char*)a.k + (int64_t)g * a.kh * S::kElem;
-  const char* vbase = (const char*)a.v + (int64_t)g * a.vh * S::kElem;
-
-  // The step's row offsets to shared memory (0, the cache's first row, for a token that is not seen);
-  // returns the mask of its seen tokens.
-  auto place = [&](uint32_t t0, int32_t page, float* scale) -> uint32_t {
-    const uint32_t t = t0 + li;
-    const bool ok = (t >= sp.first) & (t < hi) & ((uint32_t)page < a.pages);
-    const uint32_t in = ok ? t - page_index(t) * a.page_size : 0, pg = ok ? page : 0;
-    wave_fence();
-    offs[lane] = (int64_t)(pg * (uint64_t)page_step + in * (uint64_t)slot_step);
-    wave_fence();
-    if constexpr (kQuant) *scale = __builtin_nontemporal_load(scale_base + (pg * (uint64_t)a.sp + in * (uint64_t)a.ssl));
-    return (uint32_t)__ballot(ok);
-  };
-
-  KR kr[S::kTiles][S::kKeySteps];
-  VR vr[S::kVals][S::kValSteps];
-  // Where a lane's chunk kk of a row is read: past the row's end the first one's place, and half past it (8
-  // elements of 16 are left) 8 before, whose upper half they are.
-  auto key_at = [&](int kk) -> uint32_t {
-    const uint32_t e0 = (kk * 4 + j) * S::kKeyChunk;
-    return e0 >= (uint32_t)a.dk ? 0 : e0 + S::kKeyChunk > (uint32_t)a.dk ? e0 - 8 : e0;
-  };
-  const bool ragged = a.dk != DC;
-  auto load_keys = [&]() {
-#pragma unroll
-    for (int t = 0; t < S::kTiles; ++t) {
-      const char* row = kbase + offs[16 * t + r];
-#pragma unroll
-      for (int kk = 0; kk < S::kKeySteps; ++kk) {
-        kr[t][kk] = __builtin_nontemporal_load((const KR*)(row + key_at(kk) * S::kElem));
-      }
-    }
-  };
-  auto load_values = [&]() {
-#pragma unroll
-    for (int x = 0; x < S::kVals; ++x) {
-      const char* row = vbase + offs[32 + 16 * (x / 4) + 4 * j + x % 4];
-#pragma unroll
-      for (int p = 0; p < S::kValSteps; ++p) {
-        const uint32_t e0 = (p * 16 + r) * S::kValChunk;
-        vr[x][p] = __builtin_nontemporal_load((const VR*)(row + (e0 < (uint32_t)a.dv ? e0 : 0) * S::kElem));
-      }
-    }
-  };
-
-  F4 o[HT][S::kValSteps][S::kValChunk] = {};
-  float base[HT], l[HT];  // scores are taken off `base`, at most 8 below the running maximum
-#pragma unroll
-  for (int ht = 0; ht < HT; ++ht) base[ht] = -__FLT_MAX__, l[ht] = 0;
-  constexpr uint32_t kAll = S::kTokens == 32 ? 0xffffffffu : 0xffffu;
-
-  constexpr uint32_t kStep = 4 * S::kTokens;
-  uint32_t t0 = lo + w * S::kTokens;
-  if (t0 < hi) {
-    float sc = 0;
-    uint32_t seen = place(t0, page_of(t0), &sc);
-    int32_t page = page_of(t0 + kStep);
-    load_keys();
-    load_values();
-    // The last round's loads are of the cache's first row, so that they need no branch either.
-    do {
-      // scores
-      if (ragged)
-#pragma unroll
-        for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-          for (int kk = 0; kk < S::kKeySteps; ++kk) {
-            const uint32_t e0 = (kk * 4 + j) * S::kKeyChunk;
-            if (S::kKeyParts == 2 && e0 + 8 == (uint32_t)a.dk) kr[t][kk] = KR{kr[t][kk][2], kr[t][kk][3], 0, 0};
-            if (e0 >= (uint32_t)a.dk) kr[t][kk] = KR{};
-          }
-      F4 s[HT][S::kTiles];
-#pragma unroll
-      for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-        for (int ht = 0; ht < HT; ++ht) {
-          s[ht][t] = F4{};
-#pragma unroll
-          for (int kk = 0; kk < S::kKeySteps; ++kk) {
-            if constexpr (kQuant) {
-              s[ht][t] = mfma(decode<DT, CT>(KHalf{kr[t][kk][0], kr[t][kk][1]}), q[ht][2 * kk], s[ht][t]);
-              s[ht][t] = mfma(decode<DT, CT>(KHalf{kr[t][kk][2], kr[t][kk][3]}), q[ht][2 * kk + 1], s[ht][t]);
-            } else {
-              s[ht][t] = mfma(__builtin_bit_cast(M, kr[t][kk]), q[ht][kk], s[ht][t]);
-            }
-          }
-        }
-      F4 ksc[S::kTiles], vsc[S::kTiles];
-      if constexpr (kQuant) {
-        wave_fence();
-        scales[lane] = (seen >> li) & 1 ? sc : 0.f;
-        wave_fence();
-#pragma unroll
-        for (int t = 0; t < S::kTiles; ++t) {
-          ksc[t] = *(const F4*)&scales[16 * t + 4 * j] * a.scale2;
-          vsc[t] = *(const F4*)&scales[32 + 16 * t + 4 * j];
-        }
-      }
-      const uint32_t seen_next = place(t0 + kStep, page, &sc);
-      page = page_of(t0 + 2 * kStep);
-      load_keys();
-      // weights
-      // Of 16-bit products' weights two parts are taken, the value and what its rounding left: a bf16 alone
-      // would add as much error to the output as its own rounding does, and cost an fp16 model with an 8-bit
-      // cache its last three bits.
-      using P = std::conditional_t<kQuant, B8, M>;
-      using PE = std::conditional_t<kQuant, __bf16, T>;
-      P phi[HT], plo[HT];
+    // queries: lane r's head, dimensions chunk kk * 4 + j
+    const uint32_t rq = here(r), jq = here(j);
+    M q[HT][S::kKeySteps * S::kKeyParts];
+    auto dim_at = [&](int kk) -> uint32_t {
+      return ((kk / S::kKeyParts * 4 + jq) * S::kKeyParts + kk % S::kKeyParts) * S::kPart;
+    };
+    const T* qb = (const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group) * a.qh;
+    auto load_queries = [&](auto wide) {
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
-        float top = -__builtin_inff();
+        const uint32_t h = in_group + 16 * ht + rq;
+        const T* x = qb + (int64_t)(h < a.group ? h : 0) * a.qh;
 #pragma unroll
-        for (int t = 0; t < S::kTiles; ++t) {
-          if constexpr (kQuant)
-            s[ht][t] *= ksc[t];
-          else
-            s[ht][t] *= a.scale2;
-          if (seen != kAll)
+        for (int kk = 0; kk < S::kKeySteps * S::kKeyParts; ++kk) {
+          const uint32_t e0 = dim_at(kk) < (uint32_t)a.dk ? dim_at(kk) : 0;
+          if constexpr (decltype(wide)::value) {
+            q[ht][kk] = *(const M*)(x + e0);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              s[ht][t][i] = (seen >> (16 * t + 4 * j + i)) & 1 ? s[ht][t][i] : -__builtin_inff();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, s[ht][t][i]);
+            for (int e = 0; e < S::kPart; ++e) q[ht][kk][e] = x[(int64_t)(e0 + e) * a.qd];
+          }
         }
-        if (__any(top > base[ht] + 8.f)) {
-          top = fmaxf(base[ht], across_groups_max(top));
-          const float keep = __builtin_amdgcn_exp2f(base[ht] - top);
-          base[ht] = top;
-          l[ht] *= keep;
+      }
+    };
+    if (a.q_wide)
+      load_queries(std::true_type{});
+    else
+      load_queries(std::false_type{});
 #pragma unroll
-          for (int p = 0; p < S::kValSteps; ++p)
+    for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-            for (int m = 0; m < S::kValChunk; ++m) o[ht][p][m] *= keep;
+      for (int kk = 0; kk < S::kKeySteps * S::kKeyParts; ++kk)
+        if (in_group + 16 * ht + rq >= a.group || dim_at(kk) >= (uint32_t)a.dk) q[ht][kk] = M{};
+
+    // Page lookup: lanes 0 .. and 32 .. find the pages of a step's tokens, the first for keys, the second
+    // for values.  All loads of the loop below are unconditional, so that each wait is for the loads it
+    // needs and no younger ones: what is not there is read from a place that is, and left out after.
+    const uint32_t li = lane & (S::kTokens - 1);
+    const bool for_v = lane >= 32;
+    const int32_t* table = a.table + (int64_t)b * a.table_stride;
+    const uint32_t one = a.fd_page.m ? 0 : ~0u;  // pages of one slot: the quotient is the dividend
+    auto page_index = [&](uint32_t t) -> uint32_t { return (__umulhi(t, a.fd_page.m) >> a.fd_page.s) + (t & one); };
+    auto page_of = [&](uint32_t t0) -> int32_t {
+      const uint32_t t = t0 + li;
+      return table[page_index(t < hi ? t : hi - 1)];
+    };
+    const int64_t page_step = (for_v ? a.vp : a.kp) * S::kElem, slot_step = (for_v ? a.vsl : a.ksl) * S::kElem;
+    const float* scale_base = nullptr;
+    if constexpr (kQuant) scale_base = (for_v ? a.vs : a.ks) + (int64_t)g * a.sh;
+    const char* kbase = (const char*)a.k + (int64_t)g * a.kh * S::kElem;
+    const char* vbase = (const char*)a.v + (int64_t)g * a.vh * S::kElem;
+
+    // The step's row offsets to shared memory (0, the cache's first row, for a token that is not seen);
+    // returns the mask of its seen tokens.
+    auto place = [&](uint32_t t0, int32_t page, float* scale) -> uint32_t {
+      const uint32_t t = t0 + li;
+      const bool ok = (t >= sp.first) & (t < hi) & ((uint32_t)page < a.pages);
+      const uint32_t in = ok ? t - page_index(t) * a.page_size : 0, pg = ok ? page : 0;
+      wave_fence();
+      offs[lane] = (int64_t)(pg * (uint64_t)page_step + in * (uint64_t)slot_step);
+      wave_fence();
+      if constexpr (kQuant)
+        *scale = __builtin_nontemporal_load(scale_base + (pg * (uint64_t)a.sp + in * (uint64_t)a.ssl));
+      return (uint32_t)__ballot(ok);
+    };
+
+    KR kr[S::kTiles][S::kKeySteps];
+    VR vr[S::kVals][S::kValSteps];
+    // Where a lane's chunk kk of a row is read: past the row's end the first one's place, and half past it (8
+    // elements of 16 are left) 8 before, whose upper half they are.
+    auto key_at = [&](int kk) -> uint32_t {
+      const uint32_t e0 = (kk * 4 + j) * S::kKeyChunk;
+      return e0 >= (uint32_t)a.dk ? 0 : e0 + S::kKeyChunk > (uint32_t)a.dk ? e0 - 8 : e0;
+    };
+    const bool ragged = a.dk != DC;
+    auto load_keys = [&]() {
+#pragma unroll
+      for (int t = 0; t < S::kTiles; ++t) {
+        const char* row = kbase + offs[16 * t + r];
+#pragma unroll
+        for (int kk = 0; kk < S::kKeySteps; ++kk) {
+          kr[t][kk] = __builtin_nontemporal_load((const KR*)(row + key_at(kk) * S::kElem));
         }
+      }
+    };
+    auto load_values = [&]() {
+#pragma unroll
+      for (int x = 0; x < S::kVals; ++x) {
+        const char* row = vbase + offs[32 + 16 * (x / 4) + 4 * j + x % 4];
+#pragma unroll
+        for (int p = 0; p < S::kValSteps; ++p) {
+          const uint32_t e0 = (p * 16 + r) * S::kValChunk;
+          vr[x][p] = __builtin_nontemporal_load((const VR*)(row + (e0 < (uint32_t)a.dv ? e0 : 0) * S::kElem));
+        }
+      }
+    };
+
+    F4 o[HT][S::kValSteps][S::kValChunk] = {};
+    float base[HT], l[HT];  // scores are taken off `base`, at most 8 below the running maximum
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) base[ht] = -__FLT_MAX__, l[ht] = 0;
+    constexpr uint32_t kAll = 0xffffffffu;  // of 16 tokens the mask has every bit twice
+
+    constexpr uint32_t kStep = 4 * S::kTokens;
+    uint32_t t0 = lo + w * S::kTokens;
+    if (t0 < hi) {
+      float sc = 0;
+      uint32_t seen = place(t0, page_of(t0), &sc);
+      int32_t page = page_of(t0 + kStep);
+      load_keys();
+      load_values();
+      // The last round's loads are of the cache's first row, so that they need no branch either.
+      do {
+        // scores
+        if (ragged)
+#pragma unroll
+          for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+            for (int kk = 0; kk < S::kKeySteps; ++kk) {
+              const uint32_t e0 = (kk * 4 + j) * S::kKeyChunk;
+              if (kQuant && e0 + 8 == (uint32_t)a.dk) kr[t][kk] = KR{kr[t][kk][2], kr[t][kk][3], 0, 0};
+              if (e0 >= (uint32_t)a.dk) kr[t][kk] = KR{};
+            }
+        F4 s[HT][S::kTiles];
 #pragma unroll
         for (int t = 0; t < S::kTiles; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = __builtin_amdgcn_exp2f(s[ht][t][i] - base[ht]);
-            l[ht] += x;
-            if constexpr (kQuant) x *= vsc[t][i];
-            phi[ht][4 * t + i] = (PE)x;
-            if constexpr (!S::kF32) plo[ht][4 * t + i] = (PE)(x - (float)phi[ht][4 * t + i]);
+          for (int ht = 0; ht < HT; ++ht) {
+            s[ht][t] = F4{};
+#pragma unroll
+            for (int kk = 0; kk < S::kKeySteps; ++kk) {
+              if constexpr (kQuant && S::kF32) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) s[ht][t] = mfma(decode4<CT>(kr[t][kk][d]), q[ht][4 * kk + d], s[ht][t]);
+              } else if constexpr (kQuant) {
+                s[ht][t] = mfma(decode<DT, CT>(KHalf{kr[t][kk][0], kr[t][kk][1]}), q[ht][2 * kk], s[ht][t]);
+                s[ht][t] = mfma(decode<DT, CT>(KHalf{kr[t][kk][2], kr[t][kk][3]}), q[ht][2 * kk + 1], s[ht][t]);
+              } else {
+                s[ht][t] = mfma(__builtin_bit_cast(M, kr[t][kk]), q[ht][kk], s[ht][t]);
+              }
+            }
           }
-      }
-      if (seen != kAll)  // what is not seen may hold NaN
+        F4 ksc[S::kTiles], vsc[S::kTiles];
+        if constexpr (kQuant) {
+          wave_fence();
+          scales[lane] = (seen >> li) & 1 ? sc : 0.f;
+          wave_fence();
 #pragma unroll
-        for (int x = 0; x < S::kVals; ++x)
-          if (!((seen >> (16 * (x / 4) + 4 * j + x % 4)) & 1))
+          for (int t = 0; t < S::kTiles; ++t) {
+            ksc[t] = *(const F4*)&scales[16 * t + 4 * j] * a.scale2;
+            vsc[t] = *(const F4*)&scales[32 + 16 * t + 4 * j];
+          }
+        }
+        const uint32_t seen_next = place(t0 + kStep, page, &sc);
+        page = page_of(t0 + 2 * kStep);
+        load_keys();
+        // weights
+        // Of 16-bit products' weights two parts are taken, the value and what its rounding left: a bf16 alone
+        // would add as much error to the output as its own rounding does, and cost an fp16 model with an 8-bit
+        // cache its last three bits.
+        using P = std::conditional_t<kQuant && !S::kF32, B8, M>;
+        using PE = std::conditional_t<kQuant && !S::kF32, __bf16, T>;
+        P phi[HT], plo[HT];
 #pragma unroll
-            for (int p = 0; p < S::kValSteps; ++p) vr[x][p] = VR{};
-      // values
+        for (int ht = 0; ht < HT; ++ht) {
+          float top = -__builtin_inff();
 #pragma unroll
-      for (int p = 0; p < S::kValSteps; ++p) {
-        if constexpr (S::kF32) {
+          for (int t = 0; t < S::kTiles; ++t) {
+            if constexpr (kQuant)
+              s[ht][t] *= ksc[t];
+            else
+              s[ht][t] *= a.scale2;
+            if (seen != kAll)
 #pragma unroll
-          for (int m = 0; m < S::kValChunk; ++m)
+              for (int i = 0; i < 4; ++i)
+                s[ht][t][i] = (seen >> (16 * t + 4 * j + i)) & 1 ? s[ht][t][i] : -__builtin_inff();
 #pragma unroll
-            for (int ht = 0; ht < HT; ++ht)
-              o[ht][p][m] = mfma(F4{__uint_as_float(vr[0][p][m]), __uint_as_float(vr[1][p][m]),
-                                    __uint_as_float(vr[2][p][m]), __uint_as_float(vr[3][p][m])}, phi[ht], o[ht][p][m]);
-        } else if constexpr (kQuant) {
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[ht][t][i]);
+          }
+          if (__any(top > base[ht] + 8.f)) {
+            top = fmaxf(base[ht], across_groups_max(top));
+            const float keep = __builtin_amdgcn_exp2f(base[ht] - top);
+            base[ht] = top;
+            l[ht] *= keep;
 #pragma unroll
-          for (int d = 0; d < S::kValChunk / 4; ++d) {
-            auto word = [&](int x) { if constexpr (S::kValChunk == 4) return vr[x][p]; else return vr[x][p][d]; };
+            for (int p = 0; p < S::kValSteps; ++p)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // columns 4 d + 2 half and the next
+              for (int m = 0; m < S::kValChunk; ++m) o[ht][p][m] *= keep;
+          }
+#pragma unroll
+          for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float x = __builtin_amdgcn_exp2f(s[ht][t][i] - base[ht]);
+              l[ht] += x;
+              if constexpr (kQuant) x *= vsc[t][i];
+              phi[ht][4 * t + i] = (PE)x;
+              if constexpr (!S::kF32) plo[ht][4 * t + i] = (PE)(x - (float)phi[ht][4 * t + i]);
+            }
+        }
+        if (seen != kAll)  // what is not seen may hold NaN
+#pragma unroll
+          for (int x = 0; x < S::kVals; ++x)
+            if (!((seen >> (16 * (x / 4) + 4 * j + x % 4)) & 1))
+#pragma unroll
+              for (int p = 0; p < S::kValSteps; ++p) vr[x][p] = VR{};
+        // values
+#pragma unroll
+        for (int p = 0; p < S::kValSteps; ++p) {
+          if constexpr (S::kF32) {
+            F4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if constexpr (kQuant)
+                v[x] = decode4<CT>(vr[x][p]);
+              else
+                v[x] = __builtin_bit_cast(F4, vr[x][p]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht)
+                o[ht][p][m] = mfma(F4{v[0][m], v[1][m], v[2][m], v[3][m]}, phi[ht], o[ht][p][m]);
+          } else if constexpr (kQuant) {
+#pragma unroll
+            for (int d = 0; d < S::kValChunk / 4; ++d) {
+              auto word = [&](int x) { if constexpr (S::kValChunk == 4) return vr[x][p]; else return vr[x][p][d]; };
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {  // columns 4 d + 2 half and the next
+                U4 v0, v1;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const uint32_t y = __builtin_amdgcn_perm(word(2 * x + 1), word(2 * x), half ? 0x07030602 : 0x05010400);
+                  v0[x] = decode_pair<CT, false>(y);
+                  v1[x] = decode_pair<CT, true>(y);
+                }
+#pragma unroll
+                for (int ht = 0; ht < HT; ++ht) {
+                  F4& oa = o[ht][p][4 * d + 2 * half];
+                  F4& ob = o[ht][p][4 * d + 2 * half + 1];
+                  oa = mfma(__builtin_bit_cast(B8, v0), phi[ht], oa);
+                  ob = mfma(__builtin_bit_cast(B8, v1), phi[ht], ob);
+                  oa = mfma(__builtin_bit_cast(B8, v0), plo[ht], oa);
+                  ob = mfma(__builtin_bit_cast(B8, v1), plo[ht], ob);
+                }
+              }
+            }
+          } else {
+#pragma unroll
+            for (int d = 0; d < S::kValChunk / 2; ++d) {  // columns 2 d and the next
               U4 v0, v1;
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                const uint32_t y = __builtin_amdgcn_perm(word(2 * x + 1), word(2 * x), half ? 0x07030602 : 0x05010400);
-                v0[x] = decode_pair<CT, false>(y);
-                v1[x] = decode_pair<CT, true>(y);
+                v0[x] = __builtin_amdgcn_perm(vr[2 * x + 1][p][d], vr[2 * x][p][d], 0x05040100);
+                v1[x] = __builtin_amdgcn_perm(vr[2 * x + 1][p][d], vr[2 * x][p][d], 0x07060302);
               }
 #pragma unroll
               for (int ht = 0; ht < HT; ++ht) {
-                F4& oa = o[ht][p][4 * d + 2 * half];
-                F4& ob = o[ht][p][4 * d + 2 * half + 1];
-                oa = mfma(__builtin_bit_cast(B8, v0), phi[ht], oa);
-                ob = mfma(__builtin_bit_cast(B8, v1), phi[ht], ob);
-                oa = mfma(__builtin_bit_cast(B8, v0), plo[ht], oa);
-                ob = mfma(__builtin_bit_cast(B8, v1), plo[ht], ob);
+                F4& oa = o[ht][p][2 * d];
+                F4& ob = o[ht][p][2 * d + 1];
+                oa = mfma(__builtin_bit_cast(M, v0), phi[ht], oa);
+                ob = mfma(__builtin_bit_cast(M, v1), phi[ht], ob);
+                oa = mfma(__builtin_bit_cast(M, v0), plo[ht], oa);
+                ob = mfma(__builtin_bit_cast(M, v1), plo[ht], ob);
               }
             }
           }
-        } else {
+        }
+        load_values();
+        seen = seen_next;
+        t0 += kStep;
+      } while (t0 < hi);
+    }
+
+    // join the waves: maxima and sums, then 16 heads x 16 chunks of columns at a time
+    const uint32_t re = here(r), je = here(j), lane256 = here(threadIdx.x);
+    if (again) __syncthreads();
 #pragma unroll
-          for (int d = 0; d < S::kValChunk / 2; ++d) {  // columns 2 d and the next
-            U4 v0, v1;
+    for (int ht = 0; ht < HT; ++ht) {
+      const float sum = across_groups_sum(l[ht]);
+      if (je == 0) {
+        ms[w][16 * ht + re] = base[ht] == -__FLT_MAX__ ? -__builtin_inff() : base[ht];
+        ls[w][16 * ht + re] = sum;
+      }
+    }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              v0[x] = __builtin_amdgcn_perm(vr[2 * x + 1][p][d], vr[2 * x][p][d], 0x05040100);
-              v1[x] = __builtin_amdgcn_perm(vr[2 * x + 1][p][d], vr[2 * x][p][d], 0x07060302);
-            }
+    for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-            for (int ht = 0; ht < HT; ++ht) {
-              F4& oa = o[ht][p][2 * d];
-              F4& ob = o[ht][p][2 * d + 1];
-              oa = mfma(__builtin_bit_cast(M, v0), phi[ht], oa);
-              ob = mfma(__builtin_bit_cast(M, v1), phi[ht], ob);
-              oa = mfma(__builtin_bit_cast(M, v0), plo[ht], oa);
-              ob = mfma(__builtin_bit_cast(M, v1), plo[ht], ob);
-            }
+      for (int p = 0; p < S::kValSteps; ++p) {
+        if (ht || p) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int m = 0; m < S::kValChunk; m += 4)
+            *(F4*)&os[w][re * kRow + (4 * je + i) * S::kValChunk + m] =
+                F4{o[ht][p][m][i], o[ht][p][m + 1][i], o[ht][p][m + 2][i], o[ht][p][m + 3][i]};
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < S::kValChunk / 4; ++x) {
+          const uint32_t at = lane256 + 256 * x, hd = at / (4 * S::kValChunk), c4 = at % (4 * S::kValChunk) * 4;
+          const uint32_t h = in_group + 16 * ht + hd, e = p * 16 * S::kValChunk + c4;
+          if (h >= a.group || e >= (uint32_t)a.dv) continue;
+          float m4[4], top = -__builtin_inff(), total = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, m4[i] = ms[i][16 * ht + hd]);
+          F4 acc = {};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float wt = weight_of(m4[i], top);
+            total += ls[i][16 * ht + hd] * wt;
+            acc += *(const F4*)&os[i][hd * kRow + c4] * wt;
+          }
+          const uint32_t bh = b * a.heads + g * a.group + h;
+          if (run.whole) {
+            T* out = (T*)a.out + (int64_t)b * a.ob + (int64_t)(g * a.group + h) * a.oh;
+            const float inv = total > 0 ? 1.f / total : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[(int64_t)(e + i) * a.od] = (T)(total != total ? total : acc[i] * inv);
+          } else {
+            *(F4*)&a.part_o[((uint64_t)bh * a.splits + split) * a.dv + e] = acc;
+          }
+          if (e == 0) {
+            if (a.splits > 1) leave_part(a, run, bh, top, total);
+            if (run.whole && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
           }
         }
       }
-      load_values();
-      seen = seen_next;
-      t0 += kStep;
-    } while (t0 < hi);
-  }
-
-  // join the waves: maxima and sums, then 16 heads x 16 chunks of columns at a time
-  const uint32_t re = here(r), je = here(j), lane256 = here(threadIdx.x);
-  if (again) __syncthreads();
-#pragma unroll
-  for (int ht = 0; ht < HT; ++ht) {
-    const float sum = across_groups_sum(l[ht]);
-    if (je == 0) {
-      ms[w][16 * ht + re] = base[ht] == -__FLT_MAX__ ? -__builtin_inff() : base[ht];
-      ls[w][16 * ht + re] = sum;
-    }
-  }
-#pragma unroll
-  for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-    for (int p = 0; p < S::kValSteps; ++p) {
-      if (ht || p) __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int m = 0; m < S::kValChunk; m += 4)
-          *(F4*)&os[w][re * kRow + (4 * je + i) * S::kValChunk + m] =
-              F4{o[ht][p][m][i], o[ht][p][m + 1][i], o[ht][p][m + 2][i], o[ht][p][m + 3][i]};
-      __syncthreads();
-#pragma unroll
-      for (int x = 0; x < S::kValChunk / 4; ++x) {
-        const uint32_t at = lane256 + 256 * x, hd = at / (4 * S::kValChunk), c4 = at % (4 * S::kValChunk) * 4;
-        const uint32_t h = in_group + 16 * ht + hd, e = p * 16 * S::kValChunk + c4;
-        if (h >= a.group || e >= (uint32_t)a.dv) continue;
-        float m4[4], top = -__builtin_inff(), total = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, m4[i] = ms[i][16 * ht + hd]);
-        F4 acc = {};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float wt = weight_of(m4[i], top);
-          total += ls[i][16 * ht + hd] * wt;
-          acc += *(const F4*)&os[i][hd * kRow + c4] * wt;
-        }
-        const uint32_t bh = b * a.heads + g * a.group + h;
-        if (run.whole) {
-          T* out = (T*)a.out + (int64_t)b * a.ob + (int64_t)(g * a.group + h) * a.oh;
-          const float inv = total > 0 ? 1.f / total : 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) out[(int64_t)(e + i) * a.od] = (T)(total != total ? total : acc[i] * inv);
-        } else {
-          *(F4*)&a.part_o[((uint64_t)bh * a.splits + split) * a.dv + e] = acc;
-        }
-        if (e == 0) {
-          if (a.splits > 1) leave_part(a, run, bh, top, total);
-          if (run.whole && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
-        }
-      }
-    }
-  if (!run_next(a, &run)) break;
+    if (!run_next(a, &run)) break;
   }
 }
 
@@ -828,10 +861,9 @@ static int plan_attention(const lr_layout* Lq, const lr_cache* c, const lr_layou
   a->ks = c->k_scale;
   a->vs = c->v_scale;
   // The matrix kernel wants rows of whole chunks: a multiple of 8 elements (4 in fp32), contiguous and
-  // that much aligned.  Rows of an 8-bit cache under an fp32 model have no matrix form.
+  // that much aligned, and keys of at least one chunk of 16 codes.
   const int64_t v = c->dtype == LR_F32 ? 4 : 8;
-  const bool matrix = !(dtype == LR_F32 && is_quantised(c->dtype)) &&
-                      kd.size >= 16 && kd.size % v == 0 && vd.size % v == 0 &&
+  const bool matrix = (kd.size >= 16 || !is_quantised(c->dtype)) && kd.size % v == 0 && vd.size % v == 0 &&
                       rows_aligned(c->k_layout, nullptr, dtype_bytes(c->dtype), v) &&
                       rows_aligned(c->v_layout, nullptr, dtype_bytes(c->dtype), v);
   out->path = matrix ? LR_ATTENTION_MATRIX : LR_ATTENTION_ELEMENT;
@@ -862,7 +894,7 @@ static int launch_attention(const AttentionArgs& a, hipStream_t st) {
   const dim3 grid(a.splits == 1 ? a.batch * a.units : a.grid);
   if (a.path == LR_ATTENTION_ELEMENT) {
     hipLaunchKernelGGL((k_attention_element<DT, CT>), grid, dim3(256), 0, st, a);
-  } else if constexpr (!(DT == LR_F32 && CT != LR_F32)) {
+  } else {
     if (a.wide == 64 && a.unit_heads == 16)
       hipLaunchKernelGGL((k_attention_matrix<DT, CT, 64, 1>), grid, dim3(256), 0, st, a);
     else if (a.wide == 64)
@@ -908,10 +940,12 @@ int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, c
   AttentionArgs a;
   lr_attention_plan p;
   if (int rc = plan_attention(Lq, c, Lo, max_pages, dtype, window, &a, &p)) return rc;
-  if (cosize_bound(Lq) > q_capacity || cosize_bound(Lo) > out_capacity || batch > mode_of(*Lq, 2).size) return LR_ERR_BOUNDS;
+  if (cosize_bound(Lq) > q_capacity || cosize_bound(Lo) > out_capacity || batch > mode_of(*Lq, 2).size)
+    return LR_ERR_BOUNDS;
   if (table_stride < 0) return LR_ERR_INVALID;
   const int64_t e = dtype_bytes(dtype), ce = dtype_bytes(c->dtype);
-  const int64_t lse_bytes = lse ? batch * a.heads * 4 : 0, table_bytes = batch ? ((batch - 1) * table_stride + max_pages) * 4 : 0;
+  const int64_t lse_bytes = lse ? batch * a.heads * 4 : 0;
+  const int64_t table_bytes = batch ? ((batch - 1) * table_stride + max_pages) * 4 : 0;
   struct { const void* p; int64_t n; } in[] = {{q, q_capacity * e}, {c->k, c->k_capacity * ce}, {c->v, c->v_capacity * ce},
       {c->k_scale, c->k_scale ? c->scale_capacity * 4 : 0}, {c->v_scale, c->v_scale ? c->scale_capacity * 4 : 0},
       {table, table_bytes}, {lens, batch * 4}};

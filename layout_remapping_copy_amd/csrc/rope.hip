@@ -123,6 +123,15 @@ static void launch_chunks(const RopeChunkArgs& a, double bytes, hipStream_t st) 
     hipLaunchKernelGGL((k_rope_chunks<DT, V, false>), grid, dim3(256), 0, st, a);
 }
 
+template <int DT>
+static void launch_chunks_of(const RopeChunkArgs& a, int64_t v, double bytes, hipStream_t st) {
+  if constexpr (DT != LR_F32) {
+    if (v == 8) return launch_chunks<DT, 8>(a, bytes, st);
+  }
+  if (v == 4) return launch_chunks<DT, 4>(a, bytes, st);
+  launch_chunks<DT, 2>(a, bytes, st);
+}
+
 static bool same_leaves(const Mode& a, const Mode& b) {
   if (a.n != b.n) return false;
   for (int i = 0; i < a.n; ++i)
@@ -239,11 +248,12 @@ int lr_rope(const void* x, const lr_layout* Lx, int64_t x_capacity, void* y, con
   const hipStream_t st = (hipStream_t)stream;
   // the widest chunks that halves, rest and rows are whole numbers of
   int64_t v = 16 / e;
-  while (v > 1 && (a.rot / 2 % v || (a.dim - a.rot) % v || !rows_aligned(*Lx, x, e, v) || !rows_aligned(*Ly, y, e, v))) v /= 2;
+  while (v > 1 && (a.rot / 2 % v || (a.dim - a.rot) % v || !rows_aligned(*Lx, x, e, v) || !rows_aligned(*Ly, y, e, v)))
+    v /= 2;
   const double bytes = 2.0 * (double)a.heads * (double)n * a.dim * (double)e;
   RopeChunkArgs k;
-  bool chunked = v > 1 && mode_pair(xh, &k.xh) && mode_pair(yh, &k.yh) && mode_pair(xt, &k.xt) && mode_pair(yt, &k.yt) &&
-                 mode_pair(p, &k.p);
+  bool chunked = v > 1 && mode_pair(xh, &k.xh) && mode_pair(yh, &k.yh) && mode_pair(xt, &k.xt) &&
+                 mode_pair(yt, &k.yt) && mode_pair(p, &k.p);
   if (chunked) {
     k.un = units_of(a.rot, a.dim, (int32_t)v);
     chunked = k.un.count <= 256;
@@ -265,11 +275,11 @@ int lr_rope(const void* x, const lr_layout* Lx, int64_t x_capacity, void* y, con
     k.sign = a.sign;
   }
   if (chunked && dtype == LR_F32) {
-    v == 4 ? launch_chunks<LR_F32, 4>(k, bytes, st) : launch_chunks<LR_F32, 2>(k, bytes, st);
+    launch_chunks_of<LR_F32>(k, v, bytes, st);
   } else if (chunked && dtype == LR_F16) {
-    v == 8 ? launch_chunks<LR_F16, 8>(k, bytes, st) : v == 4 ? launch_chunks<LR_F16, 4>(k, bytes, st) : launch_chunks<LR_F16, 2>(k, bytes, st);
+    launch_chunks_of<LR_F16>(k, v, bytes, st);
   } else if (chunked) {
-    v == 8 ? launch_chunks<LR_BF16, 8>(k, bytes, st) : v == 4 ? launch_chunks<LR_BF16, 4>(k, bytes, st) : launch_chunks<LR_BF16, 2>(k, bytes, st);
+    launch_chunks_of<LR_BF16>(k, v, bytes, st);
   } else {
     a.units = (uint32_t)(a.rot / 2 + (a.dim - a.rot + 1) / 2);
     const double lanes = (double)a.heads * (double)n * a.units;

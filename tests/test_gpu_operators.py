@@ -597,3 +597,137 @@ def test_side_stream_and_graph(dev):
         torch.cuda.synchronize()
         assert torch.equal(out, want[i]), i
         torch.randn(1 << 20, device=dev).sum().item()    # eager work between the replays
+
+
+# ------------------------------------------------------------------------------------ splits, chunks and codes
+ATTEND_RUNS = [  # type, kind, heads, kv, dk, dv, page, order, lens, window: many sequences, many parts, ragged chunks
+    ("bf16", "e4m3", 4, 2, 72, 72, 16, "heads", [40, 300, 5], 0),
+    ("fp16", "int8", 4, 1, 24, 40, 16, "tokens", [40, 300, 5], 0),
+    ("bf16", "int8", 2, 1, 16, 8, 16, "tokens", [700], 0),
+    ("bf16", "e4m3", 3, 1, 8, 8, 16, "tokens", [70], 0),
+    ("fp32", "e4m3", 34, 1, 72, 128, 16, "heads", [1300, 2], 0),
+    ("fp32", "int8", 8, 4, 256, 200, 8, "tokens", [700, 0, 31], 300),
+    ("fp32", "e4m3", 2, 1, 64, 64, 32, "tokens", [20000], 0),
+    ("bf16", "bf16", 2, 1, 32, 32, 64, "tokens", [40000], 0),                            # over 64 parts of one sequence
+    ("bf16", "bf16", 2, 1, 18, 32, 64, "tokens", [20000], 0),                            # the same, one key a lane
+    ("bf16", "bf16", 2, 1, 32, 32, 16, "heads", [(i * 389) % 1500 for i in range(70)], 0),  # over 64 sequences, some empty
+    ("fp16", "int8", 6, 2, 32, 64, 16, "heads", [(i * 977) % 900 for i in range(150)], 500),
+    ("fp32", "fp32", 3, 3, 20, 20, 16, "heads", [(i * 389) % 1500 for i in range(67)], 0),
+    ("fp32", "fp32", 3, 3, 18, 21, 16, "heads", [(i * 389) % 700 for i in range(67)], 0),
+    ("bf16", "bf16", 1, 1, 64, 64, 16, "tokens", [0, 0, 6000, 0, 1, 0], 0),
+    ("bf16", "e4m3", 40, 1, 128, 128, 16, "tokens", [3000, 10, 2000], 777),
+]
+
+
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,order,lens,window", ATTEND_RUNS)
+def test_attention_runs(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, window):
+    test_attention(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, window)
+
+
+def test_attention_uneven_batch_is_its_parts(dev):
+    """How a sequence is cut depends on the others in the batch: alone or among others it stays within the tolerance
+    of both, and the empty ones give zeros."""
+    lens = [0, 7000, 1, 129, 0, 128]
+    cache, table, slots, (kn, vn) = attention_case(dev, "bf16", "bf16", 8, 2, 128, 128, 16, "heads", lens)
+    q = rand((6, 8, 128), torch.bfloat16, 3)
+    want, wlse, tol = attention64(q, [kn[u] for u in slots], [vn[u] for u in slots], 128 ** -0.5, torch.bfloat16, "bf16")
+    for first in (0, 1, 3):
+        b = 6 - first
+        L = f"(128,8,{b}):(1,128,1024)"
+        out, lse = torch.full((b, 8, 128), -7.0, dtype=torch.bfloat16, device=dev), torch.full((b, 8), -7.0, device=dev)
+        lr.paged_attention(q[first:].contiguous().to(dev), L, cache, table[first:].contiguous().to(dev),
+                           torch.tensor(lens[first:], dtype=torch.int32, device=dev), out, L, lse=lse)
+        close(out, want[first:], tol[first:])
+        close(lse, wlse[first:], tol.lse[first:])
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_codes_at_ties(dev, dtype, kind):
+    """Quotients on a tie and next to one, on either side, in rows whose scale is exact and in rows whose scale is
+    rounded: simple parts of the row's largest value, and for fp32 their neighbours."""
+    t, n, d = T[dtype], 200, 128
+    g = torch.Generator().manual_seed(4)
+    top = torch.randint(1, 256, (n, 1), generator=g).float()                  # 8 bits: exact in every type
+    top[:40] = torch.tensor([7.0, 127.0, 112.0, 254.0] * 10)[:, None]         # scales without rounding
+    part = torch.randint(0, 257, (n, d), generator=g).float() / 256 if kind == "e4m3" else \
+        torch.randint(0, 255, (n, d), generator=g).float() / 254
+    x = (top * part * (torch.randint(0, 2, (n, d), generator=g) * 2 - 1)).to(t)
+    small = torch.randint(0, 2, (n, d), generator=g).bool() & (torch.arange(d) >= d // 2)
+    x = torch.where(small, x * 2.0 ** -7, x)                                  # e4m3's smallest codes
+    if dtype == "fp32":
+        step = torch.randint(-2, 3, (n, d), generator=g, dtype=torch.int32)
+        x = torch.where(x == 0, x, (x.view(torch.int32) + step).view(torch.float32))
+        x = torch.minimum(x, top).maximum(-top)
+    x[:, 0] = top[:, 0].to(t)
+    x = x.reshape(n, 1, d).contiguous()
+    cache, info = make_cache(dev, kind, "tokens", n, 1, 1, d, d)
+    L = f"({d},1,{n}):(1,{d},{d})"
+    slots = torch.arange(n)
+    lr.cache_write(cache, x.to(dev), L, x.to(dev), L, slots.to(dev))
+    codes, scale = quantised64(x, kind)
+    for which in "kv":
+        got, s = content(cache, info, d, which)
+        close(s, scale.to(F64), 0.0)
+        close(got, codes, 0.0, which)
+
+
+def test_large_calls_stream(dev):
+    """Calls past 256 MiB take streaming loads and stores: the same bits as in pieces that do not."""
+    n, h, d = 12000, 48, 128
+    g = torch.Generator(device=dev).manual_seed(1)
+    x = torch.randn((n, h, d), generator=g, device=dev).to(torch.bfloat16)
+    L = f"({d},{h},{n}):(1,{d},{h * d})"
+    pos = torch.arange(n, device=dev)
+    table = lr.rope_table(d, device=dev)
+    y = lr.rope(x, L, torch.empty_like(x), L, pos, table)
+    piece = 1000
+    Lp = f"({d},{h},{piece}):(1,{d},{h * d})"
+    for i in range(0, n, piece):
+        z = lr.rope(x[i:i + piece], Lp, torch.empty_like(x[:piece]), Lp, pos[i:i + piece].contiguous(), table)
+        assert torch.equal(z, y[i:i + piece]), i
+    del y
+    page = 16
+    lay = f"({d},{h},{page},{n // page}):(1,{d},{h * d},{page * h * d})"
+
+    def fresh():
+        k, v = (torch.zeros(n * h * d, dtype=torch.int8, device=dev) for _ in range(2))
+        ks, vs = (torch.zeros(n * h, device=dev) for _ in range(2))
+        return lr.PagedCache(k, lay, v, lay, ks, vs, f"({h},{page},{n // page}):(1,{h},{page * h})")
+    slots = torch.randperm(n, generator=g, device=dev)
+    whole, parts = fresh(), fresh()
+    lr.cache_write(whole, x, L, x, L, slots, table=table, positions=pos)
+    for i in range(0, n, piece):
+        lr.cache_write(parts, x[i:i + piece], Lp, x[i:i + piece], Lp, slots[i:i + piece].contiguous(), table=table,
+                       positions=pos[i:i + piece].contiguous())
+    assert torch.equal(whole.k, parts.k) and torch.equal(whole.v, parts.v)
+    assert torch.equal(whole.k_scale, parts.k_scale) and torch.equal(whole.v_scale, parts.v_scale)
+    a, b = lr.cache_read(whole, slots, torch.empty_like(x), L, torch.empty_like(x), L)
+    c, e = (torch.empty((piece, h, d), dtype=x.dtype, device=dev) for _ in range(2))
+    for i in range(0, n, piece):
+        lr.cache_read(parts, slots[i:i + piece].contiguous(), c, Lp, e, Lp)
+        assert torch.equal(a[i:i + piece], c) and torch.equal(b[i:i + piece], e), i
+
+
+def test_rope_modes_of_many_leaves(dev):
+    """Heads and tokens of three leaves each, which the chunked kernel does not take."""
+    x = rand((2, 3, 2, 2, 2, 3, 16), torch.bfloat16, 8)             # tokens c, b, a; heads c, b, a; elements
+    s = [1]
+    for extent in reversed(x.shape[1:]):
+        s.insert(0, s[0] * extent)
+    perm = (1, 0, 2, 4, 3, 5, 6)                                     # of y's storage: neighbours that do not merge
+    yshape = [x.shape[i] for i in perm]
+    ys = [1]
+    for extent in reversed(yshape[1:]):
+        ys.insert(0, ys[0] * extent)
+    at = {p: ys[i] for i, p in enumerate(perm)}
+    Lx = f"(16,(3,2,2),(2,3,2)):(1,({s[5]},{s[4]},{s[3]}),({s[2]},{s[1]},{s[0]}))"
+    Ly = f"(16,(3,2,2),(2,3,2)):(1,({at[5]},{at[4]},{at[3]}),({at[2]},{at[1]},{at[0]}))"
+    pos = torch.arange(12) * 77
+    table = lr.rope_table(16, device=dev)
+    y = torch.full((x.numel(),), -7.0, dtype=x.dtype, device=dev)
+    lr.rope(x.to(dev), Lx, y, Ly, pos.to(dev), table)
+    # token index: a fastest; head index: a fastest
+    want, size = rotate64(x.reshape(12, 12, 16), pos, table, "half")
+    got = y.cpu().view(yshape).permute([perm.index(i) for i in range(7)]).reshape(12, 12, 16)
+    close(got, want, rope_tolerance(want, size, torch.bfloat16))
