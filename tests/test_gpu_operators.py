@@ -731,3 +731,19 @@ def test_rope_modes_of_many_leaves(dev):
     want, size = rotate64(x.reshape(12, 12, 16), pos, table, "half")
     got = y.cpu().view(yshape).permute([perm.index(i) for i in range(7)]).reshape(12, 12, 16)
     close(got, want, rope_tolerance(want, size, torch.bfloat16))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(cache="bf16", heads=4, kv_heads=4, dim=64, window=33),
+                                dict(cache="int8", heads=20, kv_heads=1, dim=80, prompt=300)])
+def test_decode_example(dev, kw):
+    """The example's steps, each within its tolerance."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode.py")
+    spec = importlib.util.spec_from_file_location("decode_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    args = dict(batch=3, heads=8, kv_heads=2, dim=128, prompt=150, steps=5, check=True)
+    args.update(kw)
+    _, out, worst = example.run(**args)
+    assert out.isfinite().all() and worst <= 1
