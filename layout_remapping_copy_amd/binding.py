@@ -586,10 +586,16 @@ def copy_plan(Ls, src_capacity: int, Ld, dst_capacity: int, elem_bytes: int, fla
 # ---------------------------------------------------------------------------
 # Device entry points (torch tensors for memory and stream only)
 # ---------------------------------------------------------------------------
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(stream) -> int:
@@ -599,9 +605,9 @@ def _stream_ptr(stream) -> int:
         return int(stream.cuda_stream)
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
+    if raw is None or not torch.cuda.is_initialized():
         return int(torch.cuda.current_stream().cuda_stream)
-    return raw(torch.cuda.current_device())
+    return raw(torch._C._cuda_getDevice())
 
 
 def _device_tensor(t, what: str):
@@ -733,17 +739,18 @@ def _dtype_code(dtype) -> int:
     return _DTYPES[dtype]
 
 
-def _device_tensors(device, **tensors):
-    """Every tensor contiguous and on `device` (None: any one GPU)."""
-    for what, t in tensors.items():
-        if not t.is_cuda:
-            raise ValueError(f"{what} must be a GPU tensor")
-        if not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{what} is on {t.device}, not on {device}")
+def _device_tensors(index, names, *tensors):
+    """Every tensor contiguous and on GPU `index` (None: any one GPU); `names`: their names, space-separated."""
+    if index is None:
+        index = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != index or index < 0 or not t.is_contiguous():
+            what = names.split()[[u is t for u in tensors].index(True)]
+            if not t.is_cuda:
+                raise ValueError(f"{what} must be a GPU tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{what} must be contiguous")
+            raise ValueError(f"{what} is on {t.device}, not on cuda:{index}")
 
 
 class RopeTable:
@@ -782,7 +789,7 @@ def rope(x, Lx, y, Ly, positions, table: RopeTable, pairs: str = "half", backwar
     """lr_rope: y = the rotation of x, from layout Lx to layout Ly, both (head_dim, heads, tokens).
     ``positions``: int64, one per token, or one per offset of the layout ``Lp``; ``n``: the first n
     tokens only.  ``backward``: x is dL/dy and y becomes dL/dx.  Returns y."""
-    _device_tensors(None, x=x, y=y, positions=positions, table=table.turns)
+    _device_tensors(None, "x y positions table", x, y, positions, table.turns)
     if x.dtype != y.dtype:
         raise TypeError("x and y must have the same type")
     Lx, Ly = _as_layout(Lx), _as_layout(Ly)
@@ -801,14 +808,14 @@ class PagedCache:
     scales ``k_scale`` and ``v_scale`` of layout ``Ls`` (heads, slots of a page, pages).  Holds the
     tensors; checked once, here."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "c")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "c", "index")
 
     def __init__(self, k, Lk, v, Lv, k_scale=None, v_scale=None, Ls=None):
         torch = _torch()
-        _device_tensors(None, k=k)
-        _device_tensors(k.device, v=v)
+        _device_tensors(None, "k v", k, v)
         if k.dtype != v.dtype:
             raise TypeError("k and v must have the same type")
+        self.index = k.get_device()
         c = lr_cache()
         c.k, c.v, c.dtype = k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype)
         c.k_layout, c.v_layout = _as_layout(Lk).c, _as_layout(Lv).c
@@ -816,7 +823,7 @@ class PagedCache:
         if k_scale is not None or v_scale is not None:
             if k_scale is None or v_scale is None or Ls is None:
                 raise ValueError("k_scale, v_scale and Ls go together")
-            _device_tensors(k.device, k_scale=k_scale, v_scale=v_scale)
+            _device_tensors(self.index, "k_scale v_scale", k_scale, v_scale)
             if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
                 raise TypeError("scales must be float32")
             c.k_scale, c.v_scale, c.scale_layout = k_scale.data_ptr(), v_scale.data_ptr(), _as_layout(Ls).c
@@ -835,7 +842,7 @@ def cache_write(cache: PagedCache, k, Lk, v, Lv, slots, table: Optional[RopeTabl
     """lr_cache_write: the keys and values of len(slots) tokens, layouts (head_dim, heads, tokens), into
     the cache's int64 ``slots`` (one outside the cache writes nothing), quantised as its type asks.  With
     ``table`` and ``positions`` the keys are rotated first.  Returns the cache."""
-    _device_tensors(cache.k.device, k=k, v=v, slots=slots)
+    _device_tensors(cache.index, "k v slots", k, v, slots)
     if k.dtype != v.dtype:
         raise TypeError("k and v must have the same type")
     if slots.dtype != _torch().int64:
@@ -845,7 +852,7 @@ def cache_write(cache: PagedCache, k, Lk, v, Lv, slots, table: Optional[RopeTabl
     if table is not None:
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _device_tensors(cache.k.device, positions=positions, table=table.turns)
+        _device_tensors(cache.index, "positions table", positions, table.turns)
         if positions.numel() < n:
             raise ValueError("positions needs one entry per slot")
         r = _rotation(table, positions, pairs)
@@ -858,7 +865,7 @@ def cache_write(cache: PagedCache, k, Lk, v, Lv, slots, table: Optional[RopeTabl
 def cache_read(cache: PagedCache, slots, k, Lk, v, Lv, stream=None):
     """lr_cache_read: the cache's ``slots`` back into k and v, layouts (head_dim, heads, tokens); zeros
     for a slot outside the cache.  Returns (k, v)."""
-    _device_tensors(cache.k.device, k=k, v=v, slots=slots)
+    _device_tensors(cache.index, "k v slots", k, v, slots)
     if k.dtype != v.dtype:
         raise TypeError("k and v must have the same type")
     if slots.dtype != _torch().int64:
@@ -895,13 +902,13 @@ def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: 
     ``window``: the last tokens seen, 0 for all; ``lse``: float32 (sequences, heads) to fill;
     ``workspace``: a byte tensor of the plan's size, allocated on the stream if not given.  Returns out."""
     torch = _torch()
-    dev = cache.k.device
-    _device_tensors(dev, q=q, out=out, lens=lens)
+    dev = cache.index
+    _device_tensors(dev, "q out lens", q, out, lens)
     if q.dtype != out.dtype:
         raise TypeError("q and out must have the same type")
     if page_table.dtype != torch.int32 or lens.dtype != torch.int32:
         raise TypeError("page_table and lens must be int32")
-    if page_table.device != dev or page_table.dim() != 2 or page_table.stride(1) != 1:
+    if page_table.get_device() != dev or page_table.dim() != 2 or page_table.stride(1) != 1:
         raise ValueError("page_table must be a 2-D GPU tensor with contiguous rows")
     batch, max_pages = lens.numel(), page_table.shape[1]
     if page_table.shape[0] < batch:
@@ -910,7 +917,7 @@ def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: 
     code = _dtype_code(q.dtype)
     lse_ptr = None
     if lse is not None:
-        _device_tensors(dev, lse=lse)
+        _device_tensors(dev, "lse", lse)
         if lse.dtype != torch.float32:
             raise TypeError("lse must be float32")
         if lse.numel() < batch * _mode_size(Lq.c, 1):
@@ -920,9 +927,9 @@ def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: 
         need = paged_attention_plan(Lq, cache, Lo, max_pages, q.dtype, window)["workspace_bytes"]
         if need:  # from the stream the kernels run on, so that its reuse waits for them
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = torch.empty(need, dtype=torch.uint8, device=cache.k.device)
     elif workspace.numel():
-        _device_tensors(dev, workspace=workspace)
+        _device_tensors(dev, "workspace", workspace)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if scale is None:
         scale = _mode_size(Lq.c, 0) ** -0.5
