@@ -47,9 +47,9 @@ constexpr uint32_t kBlock = 128;
 struct Span {
   uint32_t base, first, n, blocks;
 };
-__device__ __forceinline__ Span span_of(const AttentionArgs& a, uint32_t b) {
+__device__ __forceinline__ Span span_of(const AttentionArgs& a, int32_t len) {
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
-  int64_t n = a.lens[b];
+  int64_t n = len;
   n = n < 0 ? 0 : n > cap ? cap : n;
   const int64_t first = a.window > 0 && n > a.window ? n - a.window : 0;
   const uint32_t base = (uint32_t)first & ~31u;
@@ -110,18 +110,19 @@ __device__ __forceinline__ bool run_begin(const AttentionArgs& a, Run* r) {
   if (a.splits == 1) {  // one unit a workgroup
     r->b = blockIdx.x / a.units;
     r->u = blockIdx.x % a.units;
-    r->sp = span_of(a, r->b);
+    r->sp = span_of(a, a.lens[r->b]);
     r->deal = Deal{1, 1};
     r->w = 0;
     r->at = r->start = 0;
     r->end = r->sp.blocks;
   } else {
-    uint32_t v = lane < a.batch ? span_of(a, lane).blocks : 0;
+    int32_t len = lane < a.batch ? a.lens[lane] : 0;
+    uint32_t v = lane < a.batch ? span_of(a, len).blocks : 0;
     uint32_t upto = wave_scan(v, lane);  // the first 64 sequences
     uint64_t all = __shfl(upto, 63);
     if (a.batch > 64) {
       uint64_t more = 0;
-      for (uint32_t i = 64 + lane; i < a.batch; i += 64) more += span_of(a, i).blocks;
+      for (uint32_t i = 64 + lane; i < a.batch; i += 64) more += span_of(a, a.lens[i]).blocks;
       for (int x = 32; x; x >>= 1) more += __shfl_xor((unsigned long long)more, x);
       all += more;
     }
@@ -140,13 +141,14 @@ __device__ __forceinline__ bool run_begin(const AttentionArgs& a, Run* r) {
         const int f = __ffsll((unsigned long long)hit) - 1;
         r->b = i + f;
         r->start = (past + uniform(__shfl(upto - v, f))) * a.units;
+        r->sp = span_of(a, (int32_t)uniform(__shfl(len, f)));
         break;
       }
       past += uniform(__shfl(upto, 63));
-      v = i + 64 + lane < a.batch ? span_of(a, i + 64 + lane).blocks : 0;
+      len = i + 64 + lane < a.batch ? a.lens[i + 64 + lane] : 0;
+      v = i + 64 + lane < a.batch ? span_of(a, len).blocks : 0;
       upto = wave_scan(v, lane);
     }
-    r->sp = span_of(a, r->b);
     r->u = (uint32_t)((r->at - r->start) / r->sp.blocks);
     r->start += (uint64_t)r->u * r->sp.blocks;
   }
@@ -159,7 +161,7 @@ __device__ __forceinline__ bool run_next(const AttentionArgs& a, Run* r) {
   if (r->at >= r->end) return false;
   if (++r->u == a.units) {
     r->u = 0;
-    r->sp = span_of(a, ++r->b);
+    r->sp = span_of(a, a.lens[++r->b]);
   }
   run_unit(a, r->w, r);
   return true;
