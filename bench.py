@@ -32,6 +32,9 @@ Other modes (for rocprofv3 runs and their summaries under profiles/):
   --atom-sweep          head splits for head dims of 32-512 bytes: tiles of
                         atoms against the source order, beside a plain copy
   --layout-sweep        common layout transforms against a same-size copy
+  --operators [NAMES]   the attention operators' listed cases (all, or some,
+                        comma-separated): cold, and calls back to back on
+                        rotating inputs, as a markdown table
 """
 
 from __future__ import annotations
@@ -667,6 +670,45 @@ def batched_sweep(lr, torch, mode: str = "paths", steps: int = 20):
         torch.cuda.empty_cache()
 
 
+def operators_run(torch, names=None, reps: int = 20):
+    """Markdown table of the listed cases of perf/operators.py through the package's entry points.  Cold: 512 MiB
+    are filled before each timed call, which leaves the 256 MB cache full of lines that have to be written back.
+    Back to back: 50 calls over two states, wall time with the device's work, the host's part of a call included."""
+    import statistics
+
+    import perf.operators as P
+
+    P.own = True
+    flush = torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    print("| case | cold median us | cold best us | back to back us | GB/s | of HBM peak |")
+    print("|---|---|---|---|---|---|")
+    for case in P.listed():
+        if names and case["name"] not in names:
+            continue
+        states = [P.prepare(case, seed) for seed in (1, 2)]
+        for i in range(6):
+            P.run(states[i % 2])
+        cold = []
+        for i in range(reps):
+            flush.zero_()
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            P.run(states[i % 2])
+            b.record()
+            torch.cuda.synchronize()
+            cold.append(a.elapsed_time(b) * 1e3)
+        t0 = time.perf_counter()
+        for i in range(50):
+            P.run(states[i % 2])
+        torch.cuda.synchronize()
+        us = (time.perf_counter() - t0) / 50 * 1e6
+        gbps = P.work(case)["bytes"] / us / 1e3
+        print(f"| {case['name']} | {statistics.median(cold):.1f} | {min(cold):.1f} | {us:.1f} | {gbps:.0f} | "
+              f"{gbps / HBM_PEAK_GBPS:.2f} |", flush=True)
+        del states
+        torch.cuda.empty_cache()
+
+
 def _csv_rows(directory: str, suffix: str):
     rows = []
     for path in sorted(glob.glob(os.path.join(directory, "**", f"*{suffix}"), recursive=True)):
@@ -813,6 +855,8 @@ def main():
                     help="register-loaded LDS transposes with one against two register blocks per lane")
     ap.add_argument("--back-to-back", type=int, default=0, metavar="K",
                     help="with --launch: also time K back-to-back launches per spec")
+    ap.add_argument("--operators", nargs="?", const="", metavar="NAMES",
+                    help="the attention operators' listed cases, all or the comma-separated ones")
     args = ap.parse_args()
 
     if args.summarize_counters:
@@ -838,6 +882,9 @@ def main():
     dev = torch.device("cuda:0")
     if args.counters:
         counters_run(lr, torch, W)
+        return
+    if args.operators is not None:
+        operators_run(torch, args.operators.split(",") if args.operators else None)
         return
     if args.launch:
         launch_run(lr, torch, W, args.launch, back_to_back=args.back_to_back)

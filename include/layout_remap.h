@@ -620,14 +620,15 @@ int lr_cache_read(const lr_cache* c, const int64_t* slots, int64_t n, void* k, c
 /* How lr_paged_attention runs (host only). */
 typedef enum {
   LR_ATTENTION_ELEMENT = 0, /* any types, strides and alignment: one key per lane */
-  LR_ATTENTION_MATRIX = 1   /* matrix instructions over 16-byte aligned rows */
+  LR_ATTENTION_MATRIX = 1   /* matrix instructions: rows of keys and values contiguous, a multiple of 8 elements
+                               (4 in LR_F32) long and that much aligned; keys of an 8-bit cache at least 16 long */
 } lr_attention_path;
 
 typedef struct {
   int32_t path;            /* lr_attention_path, for 16-byte aligned buffers */
   int32_t head_tiles;      /* workgroups that share the keys of one cache head */
-  int64_t chunk;           /* tokens of one workgroup */
-  int64_t splits;          /* chunks of the longest sequence */
+  int64_t chunk;           /* tokens of the longest sequence over splits, rounded up */
+  int64_t splits;          /* the most parts a sequence is cut into; 1: one launch, nothing to join */
   int64_t workspace_bytes; /* device memory lr_paged_attention needs; 0 when splits is 1 */
 } lr_attention_plan;
 
@@ -641,9 +642,10 @@ typedef struct {
  * cache's; q's head_dim is the keys', out's the values', each at most 256.  dtype (of q and out): LR_F32,
  * LR_F16 or LR_BF16; the cache has the same type, or LR_E4M3 or LR_INT8.  lse (NULL: not wanted): device
  * float[batch][heads], log sum_t exp(scale * q . k), -inf with no token.
- * A sequence's tokens are split into chunks that are joined by a second launch; workspace: device memory
- * of at least the plan's workspace_bytes (LR_ERR_CAPACITY), 16-byte aligned, its contents don't matter.
- * The result does not depend on timing: every sum has a fixed order. */
+ * The tokens of all sequences are dealt out evenly to the workgroups; what that cuts is joined by a second
+ * launch.  workspace: device memory of at least the plan's workspace_bytes (LR_ERR_CAPACITY), 16-byte
+ * aligned, its contents don't matter.  The result does not depend on timing: every sum has an order that
+ * lens alone decides. */
 int lr_paged_attention_plan(const lr_layout* Lq, const lr_cache* c, const lr_layout* Lo, int64_t max_pages,
                             int32_t dtype, int64_t window, lr_attention_plan* out);
 int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, const lr_cache* c,
