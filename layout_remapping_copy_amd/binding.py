@@ -808,7 +808,7 @@ class PagedCache:
     scales ``k_scale`` and ``v_scale`` of layout ``Ls`` (heads, slots of a page, pages).  Holds the
     tensors; checked once, here."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "c", "index")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "c", "index", "dim")
 
     def __init__(self, k, Lk, v, Lv, k_scale=None, v_scale=None, Ls=None):
         torch = _torch()
@@ -830,6 +830,7 @@ class PagedCache:
             c.scale_capacity = min(k_scale.numel(), v_scale.numel())
         self.k, self.v, self.k_scale, self.v_scale, self.c = k, v, k_scale, v_scale, c
         cache_validate(self)
+        self.dim = _mode_size(c.k_layout, 0)
 
 
 def cache_validate(cache: PagedCache) -> None:
@@ -880,8 +881,9 @@ def _mode_size(c: lr_layout, mode: int) -> int:
     """Extent of a top-level mode (1 when the layout has fewer)."""
     n = 1
     if mode < c.nmodes:
-        for i in range(c.mode_end[mode - 1] if mode else 0, c.mode_end[mode]):
-            n *= c.shape[i]
+        ends, shape = c.mode_end, c.shape
+        for i in range(ends[mode - 1] if mode else 0, ends[mode]):
+            n *= shape[i]
     return n
 
 
@@ -902,7 +904,7 @@ def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: 
     ``window``: the last tokens seen, 0 for all; ``lse``: float32 (sequences, heads) to fill;
     ``workspace``: a byte tensor of the plan's size, allocated on the stream if not given.  Returns out."""
     torch = _torch()
-    dev = cache.index
+    dev, code = cache.index, _dtype_code(q.dtype)
     _device_tensors(dev, "q out lens", q, out, lens)
     if q.dtype != out.dtype:
         raise TypeError("q and out must have the same type")
@@ -914,7 +916,6 @@ def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: 
     if page_table.shape[0] < batch:
         raise ValueError("page_table needs a row per sequence")
     Lq, Lo = _as_layout(Lq), _as_layout(Lo)
-    code = _dtype_code(q.dtype)
     lse_ptr = None
     if lse is not None:
         _device_tensors(dev, "lse", lse)
@@ -932,7 +933,7 @@ def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: 
         _device_tensors(dev, "workspace", workspace)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if scale is None:
-        scale = _mode_size(Lq.c, 0) ** -0.5
+        scale = cache.dim ** -0.5
     _check(lib().lr_paged_attention(q.data_ptr(), Lq.c, q.numel(), cache.c, page_table.data_ptr(),
                                     page_table.stride(0), max_pages, lens.data_ptr(), batch, out.data_ptr(), Lo.c,
                                     out.numel(), lse_ptr, code, scale, window,
