@@ -747,3 +747,44 @@ def test_decode_example(dev, kw):
     args.update(kw)
     _, out, worst = example.run(**args)
     assert out.isfinite().all() and worst <= 1
+
+
+UNEVEN = [(i * 389) % 2000 for i in range(40)]
+ATTEND_WIDE = [  # enough work for four cache heads a workgroup, where a token's heads lie next to each other; and
+    # heads of 160 and 192, which have kernels of their own
+    ("bf16", "bf16", 16, 4, 128, 128, 16, "tokens", UNEVEN, 0),
+    ("fp16", "int8", 80, 4, 72, 72, 16, "tokens", UNEVEN, 0),
+    ("bf16", "e4m3", 8, 8, 80, 64, 32, "tokens", UNEVEN[:25], 700),
+    ("fp32", "fp32", 4, 4, 64, 96, 1, "tokens", UNEVEN, 0),
+    ("fp16", "fp16", 24, 12, 32, 32, 7, "tokens", UNEVEN[:20], 0),
+    ("fp32", "e4m3", 8, 4, 128, 128, 16, "tokens", UNEVEN, 0),
+    ("bf16", "bf16", 4, 4, 160, 192, 16, "tokens", UNEVEN, 0),
+    ("bf16", "bf16", 8, 4, 160, 160, 16, "heads", [700, 0, 31], 0),
+    ("fp16", "int8", 3, 3, 192, 160, 16, "tokens", [700, 0, 31], 0),
+    ("fp32", "fp32", 2, 2, 192, 136, 16, "heads", [300, 5], 0),
+    ("bf16", "e4m3", 4, 4, 256, 256, 16, "tokens", UNEVEN, 0),
+]
+
+
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,order,lens,window", ATTEND_WIDE)
+def test_attention_wide(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, window):
+    test_attention(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, window)
+
+
+def test_attention_wide_plan_off_alignment(dev):
+    """A plan for four heads a workgroup whose buffers turn out to be off 16 bytes: one key a lane instead, with the
+    same workspace."""
+    heads, kv, d, page, lens = 8, 4, 64, 16, UNEVEN
+    cache, table, slots, (kn, vn) = attention_case(dev, "bf16", "bf16", heads, kv, d, d, page, "tokens", lens)
+    pages = cache.k.numel() // (page * kv * d)
+    lay = f"({d},{kv},{page},{pages}):(1,{d},{kv * d},{page * kv * d})"
+    off = [torch.cat([t.new_zeros(1), t])[1:] for t in (cache.k, cache.v)]
+    assert off[0].data_ptr() % 16 == 2
+    moved = lr.PagedCache(off[0], lay, off[1], lay)
+    q = rand((len(lens), heads, d), torch.bfloat16, 3)
+    L = f"({d},{heads},{len(lens)}):(1,{d},{heads * d})"
+    out, lse = torch.empty((len(lens), heads, d), dtype=torch.bfloat16, device=dev), torch.empty((len(lens), heads), device=dev)
+    lr.paged_attention(q.to(dev), L, moved, table.to(dev), torch.tensor(lens, dtype=torch.int32, device=dev), out, L, lse=lse)
+    want, wlse, tol = attention64(q, [kn[u] for u in slots], [vn[u] for u in slots], d ** -0.5, torch.bfloat16, "bf16")
+    close(out, want, tol)
+    close(lse, wlse, tol.lse)
