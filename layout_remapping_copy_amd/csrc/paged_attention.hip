@@ -389,12 +389,12 @@ struct MatrixShape {
   static constexpr int kPart = kF32 ? 4 : 8;                   // inner elements a lane gives one product
   static constexpr int kKeyChunk = 16 / kElem;                 // key elements a lane loads at a time
   static constexpr int kKeyParts = kKeyChunk / kPart;
-  static constexpr int kKeySteps = DC / (4 * kKeyChunk);
-  static constexpr int kValChunk = kF32 || DC % 128 ? 4 : 8;   // value elements a lane loads at a time
-  static constexpr int kValSteps = DC / (16 * kValChunk);
+  static constexpr int kKeySteps = (DC + 4 * kKeyChunk - 1) / (4 * kKeyChunk);
+  static constexpr int kValChunk = kF32 || (DC % 128 && DC != 96) ? 4 : 8;   // value elements a lane loads at a time
+  static constexpr int kValSteps = (DC + 16 * kValChunk - 1) / (16 * kValChunk);
   static constexpr int kVals = 4 * kTiles;                     // value rows a lane loads in a step
   // waves of a SIMD, the most that needs no spills
-  static constexpr int kMinWaves = (DC >= 192 && kElem > 1) || (kF32 && DC * HT > 128) ? 1 : 2;
+  static constexpr int kMinWaves = (DC >= 160 && kElem > 1) || (kF32 && DC * HT > 128) ? 1 : 2;
 };
 
 // A workgroup has one chunk of one sequence and HT * 16 query heads that share a cache head; its four
@@ -920,7 +920,12 @@ static int plan_attention(const lr_layout* Lq, const lr_cache* c, const lr_layou
                       rows_aligned(c->v_layout, nullptr, dtype_bytes(c->dtype), v);
   out->path = matrix ? LR_ATTENTION_MATRIX : LR_ATTENTION_ELEMENT;
   const int64_t widest = std::max(kd.size, vd.size);
-  a->wide = widest <= 64 ? 64 : widest <= 128 ? 128 : widest <= 192 ? 192 : 256;
+  // Loads past a row's end are not free, though they ask for what another lane does: rows of 72 in the width of 128
+  // took 190 us where the width of 96 takes 155 (16 sequences of up to 30000 bf16 tokens, 8 heads), of 160 in 192
+  // 284 and 264.  Rows of codes, loaded 64 at a time, have no use for 96 and 160.
+  const bool codes = is_quantised(c->dtype);
+  a->wide = widest <= 64 ? 64 : widest <= 96 && !codes ? 96 : widest <= 128 ? 128 : widest <= 160 && !codes ? 160
+            : widest <= 192 ? 192 : 256;
   a->unit_heads = !matrix ? 1 : a->group > 16 && a->wide <= 128 ? 32 : 16;
   a->tiles = (a->group + a->unit_heads - 1) / a->unit_heads;
   // Four cache heads a workgroup, one a wave, where a token's heads lie next to each other: their rows then share
@@ -961,6 +966,17 @@ static void launch_matrix(const AttentionArgs& a, dim3 grid, hipStream_t st) {
     hipLaunchKernelGGL((k_attention_matrix<DT, CT, DC, HT, false>), grid, dim3(256), 0, st, a);
 }
 
+// Widths that caches of codes have no use for.
+template <int DT, int CT, int DC>
+static void launch_plain(const AttentionArgs& a, dim3 grid, hipStream_t st) {
+  if constexpr (DT == CT) {
+    if constexpr (DC <= 128) {
+      if (a.unit_heads == 32) return launch_matrix<DT, CT, DC, 2>(a, grid, st);
+    }
+    launch_matrix<DT, CT, DC, 1>(a, grid, st);
+  }
+}
+
 template <int DT, int CT>
 static int launch_attention(const AttentionArgs& a, hipStream_t st) {
   const dim3 grid(a.splits == 1 ? a.batch * a.units : a.grid);
@@ -969,6 +985,10 @@ static int launch_attention(const AttentionArgs& a, hipStream_t st) {
   } else {
     if (a.wide == 64)
       a.unit_heads == 16 ? launch_matrix<DT, CT, 64, 1>(a, grid, st) : launch_matrix<DT, CT, 64, 2>(a, grid, st);
+    else if (a.wide == 96)
+      launch_plain<DT, CT, 96>(a, grid, st);
+    else if (a.wide == 160)
+      launch_plain<DT, CT, 160>(a, grid, st);
     else if (a.wide == 128)
       a.unit_heads == 16 ? launch_matrix<DT, CT, 128, 1>(a, grid, st) : launch_matrix<DT, CT, 128, 2>(a, grid, st);
     else if (a.wide == 192)
