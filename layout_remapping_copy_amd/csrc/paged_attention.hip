@@ -922,10 +922,10 @@ static int plan_attention(const lr_layout* Lq, const lr_cache* c, const lr_layou
   const int64_t widest = std::max(kd.size, vd.size);
   // Loads past a row's end are not free, though they ask for what another lane does: rows of 72 in the width of 128
   // took 190 us where the width of 96 takes 155 (16 sequences of up to 30000 bf16 tokens, 8 heads), of 160 in 192
-  // 284 and 264.  Rows of codes, loaded 64 at a time, have no use for 96 and 160.
+  // 284 and 264, of 32 in 64 81 and 68.  Rows of codes, loaded 64 at a time, have no use for 32, 96 and 160.
   const bool codes = is_quantised(c->dtype);
-  a->wide = widest <= 64 ? 64 : widest <= 96 && !codes ? 96 : widest <= 128 ? 128 : widest <= 160 && !codes ? 160
-            : widest <= 192 ? 192 : 256;
+  a->wide = widest <= 32 && !codes ? 32 : widest <= 64 ? 64 : widest <= 96 && !codes ? 96 : widest <= 128 ? 128
+            : widest <= 160 && !codes ? 160 : widest <= 192 ? 192 : 256;
   a->unit_heads = !matrix ? 1 : a->group > 16 && a->wide <= 128 ? 32 : 16;
   a->tiles = (a->group + a->unit_heads - 1) / a->unit_heads;
   // Four cache heads a workgroup, one a wave, where a token's heads lie next to each other: their rows then share
@@ -983,7 +983,9 @@ static int launch_attention(const AttentionArgs& a, hipStream_t st) {
   if (a.path == LR_ATTENTION_ELEMENT) {
     hipLaunchKernelGGL((k_attention_element<DT, CT>), grid, dim3(256), 0, st, a);
   } else {
-    if (a.wide == 64)
+    if (a.wide == 32)
+      launch_plain<DT, CT, 32>(a, grid, st);
+    else if (a.wide == 64)
       a.unit_heads == 16 ? launch_matrix<DT, CT, 64, 1>(a, grid, st) : launch_matrix<DT, CT, 64, 2>(a, grid, st);
     else if (a.wide == 96)
       launch_plain<DT, CT, 96>(a, grid, st);

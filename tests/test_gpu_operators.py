@@ -771,6 +771,23 @@ def test_attention_wide(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, 
     test_attention(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, window)
 
 
+ATTEND_NARROW = [  # heads of up to 32, of 96 and of 160 beside the tests above: many query heads, four cache heads a workgroup
+    ("fp32", "fp32", 20, 1, 32, 32, 16, "heads", [700, 0, 31], 0),
+    ("bf16", "bf16", 40, 2, 24, 32, 16, "tokens", [700, 0, 31], 50),
+    ("fp16", "fp16", 3, 3, 8, 8, 5, "heads", [1300, 2, 16], 0),
+    ("fp32", "fp32", 4, 4, 4, 28, 16, "tokens", UNEVEN, 0),
+    ("bf16", "bf16", 80, 4, 16, 32, 16, "tokens", UNEVEN, 0),
+    ("bf16", "bf16", 20, 1, 72, 96, 16, "heads", [700, 0, 31], 0),
+    ("fp32", "fp32", 20, 1, 96, 68, 16, "heads", [700, 0, 31], 0),
+    ("fp16", "fp16", 20, 1, 136, 160, 16, "heads", [700, 0, 31], 0),
+]
+
+
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,order,lens,window", ATTEND_NARROW)
+def test_attention_narrow(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, window):
+    test_attention(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, window)
+
+
 def test_attention_wide_plan_off_alignment(dev):
     """A plan for four heads a workgroup whose buffers turn out to be off 16 bytes: one key a lane instead, with the
     same workspace."""
