@@ -27,11 +27,11 @@ struct AttentionArgs {
   FastDiv fd_page;
   uint32_t unit_heads, tiles, units;  // query heads of a wave, their tiles in a cache head, units of a sequence
   uint32_t wide_heads, block;         // cache heads of a unit (1, or 4: one a wave); tokens of a block
-  uint32_t in_step;                   // the four waves of such a unit keep in step
   uint32_t splits, min_share;         // parts of a unit at most; blocks of a workgroup at least
   uint32_t grid;                      // workgroups (splits > 1; else one a unit)
   int64_t window;
   bool q_wide;   // query rows are contiguous and 16-byte aligned
+  bool in_step;  // the four waves of four cache heads keep in step
   float scale2;  // scale * log2 e
   int32_t path, wide;         // host only: lr_attention_path and the matrix kernel's variant
 };
