@@ -84,7 +84,7 @@ __device__ __forceinline__ bool place_of(const ChunkArgs& a, int64_t slot, uint3
   return held;
 }
 
-// V finite numbers as codes, exactly, without a division each.  p = x * (1 / scale), the reciprocal off by a step at
+// V numbers, none infinite, as codes, exactly, without a division each.  p = x * (1 / scale), the reciprocal off by a step at
 // most, is within 3 steps of fp32 of the quotient.  A candidate T next to p is taken such that no tie but T itself
 // can lie between T and the quotient; the side of T that the quotient is on is the sign of x - T scale, which one
 // fma has right (T has 21 bits at most), and T moved a little to that side rounds as the quotient does.
@@ -103,6 +103,8 @@ __device__ __forceinline__ void codes_of(const float* v, float scale, float inv,
       int32_t side;
       asm("v_med3_i32 %0, %1, -1, 1" : "=v"(side) : "v"(r));
       q[k] = __int_as_float(t + side);
+      // a NaN with ones at its end would be carried out of the NaN; one of 16 bits has zeros there
+      if (DT == LR_F32) q[k] = v[k] == v[k] ? q[k] : v[k];
     }
 #pragma unroll
     for (int k = 0; k < V; k += 4) {

@@ -805,3 +805,40 @@ def test_attention_wide_plan_off_alignment(dev):
     want, wlse, tol = attention64(q, [kn[u] for u in slots], [vn[u] for u in slots], d ** -0.5, torch.bfloat16, "bf16")
     close(out, want, tol)
     close(lse, wlse, tol.lse)
+
+
+# ------------------------------------------------------------------------------------ NaN, infinities, small numbers
+QUIET = {"fp32": [0x7fffffff, 0xffffffff, 0x7ffffffc, 0xfffffffc, 0x7fc00000], "fp16": [0x7fff, 0xffff, 0x7e00],
+         "bf16": [0x7fff, 0xffff, 0x7fc0]}
+
+
+def put_bits(x, at, dtype, bits):
+    """x with the bit patterns `bits` at the flat places `at`."""
+    whole = torch.int32 if dtype == "fp32" else torch.int16
+    top = 1 << (32 if whole == torch.int32 else 16)
+    pattern = torch.tensor([b - top if b >= top // 2 else b for b in bits], dtype=whole)
+    x.view(whole).view(-1)[at] = pattern
+    return x
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("d", [128, 72, 33])
+def test_cache_write_nan(dev, dtype, kind, d, patterns=QUIET):
+    """NaN of every payload, all ones among them, at every place of a row: it stays NaN in e4m3 and becomes 0 in
+    int8, and neither the scale nor the other codes of its row notice."""
+    t, n = T[dtype], 4 * d
+    k, v = rand((n, 1, d), t, 1), rand((n, 1, d), t, 2)
+    bits = patterns[dtype]
+    rows = torch.arange(n)
+    for x, first in ((k, 0), (v, 3)):
+        put_bits(x, rows * d + rows % d, dtype, [bits[(int(i) // 2 + first) % len(bits)] for i in rows])
+        assert int(x.isnan().sum()) == n
+    cache, info = make_cache(dev, kind, "tokens", n, 1, 1, d, d)
+    L = f"({d},1,{n}):(1,{d},{d})"
+    lr.cache_write(cache, k.to(dev), L, v.to(dev), L, torch.arange(n).to(dev))
+    for x, which in ((k, "k"), (v, "v")):
+        codes, scale = quantised64(x, kind)
+        got, s = content(cache, info, d, which)
+        close(s, scale.to(F64), 0.0, which + " scales")
+        close(got, codes, 0.0, which)
