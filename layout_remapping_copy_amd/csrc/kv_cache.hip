@@ -131,14 +131,16 @@ __device__ __forceinline__ void codes_of(const float* v, float scale, float inv,
   }
 }
 
-// max(x, |y|, |z|) in one instruction, of which fmaxf would make four: a NaN is passed over.
+// max(x, |y|, |z|) in one instruction, of which fmaxf would make four; NaN if one of them is.  (v_max3_f32 passes
+// over a quiet NaN, but a signalling one, as bf16 or fp32 in memory may be, makes its result NaN, and the next
+// one passes over that with all that went in before.)
 __device__ __forceinline__ float max_abs(float x, float y, float z) {
   float r;
-  asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  asm("v_maximum3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(x), "v"(y), "v"(z));
   return r;
 }
 
-// The largest x >= 0 (as its bits, which have the same order) over the `lanes` lanes, a power of two, of a row:
+// The largest x >= 0 (as its bits, which have the same order, NaN above all) over the `lanes` lanes, a power of two, of a row:
 // within 16 lanes by exchanges that are part of the instruction (neighbours, pairs, mirrors of 8 and 16).
 __device__ __forceinline__ float row_max(float value, uint32_t lanes) {
   uint32_t x = __float_as_uint(value);
@@ -163,7 +165,7 @@ template <int CT> __device__ __forceinline__ float scale_of(float amax) {
 //
 // Rows in chunks: a lane has one unit of a token's rows, its angles in registers for `per_lane` heads; the
 // lanes of a row (a power of two next to each other) find its largest value by exchange.  A row that holds an
-// infinity is told by that value, and is done again with the care that it needs.
+// infinity or a NaN is told by that value, and is done again with the care that it needs.
 template <int DT, int CT, int V, bool NT>
 __global__ void __launch_bounds__(256) k_cache_write_chunks(ChunkArgs a) {
   using T = typename ElemOf<DT>::T;
@@ -237,11 +239,11 @@ __global__ void __launch_bounds__(256) k_cache_write_chunks(ChunkArgs a) {
 #pragma unroll
       for (int k = 0; k < V; ++k) amax = max_abs(amax, f[k], g[k]);
       amax = row_max(amax, a.grid.lanes);
-      const bool infinite = amax == __builtin_inff();
-      if (__any(infinite)) amax = largest(__builtin_inff());
+      const bool special = !(amax < __builtin_inff());  // an infinity or a NaN
+      if (__any(special)) amax = largest(__builtin_inff());
       const float scale = scale_of<CT>(amax);
       float unit = scale;
-      if (__any(infinite || amax < 0x1p-90f)) {
+      if (__any(special || amax < 0x1p-90f)) {
         // infinities become the largest code; rows so small that a product's last bits were lost are scaled up
         const float up = amax < 0x1p-90f ? 0x1p64f : 1.f;
         unit = scale * up;

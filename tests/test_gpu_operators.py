@@ -842,3 +842,14 @@ def test_cache_write_nan(dev, dtype, kind, d, patterns=QUIET):
         got, s = content(cache, info, d, which)
         close(s, scale.to(F64), 0.0, which + " scales")
         close(got, codes, 0.0, which)
+
+
+SIGNALLING = {"fp32": [0x7f800001, 0xff800001, 0x7fbfffff], "fp16": [0x7c01, 0xfdff], "bf16": [0x7f81, 0xffbf]}
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("d", [128, 72, 33])
+def test_cache_write_signalling_nan(dev, dtype, kind, d):
+    """The same of signalling NaN, which some instructions answer with a NaN where they pass over a quiet one."""
+    test_cache_write_nan(dev, dtype, kind, d, SIGNALLING)
