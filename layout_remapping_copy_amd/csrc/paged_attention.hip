@@ -366,6 +366,18 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t x) {
   }
 }
 
+// Two 16-bit numbers with infinities and NaN replaced by the largest finite number of their sign.  As signed integers
+// the positive ones have their order and the negative ones are below zero; as unsigned integers the negative
+// ones have the order of their size, above all positive ones.
+template <int DT> __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
+  typedef short I2 __attribute__((ext_vector_type(2)));
+  typedef unsigned short W2 __attribute__((ext_vector_type(2)));
+  constexpr unsigned short kMost = DT == LR_F16 ? 0x7bff : 0x7f7f;
+  const I2 y = __builtin_elementwise_min(__builtin_bit_cast(I2, x), I2{(short)kMost, (short)kMost});
+  constexpr unsigned short kLeast = kMost | 0x8000;
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(W2, y), W2{kLeast, kLeast}));
+}
+
 // x itself, unknown to the compiler: what is computed from it is not kept in registers over the loop around.
 __device__ __forceinline__ uint32_t here(uint32_t x) {
   asm volatile("" : "+v"(x));
@@ -605,7 +617,9 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
         // weights
         // Of 16-bit products' weights two parts are taken, the value and what its rounding left: a bf16 alone
         // would add as much error to the output as its own rounding does, and cost an fp16 model with an 8-bit
-        // cache its last three bits.
+        // cache its last three bits.  The second part may be zero or negative, so that an infinite value must meet
+        // the first one only: times zero, or taken off itself, it would be NaN.  An fp16 first part is not rounded to
+        // zero for the same reason; the second takes off what is too much.
         using P = std::conditional_t<kQuant && !S::kF32, B8, M>;
         using PE = std::conditional_t<kQuant && !S::kF32, __bf16, T>;
         P phi[HT], plo[HT];
@@ -642,7 +656,7 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
               float x = __builtin_amdgcn_exp2f(s[ht][t][i] - base[ht]);
               l[ht] += x;
               if constexpr (kQuant) x *= vsc[t][i];
-              phi[ht][4 * t + i] = (PE)x;
+              phi[ht][4 * t + i] = (PE)(std::is_same_v<PE, _Float16> ? fmaxf(x, 0x1p-24f) : x);
               if constexpr (!S::kF32) plo[ht][4 * t + i] = (PE)(x - (float)phi[ht][4 * t + i]);
             }
         }
@@ -707,6 +721,13 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
                 F4& ob = o[ht][p][2 * d + 1];
                 oa = mfma(__builtin_bit_cast(M, v0), phi[ht], oa);
                 ob = mfma(__builtin_bit_cast(M, v1), phi[ht], ob);
+              }
+#pragma unroll
+              for (int x = 0; x < 4; ++x) v0[x] = finite_pair<DT>(v0[x]), v1[x] = finite_pair<DT>(v1[x]);
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht) {
+                F4& oa = o[ht][p][2 * d];
+                F4& ob = o[ht][p][2 * d + 1];
                 oa = mfma(__builtin_bit_cast(M, v0), plo[ht], oa);
                 ob = mfma(__builtin_bit_cast(M, v1), plo[ht], ob);
               }

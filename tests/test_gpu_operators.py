@@ -853,3 +853,81 @@ SIGNALLING = {"fp32": [0x7f800001, 0xff800001, 0x7fbfffff], "fp16": [0x7c01, 0xf
 def test_cache_write_signalling_nan(dev, dtype, kind, d):
     """The same of signalling NaN, which some instructions answer with a NaN where they pass over a quiet one."""
     test_cache_write_nan(dev, dtype, kind, d, SIGNALLING)
+
+
+# Forms of the attention: one run a head or several, heads side by side, one key a lane, up to 32 query heads a workgroup.
+FORMS = [  # heads, kv, dk, dv, page, order, lens
+    (4, 2, 64, 64, 16, "tokens", [40, 300]),
+    (2, 1, 64, 64, 16, "heads", [2500, 7]),
+    (16, 4, 128, 128, 16, "tokens", [(i * 389) % 2000 + 1 for i in range(40)]),
+    (20, 1, 72, 96, 16, "heads", [700, 33]),
+    (2, 1, 160, 160, 16, "heads", [700, 33]),
+    (3, 3, 33, 17, 5, "tokens", [1200, 4]),
+]
+
+
+def attend_all(dev, cache, table, q, dv, lens, **kw):
+    """(out, lse) of one call, q (sequences, heads, dk) on the CPU."""
+    b, h, dk = q.shape
+    out = torch.full((b, h, dv), -7.0, dtype=q.dtype, device=dev)
+    lse = torch.full((b, h), -7.0, device=dev)
+    lr.paged_attention(q.to(dev), f"({dk},{h},{b}):(1,{dk},{h * dk})", cache, table.to(dev),
+                       torch.tensor(lens, dtype=torch.int32, device=dev), out, f"({dv},{h},{b}):(1,{dv},{h * dv})", lse=lse, **kw)
+    return out, lse
+
+
+def set_rows(cache, which, order, page, kv, d, slots, rows):
+    """The cache's rows of the given slots: rows (len(slots), kv, d)."""
+    buf = getattr(cache, which)
+    s, _ = cache_strides(order, kv, page, d)
+    pages = (buf.numel() - 1) // s[0] + 1
+    view = buf.as_strided((pages, page, kv, d), s)
+    view[(slots // page).to(buf.device), (slots % page).to(buf.device)] = rows.to(buf.dtype).to(buf.device)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("heads,kv,dk,dv,page,order,lens", FORMS)
+def test_attention_infinite_values(dev, dtype, heads, kv, dk, dv, page, order, lens):
+    """An infinite value makes its column infinite, two of different signs or a NaN make it NaN, and no other column
+    notices; infinities that are not seen do not matter."""
+    t, b = T[dtype], len(lens)
+    cache, table, slots, (kn, vn) = attention_case(dev, dtype, dtype, heads, kv, dk, dv, page, order, lens)
+    q = rand((b, heads, dk), t, 11)
+    for i, u in enumerate(slots):
+        n = len(u)
+        for column, row, value in ((0, 0, math.inf), (1, n - 1, -math.inf), (2, n // 2, math.inf), (3, n // 3, math.nan)):
+            vn[u[row], :, column] = value
+        if n > 1:
+            vn[u[0], :, 5], vn[u[1], :, 5] = math.inf, -math.inf
+            vn[u[0], :, 6], vn[u[n - 1], :, 6] = -math.inf, -math.inf
+        set_rows(cache, "v", order, page, kv, dv, u, vn[u].to(t))
+    out, lse = attend_all(dev, cache, table, q, dv, lens)
+    finite = vn.nan_to_num(0, 0, 0)
+    want, wlse, tol = attention64(q, [kn[u] for u in slots], [finite[u] for u in slots], dk ** -0.5, t, dtype)
+    for i, u in enumerate(slots):
+        for column in range(7):
+            x = vn[u][:, :, column]
+            bad = x.isnan().any() or ((x == math.inf).any() and (x == -math.inf).any())
+            if bad or x.isinf().any():
+                want[i, :, column] = math.nan if bad else x[x.isinf()].max()
+    close(out, want, tol, "out")
+    close(lse, wlse, tol.lse, "lse")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [64, 33])
+def test_attention_infinite_value_of_small_weight(dev, dtype, d):
+    """The weight of an infinite value may be e^-30 of the largest."""
+    t, n = T[dtype], 100
+    cache, table, slots, (kn, vn) = attention_case(dev, dtype, dtype, 2, 1, d, d, 16, "heads", [n])
+    u = slots[0]
+    kn[u] = 0
+    kn[u[::32], :, 0], vn[u[70], :, 1], vn[u[71], :, 2] = 30, math.inf, -math.inf
+    set_rows(cache, "k", "heads", 16, 1, d, u, kn[u])
+    set_rows(cache, "v", "heads", 16, 1, d, u, vn[u])
+    q = torch.zeros((1, 2, d), dtype=t)
+    q[..., 0] = 1
+    out, _ = attend_all(dev, cache, table, q, d, [n], scale=1.0)
+    want, _, tol = attention64(q, [kn[u]], [vn[u].nan_to_num(0, 0, 0)], 1.0, t, dtype)
+    want[..., 1], want[..., 2] = math.inf, -math.inf
+    close(out, want, tol)
