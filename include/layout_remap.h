@@ -642,7 +642,7 @@ typedef struct {
  * q, out: layouts (head_dim, heads, sequences), the first batch sequences used; heads a multiple of the
  * cache's; q's head_dim is the keys', out's the values', each at most 256.  dtype (of q and out): LR_F32,
  * LR_F16 or LR_BF16; the cache has the same type, or LR_E4M3 or LR_INT8.  lse (NULL: not wanted): device
- * float[batch][heads], log sum_t exp(scale * q . k), -inf with no token.
+ * float[batch][heads], log sum_t exp(scale * q . k), -inf with no token (and NaN, as out, where a score is).
  * The tokens of all sequences are dealt out evenly to the workgroups; what that cuts is joined by a second
  * launch.  workspace: device memory of at least the plan's workspace_bytes (LR_ERR_CAPACITY), 16-byte
  * aligned, its contents don't matter.  The result does not depend on timing: every sum has an order that

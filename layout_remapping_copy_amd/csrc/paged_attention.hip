@@ -184,6 +184,10 @@ __device__ __forceinline__ float weight_of(float m, float top) {
   return m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - top);
 }
 
+// log sum e^s of a part with maximum top and sum total: -inf without a token (0 is -inf in log2), NaN where a score
+// is, for which the maximum says nothing.
+__device__ __forceinline__ float lse_of(float top, float total) { return (top + __log2f(total)) * kLn2; }
+
 // Orders this wave's accesses to shared memory; one wave's are done in their order, so no wait is needed.
 __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(256) k_attention_element(AttentionArgs a) {
     }
     if (threadIdx.x == 0) {
       if (a.splits > 1) leave_part(a, run, bh, top, total);
-      if (run.whole && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
+      if (run.whole && a.lse) a.lse[bh] = lse_of(top, total);
     }
   } while (run_next(a, &run));
 }
@@ -770,7 +774,7 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
             }
         if (je == 0) {
           if (a.splits > 1) leave_part(a, run, bh, top, total);
-          if (run.whole && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
+          if (run.whole && a.lse) a.lse[bh] = lse_of(top, total);
         }
       }
     } else {
@@ -823,7 +827,7 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
             }
             if (e == 0) {
               if (a.splits > 1) leave_part(a, run, bh, top, total);
-              if (run.whole && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
+              if (run.whole && a.lse) a.lse[bh] = lse_of(top, total);
             }
           }
         }
@@ -889,7 +893,7 @@ __global__ void __launch_bounds__(256) k_attention_join(AttentionArgs a) {
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i)
     if (4 * c + i < (uint32_t)a.dv) out[(int64_t)(4 * c + i) * a.od] = (T)(total != total ? total : acc[i] * inv);
-  if (c == 0 && a.lse) a.lse[bh] = top == -__builtin_inff() ? top : (top + __log2f(total)) * kLn2;
+  if (c == 0 && a.lse) a.lse[bh] = lse_of(top, total);
 }
 
 // ------------------------------------------------------------------ host

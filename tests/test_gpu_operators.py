@@ -931,3 +931,23 @@ def test_attention_infinite_value_of_small_weight(dev, dtype, d):
     want, _, tol = attention64(q, [kn[u]], [vn[u].nan_to_num(0, 0, 0)], 1.0, t, dtype)
     want[..., 1], want[..., 2] = math.inf, -math.inf
     close(out, want, tol)
+
+
+@pytest.mark.parametrize("dtype,kind", [("bf16", "bf16"), ("fp16", "int8"), ("fp32", "fp32"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("heads,kv,dk,dv,page,order,lens", FORMS)
+def test_attention_nan_query(dev, dtype, kind, heads, kv, dk, dv, page, order, lens):
+    """A NaN in a head's query: its output and its lse are NaN, in one part or in several; other heads do not notice,
+    and a sequence without tokens still has none."""
+    t, lens = T[dtype], lens + [0]
+    b = len(lens)
+    cache, table, slots, (kn, vn) = attention_case(dev, dtype, kind, heads, kv, dk, dv, page, order, lens)
+    q = rand((b, heads, dk), t, 11)
+    clean = q.clone()
+    for i in range(b):
+        q[i, i % heads, (5 * i) % dk] = math.nan
+    out, lse = attend_all(dev, cache, table, q, dv, lens)
+    want, wlse, tol = attention64(clean, [kn[u] for u in slots], [vn[u] for u in slots], dk ** -0.5, t, kind)
+    for i in range(b - 1):
+        want[i, i % heads], wlse[i, i % heads] = math.nan, math.nan
+    close(out, want, tol, "out")
+    close(lse, wlse, tol.lse, "lse")
