@@ -558,7 +558,10 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
     };
 
     F4 o[HT][S::kValSteps][S::kValChunk] = {};
-    float base[HT], l[HT];  // scores are taken off `base`, at most 8 below the running maximum
+    // Scores are taken off `base`, at most 8 below the running maximum; weights in fp16 parts, whose smallest is
+    // 2^-24, off a base 7 to 15 below it: the largest is then 2^7 to 2^15, and one of 2^-32 of it still counts.
+    constexpr float kLow = std::is_same_v<M, H8> && !kQuant ? 7.f : 0.f;
+    float base[HT], l[HT];
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) base[ht] = -__FLT_MAX__, l[ht] = 0;
     constexpr uint32_t kAll = 0xffffffffu;  // of 16 tokens the mask has every bit twice
@@ -643,8 +646,8 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = fmaxf(top, s[ht][t][i]);
           }
-          if (__any(top > base[ht] + 8.f)) {
-            top = fmaxf(base[ht], across_groups_max(top));
+          if (__any(top > base[ht] + (8.f + kLow))) {
+            top = fmaxf(base[ht], across_groups_max(top) - kLow);
             const float keep = __builtin_amdgcn_exp2f(base[ht] - top);
             base[ht] = top;
             l[ht] *= keep;

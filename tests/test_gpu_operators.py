@@ -951,3 +951,47 @@ def test_attention_nan_query(dev, dtype, kind, heads, kv, dk, dv, page, order, l
         want[i, i % heads], wlse[i, i % heads] = math.nan, math.nan
     close(out, want, tol, "out")
     close(lse, wlse, tol.lse, "lse")
+
+
+def tight64(q, ks, vs, scale, weight, floor):
+    """attention64 with a tolerance without slack for the weights: `weight` relative to each and `floor` relative to
+    the largest."""
+    b, h, dk = q.shape
+    dv = vs[0].shape[-1]
+    out, tol = torch.zeros((b, h, dv), dtype=F64), torch.zeros((b, h, dv), dtype=F64)
+    for i in range(b):
+        g = h // ks[i].shape[1]
+        k, v = (x[i].to(F64).repeat_interleave(g, 1).transpose(0, 1) for x in (ks, vs))
+        s = torch.matmul(k, q[i].to(F64).unsqueeze(-1)).squeeze(-1) * scale
+        p = torch.softmax(s, -1)
+        out[i] = torch.matmul(p.unsqueeze(1), v).squeeze(1)
+        size = torch.matmul(p.unsqueeze(1), v.abs()).squeeze(1)
+        # a score: a rounding for each product of its row and for the scale; the exponential's own 2^-22
+        ds = (torch.matmul(k.abs(), q[i].to(F64).abs().unsqueeze(-1)).squeeze(-1) * abs(scale)).amax(-1) * (dk + 8) * U
+        lost = floor * p.amax(-1)[:, None] * v.abs().sum(1)
+        tol[i] = HALF[q.dtype] * out[i].abs() + (weight + (k.shape[1] + 16) * U + 2 * ds[:, None] + 2.0 ** -22) * size + lost \
+            + TINY[q.dtype]
+    return out, tol
+
+
+@pytest.mark.parametrize("heads,kv,dk,dv,page,order", [(2, 1, 64, 64, 16, "heads"), (8, 8, 64, 64, 16, "tokens"),
+                                                       (20, 1, 64, 32, 16, "heads"), (1, 1, 160, 192, 16, "heads"),
+                                                       (2, 2, 33, 20, 16, "tokens")])
+@pytest.mark.parametrize("below", [10.0, 15.0, 16.0, 17.0, 17.8])
+def test_attention_sinks_fp16(dev, heads, kv, dk, dv, page, order, below):
+    """Tokens far above all others whose values are zero, one in every 32: what the others weigh is under 2^-21 of the
+    largest weight, and they alone make up the output, which still has the accuracy of fp16."""
+    n = 20000 if order == "heads" else 60000
+    cache, table, slots, (kn, vn) = attention_case(dev, "fp16", "fp16", heads, kv, dk, dv, page, order, [n])
+    u = slots[0]
+    kn[u], vn[u] = 0, 1000 * (1 + rand((n, kv, dv), torch.float16, 3).abs().to(F64).clamp(max=4))
+    kn[u[::32], :, 0], vn[u[::32]] = below, 0
+    kn[u], vn[u] = kn[u].to(torch.float16).to(F64), vn[u].to(torch.float16).to(F64)
+    for which, x, d in (("k", kn, dk), ("v", vn, dv)):
+        set_rows(cache, which, order, page, kv, d, u, x[u])
+    q = torch.zeros((1, heads, dk), dtype=torch.float16)
+    q[..., 0] = 1
+    out, _ = attend_all(dev, cache, table, q, dv, [n], scale=1.0)
+    # two fp16 parts leave 2^-11 of 2^-11 of a weight, and at least half of 2^-24 where the largest is 2^7 or more
+    want, tol = tight64(q, [kn[u]], [vn[u]], 1.0, 2.0 ** -22, 2.0 ** -32)
+    close(out, want, tol)
