@@ -503,7 +503,8 @@ int lr_layout_copy_count_writes(const void* src, const lr_layout* Ls, int64_t sr
  * (sequence, batch), say), otherwise it has to coalesce to one leaf.  Extents are
  * those of the layout; token counts are arguments, so one layout serves every step.
  * Sums, softmax statistics and rotations are computed in 32 bits and rounded once,
- * to nearest even, where they are stored.
+ * to nearest even, where they are stored.  One factor has fewer bits: the weights that
+ * lr_paged_attention multiplies values of 16 or 8 bits by (stated there).
  *
  * Errors of every entry point, before anything is launched: LR_ERR_INVALID (NULL,
  * a negative count, wrong number of modes, a mode of several leaves where one is
@@ -646,7 +647,10 @@ typedef struct {
  * The tokens of all sequences are dealt out evenly to the workgroups; what that cuts is joined by a second
  * launch.  workspace: device memory of at least the plan's workspace_bytes (LR_ERR_CAPACITY), 16-byte
  * aligned, its contents don't matter.  The result does not depend on timing: every sum has an order that
- * lens alone decides. */
+ * lens alone decides.
+ * LR_ATTENTION_MATRIX multiplies values of an LR_F32 cache, or under LR_F32 queries, by weights of 32 bits; other
+ * values by weights in two 16-bit parts, which hold 16 bits of each weight for LR_BF16 and 8-bit caches, and 22 for
+ * LR_F16, down to 2^-32 of the largest.  The totals that the sums are divided by have the whole weights. */
 int lr_paged_attention_plan(const lr_layout* Lq, const lr_cache* c, const lr_layout* Lo, int64_t max_pages,
                             int32_t dtype, int64_t window, lr_attention_plan* out);
 int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, const lr_cache* c,

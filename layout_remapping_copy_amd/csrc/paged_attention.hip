@@ -622,9 +622,10 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
           if (a.in_step) __builtin_amdgcn_s_barrier();  // the four waves make equally many rounds
         load_keys();
         // weights
-        // Of 16-bit products' weights two parts are taken, the value and what its rounding left: a bf16 alone
-        // would add as much error to the output as its own rounding does, and cost an fp16 model with an 8-bit
-        // cache its last three bits.  The second part may be zero or negative, so that an infinite value must meet
+        // Of 16-bit products' weights two parts are taken, the value and what its rounding left, 16 bits in bf16 and 22
+        // in fp16: a bf16 alone would add as much error to the output as its own rounding does, and cost an fp16
+        // model with an 8-bit cache its last three bits; a third part would add nothing that an output of 8 or 11
+        // bits shows.  The second part may be zero or negative, so that an infinite value must meet
         // the first one only: times zero, or taken off itself, it would be NaN.  An fp16 first part is not rounded to
         // zero for the same reason; the second takes off what is too much.
         using P = std::conditional_t<kQuant && !S::kF32, B8, M>;

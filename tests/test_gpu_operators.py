@@ -995,3 +995,37 @@ def test_attention_sinks_fp16(dev, heads, kv, dk, dv, page, order, below):
     # two fp16 parts leave 2^-11 of 2^-11 of a weight, and at least half of 2^-24 where the largest is 2^7 or more
     want, tol = tight64(q, [kn[u]], [vn[u]], 1.0, 2.0 ** -22, 2.0 ** -32)
     close(out, want, tol)
+
+
+@pytest.mark.parametrize("dtype,kind,weight,floor", [("bf16", "bf16", 2.0 ** -16, 0.0), ("fp16", "fp16", 2.0 ** -22, 2.0 ** -32),
+                                                     ("fp16", "e4m3", 2.0 ** -16, 0.0), ("fp32", "fp32", 2.0 ** -24, 0.0)])
+@pytest.mark.parametrize("heads,kv,dk,dv,page,order,lens", FORMS)
+def test_attention_weights_in_two_parts(dev, dtype, kind, weight, floor, heads, kv, dk, dv, page, order, lens):
+    """Values that nearly cancel, token by token, so that the output shows what the weights' rounding leaves: 16 bits
+    of them (22 in fp16), as two parts have, not the 8 or 11 of one."""
+    t, b = T[dtype], len(lens)
+    cache, table, slots, (kn, vn) = attention_case(dev, dtype, kind, heads, kv, dk, dv, page, order, lens)
+    for u in slots:
+        m = len(u) // 2
+        vn[u[m:2 * m]] = -vn[u[:m]]
+        kn[u[m:2 * m]] = kn[u[:m]]
+        if kind in TOP:       # codes: the scale of a key changes by a step or two, and its score with it
+            for which, d in (("k", dk), ("v", dv)):
+                s, ss = cache_strides(order, kv, page, d)
+                buf, sc = getattr(cache, which), getattr(cache, which + "_scale")
+                pages = sc.numel() // (page * kv)
+                bv, sv = buf.as_strided((pages, page, kv, d), s), sc.as_strided((pages, page, kv), ss)
+                a, z = u[:m].to(dev), u[m:2 * m].to(dev)
+                bv[z // page, z % page] = bv[a // page, a % page]
+                sign = 1 + 2.0 ** -7 if which == "k" else -1
+                sv[z // page, z % page] = sv[a // page, a % page] * sign
+            kn[u[m:2 * m]] = (kn[u[:m]] * (1 + 2.0 ** -7))
+        else:
+            kn[u[m:2 * m], :, 0] += 2.0 ** -5
+            kn[u] = kn[u].to(t).to(F64)
+            for which, x, d in (("k", kn, dk), ("v", vn, dv)):
+                set_rows(cache, which, order, page, kv, d, u, x[u].to(t))
+    q = rand((b, heads, dk), t, 11)
+    out, _ = attend_all(dev, cache, table, q, dv, lens)
+    want, tol = tight64(q, [kn[u] for u in slots], [vn[u] for u in slots], dk ** -0.5, weight, floor)
+    close(out, want, tol)
