@@ -167,13 +167,17 @@ __device__ __forceinline__ float value_of(typename ElemOf<DT>::T x) {
 
 // ------------------------------------------------------------------ angles
 
-// sin and cos of a fraction of a turn given in 64 bits.  The upper 32 bits are
-// reduced to a quadrant and a rest within an eighth of a turn either way; the rest's
-// Taylor sums to x^9 and x^10 are off by under 2e-9, below a half step of fp32.
+// sin and cos of a fraction of a turn given in 64 bits, as a signed lower half and an upper one.  The upper half is
+// reduced to a quadrant and a rest within an eighth of a turn either way, the lower one is joined to the rest in one
+// rounding, so that small angles have all their bits too.  The rest's Taylor sums to x^9 and x^10 are off by under
+// 2e-9, below a half step of fp32.  With the roundings of the rest and of the sums, sin and cos of 26 million random
+// angles are off by up to 1.7 * 2^-24 (0.34 root mean square; their last rounding alone is up to 0.5), and sin of a
+// small angle by up to 3.1 * 2^-24 of itself.
 __device__ __forceinline__ void sincos_turn(uint64_t t, float* sin_out, float* cos_out) {
-  const uint32_t hi = (uint32_t)(t >> 32);
+  const uint32_t hi = (uint32_t)(t >> 32) + ((uint32_t)t >> 31);
   const uint32_t q = (hi + 0x20000000u) >> 30;
-  const float x = (float)(int32_t)(hi - (q << 30)) * 1.4629180792671596e-09f;  // 2 pi / 2^32
+  constexpr float kAngle = 1.4629180792671596e-09f;  // 2 pi / 2^32
+  const float x = __builtin_fmaf((float)(int32_t)(hi - (q << 30)), kAngle, (float)(int32_t)(uint32_t)t * (kAngle * 0x1p-32f));
   const float z = x * x;
   const float s = x + x * z * (-1.f / 6 + z * (1.f / 120 + z * (-1.f / 5040 + z * (1.f / 362880))));
   const float c = 1.f + z * (-0.5f + z * (1.f / 24 + z * (-1.f / 720 + z * (1.f / 40320 + z * (-1.f / 3628800)))));

@@ -1029,3 +1029,20 @@ def test_attention_weights_in_two_parts(dev, dtype, kind, weight, floor, heads, 
     out, _ = attend_all(dev, cache, table, q, dv, lens)
     want, tol = tight64(q, [kn[u] for u in slots], [vn[u] for u in slots], dk ** -0.5, weight, floor)
     close(out, want, tol)
+
+
+@pytest.mark.parametrize("d", [256, 30])
+def test_rope_small_angles(dev, d):
+    """Sine and cosine of the slowest pairs and the first positions, relative to themselves: an angle has 32 bits
+    however small it is.  Roundings: the angle's conversion, its constant and its product, and two in each series."""
+    n = 40
+    pos = torch.tensor([0, 1, 2, 3, 5, -1, -7] + [10 ** i for i in range(1, 7)] + list(range(100, 127)))[:n]
+    table = lr.rope_table(d, base=1e8, device=dev)
+    x = torch.zeros((n, 1, d))
+    x[..., :d // 2] = 1
+    L = f"({d},1,{n}):(1,{d},{d})"
+    y = lr.rope(x.to(dev), L, torch.empty_like(x, device=dev), L, pos.to(dev), table).cpu().to(F64)
+    a = (pos.reshape(-1, 1) * table.turns.cpu()).to(F64) * (2 * math.pi / 2.0 ** 64)
+    cos, sin = y[:, 0, :d // 2], y[:, 0, d // 2:]
+    close(sin, a.sin(), torch.where(a.abs() < math.pi / 4, 5 * U * a.sin().abs(), torch.full_like(a, 4 * U)), "sin")
+    close(cos, a.cos(), 4 * U, "cos")
