@@ -31,12 +31,13 @@ struct CacheArgs {
 
 // The code nearest x / scale, exactly: the fp32 quotient's remainder says which side of
 // the quotient the true value lies on, and a quotient that could be a tie (an even last
-// bit) is moved one step towards it.
+// bit) is moved one step towards it.  The remainder of x and scale has to be a number of
+// fp32: rows of small numbers are scaled up by the caller.
 template <int DT>
 __device__ __forceinline__ typename ElemOf<DT>::T code_of(float x, float scale) {
   constexpr float top = DT == LR_E4M3 ? 448.f : 127.f;
   if (DT == LR_INT8 && x != x) return 0;
-  const float inv = 1.f / scale;  // scale >= 2^-126: finite
+  const float inv = 1.f / scale;  // finite
   const float q0 = x * inv;
   float q = __builtin_fmaf(__builtin_fmaf(-q0, scale, x), inv, q0);
   const float rest = __builtin_fmaf(-q, scale, x);
@@ -383,10 +384,11 @@ __global__ void __launch_bounds__(256) k_cache_write(CacheArgs a) {
       if (__builtin_fabsf(p) < __builtin_inff()) amax = fmaxf(amax, __builtin_fabsf(p));
       if (__builtin_fabsf(q) < __builtin_inff()) amax = fmaxf(amax, __builtin_fabsf(q));
     }
-    float scale = 1;
+    float scale = 1, up = 1;
     if constexpr (CT == LR_E4M3 || CT == LR_INT8) {
       for (int m = 32; m; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
       scale = fmaxf(amax / (CT == LR_E4M3 ? 448.f : 127.f), 0x1p-126f);
+      up = amax < 0x1p-90f ? 0x1p64f : 1.f;
       if (lane == 0) s.scale[(int64_t)page * a.sp + (int64_t)in * a.ss + (int64_t)h * a.sh] = scale;
     }
 #pragma unroll
@@ -397,8 +399,8 @@ __global__ void __launch_bounds__(256) k_cache_write(CacheArgs a) {
       const uint32_t i = !turned ? s.rot + 2 * (u - half) : a.pairs == LR_PAIRS_HALF ? u : 2 * u;
       const uint32_t j = turned && a.pairs == LR_PAIRS_HALF ? u + half : i + 1;
       if constexpr (CT == LR_E4M3 || CT == LR_INT8) {
-        y[(int64_t)i * s.cd] = code_of<CT>(v[2 * k], scale);
-        if (j < (uint32_t)s.dim) y[(int64_t)j * s.cd] = code_of<CT>(v[2 * k + 1], scale);
+        y[(int64_t)i * s.cd] = code_of<CT>(v[2 * k] * up, scale * up);
+        if (j < (uint32_t)s.dim) y[(int64_t)j * s.cd] = code_of<CT>(v[2 * k + 1] * up, scale * up);
       } else {
         y[(int64_t)i * s.cd] = (C)v[2 * k];
         if (j < (uint32_t)s.dim) y[(int64_t)j * s.cd] = (C)v[2 * k + 1];

@@ -1046,3 +1046,27 @@ def test_rope_small_angles(dev, d):
     cos, sin = y[:, 0, :d // 2], y[:, 0, d // 2:]
     close(sin, a.sin(), torch.where(a.abs() < math.pi / 4, 5 * U * a.sin().abs(), torch.full_like(a, 4 * U)), "sin")
     close(cos, a.cos(), 4 * U, "cos")
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("d", [128, 33])
+def test_codes_of_tiny_rows(dev, kind, d):
+    """Rows whose scale is just above its least value, of numbers nearest to ties: what is left of a number after
+    its tie has bits below fp32's smallest."""
+    n = 64
+    g = torch.Generator().manual_seed(4)
+    scale = (1 + torch.randint(1, 1 << 23, (n, 1), generator=g).to(F64) / 2 ** 23) * 2.0 ** -126
+    part = torch.randint(8, 16, (n, d), generator=g).to(F64) / 8 + 1 / 16 if kind == "e4m3" else \
+        torch.randint(0, 2, (n, d), generator=g).to(F64) + 0.5
+    sign = torch.randint(0, 2, (n, d), generator=g) * 2 - 1
+    x = (scale * part * sign).float()
+    x[:, 0] = (scale[:, 0] * TOP[kind]).float()
+    x = x.reshape(n, 1, d).contiguous()
+    cache, info = make_cache(dev, kind, "tokens", n, 1, 1, d, d)
+    L = f"({d},1,{n}):(1,{d},{d})"
+    lr.cache_write(cache, x.to(dev), L, x.to(dev), L, torch.arange(n).to(dev))
+    codes, want = quantised64(x, kind)
+    for which in "kv":
+        got, s = content(cache, info, d, which)
+        close(s, want.to(F64), 0.0, which + " scales")
+        close(got, codes, 0.0, which)
