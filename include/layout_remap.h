@@ -506,9 +506,9 @@ int lr_layout_copy_count_writes(const void* src, const lr_layout* Ls, int64_t sr
  * to nearest even, where they are stored.  One factor has fewer bits: the weights that
  * lr_paged_attention multiplies values of 16 or 8 bits by (stated there).
  *
- * Errors of every entry point, before anything is launched: LR_ERR_INVALID (NULL,
- * a negative count, wrong number of modes, a mode of several leaves where one is
- * needed, a parameter out of range), LR_ERR_SWIZZLE, LR_ERR_TYPE,
+ * Errors of every entry point, before anything is launched: LR_ERR_INVALID (NULL, but
+ * for an array of no entries; a negative count, wrong number of modes, a mode of several
+ * leaves where one is needed, a parameter out of range), LR_ERR_SWIZZLE, LR_ERR_TYPE,
  * LR_ERR_SIZE_MISMATCH (extents that have to agree), LR_ERR_BOUNDS (a layout beyond
  * its buffer), LR_ERR_ALIAS (an output layout that is not injective),
  * LR_ERR_OVERLAP (an output that overlaps an input), LR_ERR_OVERFLOW (a count or an

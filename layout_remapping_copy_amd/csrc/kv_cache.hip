@@ -3,7 +3,7 @@
 
 namespace lr {
 
-int check_rotation(const lr_rotation* r, int64_t dim);
+int check_rotation(const lr_rotation* r, int64_t dim, int64_t n);
 
 constexpr int kCacheDim = 512;  // head_dim at most
 
@@ -588,7 +588,7 @@ int lr_cache_write(const lr_cache* c, const void* k, const lr_layout* Lk, int64_
   int rc = fill_cache(c, &a);
   if (rc || (rc = fill_rows(c, &a, k, Lk, k_capacity, v, Lv, v_capacity, dtype, slots, n, false))) return rc;
   if (r) {
-    if ((rc = check_rotation(r, a.side[0].dim))) return rc;
+    if ((rc = check_rotation(r, a.side[0].dim, n))) return rc;
     a.side[0].rot = r->rot_dim;
     a.turns = r->turns;
     a.positions = r->positions;

@@ -1064,7 +1064,7 @@ int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, c
                        int64_t table_stride, int64_t max_pages, const int32_t* lens, int64_t batch, void* out,
                        const lr_layout* Lo, int64_t out_capacity, float* lse, int32_t dtype, float scale, int64_t window,
                        void* workspace, int64_t workspace_bytes, void* stream) {
-  if (!q || !out || !table || !lens || batch < 0 || !std::isfinite(scale)) return LR_ERR_INVALID;
+  if (!q || !out || batch < 0 || (batch > 0 && (!table || !lens)) || !std::isfinite(scale)) return LR_ERR_INVALID;
   AttentionArgs a;
   lr_attention_plan p;
   if (int rc = plan_attention(Lq, c, Lo, max_pages, dtype, window, &a, &p)) return rc;

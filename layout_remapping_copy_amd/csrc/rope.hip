@@ -144,8 +144,8 @@ static bool same_leaves(const Mode& a, const Mode& b) {
   return true;
 }
 
-int check_rotation(const lr_rotation* r, int64_t dim) {
-  if (!r || !r->turns || !r->positions) return LR_ERR_INVALID;
+int check_rotation(const lr_rotation* r, int64_t dim, int64_t n) {
+  if (!r || !r->turns || (n > 0 && !r->positions)) return LR_ERR_INVALID;
   if (r->rot_dim < 2 || r->rot_dim > 1024 || r->rot_dim % 2 || r->rot_dim > dim) return LR_ERR_INVALID;
   if (r->pairs != LR_PAIRS_HALF && r->pairs != LR_PAIRS_INTERLEAVED) return LR_ERR_INVALID;
   return LR_OK;
@@ -209,7 +209,7 @@ int lr_rope(const void* x, const lr_layout* Lx, int64_t x_capacity, void* y, con
   const Mode xd = mode_of(*Lx, 0), yd = mode_of(*Ly, 0), xh = mode_of(*Lx, 1), yh = mode_of(*Ly, 1);
   const Mode xt = mode_of(*Lx, 2), yt = mode_of(*Ly, 2);
   if (xd.size != yd.size || xh.size != yh.size || xt.size != yt.size) return LR_ERR_SIZE_MISMATCH;
-  if ((rc = check_rotation(r, xd.size))) return rc;
+  if ((rc = check_rotation(r, xd.size, n))) return rc;
   if (n < 0) return LR_ERR_INVALID;
   if (n > xt.size) return LR_ERR_BOUNDS;
   Mode p{0, {}, 1};

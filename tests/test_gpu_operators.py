@@ -1070,3 +1070,25 @@ def test_codes_of_tiny_rows(dev, kind, d):
         got, s = content(cache, info, d, which)
         close(s, want.to(F64), 0.0, which + " scales")
         close(got, codes, 0.0, which)
+
+
+def test_calls_of_nothing(dev):
+    """No sequences, no tokens: empty tensors are taken, and nothing is written."""
+    cache, table, slots, _ = attention_case(dev, "bf16", "bf16", 4, 2, 64, 64, 16, "tokens", [40, 300])
+    kept = cache.k.clone()
+    q = rand((2, 4, 64), torch.bfloat16, 1).to(dev)
+    out, lse = torch.full((2, 4, 64), -7.0, dtype=torch.bfloat16, device=dev), torch.empty((0, 4), device=dev)
+    L = "(64,4,2):(1,64,256)"
+    none = torch.empty(0, dtype=torch.int32, device=dev)
+    lr.paged_attention(q, L, cache, table.to(dev)[:0], none, out, L, lse=lse)
+    lr.paged_attention(q, L, cache, table.to(dev), none, out, L)
+    x = rand((2, 2, 64), torch.bfloat16, 2).to(dev)
+    Lx, none = "(64,2,2):(1,64,128)", torch.empty(0, dtype=torch.int64, device=dev)
+    rt = lr.rope_table(64, device=dev)
+    lr.cache_write(cache, x, Lx, x, Lx, none, table=rt, positions=none)
+    y, z = torch.full_like(x, -7.0), torch.full_like(x, -7.0)
+    lr.cache_read(cache, none, y, Lx, z, Lx)
+    lr.rope(x, Lx, y, Lx, none, rt)
+    torch.cuda.synchronize()
+    assert (out == -7).all() and (y == -7).all() and (z == -7).all()
+    assert torch.equal(cache.k.view(torch.int16), kept.view(torch.int16))

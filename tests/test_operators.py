@@ -257,3 +257,20 @@ def test_structs_match_the_header():
     assert ctypes.sizeof(B.lr_rope_params) == 48 and ctypes.sizeof(B.lr_rotation) == 32
     assert ctypes.sizeof(B.lr_attention_plan) == 32
     assert ctypes.sizeof(B.lr_cache) == 4 * 8 + 3 * ctypes.sizeof(B.lr_layout) + 4 * 8
+
+
+def test_calls_of_nothing():
+    """Without a token or a sequence the arrays that have an entry for each may be absent."""
+    assert attend(batch=0, lens=None, table=None) == B.OK
+    assert attend(batch=0, lens=None) == B.OK and attend(batch=0, table=None) == B.OK
+    assert attend(batch=0, lens=None, table=None, q=None) == B.ERR_INVALID
+    assert attend(batch=0, lens=None, table=None, pages=0) == B.ERR_INVALID
+    assert rope(n=0, positions=None) == B.OK
+    assert rope(n=0, positions=None, turns=None) == B.ERR_INVALID and rope(n=0, positions=None, rot=66) == B.ERR_INVALID
+    L = lr.Layout("(64,2,10):(1,64,128)").c
+
+    def written(n, positions, turns=S):
+        return lr.lib().lr_cache_write(cache(), Y, L, 1280, Y + 0x100000, L, 1280, B.BF16, S if n else None, n,
+                                       B.lr_rotation(turns, positions, 64, 0, 1.0), None)
+    assert written(0, None) == B.OK and written(0, S) == B.OK
+    assert written(10, None) == B.ERR_INVALID and written(0, None, turns=None) == B.ERR_INVALID
