@@ -432,6 +432,14 @@ __global__ void __launch_bounds__(256) k_cache_read(CacheArgs a) {
   }
 }
 
+// Whether `bytes` at p overlap the cache's codes or its scales.
+static bool in_cache(const lr_cache* c, const void* p, int64_t bytes) {
+  const int64_t e = dtype_bytes(c->dtype);
+  if (overlap(p, bytes, c->k, c->k_capacity * e) || overlap(p, bytes, c->v, c->v_capacity * e)) return true;
+  return is_quantised(c->dtype) &&
+         (overlap(p, bytes, c->k_scale, c->scale_capacity * 4) || overlap(p, bytes, c->v_scale, c->scale_capacity * 4));
+}
+
 // The cache's own checks, and the part of the kernel arguments that comes from it.
 static int fill_cache(const lr_cache* c, CacheArgs* a) {
   if (!c || !c->k || !c->v) return LR_ERR_INVALID;
@@ -464,7 +472,11 @@ static int fill_cache(const lr_cache* c, CacheArgs* a) {
     const Mode h = mode_of(c->scale_layout, 0), p = mode_of(c->scale_layout, 1), g = mode_of(c->scale_layout, 2);
     if (h.size != heads || p.size != slots || g.size != pages) return LR_ERR_SIZE_MISMATCH;
     if (one_leaf(h, &a->sh) || one_leaf(p, &a->ss) || one_leaf(g, &a->sp)) return LR_ERR_INVALID;
-    if (overlap(c->k_scale, c->scale_capacity * 4, c->v_scale, c->scale_capacity * 4)) return LR_ERR_OVERLAP;
+    const int64_t bytes = c->scale_capacity * 4;
+    if (overlap(c->k_scale, bytes, c->v_scale, bytes)) return LR_ERR_OVERLAP;
+    for (const float* scale : {c->k_scale, c->v_scale})
+      if (overlap(scale, bytes, c->k, c->k_capacity * e) || overlap(scale, bytes, c->v, c->v_capacity * e))
+        return LR_ERR_OVERLAP;
   }
   a->heads = (uint32_t)heads;
   a->page_size = (uint32_t)slots;
@@ -481,7 +493,7 @@ static int fill_rows(const lr_cache* c, CacheArgs* a, const void* k, const lr_la
   const lr_layout* L[2] = {Lk, Lv};
   const void* p[2] = {k, v};
   const int64_t cap[2] = {k_capacity, v_capacity};
-  const int64_t e = dtype_bytes(dtype), ce = dtype_bytes(c->dtype);
+  const int64_t e = dtype_bytes(dtype);
   for (int i = 0; i < 2; ++i) {
     if (int rc = check_tensor(L[i], 3, cap[i], output)) return rc;
     CacheSide& s = a->side[i];
@@ -492,13 +504,9 @@ static int fill_rows(const lr_cache* c, CacheArgs* a, const void* k, const lr_la
     s.rh = mode_arg(h);
     s.rt = mode_arg(t);
     s.rows = const_cast<void*>(p[i]);
-    if (overlap(p[i], cap[i] * e, c->k, c->k_capacity * ce) || overlap(p[i], cap[i] * e, c->v, c->v_capacity * ce))
-      return LR_ERR_OVERLAP;
-    if (is_quantised(c->dtype) && (overlap(p[i], cap[i] * e, c->k_scale, c->scale_capacity * 4) ||
-                                   overlap(p[i], cap[i] * e, c->v_scale, c->scale_capacity * 4)))
-      return LR_ERR_OVERLAP;
+    if (in_cache(c, p[i], cap[i] * e) || (output && overlap(p[i], cap[i] * e, slots, n * 8))) return LR_ERR_OVERLAP;
   }
-  if (output && overlap(k, k_capacity * e, v, v_capacity * e)) return LR_ERR_OVERLAP;
+  if (output ? overlap(k, k_capacity * e, v, v_capacity * e) : in_cache(c, slots, n * 8)) return LR_ERR_OVERLAP;
   a->slots = slots;
   a->n = (uint32_t)n;
   return LR_OK;
@@ -589,6 +597,7 @@ int lr_cache_write(const lr_cache* c, const void* k, const lr_layout* Lk, int64_
   if (rc || (rc = fill_rows(c, &a, k, Lk, k_capacity, v, Lv, v_capacity, dtype, slots, n, false))) return rc;
   if (r) {
     if ((rc = check_rotation(r, a.side[0].dim, n))) return rc;
+    if (in_cache(c, r->positions, n * 8) || in_cache(c, r->turns, r->rot_dim * 4)) return LR_ERR_OVERLAP;
     a.side[0].rot = r->rot_dim;
     a.turns = r->turns;
     a.positions = r->positions;

@@ -233,6 +233,8 @@ int lr_rope(const void* x, const lr_layout* Lx, int64_t x_capacity, void* y, con
   // in place: each element is read and written by the same lane
   const bool in_place = x == y && same_leaves(xd, yd) && same_leaves(xh, yh) && same_leaves(xt, yt);
   if (!in_place && overlap(x, x_capacity * e, y, y_capacity * e)) return LR_ERR_OVERLAP;
+  if (overlap(r->positions, p_capacity * 8, y, y_capacity * e) || overlap(r->turns, r->rot_dim * 4, y, y_capacity * e))
+    return LR_ERR_OVERLAP;
   if (n == 0) return LR_OK;
   a.x = x;
   a.y = y;

@@ -274,3 +274,27 @@ def test_calls_of_nothing():
                                        B.lr_rotation(turns, positions, 64, 0, 1.0), None)
     assert written(0, None) == B.OK and written(0, S) == B.OK
     assert written(10, None) == B.ERR_INVALID and written(0, None, turns=None) == B.ERR_INVALID
+
+
+@pytest.mark.parametrize("at", [0, -8, 40])
+def test_overlap_of_outputs_with_indexes_and_tables(at):
+    """Positions, frequencies and slots are inputs too, and a cache's scales are no part of its codes."""
+    code = B.ERR_OVERLAP
+    assert rope(n=0, positions=Y + at) == code                       # 10 positions
+    assert rope(n=0, positions=Y + 5120) == B.OK and rope(n=0, positions=Y - 80) == B.OK
+    assert rope(n=0, turns=Y + at) == code                           # 32 frequencies
+    assert rope(n=0, turns=Y + 5120) == B.OK and rope(n=0, turns=Y - 256) == B.OK
+    assert rope(n=0, positions=Y + at, Lp="(5,2):(1,0)") == code
+    assert rope(n=0, x=Y, positions=Y + at) == code                  # in place
+    L = lr.Layout("(64,2,10):(1,64,128)").c
+
+    def written(slots=S, positions=S, turns=S, n=10):
+        return lr.lib().lr_cache_write(cache(), Y, L, 1280, Y + 0x100000, L, 1280, B.BF16, slots, n,
+                                       B.lr_rotation(turns, positions, 64, 0, 1.0), None)
+    for first in (X, V, W, W + 4096):                                # codes of keys and values, their scales
+        assert written(slots=first + at) == code and written(positions=first + at) == code
+        assert written(turns=first + at, n=0) == code
+    assert write(read=True, slots=Y + at) == code and write(read=True, slots=Y + 0x100000 + at) == code
+    for kw in (dict(ks=X + 16 + at), dict(vs=X + 16 + at), dict(ks=V + 16 + at), dict(vs=V + 16 + at)):
+        assert lr.lib().lr_cache_validate(cache(**kw)) == code
+    assert lr.lib().lr_cache_validate(cache(ks=X + 16384, vs=V + 16384)) == B.OK
