@@ -910,7 +910,7 @@ def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: 
         raise TypeError("q and out must have the same type")
     if page_table.dtype != torch.int32 or lens.dtype != torch.int32:
         raise TypeError("page_table and lens must be int32")
-    if page_table.get_device() != dev or page_table.dim() != 2 or page_table.stride(1) != 1:
+    if page_table.get_device() != dev or page_table.dim() != 2 or page_table.stride(1) != 1 < page_table.shape[1]:
         raise ValueError("page_table must be a 2-D GPU tensor with contiguous rows")
     batch, max_pages = lens.numel(), page_table.shape[1]
     if page_table.shape[0] < batch:

@@ -1092,3 +1092,16 @@ def test_calls_of_nothing(dev):
     torch.cuda.synchronize()
     assert (out == -7).all() and (y == -7).all() and (z == -7).all()
     assert torch.equal(cache.k.view(torch.int16), kept.view(torch.int16))
+
+
+def test_attention_table_of_one_page(dev):
+    """A table of one page a sequence has contiguous rows whatever its second stride says."""
+    lens = [3, 16, 9]
+    cache, table, slots, (kn, vn) = attention_case(dev, "bf16", "bf16", 4, 2, 64, 64, 16, "tokens", lens)
+    q = rand((3, 4, 64), torch.bfloat16, 1)
+    column = table[:, 0].contiguous().view(1, 3).t()
+    assert column.shape == (3, 1) and column.stride(1) != 1
+    out, lse = attend_all(dev, cache, column, q, 64, lens)
+    want, wlse, tol = attention64(q, [kn[u] for u in slots], [vn[u] for u in slots], 0.125, torch.bfloat16, "bf16")
+    close(out, want, tol)
+    close(lse, wlse, tol.lse)
