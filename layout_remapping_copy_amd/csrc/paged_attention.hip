@@ -41,7 +41,10 @@ struct AttentionArgs {
 // cut into blocks.  All blocks of all units, in order, are dealt out to `used` workgroups in equal runs:
 // workgroup w has the blocks [w T / used, (w + 1) T / used) of T.  A run that starts or ends inside a unit
 // leaves a part of it, joined by a second launch.  A unit of n blocks meets at most
-// 1 + ceil((n - 1) / min_share) runs, as none is shorter than min_share.
+// 1 + ceil((n - 1) / min_share) runs, as none is shorter than min_share.  That has to be at most `splits`, the
+// parts of a unit that the workspace has room for, so min_share grows with the longest unit that the page table
+// admits; where the lengths are far below it, fewer than all workgroups have a run (64 sequences of 1000 tokens, 32
+// heads on 8 of 128: 48 us under a table just wide enough, 127 with 63 runs under one for 131072 tokens).
 constexpr int64_t kRuns = 256;                     // one a CU
 constexpr uint32_t kBlock = 128, kWideBlock = 32;  // a step of four waves over tokens, or over heads
 

@@ -1105,3 +1105,34 @@ def test_attention_table_of_one_page(dev):
     want, wlse, tol = attention64(q, [kn[u] for u in slots], [vn[u] for u in slots], 0.125, torch.bfloat16, "bf16")
     close(out, want, tol)
     close(lse, wlse, tol.lse)
+
+
+WIDE_TABLES = [  # type, kind, heads, kv, dk, dv, page, order, lens, pages of the table, window
+    ("bf16", "bf16", 32, 8, 128, 128, 16, "tokens", [1000] * 64, 8192, 0),
+    ("bf16", "bf16", 32, 8, 128, 128, 16, "heads", [(i * 389) % 4097 for i in range(32)], 8192, 0),
+    ("fp16", "int8", 8, 2, 64, 64, 16, "heads", [(i * 389) % 900 for i in range(150)], 4096, 0),
+    ("fp32", "fp32", 8, 4, 64, 64, 16, "tokens", [(i * 389) % 900 for i in range(80)], 4096, 0),
+    ("bf16", "e4m3", 8, 8, 128, 128, 16, "tokens", [5000, 0, 1, 4999] * 10, 8192, 4000),
+    ("bf16", "bf16", 12, 3, 33, 17, 16, "tokens", [(i * 389) % 1200 for i in range(70)], 8192, 0),
+]
+
+
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,order,lens,width,window", WIDE_TABLES)
+def test_attention_wide_tables(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, width, window):
+    """Lengths far below the table's width: a run is then several blocks at least, the parts stay inside the
+    workspace, and what lies behind it stays as it was."""
+    t, b = T[dtype], len(lens)
+    cache, table, slots, (kn, vn) = attention_case(dev, dtype, kind, heads, kv, dk, dv, page, order, lens)
+    wide = torch.full((b, width), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    q = rand((b, heads, dk), t, 11)
+    need = lr.paged_attention_plan(f"({dk},{heads},{b}):(1,{dk},{heads * dk})", cache, f"({dv},{heads},{b}):(1,{dv},{heads * dv})",
+                                   width, t, window=window)
+    assert need["splits"] > 1
+    workspace = torch.full((need["workspace_bytes"] + 4096,), 0x5a, dtype=torch.uint8, device=dev)
+    out, lse = attend_all(dev, cache, wide, q, dv, lens, window=window, workspace=workspace)
+    seen = [u[max(0, len(u) - window):] if window else u for u in slots]
+    want, wlse, tol = attention64(q, [kn[u] for u in seen], [vn[u] for u in seen], dk ** -0.5, t, kind)
+    close(out, want, tol, "out")
+    close(lse, wlse, tol.lse, "lse")
+    assert (workspace[need["workspace_bytes"]:] == 0x5a).all()
