@@ -628,7 +628,7 @@ typedef enum {
 typedef struct {
   int32_t path;            /* lr_attention_path, for 16-byte aligned buffers */
   int32_t head_tiles;      /* workgroups that share the keys of one cache head */
-  int64_t chunk;           /* tokens of the longest sequence over splits, rounded up */
+  int64_t chunk;           /* tokens of the longest sequence over splits, rounded up (runs may be longer or shorter) */
   int64_t splits;          /* the most parts a sequence is cut into; 1: one launch, nothing to join */
   int64_t workspace_bytes; /* device memory lr_paged_attention needs; 0 when splits is 1 */
 } lr_attention_plan;
@@ -645,13 +645,14 @@ typedef struct {
  * LR_F16 or LR_BF16; the cache has the same type, or LR_E4M3 or LR_INT8.  lse (NULL: not wanted): device
  * float[batch][heads], log sum_t exp(scale * q . k), -inf with no token (and NaN, as out, where a score is).
  * The tokens of all sequences are dealt out to the workgroups in equal runs; what that cuts is joined by a second
- * launch.  The shortest run follows from max_pages (and window), as the workspace has room for plan.splits parts of a
- * sequence: a table much wider than lens asks for leaves part of the device without work.  workspace: device memory of at least the plan's workspace_bytes (LR_ERR_CAPACITY), 16-byte
- * aligned, its contents don't matter.  The result does not depend on timing: every sum has an order that
- * lens alone decides.
+ * launch.  The shortest run follows from max_pages (and window), as the workspace has room for plan.splits parts of
+ * a sequence: a table much wider than lens asks for leaves part of the device without work.  workspace: device
+ * memory of at least the plan's workspace_bytes (LR_ERR_CAPACITY), 16-byte aligned, its contents don't matter.  The
+ * result does not depend on timing: lens, max_pages, window and the layouts decide the order of every sum.
  * LR_ATTENTION_MATRIX multiplies values of an LR_F32 cache, or under LR_F32 queries, by weights of 32 bits; other
  * values by weights in two 16-bit parts, which hold 16 bits of each weight for LR_BF16 and 8-bit caches, and 22 for
- * LR_F16, down to 2^-32 of the largest.  Weights below 2^-126 of the largest are 0.  The totals that the sums are divided by have the whole weights. */
+ * LR_F16, down to 2^-32 of the largest.  Weights below 2^-126 of the largest are 0.  The totals that the sums are
+ * divided by have the whole weights. */
 int lr_paged_attention_plan(const lr_layout* Lq, const lr_cache* c, const lr_layout* Lo, int64_t max_pages,
                             int32_t dtype, int64_t window, lr_attention_plan* out);
 int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, const lr_cache* c,

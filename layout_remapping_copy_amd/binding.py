@@ -806,7 +806,7 @@ class PagedCache:
     """lr_cache over torch tensors: keys ``k`` of layout ``Lk`` and values ``v`` of layout ``Lv``, both
     (head_dim, heads, slots of a page, pages).  A float8_e4m3fn (or uint8) or int8 cache has float32
     scales ``k_scale`` and ``v_scale`` of layout ``Ls`` (heads, slots of a page, pages).  Holds the
-    tensors; checked once, here."""
+    tensors; checked here, and again by every call that takes it."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "c", "index", "dim")
 
@@ -902,7 +902,8 @@ def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: 
     heads, sequences); ``page_table``: int32 (sequences, pages of the longest), rows contiguous; ``lens``:
     int32, the tokens of each of the first len(lens) sequences.  ``scale``: 1/sqrt(head_dim) by default;
     ``window``: the last tokens seen, 0 for all; ``lse``: float32 (sequences, heads) to fill;
-    ``workspace``: a byte tensor of the plan's size, allocated on the stream if not given.  Returns out."""
+    ``workspace``: a byte tensor of the plan's size; if not given it is planned and allocated on the stream, which
+    costs the call a second plan.  Returns out."""
     torch = _torch()
     dev, code = cache.index, _dtype_code(q.dtype)
     _device_tensors(dev, "q out lens", q, out, lens)

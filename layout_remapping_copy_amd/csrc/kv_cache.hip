@@ -85,10 +85,10 @@ __device__ __forceinline__ bool place_of(const ChunkArgs& a, int64_t slot, uint3
   return held;
 }
 
-// V numbers, none infinite, as codes, exactly, without a division each.  p = x * (1 / scale), the reciprocal off by a step at
-// most, is within 3 steps of fp32 of the quotient.  A candidate T next to p is taken such that no tie but T itself
-// can lie between T and the quotient; the side of T that the quotient is on is the sign of x - T scale, which one
-// fma has right (T has 21 bits at most), and T moved a little to that side rounds as the quotient does.
+// V numbers, none infinite, as codes, exactly, without a division each.  p = x * (1 / scale), the reciprocal off by a
+// step at most, is within 3 steps of fp32 of the quotient.  A candidate T next to p is taken such that no tie but T
+// itself can lie between T and the quotient; the side of T that the quotient is on is the sign of x - T scale, which
+// one fma has right (T has 21 bits at most), and T moved a little to that side rounds as the quotient does.
 // Looking at ties only where p is near one is no cheaper: numbers of 16 bits often are simple parts of their row's
 // largest, which are ties or next to them (16389 tokens of fp16 stored: 26.9 us that way, 22.1 us this way).
 template <int DT, int CT, int V>
@@ -141,8 +141,8 @@ __device__ __forceinline__ float max_abs(float x, float y, float z) {
   return r;
 }
 
-// The largest x >= 0 (as its bits, which have the same order, NaN above all) over the `lanes` lanes, a power of two, of a row:
-// within 16 lanes by exchanges that are part of the instruction (neighbours, pairs, mirrors of 8 and 16).
+// The largest x >= 0 (as its bits, which have the same order, NaN above all) over the `lanes` lanes, a power of two,
+// of a row: within 16 lanes by exchanges that are part of the instruction (neighbours, pairs, mirrors of 8 and 16).
 __device__ __forceinline__ float row_max(float value, uint32_t lanes) {
   uint32_t x = __float_as_uint(value);
   if (lanes > 1) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xb1, 0xf, 0xf, true));
@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(256) k_cache_read_chunks(ChunkArgs a) {
   }
 }
 
-// Any strides and sizes (177 us and 1047 us for the two sizes above): one wave per row (token, head) of one side; a lane holds pairs lane, lane + 64, ...
+// Any strides and sizes (177 us and 1047 us for the two sizes above): one wave per row (token, head) of one side; a
+// lane holds pairs lane, lane + 64, ...
 template <int DT, int CT>
 __global__ void __launch_bounds__(256) k_cache_write(CacheArgs a) {
   using T = typename ElemOf<DT>::T;

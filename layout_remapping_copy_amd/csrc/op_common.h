@@ -177,7 +177,8 @@ __device__ __forceinline__ void sincos_turn(uint64_t t, float* sin_out, float* c
   const uint32_t hi = (uint32_t)(t >> 32) + ((uint32_t)t >> 31);
   const uint32_t q = (hi + 0x20000000u) >> 30;
   constexpr float kAngle = 1.4629180792671596e-09f;  // 2 pi / 2^32
-  const float x = __builtin_fmaf((float)(int32_t)(hi - (q << 30)), kAngle, (float)(int32_t)(uint32_t)t * (kAngle * 0x1p-32f));
+  const float low = (float)(int32_t)(uint32_t)t * (kAngle * 0x1p-32f);
+  const float x = __builtin_fmaf((float)(int32_t)(hi - (q << 30)), kAngle, low);
   const float z = x * x;
   const float s = x + x * z * (-1.f / 6 + z * (1.f / 120 + z * (-1.f / 5040 + z * (1.f / 362880))));
   const float c = 1.f + z * (-0.5f + z * (1.f / 24 + z * (-1.f / 720 + z * (1.f / 40320 + z * (-1.f / 3628800)))));

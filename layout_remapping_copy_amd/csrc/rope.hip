@@ -98,24 +98,24 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a) {
   using T = typename ElemOf<DT>::T;
   const uint64_t count = (uint64_t)a.heads * a.n * a.units;
   for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < count; at += (uint64_t)gridDim.x * 256) {
-  const uint64_t row = at / a.units;
-  const uint32_t u = (uint32_t)(at - row * a.units), t = (uint32_t)(row / a.heads), h = (uint32_t)(row % a.heads);
-  const T* x = (const T*)a.x + mode_offset(a.xh, h) + mode_offset(a.xt, t);
-  T* y = (T*)a.y + mode_offset(a.yh, h) + mode_offset(a.yt, t);
-  const uint32_t half = (uint32_t)a.rot / 2;
-  if (u >= half) {  // past the rotated part
-    for (uint32_t e = (uint32_t)a.rot + 2 * (u - half), k = 0; k < 2 && e < (uint32_t)a.dim; ++e, ++k)
-      y[(int64_t)e * a.yd] = x[(int64_t)e * a.xd];
-    continue;
-  }
-  const uint32_t i = a.pairs == LR_PAIRS_HALF ? u : 2 * u, j = a.pairs == LR_PAIRS_HALF ? u + half : 2 * u + 1;
-  float s, c;
-  sincos_turn((uint64_t)a.positions[mode_offset(a.p, t)] * (uint64_t)a.turns[u], &s, &c);
-  s *= a.magnitude * a.sign;
-  c *= a.magnitude;
-  const float v = value_of<DT>(x[(int64_t)i * a.xd]), w = value_of<DT>(x[(int64_t)j * a.xd]);
-  y[(int64_t)i * a.yd] = (T)(v * c - w * s);
-  y[(int64_t)j * a.yd] = (T)(w * c + v * s);
+    const uint64_t row = at / a.units;
+    const uint32_t u = (uint32_t)(at - row * a.units), t = (uint32_t)(row / a.heads), h = (uint32_t)(row % a.heads);
+    const T* x = (const T*)a.x + mode_offset(a.xh, h) + mode_offset(a.xt, t);
+    T* y = (T*)a.y + mode_offset(a.yh, h) + mode_offset(a.yt, t);
+    const uint32_t half = (uint32_t)a.rot / 2;
+    if (u >= half) {  // past the rotated part
+      for (uint32_t e = (uint32_t)a.rot + 2 * (u - half), k = 0; k < 2 && e < (uint32_t)a.dim; ++e, ++k)
+        y[(int64_t)e * a.yd] = x[(int64_t)e * a.xd];
+      continue;
+    }
+    const uint32_t i = a.pairs == LR_PAIRS_HALF ? u : 2 * u, j = a.pairs == LR_PAIRS_HALF ? u + half : 2 * u + 1;
+    float s, c;
+    sincos_turn((uint64_t)a.positions[mode_offset(a.p, t)] * (uint64_t)a.turns[u], &s, &c);
+    s *= a.magnitude * a.sign;
+    c *= a.magnitude;
+    const float v = value_of<DT>(x[(int64_t)i * a.xd]), w = value_of<DT>(x[(int64_t)j * a.xd]);
+    y[(int64_t)i * a.yd] = (T)(v * c - w * s);
+    y[(int64_t)j * a.yd] = (T)(w * c + v * s);
   }
 }
 
