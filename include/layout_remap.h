@@ -639,7 +639,7 @@ typedef struct {
  * limited to [0, max_pages * page_size].  Token t is slot t % page_size of page table[b * table_stride +
  * t / page_size]; the tokens of a page outside [0, pages) are left out.  A sequence with no token gives
  * zeros.  What the cache holds in other slots does not matter, NaN included; an infinite value that is seen
- * makes its element of out infinite, one of either sign NaN.
+ * makes its element of out infinite, one of either sign NaN (also one whose weight is 0, see below, but in LR_F16).
  * q, out: layouts (head_dim, heads, sequences), the first batch sequences used; heads a multiple of the
  * cache's; q's head_dim is the keys', out's the values', each at most 256.  dtype (of q and out): LR_F32,
  * LR_F16 or LR_BF16; the cache has the same type, or LR_E4M3 or LR_INT8.  lse (NULL: not wanted): device

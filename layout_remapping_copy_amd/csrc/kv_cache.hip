@@ -161,8 +161,9 @@ template <int CT> __device__ __forceinline__ float scale_of(float amax) {
   const float q = amax * kInv;
   return fmaxf(__builtin_fmaf(__builtin_fmaf(-kTop, q, amax), kInv, q), 0x1p-126f);
 }
-// 16389 tokens of 8 heads of 128 fp16, rotated and stored in e4m3 (102 MB moved): 22 us a call, 19 in the kernel, as
-// long as a copy of the same bytes; the vector units are busy 94 % of it.  65536 tokens: 79 us (5.2 TB/s).
+// 16389 tokens of 8 heads of 128 fp16, rotated and stored in e4m3 (102 MB moved): 20 us, as long as
+// a copy of the same bytes; the vector units are busy 96 % of it.  65536 tokens: 79 us (5.2 TB/s); the same many from
+// fp32, not rotated, 131 us, and of bf16 into a bf16 cache, rotated, 102 us (5.2 and 5.3 TB/s).
 //
 // Rows in chunks: a lane has one unit of a token's rows, its angles in registers for `per_lane` heads; the
 // lanes of a row (a power of two next to each other) find its largest value by exchange.  A row that holds an
@@ -268,8 +269,8 @@ __global__ void __launch_bounds__(256) k_cache_write_chunks(ChunkArgs a) {
 }
 
 // Rows in chunks, the other way: codes times their scale, or the elements as they are.  131072 tokens of 8 heads of
-// 128 e4m3 to bf16 (814 MB moved): 145 us, 5.6 TB/s, bound by memory (119 us at a plain copy's rate; the codes come
-// in runs of 512 bytes).  Four heads in flight instead of two: 159 us.
+// 128 e4m3 to bf16 (814 MB moved): 146 us, 5.6 TB/s, bound by memory (119 us at a plain copy's rate; the codes come
+// in runs of 512 bytes).  From a bf16 cache (1.07 GB): 184 us, 5.8 TB/s.  Four heads in flight instead of two: 159 us.
 template <int DT, int CT, int V, bool NT>
 __global__ void __launch_bounds__(256) k_cache_read_chunks(ChunkArgs a) {
   using T = typename ElemOf<DT>::T;

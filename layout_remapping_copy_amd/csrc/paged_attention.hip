@@ -428,8 +428,10 @@ struct MatrixShape {
 // transposed within the lane by byte permutes; the output's column 8 r + m is then row r of product m.
 //
 // What bounds it is the reading of the cache: 64 sequences of up to 16384 bf16 tokens, 64 query heads on 8 of 128
-// (2.15 GB) take 338 us, 6.4 TB/s, and 2 of 131071 e4m3 tokens 90 us, 6.2 TB/s, where a bare streaming read reaches
-// 7.2 (299 and 77 us).  The vector units are busy 15 % of the first, 38 % of the second, with the matrix units' part.
+// (2.15 GB) take 352 us a call, 6.1 TB/s, and 2 of 131071 e4m3 tokens 97 us, 5.7 TB/s, where a bare streaming read
+// reaches 7.2 (299 and 77 us); as many fp16 tokens 352 us, 2.21 GB of fp32 (32 sequences, 32 heads) 363 us, 6.1 TB/s,
+// and fp32 queries over 0.57 GB of e4m3 234 us, 2.4 TB/s, where the fp32 products are the bound.  The vector units are
+// busy 19 % of the first, 37 % of the second, with the matrix units' part.
 // One workgroup a CU keeps enough loads under way; two and three a CU (512 and 768 runs) took 359 and 367 us against
 // 353, as more rows of memory are open at once.  Plain loads took 20 % longer than streaming ones.
 template <int DT, int CT, int DC, int HT, bool by_heads>

@@ -31,10 +31,10 @@ struct RopeChunkArgs {
 
 // Rows in chunks of V elements: a lane has one unit of a token's rows, computes its V angles once and turns
 // `per_lane` heads with them, their loads two at a time ahead of the arithmetic.  An angle costs some 40
-// instructions, a pair's turn 6: over 8 heads the arithmetic is 38 % of the vector units' time and memory the bound.
-// 16 x 4096 x 32 x 128 bf16, heads regrouped on the way (1 GiB moved): 178 us, 6.0 TB/s, against 157 for a plain
-// copy and 170 for the same regrouping without arithmetic.  Eight tokens of one step: 3.7 us, two dependent reads
-// of memory after the arguments'; a call is 6.5 us of the host.
+// instructions, a pair's turn 6: over 8 heads the arithmetic is 37 % of the vector units' time and memory the bound.
+// 16 x 4096 x 32 x 128 bf16, heads regrouped on the way (1 GiB moved): 179 us, 6.0 TB/s, against 157 for a plain
+// copy and 170 for the same regrouping without arithmetic.  Eight tokens of one step: 4.2 us, two dependent reads
+// of memory after the arguments'; a call is 6.9 us of the host.
 template <int DT, int V, bool NT>
 __global__ void __launch_bounds__(256) k_rope_chunks(RopeChunkArgs a) {
   using T = typename ElemOf<DT>::T;
