@@ -581,6 +581,43 @@ int lr_rope(const void* x, const lr_layout* Lx, int64_t x_capacity, void* y, con
             int64_t y_capacity, int32_t dtype, const lr_rotation* r, const lr_layout* Lp, int64_t p_capacity,
             int64_t n, uint32_t flags, void* stream);
 
+/* Rotary positions with several axes (time, height and width of a video, rows and columns of an image): a token has
+ * a position on each axis, and each pair of a head turns by the position on its own axis. */
+
+/* Which pairs an axis has, by sections[a], the pairs of axis a (their sum is rot_dim/2). */
+typedef enum {
+  LR_AXES_BLOCKS = 0, /* the first sections[0] pairs are axis 0, the next sections[1] axis 1, ... */
+  LR_AXES_CYCLIC = 1  /* pair i is axis i mod axes if that is not 0 and i < axes * sections[i mod axes], else axis 0 */
+} lr_axes_order;
+
+/* Which frequencies its pairs have. */
+typedef enum {
+  LR_AXES_SHARED = 0, /* pair i has w_i of a rotation of rot_dim elements */
+  LR_AXES_OWN = 1     /* the j-th pair of axis a has w_j of a rotation of 2 * sections[a] elements */
+} lr_axes_spectrum;
+
+/* The tables of such a rotation (host only): turns as lr_rope_table's, axis[i] the axis of pair i, both of
+ * rot_dim/2 entries, kept by the caller in device memory.  axes: 1 .. 4; a section may be 0. */
+int lr_rope_axes_table(const lr_rope_params* p, const int32_t* sections, int32_t axes, int32_t order,
+                       int32_t spectrum, int64_t* turns, int32_t* axis, double* magnitude);
+
+typedef struct {
+  const int64_t* turns;     /* device, rot_dim/2 entries */
+  const int32_t* axis;      /* device, rot_dim/2 entries; one outside [0, axes) counts as axis 0 */
+  const int64_t* positions; /* device, any int64 values */
+  int32_t rot_dim;
+  int32_t pairs;            /* lr_pairs */
+  int32_t axes;             /* 1 .. 4 */
+  float magnitude;
+} lr_axes_rotation;
+
+/* lr_rope with A = positions[Lp(t, axis[pair])] * w.  Lp: layout (tokens (leaves), axes) of p_capacity entries; NULL:
+ * positions[a * n + t] for the n tokens of the call.  Everything else as lr_rope, the gradient with LR_ROPE_BACKWARD
+ * included. */
+int lr_rope_axes(const void* x, const lr_layout* Lx, int64_t x_capacity, void* y, const lr_layout* Ly,
+                 int64_t y_capacity, int32_t dtype, const lr_axes_rotation* r, const lr_layout* Lp,
+                 int64_t p_capacity, int64_t n, uint32_t flags, void* stream);
+
 /* A paged cache of keys and values: tensors of layout (head_dim, heads, slots of a page, pages), so any
  * order of heads and slots inside a page, and any padding, is a layout.  Token slot s of a cache is
  * slot s % page_size of page s / page_size.  An LR_E4M3 or LR_INT8 cache holds codes and, for each slot
@@ -611,6 +648,11 @@ int lr_cache_validate(const lr_cache* c);
 int lr_cache_write(const lr_cache* c, const void* k, const lr_layout* Lk, int64_t k_capacity, const void* v,
                    const lr_layout* Lv, int64_t v_capacity, int32_t dtype, const int64_t* slots, int64_t n,
                    const lr_rotation* r, void* stream);
+
+/* lr_cache_write with keys rotated by positions on several axes, positions[a * n + t] (r is not NULL here). */
+int lr_cache_write_axes(const lr_cache* c, const void* k, const lr_layout* Lk, int64_t k_capacity, const void* v,
+                        const lr_layout* Lv, int64_t v_capacity, int32_t dtype, const int64_t* slots, int64_t n,
+                        const lr_axes_rotation* r, void* stream);
 
 /* Read the slots slots[0..n) back: k and v (layouts as lr_cache_write) receive code * scale, or the
  * stored elements; a slot outside the cache gives zeros. */

@@ -176,6 +176,8 @@ INT8 = 4
 # lr_pairs, lr_rope_scaling, lr_attention_path
 PAIRS = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3, "bands": 4}
+AXES_ORDER = {"blocks": 0, "cyclic": 1}
+MAX_AXES = 4
 ATTENTION_PATH_NAMES = {0: "element", 1: "matrix"}
 ROPE_BACKWARD = 0x1
 
@@ -198,6 +200,18 @@ class lr_rotation(ctypes.Structure):
         ("positions", ctypes.c_void_p),
         ("rot_dim", ctypes.c_int32),
         ("pairs", ctypes.c_int32),
+        ("magnitude", ctypes.c_float),
+    ]
+
+
+class lr_axes_rotation(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_void_p),
+        ("axis", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int32),
+        ("pairs", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
         ("magnitude", ctypes.c_float),
     ]
 
@@ -282,6 +296,15 @@ _SIGS = {
     "lr_rope": (ctypes.c_int, [ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, _L, ctypes.c_int64,
                                ctypes.c_int32, _P(lr_rotation), _L, ctypes.c_int64, ctypes.c_int64, ctypes.c_uint32,
                                ctypes.c_void_p]),
+    "lr_rope_axes_table": (ctypes.c_int, [_P(lr_rope_params), _P(ctypes.c_int32), ctypes.c_int32, ctypes.c_int32,
+                                          ctypes.c_int32, _P(ctypes.c_int64), _P(ctypes.c_int32),
+                                          _P(ctypes.c_double)]),
+    "lr_rope_axes": (ctypes.c_int, [ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, _L, ctypes.c_int64,
+                                    ctypes.c_int32, _P(lr_axes_rotation), _L, ctypes.c_int64, ctypes.c_int64,
+                                    ctypes.c_uint32, ctypes.c_void_p]),
+    "lr_cache_write_axes": (ctypes.c_int, [_P(lr_cache), ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, _L,
+                                           ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                           _P(lr_axes_rotation), ctypes.c_void_p]),
     "lr_cache_validate": (ctypes.c_int, [_P(lr_cache)]),
     "lr_cache_write": (ctypes.c_int, [_P(lr_cache), ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, _L,
                                       ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
@@ -740,7 +763,8 @@ def _dtype_code(dtype) -> int:
 
 
 def _device_tensors(index, names, *tensors):
-    """Every tensor contiguous and on GPU `index` (None: any one GPU); `names`: their names, space-separated."""
+    """Every tensor contiguous and on GPU `index` (None: any one GPU); `names`: their names, space-separated.
+    Returns the GPU."""
     if index is None:
         index = tensors[0].get_device()
     for t in tensors:
@@ -751,6 +775,28 @@ def _device_tensors(index, names, *tensors):
             if not t.is_contiguous():
                 raise ValueError(f"{what} must be contiguous")
             raise ValueError(f"{what} is on {t.device}, not on cuda:{index}")
+    return index
+
+
+class _Here:
+    """The context of a call on the current device: nothing to change, and nothing to pay."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *_):
+        pass
+
+
+_HERE = _Here()
+
+
+def _on_device(index: int):
+    """A context in which GPU `index` is the current one, so that the call's stream and kernels are that GPU's."""
+    torch = _torch()
+    if torch._C._cuda_getDevice() == index:
+        return _HERE
+    return torch.cuda.device(index)
 
 
 class RopeTable:
@@ -799,6 +845,74 @@ def rope(x, Lx, y, Ly, positions, table: RopeTable, pairs: str = "half", backwar
     _check(lib().lr_rope(x.data_ptr(), Lx.c, x.numel(), y.data_ptr(), Ly.c, y.numel(), _dtype_code(x.dtype),
                          _rotation(table, positions, pairs), _as_layout(Lp).c if Lp is not None else None, count, n,
                          ROPE_BACKWARD if backward else 0, _stream_ptr(stream)), "rope")
+    return y
+
+
+class RopeAxesTable:
+    """The frequencies of a rotation with several axes and each pair's axis in device memory (lr_rope_axes_table),
+    kept by the caller."""
+
+    __slots__ = ("turns", "axis", "rot_dim", "axes", "magnitude")
+
+    def __init__(self, turns, axis, rot_dim: int, axes: int, magnitude: float):
+        self.turns, self.axis, self.rot_dim, self.axes, self.magnitude = turns, axis, rot_dim, axes, magnitude
+
+
+def rope_axes_table(rot_dim: int, sections: Sequence[int], order: str = "blocks", own: bool = False,
+                    base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original_len: float = 0.0,
+                    low: float = 1.0, high: float = 32.0, device="cuda") -> RopeAxesTable:
+    """lr_rope_axes_table: the tables for rotations of the first ``rot_dim`` elements of a head by positions on
+    len(sections) axes, of which axis a has ``sections[a]`` pairs.  ``order``: "blocks" or "cyclic" (lr_axes_order);
+    ``own``: each axis has the frequencies of a rotation of its own pairs alone, otherwise they run on over all
+    pairs.  The rest as rope_table."""
+    torch = _torch()
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling {scaling!r} is none of {sorted(ROPE_SCALING)}")
+    if order not in AXES_ORDER:
+        raise ValueError(f"order {order!r} is neither 'blocks' nor 'cyclic'")
+    p = lr_rope_params(rot_dim, ROPE_SCALING[scaling], base, factor, original_len, low, high)
+    pairs = max(1, min(rot_dim, 1024) // 2)
+    turns, axis = (ctypes.c_int64 * pairs)(), (ctypes.c_int32 * pairs)()
+    m = ctypes.c_double()
+    axes = len(sections)
+    _check(lib().lr_rope_axes_table(ctypes.byref(p), (ctypes.c_int32 * max(1, axes))(*sections), axes,
+                                    AXES_ORDER[order], int(own), turns, axis, ctypes.byref(m)), "rope_axes_table")
+    return RopeAxesTable(torch.tensor(list(turns), dtype=torch.int64).to(device),
+                         torch.tensor(list(axis), dtype=torch.int32).to(device), rot_dim, axes, m.value)
+
+
+def _axes_rotation(table: RopeAxesTable, positions, pairs: str) -> lr_axes_rotation:
+    if pairs not in PAIRS:
+        raise ValueError(f"pairs {pairs!r} is neither 'half' nor 'interleaved'")
+    if positions.dtype != table.turns.dtype:
+        raise TypeError("positions must be int64")
+    return lr_axes_rotation(table.turns.data_ptr(), table.axis.data_ptr(), positions.data_ptr(), table.rot_dim,
+                            PAIRS[pairs], table.axes, table.magnitude)
+
+
+def rope_axes(x, Lx, y, Ly, positions, table: RopeAxesTable, pairs: str = "half", backward: bool = False, Lp=None,
+              n: Optional[int] = None, stream=None):
+    """lr_rope_axes: rope by positions on several axes.  ``positions``: int64, (axes, tokens of the call), or one per
+    offset of the layout ``Lp`` (tokens, axes); ``n``: the first n tokens only (with ``Lp``).  Returns y."""
+    index = _device_tensors(None, "x y positions table axes", x, y, positions, table.turns, table.axis)
+    if x.dtype != y.dtype:
+        raise TypeError("x and y must have the same type")
+    Lx, Ly = _as_layout(Lx), _as_layout(Ly)
+    count = positions.numel()
+    if Lp is None:
+        if positions.dim() != 2 or positions.shape[0] != table.axes:
+            raise ValueError("positions must be (axes, tokens)")
+        if n is not None and n != positions.shape[1]:
+            raise ValueError("without Lp positions has one entry per axis and token of the call")
+        n = positions.shape[1]
+    else:
+        Lp = _as_layout(Lp)
+        if n is None:
+            n = _mode_size(Lp.c, 0)
+    with _on_device(index):
+        _check(lib().lr_rope_axes(x.data_ptr(), Lx.c, x.numel(), y.data_ptr(), Ly.c, y.numel(), _dtype_code(x.dtype),
+                                  _axes_rotation(table, positions, pairs), Lp.c if Lp is not None else None, count, n,
+                                  ROPE_BACKWARD if backward else 0, _stream_ptr(stream)), "rope_axes")
     return y
 
 
@@ -860,6 +974,27 @@ def cache_write(cache: PagedCache, k, Lk, v, Lv, slots, table: Optional[RopeTabl
     Lk, Lv = _as_layout(Lk), _as_layout(Lv)
     _check(lib().lr_cache_write(cache.c, k.data_ptr(), Lk.c, k.numel(), v.data_ptr(), Lv.c, v.numel(),
                                 _dtype_code(k.dtype), slots.data_ptr(), n, r, _stream_ptr(stream)), "cache_write")
+    return cache
+
+
+def cache_write_axes(cache: PagedCache, k, Lk, v, Lv, slots, table: RopeAxesTable, positions, pairs: str = "half",
+                     stream=None):
+    """lr_cache_write_axes: cache_write with keys rotated by ``positions`` (axes, len(slots)) on several axes.
+    Returns the cache."""
+    _device_tensors(cache.index, "k v slots positions table axes", k, v, slots, positions, table.turns, table.axis)
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must have the same type")
+    if slots.dtype != _torch().int64:
+        raise TypeError("slots must be int64")
+    n = slots.numel()
+    if tuple(positions.shape) != (table.axes, n):
+        raise ValueError("positions must be (axes, slots)")
+    Lk, Lv = _as_layout(Lk), _as_layout(Lv)
+    with _on_device(cache.index):
+        _check(lib().lr_cache_write_axes(cache.c, k.data_ptr(), Lk.c, k.numel(), v.data_ptr(), Lv.c, v.numel(),
+                                         _dtype_code(k.dtype), slots.data_ptr(), n,
+                                         _axes_rotation(table, positions, pairs), _stream_ptr(stream)),
+               "cache_write_axes")
     return cache
 
 

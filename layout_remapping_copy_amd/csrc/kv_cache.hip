@@ -1,9 +1,11 @@
-// The paged cache of keys and values: lr_cache_validate, lr_cache_write, lr_cache_read.
+// The paged cache of keys and values: lr_cache_validate, lr_cache_write, lr_cache_write_axes, lr_cache_read.
 #include "op_common.h"
 
 namespace lr {
 
 int check_rotation(const lr_rotation* r, int64_t dim, int64_t n);
+int check_axes(const lr_axes_rotation& r, int64_t n, AxesArg* out);
+lr_rotation rotation_of(const lr_axes_rotation& r);
 
 constexpr int kCacheDim = 512;  // head_dim at most
 
@@ -27,6 +29,7 @@ struct CacheArgs {
   int32_t pairs;
   int64_t cache_slots;
   uint32_t page_size, heads, n;
+  AxesArg axes;
 };
 
 // The code nearest x / scale, exactly: the fp32 quotient's remainder says which side of
@@ -74,6 +77,7 @@ struct ChunkArgs {
   uint32_t page_size, heads, n;
   float magnitude;
   int32_t pairs;
+  AxesArg axes;
 };
 
 // Page and slot of a token's place; false for none.
@@ -168,7 +172,7 @@ template <int CT> __device__ __forceinline__ float scale_of(float amax) {
 // Rows in chunks: a lane has one unit of a token's rows, its angles in registers for `per_lane` heads; the
 // lanes of a row (a power of two next to each other) find its largest value by exchange.  A row that holds an
 // infinity or a NaN is told by that value, and is done again with the care that it needs.
-template <int DT, int CT, int V, bool NT>
+template <int DT, int CT, int V, bool NT, bool AXES>
 __global__ void __launch_bounds__(256) k_cache_write_chunks(ChunkArgs a) {
   using T = typename ElemOf<DT>::T;
   using C = typename ElemOf<CT>::T;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(256) k_cache_write_chunks(ChunkArgs a) {
   };
   load(h);
   float c[V], s[V];
-  if (turned) angles_of<V>(a.turns, a.positions[t], u, sd.un.rot, half, a.magnitude, 1.f, c, s);
+  if (turned) angles_of<V, AXES>(a.turns, a.positions + t, a.axes, u, sd.un.rot, half, a.magnitude, 1.f, c, s);
   for (uint32_t n = 0; n < count; ++n, h += step) {
     const bool mine = held && h < a.heads;
     v = vn, w = wn;
@@ -374,7 +378,12 @@ __global__ void __launch_bounds__(256) k_cache_write(CacheArgs a) {
       float p = value_of<DT>(x[(int64_t)i * s.rd]), q = j < (uint32_t)s.dim ? value_of<DT>(x[(int64_t)j * s.rd]) : 0.f;
       if (turned) {
         float sn, cs;
-        sincos_turn((uint64_t)a.positions[t] * (uint64_t)a.turns[u], &sn, &cs);
+        int64_t at = t;
+        if (a.axes.axis) {
+          const int32_t axis = a.axes.axis[u];
+          at += (uint32_t)axis < (uint32_t)a.axes.axes ? axis * a.axes.stride : 0;
+        }
+        sincos_turn((uint64_t)a.positions[at] * (uint64_t)a.turns[u], &sn, &cs);
         sn *= a.magnitude;
         cs *= a.magnitude;
         const float w = p * cs - q * sn;
@@ -577,7 +586,65 @@ static int fill_chunks(const lr_cache* c, const CacheArgs& a, const lr_layout* L
   k->n = a.n;
   k->magnitude = a.magnitude;
   k->pairs = a.pairs;
+  k->axes = a.axes;
   return row_grid_fits(k->grid) ? v : 0;
+}
+
+template <int D, int C, bool AXES>
+static int launch_write(const ChunkArgs& a, int wide, bool nt, hipStream_t st) {
+  const dim3 grid(a.grid.blocks_x, a.grid.blocks_y, 2);
+  if constexpr (D != LR_F32) {
+    if (wide == 8) {
+      if (nt)
+        hipLaunchKernelGGL((k_cache_write_chunks<D, C, 8, true, AXES>), grid, dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL((k_cache_write_chunks<D, C, 8, false, AXES>), grid, dim3(256), 0, st, a);
+      return check_op_launch();
+    }
+  }
+  if (nt)
+    hipLaunchKernelGGL((k_cache_write_chunks<D, C, 4, true, AXES>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_cache_write_chunks<D, C, 4, false, AXES>), grid, dim3(256), 0, st, a);
+  return check_op_launch();
+}
+
+// lr_cache_write, and with `ax` lr_cache_write_axes: r is then its frequencies.
+static int write_call(const lr_cache* c, const void* k, const lr_layout* Lk, int64_t k_capacity, const void* v,
+                      const lr_layout* Lv, int64_t v_capacity, int32_t dtype, const int64_t* slots, int64_t n,
+                      const lr_rotation* r, const lr_axes_rotation* ax, void* stream) {
+  CacheArgs a;
+  int rc = fill_cache(c, &a);
+  if (rc || (rc = fill_rows(c, &a, k, Lk, k_capacity, v, Lv, v_capacity, dtype, slots, n, false))) return rc;
+  if (r) {
+    if ((rc = check_rotation(r, a.side[0].dim, n))) return rc;
+    if (ax && (rc = check_axes(*ax, n, &a.axes))) return rc;
+    if (in_cache(c, r->positions, n * 8 * (ax ? ax->axes : 1)) || in_cache(c, r->turns, r->rot_dim * 4))
+      return LR_ERR_OVERLAP;
+    if (ax && in_cache(c, ax->axis, ax->rot_dim * 2)) return LR_ERR_OVERLAP;
+    a.side[0].rot = r->rot_dim;
+    a.turns = r->turns;
+    a.positions = r->positions;
+    a.pairs = r->pairs;
+    a.magnitude = r->magnitude;
+  }
+  if (n == 0) return LR_OK;
+  const hipStream_t st = (hipStream_t)stream;
+  ChunkArgs chunks;
+  double bytes;
+  const int wide = fill_chunks(c, a, Lk, Lv, dtype, true, &chunks, &bytes);
+  const bool nt = bytes > kStreamBytes;
+  if (wide)
+    return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
+      constexpr int D = decltype(dt)::value, C = decltype(ct)::value;
+      return ax ? launch_write<D, C, true>(chunks, wide, nt, st) : launch_write<D, C, false>(chunks, wide, nt, st);
+    });
+  const int64_t rows = 2 * n * (int64_t)a.heads, groups = std::min<int64_t>((rows + 3) / 4, 1 << 22);
+  return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
+    hipLaunchKernelGGL((k_cache_write<decltype(dt)::value, decltype(ct)::value>), dim3((unsigned)groups), dim3(256), 0,
+                       st, a);
+    return check_op_launch();
+  });
 }
 
 }  // namespace lr
@@ -594,49 +661,15 @@ int lr_cache_validate(const lr_cache* c) {
 int lr_cache_write(const lr_cache* c, const void* k, const lr_layout* Lk, int64_t k_capacity, const void* v,
                    const lr_layout* Lv, int64_t v_capacity, int32_t dtype, const int64_t* slots, int64_t n,
                    const lr_rotation* r, void* stream) {
-  CacheArgs a;
-  int rc = fill_cache(c, &a);
-  if (rc || (rc = fill_rows(c, &a, k, Lk, k_capacity, v, Lv, v_capacity, dtype, slots, n, false))) return rc;
-  if (r) {
-    if ((rc = check_rotation(r, a.side[0].dim, n))) return rc;
-    if (in_cache(c, r->positions, n * 8) || in_cache(c, r->turns, r->rot_dim * 4)) return LR_ERR_OVERLAP;
-    a.side[0].rot = r->rot_dim;
-    a.turns = r->turns;
-    a.positions = r->positions;
-    a.pairs = r->pairs;
-    a.magnitude = r->magnitude;
-  }
-  if (n == 0) return LR_OK;
-  const hipStream_t st = (hipStream_t)stream;
-  ChunkArgs chunks;
-  double bytes;
-  const int wide = fill_chunks(c, a, Lk, Lv, dtype, true, &chunks, &bytes);
-  const bool nt = bytes > kStreamBytes;
-  if (wide)
-    return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
-      constexpr int D = decltype(dt)::value, C = decltype(ct)::value;
-      const dim3 grid(chunks.grid.blocks_x, chunks.grid.blocks_y, 2);
-      if constexpr (D != LR_F32) {
-        if (wide == 8) {
-          if (nt)
-            hipLaunchKernelGGL((k_cache_write_chunks<D, C, 8, true>), grid, dim3(256), 0, st, chunks);
-          else
-            hipLaunchKernelGGL((k_cache_write_chunks<D, C, 8, false>), grid, dim3(256), 0, st, chunks);
-          return check_op_launch();
-        }
-      }
-      if (nt)
-        hipLaunchKernelGGL((k_cache_write_chunks<D, C, 4, true>), grid, dim3(256), 0, st, chunks);
-      else
-        hipLaunchKernelGGL((k_cache_write_chunks<D, C, 4, false>), grid, dim3(256), 0, st, chunks);
-      return check_op_launch();
-    });
-  const int64_t rows = 2 * n * (int64_t)a.heads, groups = std::min<int64_t>((rows + 3) / 4, 1 << 22);
-  return with_types(dtype, c->dtype, [&](auto dt, auto ct) {
-    hipLaunchKernelGGL((k_cache_write<decltype(dt)::value, decltype(ct)::value>), dim3((unsigned)groups), dim3(256), 0,
-                       st, a);
-    return check_op_launch();
-  });
+  return write_call(c, k, Lk, k_capacity, v, Lv, v_capacity, dtype, slots, n, r, nullptr, stream);
+}
+
+int lr_cache_write_axes(const lr_cache* c, const void* k, const lr_layout* Lk, int64_t k_capacity, const void* v,
+                        const lr_layout* Lv, int64_t v_capacity, int32_t dtype, const int64_t* slots, int64_t n,
+                        const lr_axes_rotation* r, void* stream) {
+  if (!r) return LR_ERR_INVALID;
+  const lr_rotation one = rotation_of(*r);
+  return write_call(c, k, Lk, k_capacity, v, Lv, v_capacity, dtype, slots, n, &one, r, stream);
 }
 
 int lr_cache_read(const lr_cache* c, const int64_t* slots, int64_t n, void* k, const lr_layout* Lk, int64_t k_capacity,

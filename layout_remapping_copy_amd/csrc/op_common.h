@@ -230,15 +230,46 @@ template <bool NT, class Vec> __device__ __forceinline__ void store_chunk(void* 
 // with plain accesses and 14.4 with streaming ones when the caches hold them (17 either way when not).
 constexpr double kStreamBytes = 256.0 * (1 << 20);
 
+// Positions on several axes: pair i turns by the position on axis[i], whose positions lie `stride` after the axis before.
+constexpr int kMaxAxes = 4;
+struct AxesArg {
+  const int32_t* axis;  // of each pair; null for one axis
+  int64_t stride;
+  int32_t axes;
+};
+// A token's positions on all axes, read side by side: reading the one that a pair asks for would wait for its axis first.
+struct AxisPositions {
+  int64_t p[kMaxAxes];
+  __device__ __forceinline__ int64_t of(int32_t axis) const {  // the first one's for an axis that is none
+    int64_t x = p[0];
+#pragma unroll
+    for (int k = 1; k < kMaxAxes; ++k) x = axis == k ? p[k] : x;
+    return x;
+  }
+};
+__device__ __forceinline__ AxisPositions axis_positions(const int64_t* first, const AxesArg& x) {
+  AxisPositions r;
+#pragma unroll
+  for (int k = 0; k < kMaxAxes; ++k) r.p[k] = first[k < x.axes ? k * x.stride : 0];
+  return r;
+}
+
 // cos and sin of the angles of one unit's V pairs: pair k of a half layout is element k of both chunks, pairs
-// of an interleaved one lie inside the first chunk, then the second.
-template <int V>
-__device__ __forceinline__ void angles_of(const int64_t* turns, int64_t position, uint32_t u, int32_t rot, bool half,
-                                          float magnitude, float sign, float* c, float* s) {
+// of an interleaved one lie inside the first chunk, then the second.  `position`: the token's first.
+template <int V, bool AXES>
+__device__ __forceinline__ void angles_of(const int64_t* turns, const int64_t* position, const AxesArg& x, uint32_t u,
+                                          int32_t rot, bool half, float magnitude, float sign, float* c, float* s) {
+  AxisPositions p;
+  int64_t one = 0;
+  if constexpr (AXES)
+    p = axis_positions(position, x);
+  else
+    one = *position;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const uint32_t pair = half ? u * V + k : u * (V / 2) + (k < V / 2 ? k : rot / 4 + k - V / 2);
-    sincos_turn((uint64_t)position * (uint64_t)turns[pair], &s[k], &c[k]);
+    if constexpr (AXES) one = p.of(x.axis[pair]);
+    sincos_turn((uint64_t)one * (uint64_t)turns[pair], &s[k], &c[k]);
     s[k] *= magnitude * sign;
     c[k] *= magnitude;
   }

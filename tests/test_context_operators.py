@@ -1,0 +1,166 @@
+"""Host side of the operators for long and many-sided contexts (no GPU): the tables of positions with several axes,
+the plans, and every refusal.
+
+Refusals are checked before anything is launched, so made-up pointers do: nothing is read through them.
+"""
+
+import ctypes
+import math
+
+import pytest
+
+import layout_remapping_copy_amd as lr
+from layout_remapping_copy_amd import binding as B
+
+torch = pytest.importorskip("torch")
+
+
+# -------------------------------------------------------------------------------- tables of several axes
+def plain_turns(rot, **kw):
+    return lr.rope_table(rot, device="cpu", **kw).turns.tolist()
+
+
+def axis_of(i, sections, order):
+    """The axis of pair i, straight from the definition."""
+    if order == "blocks":
+        return next(a for a in range(len(sections)) if i < sum(sections[:a + 1]))
+    a = i % len(sections)
+    return a if a and i < len(sections) * sections[a] else 0
+
+
+@pytest.mark.parametrize("order", ["blocks", "cyclic"])
+@pytest.mark.parametrize("sections", [[8], [24, 20, 20], [16, 24, 24], [3, 2, 2], [1, 1], [20, 20], [4, 0, 3], [2, 1, 1, 1],
+                                      [256, 128, 128], [0, 5]])
+def test_axes_tables(sections, order):
+    rot = 2 * sum(sections)
+    if order == "cyclic" and any(s and a + (s - 1) * len(sections) >= rot // 2 for a, s in enumerate(sections) if a):
+        with pytest.raises(lr.LayoutRemapError):
+            lr.rope_axes_table(rot, sections, order=order, device="cpu")
+        return
+    want = [axis_of(i, sections, order) for i in range(rot // 2)]
+    assert [want.count(a) for a in range(len(sections))] == sections
+    kw = dict(base=500000.0, scaling="bands", factor=4.0, original_len=8192, low=1.0, high=4.0)
+    t = lr.rope_axes_table(rot, sections, order=order, device="cpu", **kw)
+    assert t.axis.tolist() == want and t.axes == len(sections) and t.rot_dim == rot and t.magnitude == 1.0
+    assert t.turns.tolist() == plain_turns(rot, **kw)
+    own = lr.rope_axes_table(rot, sections, order=order, own=True, device="cpu", **kw)
+    assert own.axis.tolist() == want
+    for a, s in enumerate(sections):
+        mine = [own.turns.tolist()[i] for i in range(rot // 2) if want[i] == a]
+        assert mine == (plain_turns(2 * s, **kw) if s else [])
+
+
+def test_axes_magnitude():
+    t = lr.rope_axes_table(64, [16, 16], scaling="parts", factor=8.0, original_len=4096, device="cpu")
+    assert abs(t.magnitude - (0.1 * math.log(8.0) + 1)) < 1e-15
+
+
+@pytest.mark.parametrize("kw", [dict(sections=[]), dict(sections=[32, 1]), dict(sections=[31]), dict(sections=[33, -1]),
+                                dict(sections=[8, 8, 8, 4, 4]), dict(rot=0, sections=[0]), dict(rot=63), dict(rot=1026),
+                                dict(sections=[8, 24], order="cyclic"), dict(base=1.0),
+                                dict(scaling="linear", factor=0.0), dict(scaling="linear", factor=0.0, own=True)])
+def test_axes_table_refusals(kw):
+    kw = dict(kw)
+    with pytest.raises(lr.LayoutRemapError) as e:
+        lr.rope_axes_table(kw.pop("rot", 64), kw.pop("sections", [16, 16]), device="cpu", **kw)
+    assert e.value.code == B.ERR_INVALID
+
+
+def test_axes_table_arguments():
+    p, s = B.lr_rope_params(4, 0, 10000.0, 1.0, 0.0, 1.0, 32.0), (ctypes.c_int32 * 2)(1, 1)
+    turns, axis, m = (ctypes.c_int64 * 2)(), (ctypes.c_int32 * 2)(), ctypes.c_double()
+
+    def call(p=p, s=s, axes=2, order=0, spectrum=0, turns=turns, axis=axis, m=m):
+        return lr.lib().lr_rope_axes_table(p, s, axes, order, spectrum, turns, axis, m)
+    assert call() == B.OK
+    for kw in (dict(p=None), dict(s=None), dict(turns=None), dict(axis=None), dict(m=None), dict(axes=0), dict(axes=5),
+               dict(axes=-1), dict(order=2), dict(order=-1), dict(spectrum=2), dict(spectrum=-1)):
+        assert call(**kw) == B.ERR_INVALID
+    with pytest.raises(ValueError):
+        lr.rope_axes_table(64, [32], order="rows", device="cpu")
+    with pytest.raises(ValueError):
+        lr.rope_axes_table(64, [32], scaling="twice", device="cpu")
+
+
+# -------------------------------------------------------------------------------- refusals: several axes
+X, Y, V, W, S = 0x100000, 0x40000000, 0x80000000, 0xc0000000, 0x200000  # far apart, never read
+A = S + 0x10000
+
+
+def rope_axes(**kw):
+    a = dict(x=X, Lx="(64,4,10):(1,64,256)", cx=2560, y=Y, Ly="(64,4,10):(1,64,256)", cy=2560, dtype=B.BF16,
+             turns=S, axis=A, positions=S + 0x1000, rot=64, pairs=0, axes=3, Lp=None, cp=30, n=10, flags=0)
+    a.update(kw)
+    lay = {k: (lr.Layout(a[k]).c if a[k] is not None else None) for k in ("Lx", "Ly", "Lp")}
+    r = B.lr_axes_rotation(a["turns"], a["axis"], a["positions"], a["rot"], a["pairs"], a["axes"], 1.0) if a["rot"] is not None else None
+    return lr.lib().lr_rope_axes(a["x"], lay["Lx"], a["cx"], a["y"], lay["Ly"], a["cy"], a["dtype"], r, lay["Lp"], a["cp"],
+                                 a["n"], a["flags"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), B.ERR_INVALID), (dict(y=None), B.ERR_INVALID), (dict(Lx=None), B.ERR_INVALID),
+    (dict(rot=None), B.ERR_INVALID), (dict(turns=None), B.ERR_INVALID), (dict(positions=None), B.ERR_INVALID),
+    (dict(axis=None), B.ERR_INVALID), (dict(axes=0), B.ERR_INVALID), (dict(axes=5), B.ERR_INVALID),
+    (dict(dtype=B.INT8), B.ERR_TYPE), (dict(rot=66), B.ERR_INVALID), (dict(rot=31), B.ERR_INVALID),
+    (dict(pairs=-1), B.ERR_INVALID), (dict(flags=4), B.ERR_INVALID), (dict(n=-1), B.ERR_INVALID),
+    (dict(n=11, cp=33), B.ERR_BOUNDS), (dict(cp=29), B.ERR_BOUNDS), (dict(cx=2559), B.ERR_BOUNDS),
+    (dict(Lp="(10,3):(1,10)", n=0), B.OK), (dict(Lp="(10,3):(1,10)", cp=29), B.ERR_BOUNDS),
+    (dict(Lp="(10,2):(1,10)"), B.ERR_SIZE_MISMATCH), (dict(Lp="(9,3):(1,10)"), B.ERR_SIZE_MISMATCH),
+    (dict(Lp="10:1"), B.ERR_INVALID), (dict(Lp="(10,3,1):(1,10,0)"), B.ERR_INVALID),
+    (dict(Lp="(10,(2,2)):(1,(10,30))", axes=4, cp=99), B.ERR_INVALID),
+    (dict(Ly="(64,4,9):(1,64,256)"), B.ERR_SIZE_MISMATCH), (dict(Ly="(64,4,10):(1,64,0)"), B.ERR_ALIAS),
+    (dict(y=X + 64), B.ERR_OVERLAP)])
+def test_rope_axes_refusals(kw, code):
+    assert rope_axes(**kw) == code
+
+
+@pytest.mark.parametrize("at", [0, -8, 40])
+def test_rope_axes_overlap(at):
+    assert rope_axes(n=0, positions=Y + at) == B.ERR_OVERLAP and rope_axes(n=0, positions=Y - 240) == B.OK
+    assert rope_axes(n=0, axis=Y + at) == B.ERR_OVERLAP and rope_axes(n=0, axis=Y - 128) == B.OK
+    assert rope_axes(n=0, turns=Y + at) == B.ERR_OVERLAP and rope_axes(n=0, turns=Y - 256) == B.OK
+    assert rope_axes(n=0, positions=None, cp=0) == B.OK and rope_axes(n=0, axis=None) == B.ERR_INVALID
+
+
+def cache(dtype=B.E4M3, **kw):
+    a = dict(k=X, v=V, Lk="(64,2,16,8):(1,64,128,2048)", Lv="(64,2,16,8):(1,64,128,2048)", ck=16384, cv=16384,
+             ks=W, vs=W + 4096, Ls="(2,16,8):(1,2,32)", cs=256)
+    if dtype not in (B.E4M3, B.INT8):
+        a.update(ks=None, vs=None)
+    a.update(kw)
+    c = B.lr_cache()
+    c.k, c.v, c.k_scale, c.v_scale, c.dtype = a["k"], a["v"], a["ks"], a["vs"], dtype
+    c.k_layout, c.v_layout, c.scale_layout = (lr.Layout(a[n]).c for n in ("Lk", "Lv", "Ls"))
+    c.k_capacity, c.v_capacity, c.scale_capacity = a["ck"], a["cv"], a["cs"]
+    return c
+
+
+def write_axes(c=None, **kw):
+    a = dict(k=Y, v=Y + 0x100000, L="(64,2,10):(1,64,128)", dtype=B.BF16, slots=S, n=10, turns=S + 0x1000, axis=A,
+             positions=S + 0x2000, rot=64, pairs=0, axes=2)
+    a.update(kw)
+    c = c if c is not None else cache()
+    r = B.lr_axes_rotation(a["turns"], a["axis"], a["positions"], a["rot"], a["pairs"], a["axes"], 1.0) if a["rot"] is not None else None
+    L = lr.Layout(a["L"]).c
+    return lr.lib().lr_cache_write_axes(c, a["k"], L, 1280, a["v"], L, 1280, a["dtype"], a["slots"], a["n"], r, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=0), B.OK), (dict(rot=None), B.ERR_INVALID), (dict(axes=0), B.ERR_INVALID), (dict(axes=5), B.ERR_INVALID),
+    (dict(axis=None), B.ERR_INVALID), (dict(turns=None), B.ERR_INVALID), (dict(positions=None), B.ERR_INVALID),
+    (dict(rot=66), B.ERR_INVALID), (dict(n=-1), B.ERR_INVALID), (dict(n=11), B.ERR_BOUNDS), (dict(dtype=B.E4M3), B.ERR_TYPE),
+    (dict(axis=X), B.ERR_OVERLAP), (dict(axis=W - 64, n=0), B.ERR_OVERLAP), (dict(positions=V - 80), B.ERR_OVERLAP),
+    (dict(positions=V - 160, n=0), B.OK), (dict(turns=W + 4096), B.ERR_OVERLAP), (dict(slots=X), B.ERR_OVERLAP)])
+def test_write_axes_refusals(kw, code):
+    assert write_axes(**kw) == code
+
+
+def test_axes_binding_refusals():
+    x, t = torch.zeros(640), lr.rope_axes_table(64, [16, 16], device="cpu")
+    with pytest.raises(ValueError):
+        lr.rope_axes(x, "(64,1,10):(1,64,64)", x, "(64,1,10):(1,64,64)", torch.zeros(2, 10, dtype=torch.int64), t)
+    with pytest.raises(ValueError):
+        B._axes_rotation(t, torch.arange(3), "thirds")
+    with pytest.raises(TypeError):
+        B._axes_rotation(t, torch.arange(3, dtype=torch.int32), "half")
+    assert ctypes.sizeof(B.lr_axes_rotation) == 40
