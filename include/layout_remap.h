@@ -703,6 +703,68 @@ int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, c
                        int32_t dtype, float scale, int64_t window, void* workspace, int64_t workspace_bytes,
                        void* stream);
 
+/* Attention of one new token a sequence where the whole batch shares a prefix, which is read once for all:
+ *   out[b, h] = softmax over the prefix's tokens and then the sequence's own, as lr_paged_attention.
+ * The prefix is tokens 0 .. P - 1 of the pages prefix[0..prefix_pages) (device), P = prefix_len[0] (device) limited to
+ * [0, prefix_pages * page_size); sequence b's own lens[b] tokens lie in the pages table[b * table_stride + ...] as those
+ * of lr_paged_attention do.  A negative lens[b] marks a row without a sequence, which gives zeros (lse -inf) and not the
+ * prefix's attention.  Everything else as lr_paged_attention without a window; the weights of values of 16 or 8 bits have
+ * the same bits.  workspace: at least the plan's workspace_bytes, 16-byte aligned; never 0. */
+typedef struct {
+  int32_t path;            /* lr_attention_path, for 16-byte aligned buffers */
+  int32_t row_tiles;       /* workgroups that share the prefix's keys of one cache head */
+  int64_t prefix_splits;   /* the most parts the prefix is cut into */
+  int64_t own_splits;      /* the most parts a sequence's own tokens are cut into */
+  int64_t workspace_bytes;
+} lr_prefix_plan;
+int lr_prefix_attention_plan(const lr_layout* Lq, const lr_cache* c, const lr_layout* Lo, int64_t prefix_pages,
+                             int64_t max_pages, int32_t dtype, lr_prefix_plan* out);
+int lr_prefix_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, const lr_cache* c, const int32_t* prefix,
+                        int64_t prefix_pages, const int32_t* prefix_len, const int32_t* table, int64_t table_stride,
+                        int64_t max_pages, const int32_t* lens, int64_t batch, void* out, const lr_layout* Lo,
+                        int64_t out_capacity, float* lse, int32_t dtype, float scale, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------- attention over selected blocks */
+
+/* A long sequence is attended to in part: each page of the cache is a block with a key of its own, the mean of its
+ * tokens' keys; every step scores the blocks by their keys, and attends to the tokens of the best ones only. */
+
+/* The keys of the blocks that the tokens in slots[0..n) (device, as lr_cache_write, after it) were written to:
+ *   keys[., h, p] = mean of the keys of slots 0 .. s of page p,
+ * s the place in the page of its newest slot.  A page's slots are filled in their order, and those of one page that are
+ * given have to stand next to each other in ascending order.  A slot outside the cache is passed over; pages that no
+ * slot lies in keep their keys.  keys: layout (head_dim, heads, pages) of the cache's
+ * extents, in the model's type dtype (the cache's own, or any for LR_E4M3 and LR_INT8).  Summed in 64 bits, the mean
+ * rounded to 32 bits and then to dtype. */
+int lr_block_keys(const lr_cache* c, const int64_t* slots, int64_t n, void* keys, const lr_layout* Lkeys,
+                  int64_t keys_capacity, int32_t dtype, void* stream);
+
+/* The blocks that each sequence and cache head attends to.  Sequence b has n_b = ceil(lens[b] / page_size) blocks
+ * (within [0, max_pages]), block j being page table[b * table_stride + j].  Where n_b <= count all of them are
+ * chosen; else the first `first`, the last `last` (first + last <= count), and those of the others with the highest
+ *   score(b, g, j) = max over the query heads h of cache head g of q[b, h] . keys[., g, table[b * table_stride + j]],
+ * computed in 64 bits, of equal ones the lowest j.  A NaN product, and a page outside [0, pages), counts as -inf.
+ * q: layout (head_dim, heads, sequences), keys: (head_dim, cache heads, pages), head_dim at most 256, both of type dtype.
+ * blocks: device int32[batch][cache heads][count], block numbers in ascending order, then -1.  workspace: device memory
+ * of at least the plan's size, 16-byte aligned. */
+int lr_block_select_plan(const lr_layout* Lq, const lr_layout* Lkeys, int64_t max_pages, int64_t* workspace_bytes);
+int lr_block_select(const void* q, const lr_layout* Lq, int64_t q_capacity, const void* keys, const lr_layout* Lkeys,
+                    int64_t keys_capacity, int32_t dtype, const int32_t* table, int64_t table_stride, int64_t max_pages,
+                    const int32_t* lens, int64_t page_size, int64_t batch, int64_t first, int64_t last,
+                    int32_t* blocks, int64_t count, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* lr_paged_attention over the tokens of the listed blocks alone: those t < lens[b] of blocks[b][g][i] = t / page_size
+ * (device int32[batch][cache heads][count]), for i < min(count, n_b), the blocks of the sequence.  An entry outside
+ * [0, n_b) is left out; a block that is listed twice counts twice.  No window; everything else as lr_paged_attention
+ * with its plan, of the `count` pages of a list. */
+int lr_block_attention_plan(const lr_layout* Lq, const lr_cache* c, const lr_layout* Lo, int64_t count, int32_t dtype,
+                            lr_attention_plan* out);
+int lr_block_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, const lr_cache* c, const int32_t* blocks,
+                       int64_t count, const int32_t* table, int64_t table_stride, int64_t max_pages,
+                       const int32_t* lens, int64_t batch, void* out, const lr_layout* Lo, int64_t out_capacity,
+                       float* lse, int32_t dtype, float scale, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------ misc */
 
 /* Static text for a status code. */

@@ -242,6 +242,16 @@ class lr_attention_plan(ctypes.Structure):
     ]
 
 
+class lr_prefix_plan(ctypes.Structure):
+    _fields_ = [
+        ("path", ctypes.c_int32),
+        ("row_tiles", ctypes.c_int32),
+        ("prefix_splits", ctypes.c_int64),
+        ("own_splits", ctypes.c_int64),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 class LibraryNotBuilt(RuntimeError):
     pass
 
@@ -319,6 +329,27 @@ _SIGS = {
                                           ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
                                           ctypes.c_float, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
                                           ctypes.c_void_p]),
+    "lr_prefix_attention_plan": (ctypes.c_int, [_L, _P(lr_cache), _L, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                                _P(lr_prefix_plan)]),
+    "lr_prefix_attention": (ctypes.c_int, [ctypes.c_void_p, _L, ctypes.c_int64, _P(lr_cache), ctypes.c_void_p,
+                                           ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                           ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, _L,
+                                           ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float,
+                                           ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "lr_block_keys": (ctypes.c_int, [_P(lr_cache), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, _L, ctypes.c_int64,
+                                     ctypes.c_int32, ctypes.c_void_p]),
+    "lr_block_select_plan": (ctypes.c_int, [_L, _L, ctypes.c_int64, _P(ctypes.c_int64)]),
+    "lr_block_select": (ctypes.c_int, [ctypes.c_void_p, _L, ctypes.c_int64, ctypes.c_void_p, _L, ctypes.c_int64,
+                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "lr_block_attention_plan": (ctypes.c_int, [_L, _P(lr_cache), _L, ctypes.c_int64, ctypes.c_int32,
+                                               _P(lr_attention_plan)]),
+    "lr_block_attention": (ctypes.c_int, [ctypes.c_void_p, _L, ctypes.c_int64, _P(lr_cache), ctypes.c_void_p,
+                                          ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, _L, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p,
+                                          ctypes.c_int64, ctypes.c_void_p]),
     "lr_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "lr_last_hip_error": (ctypes.c_char_p, []),
     "lr_version": (ctypes.c_char_p, []),
@@ -1075,4 +1106,164 @@ def paged_attention(q, Lq, cache: PagedCache, page_table, lens, out, Lo, scale: 
                                     out.numel(), lse_ptr, code, scale, window,
                                     workspace.data_ptr() if ws_bytes else None, ws_bytes, _stream_ptr(stream)),
            "paged_attention")
+    return out
+
+
+def _sequences(dev, q, Lq, out, page_table, lens, lse):
+    """The checks that the attentions over a cache on GPU `dev` share; the pointer of lse, or None."""
+    torch = _torch()
+    _device_tensors(dev, "q out lens", q, out, lens)
+    if q.dtype != out.dtype:
+        raise TypeError("q and out must have the same type")
+    _page_table(dev, page_table, lens)
+    if lse is None:
+        return None
+    _device_tensors(dev, "lse", lse)
+    if lse.dtype != torch.float32:
+        raise TypeError("lse must be float32")
+    if lse.numel() < lens.numel() * _mode_size(Lq.c, 1):
+        raise ValueError("lse needs one entry per sequence and head")
+    return lse.data_ptr()
+
+
+def _page_table(dev, page_table, lens):
+    int32 = _torch().int32
+    if page_table.dtype != int32 or lens.dtype != int32:
+        raise TypeError("page_table and lens must be int32")
+    if page_table.get_device() != dev or page_table.dim() != 2 or page_table.stride(1) != 1 < page_table.shape[1]:
+        raise ValueError("page_table must be a 2-D GPU tensor with contiguous rows")
+    if page_table.shape[0] < lens.numel():
+        raise ValueError("page_table needs a row per sequence")
+
+
+def _workspace(dev, workspace, need, device, stream):
+    """(pointer, bytes, the tensor that holds them) of a workspace that is given, or of `need()` bytes from the stream
+    the kernels run on, so that its reuse waits for them."""
+    torch = _torch()
+    if workspace is None:
+        size = need()
+        if size:
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+                workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    elif workspace.numel():
+        _device_tensors(dev, "workspace", workspace)
+    size = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return (workspace.data_ptr() if size else None), size, workspace
+
+
+def prefix_attention_plan(Lq, cache: PagedCache, Lo, prefix_pages: int, max_pages: int, dtype) -> dict:
+    """lr_prefix_attention_plan: the path, splits and workspace of prefix_attention (host only)."""
+    p = lr_prefix_plan()
+    _check(lib().lr_prefix_attention_plan(_as_layout(Lq).c, cache.c, _as_layout(Lo).c, prefix_pages, max_pages,
+                                          _dtype_code(dtype), p), "prefix_attention_plan")
+    return {"path": ATTENTION_PATH_NAMES[p.path], "row_tiles": p.row_tiles, "prefix_splits": p.prefix_splits,
+            "own_splits": p.own_splits, "workspace_bytes": p.workspace_bytes}
+
+
+def prefix_attention(q, Lq, cache: PagedCache, prefix, prefix_len, page_table, lens, out, Lo,
+                     scale: Optional[float] = None, lse=None, workspace=None, stream=None):
+    """lr_prefix_attention: attention of one token a sequence over a prefix that the whole batch shares, and then the
+    sequence's own tokens.  ``prefix``: int32, the prefix's pages; ``prefix_len``: int32, one entry, its tokens; the
+    rest as paged_attention (a negative entry of ``lens``: no sequence, zeros).  Returns out."""
+    dev = cache.index
+    Lq, Lo = _as_layout(Lq), _as_layout(Lo)
+    lse_ptr = _sequences(dev, q, Lq, out, page_table, lens, lse)
+    _device_tensors(dev, "prefix prefix_len", prefix, prefix_len)
+    if prefix.dtype != lens.dtype or prefix_len.dtype != lens.dtype:
+        raise TypeError("prefix and prefix_len must be int32")
+    if prefix_len.numel() != 1:
+        raise ValueError("prefix_len has one entry")
+    pages, max_pages = prefix.numel(), page_table.shape[1]
+    if scale is None:
+        scale = cache.dim ** -0.5
+    with _on_device(dev):
+        ws, ws_bytes, held = _workspace(dev, workspace, lambda: prefix_attention_plan(
+            Lq, cache, Lo, pages, max_pages, q.dtype)["workspace_bytes"], cache.k.device, stream)
+        _check(lib().lr_prefix_attention(q.data_ptr(), Lq.c, q.numel(), cache.c, prefix.data_ptr(), pages,
+                                         prefix_len.data_ptr(), page_table.data_ptr(), page_table.stride(0), max_pages,
+                                         lens.data_ptr(), lens.numel(), out.data_ptr(), Lo.c, out.numel(), lse_ptr,
+                                         _dtype_code(q.dtype), scale, ws, ws_bytes, _stream_ptr(stream)),
+               "prefix_attention")
+    return out
+
+
+def block_keys(cache: PagedCache, slots, keys, Lkeys, stream=None):
+    """lr_block_keys: the keys of the blocks (pages) that the tokens in the int64 ``slots`` were written to, the mean of
+    their tokens' keys, into ``keys`` of layout (head_dim, heads, pages).  Called with the slots of a cache_write, after
+    it.  Returns keys."""
+    _device_tensors(cache.index, "slots keys", slots, keys)
+    if slots.dtype != _torch().int64:
+        raise TypeError("slots must be int64")
+    Lkeys = _as_layout(Lkeys)
+    with _on_device(cache.index):
+        _check(lib().lr_block_keys(cache.c, slots.data_ptr(), slots.numel(), keys.data_ptr(), Lkeys.c, keys.numel(),
+                                   _dtype_code(keys.dtype), _stream_ptr(stream)), "block_keys")
+    return keys
+
+
+def block_select_plan(Lq, Lkeys, max_pages: int) -> dict:
+    """lr_block_select_plan: the workspace of block_select (host only)."""
+    n = ctypes.c_int64()
+    _check(lib().lr_block_select_plan(_as_layout(Lq).c, _as_layout(Lkeys).c, max_pages, ctypes.byref(n)),
+           "block_select_plan")
+    return {"workspace_bytes": n.value}
+
+
+def block_select(q, Lq, keys, Lkeys, page_table, lens, page_size: int, blocks, first: int = 1, last: int = 1,
+                 workspace=None, stream=None):
+    """lr_block_select: the blocks that each sequence and cache head attends to, by the highest product of a query head
+    with the block's key, the ``first`` and the ``last`` ones always among them, into ``blocks``, int32 (sequences,
+    cache heads, count): block numbers in ascending order, then -1.  q: layout (head_dim, heads, sequences); keys:
+    (head_dim, cache heads, pages); page_table and lens as paged_attention.  Returns blocks."""
+    dev = _device_tensors(None, "q keys lens blocks", q, keys, lens, blocks)
+    if q.dtype != keys.dtype:
+        raise TypeError("q and keys must have the same type")
+    _page_table(dev, page_table, lens)
+    Lq, Lkeys = _as_layout(Lq), _as_layout(Lkeys)
+    if blocks.dtype != lens.dtype:
+        raise TypeError("blocks must be int32")
+    if blocks.dim() != 3 or blocks.shape[0] < lens.numel() or blocks.shape[1] != _mode_size(Lkeys.c, 1):
+        raise ValueError("blocks must be (sequences, cache heads, count)")
+    max_pages = page_table.shape[1]
+    with _on_device(dev):
+        ws, ws_bytes, held = _workspace(dev, workspace, lambda: block_select_plan(Lq, Lkeys, max_pages)["workspace_bytes"],
+                                        q.device, stream)
+        _check(lib().lr_block_select(q.data_ptr(), Lq.c, q.numel(), keys.data_ptr(), Lkeys.c, keys.numel(),
+                                     _dtype_code(q.dtype), page_table.data_ptr(), page_table.stride(0), max_pages,
+                                     lens.data_ptr(), page_size, lens.numel(), first, last, blocks.data_ptr(),
+                                     blocks.shape[2], ws, ws_bytes, _stream_ptr(stream)), "block_select")
+    return blocks
+
+
+def block_attention_plan(Lq, cache: PagedCache, Lo, count: int, dtype) -> dict:
+    """lr_block_attention_plan: the path, split and workspace of block_attention (host only)."""
+    p = lr_attention_plan()
+    _check(lib().lr_block_attention_plan(_as_layout(Lq).c, cache.c, _as_layout(Lo).c, count, _dtype_code(dtype), p),
+           "block_attention_plan")
+    return {"path": ATTENTION_PATH_NAMES[p.path], "head_tiles": p.head_tiles, "chunk": p.chunk, "splits": p.splits,
+            "workspace_bytes": p.workspace_bytes}
+
+
+def block_attention(q, Lq, cache: PagedCache, blocks, page_table, lens, out, Lo, scale: Optional[float] = None, lse=None,
+                    workspace=None, stream=None):
+    """lr_block_attention: attention of one token a sequence over the tokens of the listed ``blocks`` alone, int32
+    (sequences, cache heads, count) as block_select leaves them; the rest as paged_attention.  Returns out."""
+    dev = cache.index
+    Lq, Lo = _as_layout(Lq), _as_layout(Lo)
+    lse_ptr = _sequences(dev, q, Lq, out, page_table, lens, lse)
+    _device_tensors(dev, "blocks", blocks)
+    if blocks.dtype != lens.dtype:
+        raise TypeError("blocks must be int32")
+    if blocks.dim() != 3 or blocks.shape[0] < lens.numel() or blocks.shape[1] != _mode_size(cache.c.k_layout, 1):
+        raise ValueError("blocks must be (sequences, cache heads, count)")
+    count, max_pages = blocks.shape[2], page_table.shape[1]
+    if scale is None:
+        scale = cache.dim ** -0.5
+    with _on_device(dev):
+        ws, ws_bytes, held = _workspace(dev, workspace, lambda: block_attention_plan(
+            Lq, cache, Lo, count, q.dtype)["workspace_bytes"], cache.k.device, stream)
+        _check(lib().lr_block_attention(q.data_ptr(), Lq.c, q.numel(), cache.c, blocks.data_ptr(), count,
+                                        page_table.data_ptr(), page_table.stride(0), max_pages, lens.data_ptr(),
+                                        lens.numel(), out.data_ptr(), Lo.c, out.numel(), lse_ptr, _dtype_code(q.dtype),
+                                        scale, ws, ws_bytes, _stream_ptr(stream)), "block_attention")
     return out

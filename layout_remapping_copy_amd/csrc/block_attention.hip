@@ -1,0 +1,542 @@
+// Attention over the blocks of a paged cache that a cheap score selects: lr_block_keys, lr_block_select and
+// lr_block_attention, with their plans.  A block is a page.
+#include "attention.h"
+
+namespace lr {
+
+// ------------------------------------------------------------------ the blocks' keys
+
+struct BlockKeysArgs {
+  const void* k;
+  const float* ks;
+  void* out;
+  const int64_t* slots;
+  int64_t kd, kh, ksl, kp, sh, ssl, sp, od, oh, op;
+  int64_t cache_slots;
+  FastDiv fd_page;
+  uint32_t page_size, heads, n, chunk;
+  int32_t dim;
+};
+
+// A wave has one cache head and `chunk` entries of slots, and makes the mean of every page whose newest slot is among
+// them.  A row of a page is a group of lanes with V elements each, as many rows at a time as the wave has groups, their
+// loads four ahead.  Sums are held in 64 bits, in which those of a page of codes or 16-bit keys are exact but for
+// extreme ranges: the mean is rounded once, and which blocks a score selects does not hang on the order of a sum.
+template <int DT, int CT, int V>
+__global__ void __launch_bounds__(64) k_block_keys(BlockKeysArgs a) {
+  using T = typename ElemOf<DT>::T;
+  using C = typename ElemOf<CT>::T;
+  using Vec = typename Chunk<C, V>::Vec;
+  constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
+  const uint32_t lane = threadIdx.x, h = blockIdx.y;
+  const uint64_t first = (uint64_t)blockIdx.x * a.chunk, at = first + lane;
+  const bool mine = lane < a.chunk && at < a.n;
+  const int64_t slot = mine ? a.slots[at] : -1, next = mine && at + 1 < a.n ? a.slots[at + 1] : -1;
+  const bool held = (uint64_t)slot < (uint64_t)a.cache_slots;
+  const uint32_t page = held ? op_div((uint32_t)slot, a.fd_page) : 0, in = held ? (uint32_t)slot - page * a.page_size : 0;
+  // the newest of its page, unless the next entry is a later slot of the same page
+  const bool later = next > slot && next < (int64_t)(page + (uint64_t)1) * a.page_size;
+  uint64_t todo = __ballot(held && !later);
+  uint32_t lanes = 1;  // of a row, a power of two
+  while (lanes * V < (uint32_t)a.dim && lanes < 64) lanes *= 2;
+  const uint32_t rows = 64 / lanes, row = lane / lanes, col = lane % lanes * V;
+  while (todo) {
+    const int f = __ffsll((unsigned long long)todo) - 1;
+    todo &= todo - 1;
+    const uint32_t p = uniform(__shfl(page, f)), count = uniform(__shfl(in, f)) + 1;
+    const C* k = (const C*)a.k + (int64_t)p * a.kp + (int64_t)h * a.kh;
+    const float* ks = kQuant ? a.ks + (int64_t)p * a.sp + (int64_t)h * a.sh : nullptr;
+    T* out = (T*)a.out + (int64_t)p * a.op + (int64_t)h * a.oh;
+    for (uint32_t e0 = 0; e0 < (uint32_t)a.dim; e0 += lanes * V) {
+      const uint32_t e = e0 + col;
+      const bool ok = e < (uint32_t)a.dim;
+      double sum[V] = {};
+      for (uint32_t t0 = 0; t0 < count; t0 += 4 * rows) {
+        Vec x[4];
+        float s[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const uint32_t t = t0 + z * rows + row < count ? t0 + z * rows + row : 0;
+          const C* r = k + (int64_t)t * a.ksl + (ok ? (int64_t)e * a.kd : 0);
+          x[z] = *(const Vec*)r;
+          s[z] = 1.f;
+          if constexpr (kQuant) s[z] = ks[(int64_t)t * a.ssl];
+        }
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          if (t0 + z * rows + row >= count) continue;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const double v = (double)value_of<CT>(V == 1 ? x[z][0] : x[z][i]);
+            sum[i] += kQuant ? v * (double)s[z] : v;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        for (uint32_t x = lanes; x < 64; x *= 2) sum[i] += __shfl_xor(sum[i], (int)x);
+      }
+      if (row == 0 && ok) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[(int64_t)(e + i) * a.od] = (T)(float)(sum[i] / (double)count);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ scores and the choice
+
+struct SelectArgs {
+  const void *q, *keys;
+  const int32_t *table, *lens;
+  int32_t* out;
+  double* scores;  // (sequence, cache head, max_pages)
+  int64_t qd, qh, qb, kd, kh, kp;
+  int64_t table_stride;
+  FastDiv fd_page, fd_heads, fd_runs;  // by the page's size, by kv_heads, by runs
+  uint32_t page_size, pages, max_pages, kv_heads, group, batch;
+  uint32_t count, first, last;
+  uint32_t runs, rounds;  // workgroups of a row of scores, 64 blocks of each
+  int32_t dim;
+};
+__device__ __forceinline__ uint32_t blocks_of(const SelectArgs& a, int32_t len) {
+  const uint32_t b = len > 0 ? op_div((uint32_t)len - 1, a.fd_page) + 1 : 0;
+  return b < a.max_pages ? b : a.max_pages;
+}
+
+typedef double D4 __attribute__((ext_vector_type(4)));
+
+// score(b, g, j) = max over the query heads h of cache head g of q[b, h] . key[table[b, j], g], in 64 bits: which blocks
+// are chosen hangs on scores that differ in their last bits, so these are as good as exact.  16 blocks x 16 heads are a
+// product of 64-bit matrix instructions, as fast as the vector units' 64 bits, with the sums over the lanes done; they
+// take 2048 cycles of a SIMD for 16 blocks of 128, so that reading 256 bytes a block stays the longer part.  The keys
+// come from memory as the product's first operand (16 rows, each lane a chunk of 16 bytes), the queries lie in shared
+// memory in the order of the second.
+template <int DT, int DC, bool WIDE>
+__global__ void __launch_bounds__(256) k_block_scores(SelectArgs a) {
+  using T = typename ElemOf<DT>::T;
+  constexpr uint32_t E = DT == LR_F32 ? 4 : 8;  // elements of a chunk
+  using Vec = typename Chunk<T, (int)E>::Vec;
+  constexpr uint32_t kChunks = DC / (4 * E);
+  __shared__ double qs[DC / 4 * 64];
+  const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64), r = lane & 15, j = lane >> 4;
+  const uint32_t bg = op_div(blockIdx.x, a.fd_runs), b = op_div(bg, a.fd_heads), g = bg - b * a.kv_heads;
+  const uint32_t many = blocks_of(a, a.lens[b]);
+  const uint32_t begin = (blockIdx.x - bg * a.runs) * 64 * a.rounds;
+  if (begin >= many || many <= a.count) return;  // all are taken: nothing to compare
+  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+  double* scores = a.scores + (uint64_t)bg * a.max_pages;
+  const uint32_t tiles = (a.group + 15) / 16;
+  for (uint32_t tile = 0; tile < tiles; ++tile) {
+    if (tile) __syncthreads();
+    for (uint32_t x = threadIdx.x; x < kChunks * E * 64; x += 256) {
+      const uint32_t s = x / 64, l = x % 64, h = tile * 16 + l % 16, e = (s / E * 4 + l / 16) * E + s % E;
+      const bool ok = h < a.group && e < (uint32_t)a.dim;
+      const T* q = (const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group + (ok ? h : 0)) * a.qh;
+      qs[x] = ok ? (double)value_of<DT>(q[(int64_t)e * a.qd]) : 0.0;
+    }
+    __syncthreads();
+    const bool head = tile * 16 + r < a.group;
+    for (uint32_t t = 0; t < a.rounds; ++t) {
+      const uint32_t j0 = begin + t * 64 + w * 16, at = j0 + r;
+      if (j0 >= many) break;
+      int32_t page = at < many ? table[at] : -1;
+      const bool there = (uint32_t)page < a.pages;
+      const T* key = (const T*)a.keys + (int64_t)(there ? page : 0) * a.kp + (int64_t)g * a.kh;
+      Vec k[kChunks];
+#pragma unroll
+      for (uint32_t c = 0; c < kChunks; ++c) {
+        const uint32_t e0 = (c * 4 + j) * E;
+        if constexpr (WIDE) {
+          k[c] = *(const Vec*)(key + (e0 < (uint32_t)a.dim ? e0 : 0));
+          if (e0 >= (uint32_t)a.dim) k[c] = Vec{};
+        } else {
+#pragma unroll
+          for (uint32_t i = 0; i < E; ++i) k[c][i] = e0 + i < (uint32_t)a.dim ? key[(int64_t)(e0 + i) * a.kd] : (T)0.f;
+        }
+      }
+      D4 acc = {};
+#pragma unroll
+      for (uint32_t c = 0; c < kChunks; ++c) {
+#pragma unroll
+        for (uint32_t i = 0; i < E; ++i)
+          acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)value_of<DT>(k[c][i]), qs[(c * E + i) * 64 + lane], acc, 0, 0, 0);
+      }
+      // lane r, j has head r of blocks j, 4 + j, 8 + j, 12 + j
+      const uint64_t seen = __ballot(there);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        double x = head ? acc[i] : -__builtin_inf();
+#pragma unroll
+        for (int d = 8; d; d >>= 1) x = fmax(x, __shfl_xor(x, d));  // passes over NaN
+        const uint32_t row = 4 * i + j;
+        if (r == 0 && j0 + row < many) {
+          x = x == x && (seen >> row & 1) ? x : -__builtin_inf();
+          if (tile) x = fmax(x, scores[j0 + row]);
+          scores[j0 + row] = x;
+        }
+      }
+    }
+  }
+}
+
+// A score's bits as an integer of the same order (-0 as 0).
+__device__ __forceinline__ uint64_t order_of(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+  return u >> 63 ? ~u : u | (uint64_t)1 << 63;
+}
+
+// One workgroup chooses for one sequence and cache head: the first and the last blocks, and of the others the best.
+// The score at the border is found a digit of 8 bits at a time, from the highest bit in which any two scores differ,
+// until a digit's scores are all taken or all bits are known; the chosen blocks are then written in their order, of
+// equal scores at the border the first ones.
+constexpr uint32_t kHeldScores = 4096;  // in shared memory; more are read again for each digit
+template <int LANES>
+__global__ void __launch_bounds__(LANES) k_block_choose(SelectArgs a) {
+  __shared__ uint64_t held[kHeldScores];
+  __shared__ uint32_t hist[256];
+  __shared__ uint64_t ends[2][LANES / 64];
+  __shared__ uint32_t found[3];
+  __shared__ uint32_t before[2][2][LANES / 64];
+  const uint32_t lane = threadIdx.x & 63, w = threadIdx.x / 64, bg = blockIdx.x, b = op_div(bg, a.fd_heads);
+  const uint32_t many = blocks_of(a, a.lens[b]);
+  int32_t* out = a.out + (uint64_t)bg * a.count;
+  if (many <= a.count) {
+    for (uint32_t i = threadIdx.x; i < a.count; i += LANES) out[i] = i < many ? (int32_t)i : -1;
+    return;
+  }
+  const double* scores = a.scores + (uint64_t)bg * a.max_pages;
+  const uint32_t lo = a.first, hi = many - a.last;  // of these is chosen
+  uint32_t need = a.count - a.first - a.last;
+  uint64_t border = ~(uint64_t)0;  // taken: above it, and the first `equal` of those on it
+  uint32_t equal = 0;
+  const bool fits = hi - lo <= kHeldScores;
+  auto score = [&](uint32_t i) { return fits ? held[i - lo] : order_of(scores[i]); };
+  if (need) {
+    uint64_t least = ~(uint64_t)0, most = 0;
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += LANES) {
+      const uint64_t s = order_of(scores[i]);
+      if (fits) held[i - lo] = s;
+      least = s < least ? s : least;
+      most = s > most ? s : most;
+    }
+    for (int d = 32; d; d >>= 1) {
+      const uint64_t x = __shfl_xor((unsigned long long)least, d), y = __shfl_xor((unsigned long long)most, d);
+      least = x < least ? x : least;
+      most = y > most ? y : most;
+    }
+    if (lane == 0) ends[0][w] = least, ends[1][w] = most;
+    __syncthreads();
+    for (uint32_t i = 0; i < LANES / 64; ++i) {
+      least = ends[0][i] < least ? ends[0][i] : least;
+      most = ends[1][i] > most ? ends[1][i] : most;
+    }
+    uint32_t bit = least == most ? 0 : 64 - (uint32_t)__builtin_clzll(least ^ most);  // bits not known yet
+    border = bit < 64 ? most >> bit << bit : 0;
+    equal = need;
+    while (bit) {
+      const uint32_t from = bit > 8 ? bit - 8 : 0, bins = 1u << (bit - from);
+      for (uint32_t i = threadIdx.x; i < 256; i += LANES) hist[i] = 0;
+      __syncthreads();
+      for (uint32_t i = lo + threadIdx.x; i < hi; i += LANES) {
+        const uint64_t s = score(i);
+        if (bit == 64 || s >> bit == border >> bit) atomicAdd(&hist[(uint32_t)(s >> from) & (bins - 1)], 1u);
+      }
+      __syncthreads();
+      if (w == 0) {  // four bins a lane, from the highest down
+        uint32_t c[4], sum = 0;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) sum += c[z] = hist[255 - (4 * lane + z)];
+        uint32_t above = wave_scan(sum, lane) - sum;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          if (above < need && above + c[z] >= need) found[0] = 255 - (4 * lane + z), found[1] = need - above, found[2] = c[z];
+          above += c[z];
+        }
+      }
+      __syncthreads();
+      border |= (uint64_t)found[0] << from;
+      need = equal = found[1];
+      bit = from;
+      if (found[2] == need) {  // all scores that begin so
+        equal = ~0u;
+        break;
+      }
+    }
+  }
+  const bool some = equal && equal != ~0u;  // of equal scores the first ones
+  uint32_t done = 0, level = 0;             // written; met on the border
+  for (uint32_t i0 = 0, turn = 0; i0 < many; i0 += LANES, turn ^= 1) {
+    const uint32_t i = i0 + threadIdx.x;
+    const bool choice = i >= lo && i < hi;
+    const uint64_t s = choice && equal ? score(i) : 0, below = ((uint64_t)1 << lane) - 1;
+    const bool on = choice && equal && s == border;
+    bool take = i < many && (!choice || (equal && (s > border || (on && !some))));
+    if (some) {
+      const uint64_t ons = __ballot(on);
+      if (lane == 0) before[turn][0][w] = (uint32_t)__popcll(ons);
+      __syncthreads();
+      uint32_t rank = level + (uint32_t)__popcll(ons & below);
+      for (uint32_t z = 0; z < LANES / 64; ++z) {
+        const uint32_t c = before[turn][0][z];
+        if (z < w) rank += c;
+        level += c;
+      }
+      take = take || (on && rank < equal);
+    }
+    const uint64_t takes = __ballot(take);
+    if (lane == 0) before[turn][1][w] = (uint32_t)__popcll(takes);
+    __syncthreads();
+    uint32_t at = done + (uint32_t)__popcll(takes & below);
+    for (uint32_t z = 0; z < LANES / 64; ++z) {
+      const uint32_t c = before[turn][1][z];
+      if (z < w) at += c;
+      done += c;
+    }
+    if (take) out[at] = (int32_t)i;
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+// A tensor of one row of head_dim elements for each head and item: layout (head_dim, heads, items).
+struct Rows {
+  int64_t dim, heads, items, d, h, i;  // extents and strides
+};
+static int rows_of(const lr_layout* L, int64_t capacity, bool output, Rows* r) {
+  if (int rc = check_tensor(L, 3, capacity, output)) return rc;
+  const Mode d = mode_of(*L, 0), h = mode_of(*L, 1), i = mode_of(*L, 2);
+  if (one_leaf(d, &r->d) || one_leaf(h, &r->h) || one_leaf(i, &r->i)) return LR_ERR_INVALID;
+  r->dim = d.size;
+  r->heads = h.size;
+  r->items = i.size;
+  return LR_OK;
+}
+
+template <int DT, int CT, int V>
+static int launch_keys(const BlockKeysArgs& a, dim3 grid, hipStream_t st) {
+  hipLaunchKernelGGL((k_block_keys<DT, CT, V>), grid, dim3(64), 0, st, a);
+  return check_op_launch();
+}
+// In chunks of v elements, or one at a time.
+template <int DT, int CT>
+static int launch_keys_of(const BlockKeysArgs& a, int64_t v, dim3 grid, hipStream_t st) {
+  constexpr int kMost = CT == LR_F32 ? 4 : CT == LR_E4M3 || CT == LR_INT8 ? 16 : 8;
+  if (v == kMost) return launch_keys<DT, CT, kMost>(a, grid, st);
+  if (v == kMost / 2 && v == 8) return launch_keys<DT, CT, 8>(a, grid, st);
+  return launch_keys<DT, CT, 1>(a, grid, st);
+}
+
+template <int DT, int DC> static int launch_scores(const SelectArgs& a, bool wide, dim3 grid, hipStream_t st) {
+  if (wide)
+    hipLaunchKernelGGL((k_block_scores<DT, DC, true>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_block_scores<DT, DC, false>), grid, dim3(256), 0, st, a);
+  return check_op_launch();
+}
+
+static int plan_select(const lr_layout* Lq, int64_t q_capacity, const lr_layout* Lk, int64_t keys_capacity,
+                       int64_t max_pages, Rows* q, Rows* k, int64_t* bytes) {
+  int rc = rows_of(Lq, q_capacity, false, q);
+  if (rc || (rc = rows_of(Lk, keys_capacity, false, k))) return rc;
+  if (q->dim != k->dim || q->heads % k->heads) return LR_ERR_SIZE_MISMATCH;
+  if (q->dim > kAttentionDim || max_pages < 1) return LR_ERR_INVALID;
+  const double runs = (double)q->items * (double)k->heads * (double)((max_pages + 63) / 64);
+  if (max_pages > kMaxCount || runs > (double)kMaxCount) return LR_ERR_OVERFLOW;
+  *bytes = q->items * k->heads * max_pages * 8;
+  return LR_OK;
+}
+
+static int plan_blocks(const lr_layout* Lq, const lr_cache* c, const lr_layout* Lo, int64_t max_pages, int64_t count,
+                       int32_t dtype, AttentionArgs* a, lr_attention_plan* out) {
+  if (int rc = attention_shapes(Lq, c, Lo, max_pages, dtype, a, out)) return rc;
+  if (count < 1) return LR_ERR_INVALID;
+  if (count > kMaxCount / a->page_size) return LR_ERR_OVERFLOW;
+  a->count = (uint32_t)count;
+  return attention_split(mode_of(*Lq, 2).size, count * a->page_size, true, a, out);
+}
+
+}  // namespace lr
+
+using namespace lr;
+
+extern "C" {
+
+int lr_block_keys(const lr_cache* c, const int64_t* slots, int64_t n, void* keys, const lr_layout* Lkeys,
+                  int64_t keys_capacity, int32_t dtype, void* stream) {
+  if (int rc = lr_cache_validate(c)) return rc;
+  if (!keys || n < 0 || (n > 0 && !slots)) return LR_ERR_INVALID;
+  if (!is_model_type(dtype) || (!is_quantised(c->dtype) && c->dtype != dtype)) return LR_ERR_TYPE;
+  Rows o;
+  if (int rc = rows_of(Lkeys, keys_capacity, true, &o)) return rc;
+  const Mode kd = mode_of(c->k_layout, 0), kh = mode_of(c->k_layout, 1), ks = mode_of(c->k_layout, 2);
+  const Mode kp = mode_of(c->k_layout, 3);
+  if (o.dim != kd.size || o.heads != kh.size || o.items != kp.size) return LR_ERR_SIZE_MISMATCH;
+  if (kh.size > 65535 || n > kMaxCount) return LR_ERR_OVERFLOW;
+  const int64_t e = dtype_bytes(dtype), ce = dtype_bytes(c->dtype);
+  const Buffer in[] = {{slots, n * 8}, {c->k, c->k_capacity * ce}, {c->v, c->v_capacity * ce},
+                       {c->k_scale, c->scale_capacity * 4}, {c->v_scale, c->scale_capacity * 4}};
+  const Buffer made[] = {{keys, keys_capacity * e}};
+  if (int rc = check_overlaps(in, 5, made, 1)) return rc;
+  if (n == 0) return LR_OK;
+  BlockKeysArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.k = c->k;
+  a.ks = c->k_scale;
+  a.out = keys;
+  a.slots = slots;
+  one_leaf(kd, &a.kd), one_leaf(kh, &a.kh), one_leaf(ks, &a.ksl), one_leaf(kp, &a.kp);  // checked with the cache
+  if (is_quantised(c->dtype)) {
+    one_leaf(mode_of(c->scale_layout, 0), &a.sh);
+    one_leaf(mode_of(c->scale_layout, 1), &a.ssl);
+    one_leaf(mode_of(c->scale_layout, 2), &a.sp);
+  }
+  a.od = o.d;
+  a.oh = o.h;
+  a.op = o.i;
+  a.page_size = (uint32_t)ks.size;
+  a.fd_page = make_fastdiv(a.page_size);
+  a.cache_slots = kp.size * ks.size;
+  a.heads = (uint32_t)kh.size;
+  a.n = (uint32_t)n;
+  a.dim = (int32_t)kd.size;
+  // 64 entries a wave, fewer where that would leave part of the device without one: a step's entries are each the
+  // newest of their page, a prompt's one in page_size
+  const int64_t waves = 8192;
+  a.chunk = (uint32_t)std::min<int64_t>(64, std::max<int64_t>(1, n * kh.size / waves));
+  int64_t v = 16 / ce;
+  while (v > 1 && (a.dim % v || !rows_aligned(c->k_layout, c->k, ce, v))) v /= 2;
+  const dim3 grid((unsigned)((n + a.chunk - 1) / a.chunk), a.heads);
+  const hipStream_t st = (hipStream_t)stream;
+  return with_model_type(dtype, [&](auto dt) {
+    constexpr int D = decltype(dt)::value;
+    if (c->dtype == LR_E4M3) return launch_keys_of<D, LR_E4M3>(a, v, grid, st);
+    if (c->dtype == LR_INT8) return launch_keys_of<D, LR_INT8>(a, v, grid, st);
+    return launch_keys_of<D, D>(a, v, grid, st);
+  });
+}
+
+int lr_block_select_plan(const lr_layout* Lq, const lr_layout* Lkeys, int64_t max_pages, int64_t* workspace_bytes) {
+  if (!workspace_bytes) return LR_ERR_INVALID;
+  Rows q, k;
+  return plan_select(Lq, INT64_MAX, Lkeys, INT64_MAX, max_pages, &q, &k, workspace_bytes);
+}
+
+int lr_block_select(const void* q, const lr_layout* Lq, int64_t q_capacity, const void* keys, const lr_layout* Lkeys,
+                    int64_t keys_capacity, int32_t dtype, const int32_t* table, int64_t table_stride, int64_t max_pages,
+                    const int32_t* lens, int64_t page_size, int64_t batch, int64_t first, int64_t last, int32_t* blocks,
+                    int64_t count, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!q || !keys || !blocks || batch < 0 || (batch > 0 && (!table || !lens)) || table_stride < 0) return LR_ERR_INVALID;
+  if (!is_model_type(dtype)) return LR_ERR_TYPE;
+  Rows r, k;
+  int64_t need;
+  if (int rc = plan_select(Lq, q_capacity, Lkeys, keys_capacity, max_pages, &r, &k, &need)) return rc;
+  if (batch > r.items) return LR_ERR_BOUNDS;
+  if (page_size < 1 || first < 0 || last < 0 || count < 1 || first > count || last > count - first) return LR_ERR_INVALID;
+  if (max_pages > kMaxCount / page_size || count > kMaxCount) return LR_ERR_OVERFLOW;
+  if (!workspace || workspace_bytes < need) return LR_ERR_CAPACITY;
+  if ((uintptr_t)workspace % 16) return LR_ERR_INVALID;
+  const int64_t e = dtype_bytes(dtype);
+  const Buffer in[] = {{q, q_capacity * e}, {keys, keys_capacity * e}, {lens, batch * 4},
+                       {table, batch ? ((batch - 1) * table_stride + max_pages) * 4 : 0}};
+  const Buffer made[] = {{blocks, batch * k.heads * count * 4}, {workspace, need}};
+  if (int rc = check_overlaps(in, 4, made, 2)) return rc;
+  if (batch == 0) return LR_OK;
+  SelectArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.keys = keys;
+  a.table = table;
+  a.lens = lens;
+  a.out = blocks;
+  a.scores = (double*)workspace;
+  a.qd = r.d, a.qh = r.h, a.qb = r.i;
+  a.kd = k.d, a.kh = k.h, a.kp = k.i;
+  a.table_stride = table_stride;
+  a.page_size = (uint32_t)page_size;
+  a.fd_page = make_fastdiv(a.page_size);
+  a.pages = (uint32_t)k.items;
+  a.max_pages = (uint32_t)max_pages;
+  a.kv_heads = (uint32_t)k.heads;
+  a.fd_heads = make_fastdiv(a.kv_heads);
+  a.group = (uint32_t)(r.heads / k.heads);
+  a.batch = (uint32_t)batch;
+  a.count = (uint32_t)count;
+  a.first = (uint32_t)first;
+  a.last = (uint32_t)last;
+  a.dim = (int32_t)r.dim;
+  const hipStream_t st = (hipStream_t)stream;
+  const int64_t rows = batch * k.heads;
+  if (max_pages > count) {  // else nothing is compared
+    const int64_t tiles = (max_pages + 63) / 64;
+    a.rounds = (uint32_t)std::min<int64_t>(8, std::max<int64_t>(1, rows * tiles / 2048));
+    a.runs = (uint32_t)((tiles + a.rounds - 1) / a.rounds);
+    a.fd_runs = make_fastdiv(a.runs);
+    const bool wide = r.dim % (16 / e) == 0 && rows_aligned(*Lkeys, keys, e, 16 / e);
+    const dim3 grid((unsigned)(rows * a.runs));
+    const int rc = with_model_type(dtype, [&](auto dt) {
+      constexpr int D = decltype(dt)::value;
+      if (a.dim <= 64) return launch_scores<D, 64>(a, wide, grid, st);
+      if (a.dim <= 128) return launch_scores<D, 128>(a, wide, grid, st);
+      return launch_scores<D, 256>(a, wide, grid, st);
+    });
+    if (rc) return rc;
+  }
+  if (max_pages > 1024)
+    hipLaunchKernelGGL((k_block_choose<1024>), dim3((unsigned)rows), dim3(1024), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_block_choose<256>), dim3((unsigned)rows), dim3(256), 0, st, a);
+  return check_op_launch();
+}
+
+int lr_block_attention_plan(const lr_layout* Lq, const lr_cache* c, const lr_layout* Lo, int64_t count, int32_t dtype,
+                            lr_attention_plan* out) {
+  if (!out) return LR_ERR_INVALID;
+  AttentionArgs a;
+  return plan_blocks(Lq, c, Lo, 1, count, dtype, &a, out);
+}
+
+int lr_block_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, const lr_cache* c, const int32_t* blocks,
+                       int64_t count, const int32_t* table, int64_t table_stride, int64_t max_pages,
+                       const int32_t* lens, int64_t batch, void* out, const lr_layout* Lo, int64_t out_capacity,
+                       float* lse, int32_t dtype, float scale, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!q || !out || batch < 0 || (batch > 0 && (!blocks || !table || !lens)) || !std::isfinite(scale) || table_stride < 0)
+    return LR_ERR_INVALID;
+  AttentionArgs a;
+  lr_attention_plan p;
+  if (int rc = plan_blocks(Lq, c, Lo, max_pages, count, dtype, &a, &p)) return rc;
+  if (cosize_bound(Lq) > q_capacity || cosize_bound(Lo) > out_capacity || batch > mode_of(*Lq, 2).size)
+    return LR_ERR_BOUNDS;
+  if (p.workspace_bytes && (!workspace || workspace_bytes < p.workspace_bytes)) return LR_ERR_CAPACITY;
+  if (p.workspace_bytes && (uintptr_t)workspace % 16) return LR_ERR_INVALID;
+  const int64_t e = dtype_bytes(dtype), ce = dtype_bytes(c->dtype), rows = batch * a.heads;
+  const Buffer in[] = {{q, q_capacity * e}, {c->k, c->k_capacity * ce}, {c->v, c->v_capacity * ce},
+                       {c->k_scale, c->scale_capacity * 4}, {c->v_scale, c->scale_capacity * 4},
+                       {table, batch ? ((batch - 1) * table_stride + max_pages) * 4 : 0}, {lens, batch * 4},
+                       {blocks, batch * a.kv_heads * count * 4}};
+  const Buffer made[] = {{out, out_capacity * e}, {lse, lse ? rows * 4 : 0}, {workspace, p.workspace_bytes}};
+  if (int rc = check_overlaps(in, 8, made, 3)) return rc;
+  if (batch == 0) return LR_OK;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.blocks = blocks;
+  a.table = table;
+  a.table_stride = table_stride;
+  a.lens = lens;
+  a.batch = (uint32_t)batch;
+  a.scale2 = scale * kLog2e;
+  a.part_o = (float*)workspace;
+  a.part_ml = (float*)workspace + (p.workspace_bytes / 4 - 2 * mode_of(*Lq, 2).size * a.heads * p.splits);
+  attention_buffers(c, Lq, q, dtype, p.path, &a);
+  const hipStream_t st = (hipStream_t)stream;
+  const int rc = with_model_type(dtype, [&](auto dt) {
+    constexpr int D = decltype(dt)::value;
+    if (c->dtype == LR_E4M3) return launch_pass<D, LR_E4M3, true>(a, st);
+    if (c->dtype == LR_INT8) return launch_pass<D, LR_INT8, true>(a, st);
+    return launch_pass<D, D, true>(a, st);
+  });
+  return rc || a.splits == 1 ? rc : launch_attention_join(a, dtype, st);
+}
+
+}  // extern "C"

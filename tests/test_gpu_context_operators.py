@@ -1,7 +1,8 @@
 """The operators for long and many-sided contexts on the GPU against plain 64-bit forms computed here on the CPU.
 
 Tolerances count roundings: storing a value in type T is off by at most half a step, HALF[T] relative
-(or half the smallest subnormal), and every 32-bit operation by 2^-24 of its result.
+(or half the smallest subnormal), and every 32-bit operation by 2^-24 of its result.  The forms in 64 bits that the
+attention of test_gpu_operators has are used here too.
 """
 
 import math
@@ -11,38 +12,10 @@ import pytest
 torch = pytest.importorskip("torch")
 import layout_remapping_copy_amd as lr  # noqa: E402
 
+from test_gpu_operators import (F64, HALF, T, TINY, TOP, U, attention64, attention_case, cache_strides, close, content,  # noqa: E402,F401
+                                dev, make_cache, quantised64, rand, rope_tolerance, tight64)
+
 pytestmark = pytest.mark.gpu
-
-F64 = torch.float64
-HALF = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
-TINY = {torch.float32: 2.0 ** -150, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
-T = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn,
-     "int8": torch.int8}
-TOP = {"e4m3": 448.0, "int8": 127.0}
-U = 2.0 ** -24
-
-
-@pytest.fixture(scope="module")
-def dev():
-    if not torch.cuda.is_available():
-        pytest.skip("no GPU")
-    lr.lib()
-    return torch.device("cuda:0")
-
-
-def close(got, want, tol, what=""):
-    got, want = got.to(F64).cpu(), want.to(F64)
-    assert got.shape == want.shape
-    same = (got == want) | (got.isnan() & want.isnan())
-    off = (got - want).abs()
-    bad = ~same & ~(off <= tol)
-    assert not bad.any(), (what, int(bad.sum()), float(off[bad][0]), float((tol.expand_as(off) if torch.is_tensor(tol) else
-                                                                           torch.tensor(tol).expand_as(off))[bad][0]))
-
-
-def rand(shape, dtype, seed):
-    g = torch.Generator().manual_seed(seed)
-    return torch.randn(shape, generator=g, dtype=torch.float32).to(dtype)
 
 
 def ints(lo, hi, shape, seed):
@@ -64,11 +37,6 @@ def rotate64(x, positions, table, pairs, sign=1):
     size = torch.zeros_like(y)   # |p| + |q| of each rotated element: what its 32-bit error is relative to
     size[..., u] = size[..., v] = (p.abs() + q.abs()) * m
     return y, size
-
-
-def rope_tolerance(want, size, dtype):
-    # cos and sin 2^-23 off, one rounding each for the magnitude, the products and the sum
-    return HALF[dtype] * want.abs() + 8 * U * size + TINY[dtype]
 
 
 AXES = [  # type, tokens, heads, dim, sections, order, own, pairs, order of y
@@ -196,48 +164,6 @@ def test_rope_axes_of_no_axis(dev):
 
 
 # ------------------------------------------------------------------------------------ the cache
-def cache_strides(order, h, p, d, pad=0):
-    """(pages, slots, heads, dim) strides of a cache tensor and (pages, slots, heads) of its scales."""
-    r = d + pad
-    if order == "tokens":
-        return (p * h * r, h * r, r, 1), (p * h, h, 1)
-    if order == "heads":
-        return (h * p * r, r, p * r, 1), (h * p, 1, p)
-    return (h * p * d, 1, p, h * p), (p * h, h, 1)      # "column": the head dimension outermost in a page
-
-
-def make_cache(dev, kind, order, pages, p, h, dk, dv, pad=0):
-    t = T[kind]
-    tensors, layouts = [], []
-    for d in (dk, dv):
-        s, ss = cache_strides(order, h, p, d, pad)
-        n = 1 + (pages - 1) * s[0] + (p - 1) * s[1] + (h - 1) * s[2] + (d - 1) * s[3]
-        tensors.append(torch.zeros(n, dtype=t if kind != "e4m3" else torch.uint8, device=dev))
-        layouts.append(f"({d},{h},{p},{pages}):({s[3]},{s[2]},{s[1]},{s[0]})")
-    ks = vs = Ls = None
-    if kind in TOP:
-        ks, vs = (torch.full((pages * p * h,), -1.0, device=dev) for _ in range(2))
-        Ls = f"({h},{p},{pages}):({ss[2]},{ss[1]},{ss[0]})"
-    return lr.PagedCache(tensors[0], layouts[0], tensors[1], layouts[1], ks, vs, Ls), (order, pages, p, h, pad)
-
-
-def content(cache, info, d, which):
-    """(codes as their values, scales or None) of a cache side as (pages * slots, heads, ...), on the CPU."""
-    order, pages, p, h, pad = info
-    s, ss = cache_strides(order, h, p, d, pad)
-    x = getattr(cache, which).cpu().as_strided((pages, p, h, d), s).reshape(pages * p, h, d)
-    if x.dtype == torch.uint8:
-        x = x.contiguous().view(torch.float8_e4m3fn).float()
-    sc = getattr(cache, which + "_scale")
-    return x, None if sc is None else sc.cpu().as_strided((pages, p, h), ss).reshape(pages * p, h)
-
-
-def stored(cache, info, d, which):
-    """What the cache stands for, in 64 bits."""
-    x, s = content(cache, info, d, which)
-    return x.to(F64) if s is None else x.to(F64) * s.to(F64)[..., None]
-
-
 @pytest.mark.parametrize("pairs", ["half", "interleaved"])
 @pytest.mark.parametrize("dtype,kind,n,h,d,sections,order,page", [
     ("bf16", "e4m3", 70, 8, 128, [24, 20, 20], "cyclic", 16), ("fp16", "int8", 33, 2, 96, [16, 16], "blocks", 16),
@@ -275,3 +201,535 @@ def test_cache_write_axes(dev, dtype, kind, n, h, d, sections, order, page, pair
     close(scale, (amax / TOP[kind])[keep], ((err + 2 * U * amax) / TOP[kind])[keep])
     step = 2.0 ** -4 * want[keep].abs() + 2.0 ** -10 * scale[..., None] if kind == "e4m3" else 0.5 * scale[..., None]
     close(got[slots[keep]].to(F64) * scale[..., None], want[keep], step * (1 + 2.0 ** -10) + 8 * U * size[keep])
+
+
+# ------------------------------------------------------------------------------------ a shared prefix
+def int32(x, dev):
+    return torch.tensor(x, dtype=torch.int32, device=dev)
+
+
+def prefix_case(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, lens, **kw):
+    """attention_case whose first sequence is the prefix: the cache, the prefix's pages, the others' table, the slots of
+    the prefix and of each sequence, and the numbers."""
+    cache, table, slots, sides = attention_case(dev, dtype, kind, heads, kv, dk, dv, page, order,
+                                                [prefix] + [max(n, 0) for n in lens], **kw)
+    return cache, table[0].contiguous(), table[1:].contiguous(), slots[0], slots[1:], sides
+
+
+PREFIX = [  # type, kind, heads, kv, dk, dv, page, order, prefix, lens
+    ("bf16", "bf16", 8, 2, 128, 128, 16, "tokens", 300, [1, 15, 0, 129]),
+    ("bf16", "bf16", 32, 8, 128, 128, 16, "heads", 1000, [5, 0, 33, 200, 64]),
+    ("fp16", "fp16", 8, 8, 64, 64, 16, "heads", 77, [1, 2, 31]),
+    ("fp32", "fp32", 6, 3, 128, 128, 16, "tokens", 130, [1, 0, 65]),
+    ("bf16", "e4m3", 32, 8, 128, 128, 64, "heads", 700, [1, 63, 64, 65, 300]),
+    ("fp16", "int8", 20, 1, 80, 80, 32, "tokens", 500, [1, 40, 90]),
+    ("fp32", "int8", 5, 1, 64, 64, 16, "tokens", 100, [3, 10]),
+    ("bf16", "bf16", 16, 1, 192, 128, 16, "tokens", 257, [0, 64, 3]),
+    ("bf16", "bf16", 48, 1, 256, 256, 16, "heads", 200, [31] * 5),
+    ("fp16", "fp16", 7, 1, 72, 72, 8, "tokens", 333, [9] * 12),
+    ("bf16", "bf16", 4, 2, 33, 17, 5, "tokens", 250, [1, 4, 5, 6]),
+    ("bf16", "e4m3", 14, 2, 112, 112, 1, "tokens", 77, [1, 20]),
+    ("fp32", "e4m3", 4, 2, 96, 80, 8, "heads", 33, [3, 100]),
+    ("bf16", "bf16", 4, 4, 128, 128, 16, "column", 100, [20, 0]),
+    ("bf16", "bf16", 8, 8, 32, 32, 128, "tokens", 2049, [300] * 40),
+    ("bf16", "bf16", 64, 8, 128, 128, 16, "heads", 3000, [(37 * i) % 50 for i in range(24)]),
+    ("fp16", "fp16", 64, 8, 128, 128, 16, "tokens", 1500, [(37 * i) % 50 for i in range(24)]),
+    ("bf16", "int8", 64, 4, 128, 128, 16, "tokens", 1500, [(37 * i) % 50 for i in range(24)]),
+    ("bf16", "bf16", 1, 1, 64, 64, 16, "tokens", 1, [0]),
+    ("bf16", "bf16", 2, 1, 128, 128, 16, "tokens", 5000, [1]),
+    ("bf16", "bf16", 10, 2, 160, 96, 16, "tokens", 333, [7] * 30),
+    ("fp16", "e4m3", 32, 4, 96, 96, 32, "heads", 2000, [(13 * i) % 40 for i in range(24)]),
+]
+
+
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,order,prefix,lens", PREFIX)
+def test_prefix_attention(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, lens):
+    t, b = T[dtype], len(lens)
+    cache, first, table, shared, slots, (kn, vn) = prefix_case(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, lens)
+    q = rand((b, heads, dk), t, 11)
+    out = torch.full((b, heads, dv), -7.0, dtype=t, device=dev)
+    lse = torch.full((b, heads), -7.0, device=dev)
+    Lq, Lo = f"({dk},{heads},{b}):(1,{dk},{heads * dk})", f"({dv},{heads},{b}):(1,{dv},{heads * dv})"
+    lr.prefix_attention(q.to(dev), Lq, cache, first.to(dev), int32([prefix], dev), table.to(dev), int32(lens, dev), out, Lo,
+                        lse=lse)
+    seen = [torch.cat([shared, u]) for u in slots]
+    want, wlse, tol = attention64(q, [kn[u] for u in seen], [vn[u] for u in seen], dk ** -0.5, t, kind)
+    close(out, want, tol, "out")
+    close(lse, wlse, tol.lse, "lse")
+
+
+@pytest.mark.parametrize("dtype,kind", [("bf16", "bf16"), ("fp32", "fp32"), ("fp16", "e4m3")])
+def test_prefix_attention_rows_and_lengths(dev, dtype, kind):
+    """Rows without a sequence, an empty prefix, lengths past the tables, pages that are none, a part of the batch, a
+    table and a prefix wider than needed."""
+    t, heads, kv, d, page = T[dtype], 8, 2, 64, 16
+    lens = [20, -1, 0, 50]
+    cache, first, table, shared, slots, (kn, vn) = prefix_case(dev, dtype, kind, heads, kv, d, d, page, "tokens", 90, lens)
+    b = len(lens)
+    q = rand((b + 1, heads, d), t, 3)
+    L = f"({d},{heads},{b + 1}):(1,{d},{heads * d})"
+    for prefix, own in ((90, lens), (0, lens), (-5, [20, 0, 0, 50]), (33, [5, -2 ** 31, 1, 0])):
+        out = torch.full((b + 1, heads, d), -7.0, dtype=t, device=dev)
+        lse = torch.full((b, heads), -7.0, device=dev)
+        lr.prefix_attention(q.to(dev), L, cache, first.to(dev), int32([prefix], dev), table.to(dev), int32(own, dev), out, L,
+                            lse=lse)
+        seen = [torch.cat([shared[:max(prefix, 0)], u[:n]]) if n >= 0 else u[:0] for u, n in zip(slots, own)]
+        want, wlse, tol = attention64(q[:b], [kn[u] for u in seen], [vn[u] for u in seen], d ** -0.5, t, kind)
+        close(out[:b], want, tol, (prefix, "out"))
+        close(lse, wlse, tol.lse, (prefix, "lse"))
+        assert (out[b] == -7).all()
+    # lengths past what the tables have room for, and pages outside the cache, which are left out
+    full = first[:6].clone()                                            # 90 tokens: 6 pages, of which 5 are full
+    full[1], full[3] = -1, 1 << 30
+    out, lse = torch.empty((b, heads, d), dtype=t, device=dev), torch.empty((b, heads), device=dev)
+    L4 = f"({d},{heads},{b}):(1,{d},{heads * d})"
+    lr.prefix_attention(q[:b].to(dev), L4, cache, full[:5].contiguous().to(dev), int32([2 ** 31 - 1], dev),
+                        table[:, :1].contiguous().to(dev), int32([2 ** 31 - 1, -1, 0, 2 ** 31 - 1], dev), out, L4, lse=lse)
+    keep = torch.cat([shared[i * page:(i + 1) * page] for i in (0, 2, 4)])
+    seen = [torch.cat([keep, slots[0][:page]]), keep[:0], keep, torch.cat([keep, slots[3][:page]])]
+    want, wlse, tol = attention64(q[:b], [kn[u] for u in seen], [vn[u] for u in seen], d ** -0.5, t, kind)
+    close(out, want, tol, "past")
+    close(lse, wlse, tol.lse, "past lse")
+
+
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,order,prefix,lens", [PREFIX[1], PREFIX[3], PREFIX[4], PREFIX[10], PREFIX[15]])
+def test_prefix_attention_is_paged_attention(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, lens):
+    """Over whole pages of a prefix the result is paged_attention's over tables that begin with them, within both's
+    tolerances; and twice the same call gives the same bits."""
+    t, b, prefix = T[dtype], len(lens), -(-prefix // page) * page
+    cache, first, table, shared, slots, (kn, vn) = prefix_case(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, lens)
+    q = rand((b, heads, dk), t, 11)
+    Lq, Lo = f"({dk},{heads},{b}):(1,{dk},{heads * dk})", f"({dv},{heads},{b}):(1,{dv},{heads * dv})"
+    n = prefix // page
+    both = torch.cat([first[:n].expand(b, n), table], 1).contiguous()
+    one, two, again = (torch.empty((b, heads, dv), dtype=t, device=dev) for _ in range(3))
+    args = (q.to(dev), Lq, cache, first[:n].contiguous().to(dev), int32([prefix], dev), table.to(dev), int32(lens, dev))
+    lr.prefix_attention(*args, one, Lo)
+    lr.prefix_attention(*args, again, Lo)
+    assert torch.equal(one, again)
+    lr.paged_attention(q.to(dev), Lq, cache, both.to(dev), int32([prefix + max(m, 0) for m in lens], dev), two, Lo)
+    seen = [torch.cat([shared, u]) for u in slots]
+    want, _, tol = attention64(q, [kn[u] for u in seen], [vn[u] for u in seen], dk ** -0.5, t, kind)
+    close(one, two.to(F64).cpu(), 2 * tol)
+
+
+@pytest.mark.parametrize("dtype,kind", [("bf16", "bf16"), ("fp32", "fp32"), ("bf16", "int8")])
+@pytest.mark.parametrize("wide", [True, False])
+def test_prefix_attention_strides(dev, dtype, kind, wide):
+    """Queries and outputs with strides, offset buffers, padded cache rows; other elements stay as they were."""
+    t, b, heads, kv, d, page = T[dtype], 9, 16, 2, 64, 16
+    pad = 8 if wide else 3
+    cache, first, table, shared, slots, (kn, vn) = prefix_case(dev, dtype, kind, heads, kv, d, d, page, "heads", 200,
+                                                               [3 * i for i in range(b)], pad=pad)
+    row = d + pad
+    q = rand((b, heads, d), t, 5)
+    flat = torch.full((heads * b * row + 1,), float("nan"), dtype=t)
+    flat[1:].as_strided((b, heads, d), (row, b * row, 1)).copy_(q)
+    out = torch.full((heads * b * row + 1,), -7.0, dtype=t, device=dev)
+    L = f"({d},{heads},{b}):(1,{b * row},{row})"
+    lr.prefix_attention(flat.to(dev)[1:], L, cache, first.to(dev), int32([200], dev), table.to(dev),
+                        int32([3 * i for i in range(b)], dev), out[1:], L, scale=0.3)
+    seen = [torch.cat([shared, u]) for u in slots]
+    want, _, tol = attention64(q, [kn[u] for u in seen], [vn[u] for u in seen], 0.3, t, kind)
+    close(out.cpu()[1:].as_strided((b, heads, d), (row, b * row, 1)), want, tol)
+    assert int((out == -7).sum()) == out.numel() - b * heads * d
+
+
+@pytest.mark.parametrize("dtype,kind,d", [("bf16", "bf16", 128), ("fp16", "fp16", 128), ("fp32", "fp32", 64), ("bf16", "e4m3", 128)])
+def test_prefix_attention_large_scores(dev, dtype, kind, d):
+    """Scores of some thousands on one side of the prefix's end only: the other side's weight is nothing."""
+    t, heads, kv, page, b = T[dtype], 32, 2, 16, 6
+    cache, first, table, shared, slots, (kn, vn) = prefix_case(dev, dtype, kind, heads, kv, d, d, page, "heads", 400, [30] * b)
+    q = rand((b, heads, d), t, 5) * 4
+    out, lse = torch.empty((b, heads, d), dtype=t, device=dev), torch.empty((b, heads), device=dev)
+    L = f"({d},{heads},{b}):(1,{d},{heads * d})"
+    lr.prefix_attention(q.to(dev), L, cache, first.to(dev), int32([400], dev), table.to(dev), int32([30] * b, dev), out, L,
+                        scale=4.0, lse=lse)
+    seen = [torch.cat([shared, u]) for u in slots]
+    want, wlse, tol = attention64(q, [kn[u] for u in seen], [vn[u] for u in seen], 4.0, t, kind)
+    close(out, want, tol)
+    close(lse, wlse, tol.lse)
+
+
+def put_rows(cache, which, order, page, kv, d, slots, rows):
+    pages = cache.k.numel() // (page * kv * d)
+    s, _ = cache_strides(order, kv, page, d)
+    x = getattr(cache, which).as_strided((pages, page, kv, d), s)
+    x[slots.to(x.device) // page, slots.to(x.device) % page] = rows.to(x.device)
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", 32), ("fp16", 32), ("fp32", 32), ("bf16", 3)])
+def test_prefix_attention_special_values(dev, dtype, heads):
+    """An infinite value of the prefix makes its element infinite in every row, a NaN query its own rows NaN."""
+    t, kv, d, page, b = T[dtype], 1, 128, 16, 5
+    cache, first, table, shared, slots, (kn, vn) = prefix_case(dev, dtype, dtype, heads, kv, d, d, page, "tokens", 150, [9] * b)
+    rows = vn[shared[77:78]].clone()
+    rows[0, 0, 3], rows[0, 0, 64] = math.inf, -math.inf
+    put_rows(cache, "v", "tokens", page, kv, d, shared[77:78], rows.to(t))
+    q = rand((b, heads, d), t, 5)
+    q[2, 1, 5] = math.nan
+    out, lse = torch.empty((b, heads, d), dtype=t, device=dev), torch.empty((b, heads), device=dev)
+    L = f"({d},{heads},{b}):(1,{d},{heads * d})"
+    lr.prefix_attention(q.to(dev), L, cache, first.to(dev), int32([150], dev), table.to(dev), int32([9] * b, dev), out, L, lse=lse)
+    out, lse = out.cpu(), lse.cpu()
+    seen = [torch.cat([shared, u]) for u in slots]
+    clean = torch.where(q.isnan(), torch.zeros_like(q), q)
+    want, wlse, tol = attention64(clean, [kn[u] for u in seen], [vn[u] for u in seen], d ** -0.5, t, dtype)
+    want[..., 3], want[..., 64] = math.inf, -math.inf
+    want[2, 1], wlse[2, 1] = math.nan, math.nan
+    close(out, want, tol)
+    close(lse, wlse, tol.lse)
+
+
+# ------------------------------------------------------------------------------------ blocks: their keys
+KEYS = [  # type, kind, heads, d, page, order, lens
+    ("bf16", "bf16", 8, 128, 16, "tokens", [100, 1, 16, 17]), ("bf16", "e4m3", 8, 128, 64, "heads", [300, 64, 1]),
+    ("fp16", "int8", 2, 80, 32, "tokens", [70, 33]), ("fp32", "fp32", 3, 96, 8, "heads", [20, 8, 7]),
+    ("fp32", "e4m3", 1, 256, 128, "tokens", [200]), ("bf16", "bf16", 2, 33, 5, "tokens", [23, 4, 5]),
+    ("fp16", "fp16", 1, 512, 16, "tokens", [40]), ("bf16", "int8", 4, 72, 1, "tokens", [9]),
+    ("bf16", "bf16", 2, 64, 16, "column", [50]), ("bf16", "e4m3", 3, 24, 16, "heads", [3000, 5]),
+    ("fp16", "e4m3", 5, 300, 48, "tokens", [100]), ("bf16", "bf16", 16, 128, 16, "heads", [20000, 9000]),
+]
+
+
+@pytest.mark.parametrize("dtype,kind,h,d,page,order,lens", KEYS)
+def test_block_keys(dev, dtype, kind, h, d, page, order, lens):
+    """The keys after a prompt and after one more token a sequence, against means in 64 bits; other pages' keys stay."""
+    t = T[dtype]
+    grown = [n + 1 for n in lens]
+    cache, table, slots, (kn, _) = attention_case(dev, dtype, kind, h, h, d, d, page, order, grown)
+    pages = cache.k.numel() // (page * h * d)
+    keys = torch.full((pages, h, d), -7.0, dtype=t, device=dev)
+    L = f"({d},{h},{pages}):(1,{d},{h * d})"
+    want = torch.full((pages, h, d), -7.0, dtype=F64)
+    size = torch.zeros((pages, h, d), dtype=F64)
+
+    def expect(i, n):                                                   # the blocks that sequence i's first n tokens lie in
+        for j in range(-(-n // page)):
+            rows = kn[slots[i][j * page:min(n, (j + 1) * page)]]
+            want[table[i, j]], size[table[i, j]] = rows.mean(0), rows.abs().mean(0)
+    prompt = torch.cat([u[:n] for u, n in zip(slots, lens)] + [torch.tensor([-1, pages * page, 2 ** 40])])
+    lr.block_keys(cache, prompt.to(dev), keys, L)
+    for i, n in enumerate(lens):
+        expect(i, n)
+    # sums in 64 bits, then two roundings
+    close(keys, want, (HALF[t] * (1 + 2 * U) + U) * want.abs() + 2.0 ** -50 * size + TINY[t])
+    step = torch.stack([u[-1] for u in slots])
+    lr.block_keys(cache, step.to(dev), keys, L)
+    for i, n in enumerate(grown):
+        expect(i, n)
+    close(keys, want, (HALF[t] * (1 + 2 * U) + U) * want.abs() + 2.0 ** -50 * size + TINY[t])
+    assert lr.block_keys(cache, step[:0].to(dev), keys, L) is keys
+
+
+def test_block_keys_layout(dev):
+    """Keys with a layout of their own (pages next to each other), in another type than an 8-bit cache's queries."""
+    h, d, page = 2, 64, 16
+    cache, table, slots, (kn, _) = attention_case(dev, "bf16", "int8", h, h, d, d, page, "tokens", [40])
+    pages = cache.k.numel() // (page * h * d)
+    keys = torch.full((d * h * pages,), -7.0, device=dev)
+    lr.block_keys(cache, slots[0].to(dev), keys, f"({d},{h},{pages}):({pages},{d * pages},1)")
+    got = keys.cpu().as_strided((pages, h, d), (1, d * pages, pages))
+    for j in range(3):
+        rows = kn[slots[0][j * page:(j + 1) * page]]
+        close(got[table[0, j]], rows.mean(0), 2 * U * rows.mean(0).abs() + 2.0 ** -50)
+    assert int((keys == -7).sum()) == (pages - 3) * h * d
+
+
+# ------------------------------------------------------------------------------------ blocks: the choice
+def chosen64(q, keys, table, lens, page, count, first, last):
+    """The choice by its definition: scores in 64 bits, sorted by (score, index)."""
+    b, heads, d = q.shape
+    pages, kv, _ = keys.shape
+    out = torch.full((b, kv, count), -1, dtype=torch.int32)
+    for i, n in enumerate(lens):
+        many = min(-(-max(n, 0) // page), table.shape[1])
+        for g in range(kv):
+            if many <= count:
+                out[i, g, :many] = torch.arange(many)
+                continue
+            at = table[i, :many].long()
+            ok = (at >= 0) & (at < pages)
+            k = keys[torch.where(ok, at, 0), g].to(F64)
+            s = (k @ q[i, g * heads // kv:(g + 1) * heads // kv].to(F64).t())
+            s = torch.where(s.isnan(), -math.inf, s).amax(-1)
+            s = torch.where(ok, s, -math.inf).tolist()
+            middle = sorted(range(first, many - last), key=lambda j: (-s[j], j))[:count - first - last]
+            out[i, g] = torch.tensor(list(range(first)) + sorted(middle) + list(range(many - last, many)))
+    return out
+
+
+SELECT = [  # type, heads, kv, d, page, lens, count, first, last
+    ("bf16", 32, 8, 128, 16, [4000, 1, 0, 300, 257], 16, 1, 2), ("fp16", 4, 4, 64, 64, [5000, 640, 641], 10, 0, 1),
+    ("fp32", 6, 2, 96, 8, [1000, 37], 5, 1, 1), ("bf16", 40, 1, 256, 16, [3000], 40, 4, 4),
+    ("bf16", 5, 1, 33, 5, [700, 2], 8, 0, 0), ("fp16", 7, 7, 72, 1, [900], 100, 10, 20), ("fp32", 1, 1, 20, 3, [500], 1, 0, 0),
+    ("fp32", 3, 1, 130, 3, [500], 2, 1, 1), ("bf16", 66, 2, 128, 16, [2000], 12, 1, 1),
+    ("bf16", 2, 1, 64, 1, [70000, 4097, 4096], 64, 1, 1), ("bf16", 16, 2, 128, 16, [40000] * 3, 2000, 1, 1),
+    ("bf16", 8, 8, 128, 16, [17 * i for i in range(70)], 9, 1, 1),
+]
+
+
+@pytest.mark.parametrize("dtype,heads,kv,d,page,lens,count,first,last", SELECT)
+@pytest.mark.parametrize("values", ["normal", "few"])
+def test_block_select(dev, dtype, heads, kv, d, page, lens, count, first, last, values):
+    """The choice is exact.  Keys of few values have many equal scores, of which the first are taken."""
+    t, b = T[dtype], len(lens)
+    width = max(-(-n // page) for n in lens) + 1
+    pages = width * b + 2
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(1)).int()[:width * b].view(b, width)
+    q, keys = rand((b, heads, d), t, 2), rand((pages, kv, d), t, 3)
+    if values == "few":
+        q, keys = ints(-1, 2, (b, heads, d), 2).to(t), torch.zeros((pages, kv, d), dtype=t)
+        keys[..., 0] = ints(-2, 3, (pages, kv), 3).to(t)
+    out = torch.full((b + 1, kv, count), -7, dtype=torch.int32, device=dev)
+    Lq, Lk = f"({d},{heads},{b}):(1,{d},{heads * d})", f"({d},{kv},{pages}):(1,{d},{kv * d})"
+    lr.block_select(q.to(dev), Lq, keys.to(dev), Lk, table.to(dev), int32(lens, dev), page, out, first=first, last=last)
+    want = chosen64(q, keys, table, lens, page, count, first, last)
+    assert torch.equal(out[:b].cpu(), want) and (out[b] == -7).all()
+
+
+def test_block_select_special_scores(dev):
+    """Infinities, NaN, zeros of both signs, pages that are none, lengths past the table, strided and offset tensors."""
+    b, heads, kv, d, page, width = 3, 4, 2, 32, 16, 40
+    pages = 130
+    table = torch.arange(b * width).int().view(b, width)
+    table[0, 5], table[0, 6], table[1, 7], table[1, 0] = -1, pages, 1 << 30, -2 ** 31
+    q, keys = rand((b, heads, d), torch.float32, 2), rand((pages, kv, d), torch.float32, 3)
+    keys[3], keys[4, :, 2], keys[9], keys[10], keys[44, 0, 1], keys[45] = 0.0, math.inf, -0.0, 0.0, math.nan, -math.inf
+    q[2, 0] = math.nan                                                  # the other head of its cache head decides
+    q[1, 2:] = math.nan                                                 # no head does: all scores equal
+    q[0, 1] = 0.0
+    lens = [width * page, 2 ** 31 - 1, width * page - 3]
+    row = d + 3
+    qb, kb = torch.full((heads * b * row + 1,), math.nan), torch.full((kv * pages * row + 1,), math.nan)
+    qb[1:].as_strided((b, heads, d), (row, b * row, 1)).copy_(q)
+    kb[1:].as_strided((pages, kv, d), (row, pages * row, 1)).copy_(keys)
+    for count, first, last in ((7, 1, 1), (7, 0, 0), (30, 3, 2), (39, 0, 0)):
+        out = torch.full((b, kv, count), -7, dtype=torch.int32, device=dev)
+        want = chosen64(q, keys, table, lens, page, count, first, last)
+        lr.block_select(q.to(dev), f"({d},{heads},{b}):(1,{d},{heads * d})", keys.to(dev), f"({d},{kv},{pages}):(1,{d},{kv * d})",
+                        table.to(dev), int32(lens, dev), page, out, first=first, last=last)
+        assert torch.equal(out.cpu(), want), (count, first, last)
+        lr.block_select(qb.to(dev)[1:], f"({d},{heads},{b}):(1,{b * row},{row})", kb.to(dev)[1:],
+                        f"({d},{kv},{pages}):(1,{pages * row},{row})", table.to(dev), int32(lens, dev), page, out.fill_(-7),
+                        first=first, last=last)
+        assert torch.equal(out.cpu(), want), ("strided", count, first, last)
+
+
+def test_block_select_by_last_bits(dev):
+    """Scores that differ in the 40th bit, and scores of every size: the border is found at any bit."""
+    d, page, n = 32, 1, 3000
+    g = torch.Generator().manual_seed(1)
+    table = torch.randperm(n, generator=g).int().view(1, n)
+    q = torch.zeros((1, 1, d))
+    q[0, 0, :2] = torch.tensor([1.0, 2.0 ** -40])
+    keys = torch.zeros((n, 1, d))
+    keys[:, 0, 0], keys[:, 0, 1] = 1.0, torch.randperm(n, generator=g).float()
+    huge = torch.zeros((n, 1, d))
+    huge[:, 0, 0] = torch.randn(n, generator=g) * torch.exp2(torch.randint(-120, 120, (n,), generator=g).float())
+    for k in (keys, huge):
+        for count in (1, 2, 100, 1500, 2999):
+            out = torch.empty((1, 1, count), dtype=torch.int32, device=dev)
+            lr.block_select(q.to(dev), f"({d},1,1):(1,{d},{d})", k.to(dev), f"({d},1,{n}):(1,{d},{d})", table.to(dev), int32([n], dev),
+                            page, out, first=0, last=0)
+            assert torch.equal(out.cpu(), chosen64(q, k, table, [n], page, count, 0, 0)), count
+
+
+# ------------------------------------------------------------------------------------ blocks: their attention
+def blocks_seen(slots, blocks, n, page):
+    """The slots of the tokens that a head's list of blocks holds, in the list's order."""
+    many = -(-n // page)
+    parts = [slots[j * page:min((j + 1) * page, n)] for j in blocks[:many].tolist() if 0 <= j < many]
+    return torch.cat(parts) if parts else slots[:0]
+
+
+def head_attention64(q, kn, vn, seen, kv, scale, t, kind):
+    """attention64 of each (sequence, cache head) by itself; seen[i][g]: slots."""
+    b, heads, dk = q.shape
+    grp = heads // kv
+    pairs = [(i, g) for i in range(b) for g in range(kv)]
+    want, lse, tol = attention64(q.reshape(b * kv, grp, dk), [kn[seen[i][g]][:, g:g + 1] for i, g in pairs],
+                                 [vn[seen[i][g]][:, g:g + 1] for i, g in pairs], scale, t, kind)
+    out = tol.reshape(b, heads, -1)
+    out.lse = tol.lse.reshape(b, heads)
+    return want.reshape(b, heads, -1), lse.reshape(b, heads), out
+
+
+BLOCKS = [  # type, kind, heads, kv, dk, dv, page, order, lens, count
+    ("bf16", "bf16", 8, 2, 128, 128, 16, "tokens", [1, 15, 0, 129, 700], 5),
+    ("bf16", "bf16", 32, 8, 128, 128, 64, "heads", [1000, 64, 65, 3000], 9),
+    ("fp16", "fp16", 8, 8, 64, 64, 16, "heads", [31, 500], 40), ("fp32", "fp32", 6, 3, 128, 128, 16, "tokens", [0, 65, 300], 4),
+    ("bf16", "e4m3", 32, 8, 128, 128, 64, "heads", [63, 1000, 64], 6), ("fp16", "int8", 20, 1, 80, 80, 32, "tokens", [40, 900], 11),
+    ("fp32", "int8", 5, 1, 64, 64, 16, "tokens", [100], 3), ("bf16", "bf16", 16, 1, 192, 128, 16, "tokens", [257, 64], 7),
+    ("bf16", "bf16", 48, 1, 256, 256, 16, "heads", [200, 31], 5), ("fp16", "fp16", 7, 1, 72, 72, 8, "tokens", [9, 333], 17),
+    ("bf16", "bf16", 4, 2, 33, 17, 5, "tokens", [4, 6, 250], 21), ("bf16", "e4m3", 14, 2, 112, 112, 1, "tokens", [77, 1], 30),
+    ("fp32", "e4m3", 4, 2, 96, 80, 8, "heads", [100], 6), ("bf16", "bf16", 4, 4, 128, 128, 16, "column", [20, 100], 3),
+    ("bf16", "bf16", 2, 1, 160, 96, 16, "tokens", [4000], 200), ("bf16", "int8", 8, 4, 32, 32, 128, "tokens", [9000, 2049], 30),
+    ("bf16", "bf16", 64, 8, 128, 128, 16, "tokens", [(389 * i) % 1500 for i in range(70)], 20),
+]
+
+
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,order,lens,count", BLOCKS)
+def test_block_attention(dev, dtype, kind, heads, kv, dk, dv, page, order, lens, count):
+    """Each cache head with a list of its own, in any order, with holes, the last block, ended lists."""
+    t, b = T[dtype], len(lens)
+    cache, table, slots, (kn, vn) = attention_case(dev, dtype, kind, heads, kv, dk, dv, page, order, lens)
+    g = torch.Generator().manual_seed(7)
+    blocks = torch.full((b, kv, count), -1, dtype=torch.int32)
+    for i, n in enumerate(lens):
+        many = -(-n // page)
+        for h in range(kv):
+            own = torch.randperm(max(many, 1), generator=g)[:min(many, count)].int()
+            if h == 0 and many:
+                own[-1] = many - 1                                      # the block that ends with the sequence (twice, perhaps)
+            blocks[i, h, :len(own)] = own
+    if b > 1 and lens[-1] > page:
+        blocks[-1, 0, 0], blocks[-1, -1, min(1, count - 1)] = -1, 1 << 30
+    q = rand((b, heads, dk), t, 11)
+    out, lse = torch.full((b, heads, dv), -7.0, dtype=t, device=dev), torch.full((b, heads), -7.0, device=dev)
+    Lq, Lo = f"({dk},{heads},{b}):(1,{dk},{heads * dk})", f"({dv},{heads},{b}):(1,{dv},{heads * dv})"
+    lr.block_attention(q.to(dev), Lq, cache, blocks.to(dev), table.to(dev), int32(lens, dev), out, Lo, lse=lse)
+    seen = [[blocks_seen(slots[i], blocks[i, h], lens[i], page) for h in range(kv)] for i in range(b)]
+    want, wlse, tol = head_attention64(q, kn, vn, seen, kv, dk ** -0.5, t, kind)
+    close(out, want, tol, "out")
+    close(lse, wlse, tol.lse, "lse")
+
+
+@pytest.mark.parametrize("dtype,kind,d", [("bf16", "bf16", 64), ("bf16", "e4m3", 64), ("bf16", "bf16", 33)])
+def test_block_attention_lists(dev, dtype, kind, d):
+    """Lists of nothing, of more entries than the sequence has blocks, of one block over and over, of blocks behind the
+    sequence's end and past the table; lengths past the table; pages that are none."""
+    t, heads, kv, page = T[dtype], 4, 2, 16
+    lens = [100, 50, 33]
+    cache, table, slots, (kn, vn) = attention_case(dev, dtype, kind, heads, kv, d, d, page, "tokens", lens)
+    blocks = torch.tensor([[[-1] * 7, [3, 3, 3, 3, 3, 3, 3]],
+                           [[0, 1, 2, 3, 3, 2, 1], [3, -2 ** 31, 2 ** 31 - 1, 0, 0, 0, 0]],
+                           [[5, 3, 7, 0, 1, 2, 2], [2, 1, 0, 2, 1, 0, 2]]], dtype=torch.int32)
+    q, L = rand((3, heads, d), t, 11), f"({d},{heads},3):(1,{d},{heads * d})"
+    out, lse = torch.empty((3, heads, d), dtype=t, device=dev), torch.empty((3, heads), device=dev)
+    lr.block_attention(q.to(dev), L, cache, blocks.to(dev), table.to(dev), int32(lens, dev), out, L, lse=lse)
+    seen = [[blocks_seen(slots[i], blocks[i, h], lens[i], page) for h in range(kv)] for i in range(3)]
+    want, wlse, tol = head_attention64(q, kn, vn, seen, kv, d ** -0.5, t, kind)
+    close(out, want, tol)
+    close(lse, wlse, tol.lse)
+    assert (out[0, :2] == 0).all() and (lse[0, :2] == -math.inf).all()
+    narrow = table[:, :3].clone()                                        # 48 tokens at most, whatever the lengths say
+    narrow[0, 1] = -1
+    lr.block_attention(q.to(dev), L, cache, blocks.to(dev), narrow.contiguous().to(dev), int32([100, 2 ** 31 - 1, -9], dev), out, L,
+                       lse=lse)
+    blocks[0] = torch.where(blocks[0] == 1, -1, blocks[0])
+    seen = [[blocks_seen(slots[i], blocks[i, h], n, page) for h in range(kv)] for i, n in enumerate((48, 48, 0))]
+    want, wlse, tol = head_attention64(q, kn, vn, seen, kv, d ** -0.5, t, kind)
+    close(out, want, tol)
+    close(lse, wlse, tol.lse)
+
+
+def test_block_attention_of_all_is_paged_attention(dev):
+    t, lens, heads, kv, d, page = torch.bfloat16, [700, 33, 0, 1600], 16, 4, 128, 16
+    cache, table, slots, (kn, vn) = attention_case(dev, "bf16", "bf16", heads, kv, d, d, page, "heads", lens)
+    q, L = rand((4, heads, d), t, 11).to(dev), f"({d},{heads},4):(1,{d},{heads * d})"
+    blocks = torch.arange(100, dtype=torch.int32).expand(4, kv, 100).contiguous().to(dev)
+    one, two = (torch.empty((4, heads, d), dtype=t, device=dev) for _ in range(2))
+    lr.block_attention(q, L, cache, blocks, table.to(dev), int32(lens, dev), one, L)
+    lr.paged_attention(q, L, cache, table.to(dev), int32(lens, dev), two, L)
+    want, _, tol = attention64(q.cpu(), [kn[u] for u in slots], [vn[u] for u in slots], d ** -0.5, t, "bf16")
+    close(one, want, tol)
+    close(two, want, tol)
+
+
+# ------------------------------------------------------------------------------------ together
+def test_steps_on_streams_and_in_a_graph(dev):
+    """Decoding steps as they would be used: positions of three axes, keys turned as they are stored, the blocks' keys,
+    their choice and their attention, and attention over a shared prefix; on another stream, then captured and
+    replayed with new inputs, against the same calls made eagerly."""
+    b, h, kv, d, page, width, count = 3, 8, 2, 64, 16, 40, 6
+    pages = b * width + 4
+    perm = torch.randperm(pages, generator=torch.Generator().manual_seed(5)).int().to(dev)
+    table, prefix = perm[:b * width].view(b, width).contiguous(), perm[b * width:].contiguous()
+    rt = lr.rope_axes_table(d, [12, 10, 10], order="cyclic", device=dev)
+    L, Lk = lr.Layout(f"({d},{h},{b}):(1,{d},{h * d})"), lr.Layout(f"({d},{kv},{b}):(1,{d},{kv * d})")
+    Lkeys = lr.Layout(f"({d},{kv},{pages}):(1,{d},{kv * d})")
+    plen = int32([60], dev)
+
+    def fresh():
+        """A cache whose prefix and first tokens are written, and their blocks' keys."""
+        k, v = (torch.zeros(pages * page * kv * d, dtype=torch.uint8, device=dev) for _ in range(2))
+        ks, vs = (torch.zeros(pages * page * kv, device=dev) for _ in range(2))
+        lay = f"({d},{kv},{page},{pages}):(1,{d},{kv * d},{page * kv * d})"
+        cache = lr.PagedCache(k, lay, v, lay, ks, vs, f"({kv},{page},{pages}):(1,{kv},{page * kv})")
+        n = 60 + 300 * b
+        at = torch.arange(300, device=dev)
+        slots = torch.cat([prefix.long()[at[:60] // page] * page + at[:60] % page]
+                          + [table[i].long()[at // page] * page + at % page for i in range(b)])
+        x = rand((n, kv, d), torch.bfloat16, 77).to(dev)
+        Ln = f"({d},{kv},{n}):(1,{d},{kv * d})"
+        lr.cache_write_axes(cache, x, Ln, x, Ln, slots, rt, ints(0, 500, (3, n), 6).to(dev))
+        keys = torch.zeros((pages, kv, d), dtype=torch.bfloat16, device=dev)
+        lr.block_keys(cache, slots, keys, Lkeys)
+        return cache, keys
+
+    def inputs(i):
+        pos = torch.tensor([300 + i] * b, device=dev)
+        q, k, v = (rand((b, n, d), torch.bfloat16, 100 * i + n + j).to(dev) for j, n in enumerate((h, kv, kv)))
+        slots = table.long()[torch.arange(b, device=dev), pos // page] * page + pos % page
+        return q, k, v, ints(0, 400, (3, b), i).to(dev), slots, (pos + 1).int()
+
+    plans = (lr.prefix_attention_plan(L, fresh()[0], L, prefix.numel(), width, torch.bfloat16),
+             lr.block_attention_plan(L, fresh()[0], L, count, torch.bfloat16), lr.block_select_plan(L, Lkeys, width))
+    spaces = [torch.empty(max(p["workspace_bytes"], 1), dtype=torch.uint8, device=dev) for p in plans]
+
+    def made():
+        return (torch.empty((b, h, d), dtype=torch.bfloat16, device=dev), torch.empty((b, kv, count), dtype=torch.int32, device=dev),
+                torch.empty((b, h, d), dtype=torch.bfloat16, device=dev), torch.empty((b, h, d), dtype=torch.bfloat16, device=dev))
+
+    def step(held, x, out, ws, stream=None):
+        (cache, keys), (q, k, v, pos, slots, lens), (qr, blocks, one, two) = held, x, out
+        w = ws if ws else (None,) * 3
+        lr.rope_axes(q, L, qr, L, pos, rt, stream=stream)
+        lr.cache_write_axes(cache, k, Lk, v, Lk, slots, rt, pos, stream=stream)
+        lr.block_keys(cache, slots, keys, Lkeys, stream=stream)
+        lr.block_select(qr, L, keys, Lkeys, table, lens, page, blocks, workspace=w[2], stream=stream)
+        lr.block_attention(qr, L, cache, blocks, table, lens, one, L, workspace=w[1], stream=stream)
+        lr.prefix_attention(qr, L, cache, prefix, plen, table, lens, two, L, workspace=w[0], stream=stream)
+
+    xs = [inputs(i) for i in range(5)]
+    eager, want = fresh(), []
+    for x in xs:
+        want.append(made())
+        step(eager, x, want[-1], spaces)
+    torch.cuda.synchronize()
+    # the choice and the attentions against 64 bits, from what the cache then holds
+    cache, keys = eager
+    q, blocks = want[-1][0].cpu(), want[-1][1].cpu()
+    assert torch.equal(blocks, chosen64(q, keys.cpu(), table.cpu(), [305] * b, page, count, 1, 1))
+    info = ("tokens", pages, page, kv, 0)
+    kn, vn = (c.to(F64) * s.to(F64)[..., None] for c, s in (content(cache, info, d, w) for w in ("k", "v")))
+    at = torch.arange(305)
+    slots = [table[i].cpu().long()[at // page] * page + at % page for i in range(b)]
+    seen = [[blocks_seen(slots[i], blocks[i, g], 305, page) for g in range(kv)] for i in range(b)]
+    exact, _, tol = head_attention64(q, kn, vn, seen, kv, d ** -0.5, torch.bfloat16, "e4m3")
+    close(want[-1][2], exact, tol, "blocks")
+    shared = prefix.cpu().long()[at[:60] // page] * page + at[:60] % page
+    seen = [torch.cat([shared, u]) for u in slots]
+    exact, _, tol = attention64(q, [kn[u] for u in seen], [vn[u] for u in seen], d ** -0.5, torch.bfloat16, "e4m3")
+    close(want[-1][3], exact, tol, "prefix")
+    # another stream, workspaces allocated by the calls
+    side, held = torch.cuda.Stream(), fresh()
+    for i, x in enumerate(xs):
+        out = made()
+        torch.cuda.synchronize()
+        step(held, x, out, None, stream=side)
+        side.synchronize()
+        assert all(torch.equal(a, w) for a, w in zip(out, want[i])), i
+    # a graph, its inputs copied in before each replay
+    held, x, out = fresh(), [z.clone() for z in xs[0]], made()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(held, x, out, spaces)
+    for i in range(5):
+        for dst, src in zip(x, xs[i]):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, w) for a, w in zip(out, want[i])), i
+        torch.randn(1 << 20, device=dev).sum().item()                    # eager work between the replays
