@@ -18,18 +18,20 @@ struct BlockKeysArgs {
   int32_t dim;
 };
 
-// A wave has one cache head and `chunk` entries of slots, and makes the mean of every page whose newest slot is among
-// them.  A row of a page is a group of lanes with V elements each, as many rows at a time as the wave has groups, their
-// loads four ahead.  Sums are held in 64 bits, in which those of a page of codes or 16-bit keys are exact but for
-// extreme ranges: the mean is rounded once, and which blocks a score selects does not hang on the order of a sum.
+// A workgroup has `chunk` entries of slots and makes the mean of every page whose newest slot is among them; its waves
+// take cache heads of one page side by side, which share lines of memory, their scales above all.  A row of a page is a
+// group of lanes with V elements each, as many rows at a time as the wave has groups, their loads four ahead.  Sums are
+// held in 64 bits, in which those of a page of codes or 16-bit keys are exact but for extreme ranges: which blocks a
+// score selects does not hang on the order of a sum.  The groups' sums are added by halves, each half of the lanes
+// keeping half of the columns, so that a lane ends with few to divide and store.
 template <int DT, int CT, int V>
-__global__ void __launch_bounds__(64) k_block_keys(BlockKeysArgs a) {
+__global__ void __launch_bounds__(256) k_block_keys(BlockKeysArgs a) {
   using T = typename ElemOf<DT>::T;
   using C = typename ElemOf<CT>::T;
   using Vec = typename Chunk<C, V>::Vec;
   constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
-  const uint32_t lane = threadIdx.x, h = blockIdx.y;
-  const uint64_t first = (uint64_t)blockIdx.x * a.chunk, at = first + lane;
+  const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
+  const uint64_t at = (uint64_t)blockIdx.x * a.chunk + lane;
   const bool mine = lane < a.chunk && at < a.n;
   const int64_t slot = mine ? a.slots[at] : -1, next = mine && at + 1 < a.n ? a.slots[at + 1] : -1;
   const bool held = (uint64_t)slot < (uint64_t)a.cache_slots;
@@ -40,45 +42,69 @@ __global__ void __launch_bounds__(64) k_block_keys(BlockKeysArgs a) {
   uint32_t lanes = 1;  // of a row, a power of two
   while (lanes * V < (uint32_t)a.dim && lanes < 64) lanes *= 2;
   const uint32_t rows = 64 / lanes, row = lane / lanes, col = lane % lanes * V;
-  while (todo) {
+  const uint32_t side = min(a.heads, 4u) == 3 ? 4 : min(a.heads, 4u), mates = 4 / side;  // heads, pages at a time
+  for (uint32_t rank = 0; todo; ++rank) {
     const int f = __ffsll((unsigned long long)todo) - 1;
     todo &= todo - 1;
+    if (rank % mates != w / side) continue;
     const uint32_t p = uniform(__shfl(page, f)), count = uniform(__shfl(in, f)) + 1;
-    const C* k = (const C*)a.k + (int64_t)p * a.kp + (int64_t)h * a.kh;
-    const float* ks = kQuant ? a.ks + (int64_t)p * a.sp + (int64_t)h * a.sh : nullptr;
-    T* out = (T*)a.out + (int64_t)p * a.op + (int64_t)h * a.oh;
-    for (uint32_t e0 = 0; e0 < (uint32_t)a.dim; e0 += lanes * V) {
-      const uint32_t e = e0 + col;
-      const bool ok = e < (uint32_t)a.dim;
-      double sum[V] = {};
-      for (uint32_t t0 = 0; t0 < count; t0 += 4 * rows) {
-        Vec x[4];
-        float s[4];
+    for (uint32_t h = blockIdx.y * 4 + w % side; h < min(a.heads, (blockIdx.y + 1) * 4); h += side) {
+      const C* k = (const C*)a.k + (int64_t)p * a.kp + (int64_t)h * a.kh;
+      const float* ks = kQuant ? a.ks + (int64_t)p * a.sp + (int64_t)h * a.sh : nullptr;
+      T* out = (T*)a.out + (int64_t)p * a.op + (int64_t)h * a.oh;
+      for (uint32_t e0 = 0; e0 < (uint32_t)a.dim; e0 += lanes * V) {
+        const bool ok = e0 + col < (uint32_t)a.dim;
+        double sum[V] = {};
+        for (uint32_t t0 = 0; t0 < count; t0 += 4 * rows) {
+          Vec x[4];
+          float s[4];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const uint32_t t = t0 + z * rows + row < count ? t0 + z * rows + row : 0;
-          const C* r = k + (int64_t)t * a.ksl + (ok ? (int64_t)e * a.kd : 0);
-          x[z] = *(const Vec*)r;
-          s[z] = 1.f;
-          if constexpr (kQuant) s[z] = ks[(int64_t)t * a.ssl];
-        }
+          for (uint32_t z = 0; z < 4; ++z) {
+            if (t0 + z * rows >= count) continue;  // the same for all lanes
+            const uint32_t t = min(t0 + z * rows + row, count - 1);
+            x[z] = *(const Vec*)(k + (int64_t)t * a.ksl + (ok ? (int64_t)(e0 + col) * a.kd : 0));
+            if constexpr (kQuant) s[z] = ks[(int64_t)t * a.ssl];
+          }
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          if (t0 + z * rows + row >= count) continue;
+          for (uint32_t z = 0; z < 4; ++z) {
+            if (t0 + z * rows + row >= count) continue;
+            float v[V];
+            if constexpr (kQuant && V > 1) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const double v = (double)value_of<CT>(V == 1 ? x[z][0] : x[z][i]);
-            sum[i] += kQuant ? v * (double)s[z] : v;
+              for (int i = 0; i < V; i += 4) {
+                const F4 d = decode4<CT>(((const uint32_t*)&x[z])[i / 4]);
+                v[i] = d[0], v[i + 1] = d[1], v[i + 2] = d[2], v[i + 3] = d[3];
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < V; ++i) v[i] = value_of<CT>(x[z][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] = kQuant ? __builtin_fma((double)v[i], (double)s[z], sum[i]) : sum[i] + (double)v[i];
           }
         }
-      }
+        uint32_t first = 0, left = V;  // the columns that this lane is left with
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        for (uint32_t x = lanes; x < 64; x *= 2) sum[i] += __shfl_xor(sum[i], (int)x);
-      }
-      if (row == 0 && ok) {
+        for (int d = 32, n = V; d; d >>= 1, n = n > 1 ? n / 2 : 1) {
+          if ((uint32_t)d < lanes) continue;
+          const bool high = lane & d;
+          if (n > 1) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) out[(int64_t)(e + i) * a.od] = (T)(float)(sum[i] / (double)count);
+            for (int i = 0; i < n / 2; ++i) {
+              double low = sum[i], up = sum[n / 2 + i];
+              asm("" : "+v"(low), "+v"(up));  // values: not one element of sum at an index of the lane's own
+              sum[i] = (high ? up : low) + __shfl_xor(high ? low : up, d);
+            }
+            first += high ? n / 2 : 0;
+            left = n / 2;
+          } else {
+            sum[0] += __shfl_xor(sum[0], d);
+          }
+        }
+        const double part = 1.0 / (double)count;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if ((uint32_t)i < left && ok) out[(int64_t)(e0 + col + first + i) * a.od] = (T)(float)(sum[i] * part);
       }
     }
   }
@@ -109,61 +135,62 @@ typedef double D4 __attribute__((ext_vector_type(4)));
 // score(b, g, j) = max over the query heads h of cache head g of q[b, h] . key[table[b, j], g], in 64 bits: which blocks
 // are chosen hangs on scores that differ in their last bits, so these are as good as exact.  16 blocks x 16 heads are a
 // product of 64-bit matrix instructions, as fast as the vector units' 64 bits, with the sums over the lanes done; they
-// take 2048 cycles of a SIMD for 16 blocks of 128, so that reading 256 bytes a block stays the longer part.  The keys
-// come from memory as the product's first operand (16 rows, each lane a chunk of 16 bytes), the queries lie in shared
-// memory in the order of the second.
+// take 2048 cycles of a SIMD for 16 blocks of 128.  Keys and queries come from memory as the products' operands
+// themselves (16 rows, each lane a chunk of 16 bytes), so that waves share nothing; a wave takes every fourth tile of
+// its workgroup's, the next one's keys under way.
 template <int DT, int DC, bool WIDE>
 __global__ void __launch_bounds__(256) k_block_scores(SelectArgs a) {
   using T = typename ElemOf<DT>::T;
   constexpr uint32_t E = DT == LR_F32 ? 4 : 8;  // elements of a chunk
   using Vec = typename Chunk<T, (int)E>::Vec;
   constexpr uint32_t kChunks = DC / (4 * E);
-  __shared__ double qs[DC / 4 * 64];
   const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64), r = lane & 15, j = lane >> 4;
   const uint32_t bg = op_div(blockIdx.x, a.fd_runs), b = op_div(bg, a.fd_heads), g = bg - b * a.kv_heads;
   const uint32_t many = blocks_of(a, a.lens[b]);
-  const uint32_t begin = (blockIdx.x - bg * a.runs) * 64 * a.rounds;
-  if (begin >= many || many <= a.count) return;  // all are taken: nothing to compare
+  const uint32_t begin = (blockIdx.x - bg * a.runs) * 64 * a.rounds + 16 * w, end = min(begin + 64 * a.rounds, many);
+  if (begin >= end || many <= a.count) return;  // all are taken: nothing to compare
   const int32_t* table = a.table + (int64_t)b * a.table_stride;
   double* scores = a.scores + (uint64_t)bg * a.max_pages;
-  const uint32_t tiles = (a.group + 15) / 16;
-  for (uint32_t tile = 0; tile < tiles; ++tile) {
-    if (tile) __syncthreads();
-    for (uint32_t x = threadIdx.x; x < kChunks * E * 64; x += 256) {
-      const uint32_t s = x / 64, l = x % 64, h = tile * 16 + l % 16, e = (s / E * 4 + l / 16) * E + s % E;
-      const bool ok = h < a.group && e < (uint32_t)a.dim;
-      const T* q = (const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group + (ok ? h : 0)) * a.qh;
-      qs[x] = ok ? (double)value_of<DT>(q[(int64_t)e * a.qd]) : 0.0;
+  auto load = [&](const T* row, int64_t stride, bool there, Vec* x) {
+#pragma unroll
+    for (uint32_t c = 0; c < kChunks; ++c) {
+      const uint32_t e0 = (c * 4 + j) * E;
+      if constexpr (WIDE) {
+        x[c] = *(const Vec*)(row + (e0 < (uint32_t)a.dim ? e0 : 0));
+        if (!there || e0 >= (uint32_t)a.dim) x[c] = Vec{};
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < E; ++i)
+          x[c][i] = there && e0 + i < (uint32_t)a.dim ? row[(int64_t)(e0 + i) * stride] : (T)0.f;
+      }
     }
-    __syncthreads();
-    const bool head = tile * 16 + r < a.group;
-    for (uint32_t t = 0; t < a.rounds; ++t) {
-      const uint32_t j0 = begin + t * 64 + w * 16, at = j0 + r;
-      if (j0 >= many) break;
-      int32_t page = at < many ? table[at] : -1;
-      const bool there = (uint32_t)page < a.pages;
-      const T* key = (const T*)a.keys + (int64_t)(there ? page : 0) * a.kp + (int64_t)g * a.kh;
+  };
+  auto page_at = [&](uint32_t j0) { return j0 + r < many ? table[j0 + r] : -1; };
+  auto key_of = [&](int32_t page) {
+    return (const T*)a.keys + (int64_t)((uint32_t)page < a.pages ? page : 0) * a.kp + (int64_t)g * a.kh;
+  };
+  for (uint32_t h0 = 0; h0 < a.group; h0 += 16) {
+    Vec q[kChunks], next[kChunks];
+    int32_t page = page_at(begin);
+    const bool head = h0 + r < a.group;
+    load((const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group + (head ? h0 + r : 0)) * a.qh, a.qd, head, q);
+    load(key_of(page), a.kd, true, next);
+    for (uint32_t j0 = begin; j0 < end; j0 += 64) {
       Vec k[kChunks];
 #pragma unroll
-      for (uint32_t c = 0; c < kChunks; ++c) {
-        const uint32_t e0 = (c * 4 + j) * E;
-        if constexpr (WIDE) {
-          k[c] = *(const Vec*)(key + (e0 < (uint32_t)a.dim ? e0 : 0));
-          if (e0 >= (uint32_t)a.dim) k[c] = Vec{};
-        } else {
-#pragma unroll
-          for (uint32_t i = 0; i < E; ++i) k[c][i] = e0 + i < (uint32_t)a.dim ? key[(int64_t)(e0 + i) * a.kd] : (T)0.f;
-        }
+      for (uint32_t c = 0; c < kChunks; ++c) k[c] = next[c];
+      const uint64_t seen = __ballot((uint32_t)page < a.pages);
+      if (j0 + 64 < end) {
+        page = page_at(j0 + 64);
+        load(key_of(page), a.kd, true, next);
       }
       D4 acc = {};
 #pragma unroll
-      for (uint32_t c = 0; c < kChunks; ++c) {
+      for (uint32_t c = 0; c < kChunks; ++c)
 #pragma unroll
         for (uint32_t i = 0; i < E; ++i)
-          acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)value_of<DT>(k[c][i]), qs[(c * E + i) * 64 + lane], acc, 0, 0, 0);
-      }
+          acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)value_of<DT>(k[c][i]), (double)value_of<DT>(q[c][i]), acc, 0, 0, 0);
       // lane r, j has head r of blocks j, 4 + j, 8 + j, 12 + j
-      const uint64_t seen = __ballot(there);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         double x = head ? acc[i] : -__builtin_inf();
@@ -172,7 +199,7 @@ __global__ void __launch_bounds__(256) k_block_scores(SelectArgs a) {
         const uint32_t row = 4 * i + j;
         if (r == 0 && j0 + row < many) {
           x = x == x && (seen >> row & 1) ? x : -__builtin_inf();
-          if (tile) x = fmax(x, scores[j0 + row]);
+          if (h0) x = fmax(x, scores[j0 + row]);
           scores[j0 + row] = x;
         }
       }
@@ -189,15 +216,15 @@ __device__ __forceinline__ uint64_t order_of(double x) {
 // One workgroup chooses for one sequence and cache head: the first and the last blocks, and of the others the best.
 // The score at the border is found a digit of 8 bits at a time, from the highest bit in which any two scores differ,
 // until a digit's scores are all taken or all bits are known; the chosen blocks are then written in their order, of
-// equal scores at the border the first ones.
-constexpr uint32_t kHeldScores = 4096;  // in shared memory; more are read again for each digit
-template <int LANES>
+// equal scores at the border the first ones.  A lane keeps the first HELD scores of its own; those of longer rows are
+// read again for each digit.
+template <int LANES, int HELD>
 __global__ void __launch_bounds__(LANES) k_block_choose(SelectArgs a) {
-  __shared__ uint64_t held[kHeldScores];
+  constexpr uint32_t kWaves = LANES / 64;
   __shared__ uint32_t hist[256];
-  __shared__ uint64_t ends[2][LANES / 64];
+  __shared__ uint64_t ends[2][kWaves];
   __shared__ uint32_t found[3];
-  __shared__ uint32_t before[2][2][LANES / 64];
+  __shared__ uint32_t before[2][2][HELD * kWaves];
   const uint32_t lane = threadIdx.x & 63, w = threadIdx.x / 64, bg = blockIdx.x, b = op_div(bg, a.fd_heads);
   const uint32_t many = blocks_of(a, a.lens[b]);
   int32_t* out = a.out + (uint64_t)bg * a.count;
@@ -210,24 +237,37 @@ __global__ void __launch_bounds__(LANES) k_block_choose(SelectArgs a) {
   uint32_t need = a.count - a.first - a.last;
   uint64_t border = ~(uint64_t)0;  // taken: above it, and the first `equal` of those on it
   uint32_t equal = 0;
-  const bool fits = hi - lo <= kHeldScores;
-  auto score = [&](uint32_t i) { return fits ? held[i - lo] : order_of(scores[i]); };
+  uint64_t held[HELD];
+#pragma unroll
+  for (uint32_t k = 0; k < HELD; ++k) {
+    const uint32_t i = k * LANES + threadIdx.x;
+    held[k] = order_of(i >= lo && i < hi ? scores[i] : 0.0);
+  }
+  // f(i, score) for this lane's blocks that are chosen from
+  auto each = [&](auto f) {
+#pragma unroll
+    for (uint32_t k = 0; k < HELD; ++k) {
+      const uint32_t i = k * LANES + threadIdx.x;
+      if (i >= lo && i < hi) f(held[k]);
+    }
+    for (uint32_t i = HELD * LANES + threadIdx.x; i < hi; i += LANES)
+      if (i >= lo) f(order_of(scores[i]));
+  };
   if (need) {
     uint64_t least = ~(uint64_t)0, most = 0;
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += LANES) {
-      const uint64_t s = order_of(scores[i]);
-      if (fits) held[i - lo] = s;
+    each([&](uint64_t s) {
       least = s < least ? s : least;
       most = s > most ? s : most;
-    }
+    });
     for (int d = 32; d; d >>= 1) {
       const uint64_t x = __shfl_xor((unsigned long long)least, d), y = __shfl_xor((unsigned long long)most, d);
       least = x < least ? x : least;
       most = y > most ? y : most;
     }
     if (lane == 0) ends[0][w] = least, ends[1][w] = most;
+    for (uint32_t i = threadIdx.x; i < 256; i += LANES) hist[i] = 0;
     __syncthreads();
-    for (uint32_t i = 0; i < LANES / 64; ++i) {
+    for (uint32_t i = 0; i < kWaves; ++i) {
       least = ends[0][i] < least ? ends[0][i] : least;
       most = ends[1][i] > most ? ends[1][i] : most;
     }
@@ -236,17 +276,17 @@ __global__ void __launch_bounds__(LANES) k_block_choose(SelectArgs a) {
     equal = need;
     while (bit) {
       const uint32_t from = bit > 8 ? bit - 8 : 0, bins = 1u << (bit - from);
-      for (uint32_t i = threadIdx.x; i < 256; i += LANES) hist[i] = 0;
-      __syncthreads();
-      for (uint32_t i = lo + threadIdx.x; i < hi; i += LANES) {
-        const uint64_t s = score(i);
+      each([&](uint64_t s) {
         if (bit == 64 || s >> bit == border >> bit) atomicAdd(&hist[(uint32_t)(s >> from) & (bins - 1)], 1u);
-      }
+      });
       __syncthreads();
-      if (w == 0) {  // four bins a lane, from the highest down
+      if (w == 0) {  // four bins a lane, from the highest down; empty again for the next digit
         uint32_t c[4], sum = 0;
 #pragma unroll
-        for (int z = 0; z < 4; ++z) sum += c[z] = hist[255 - (4 * lane + z)];
+        for (int z = 0; z < 4; ++z) {
+          sum += c[z] = hist[255 - (4 * lane + z)];
+          hist[255 - (4 * lane + z)] = 0;
+        }
         uint32_t above = wave_scan(sum, lane) - sum;
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
@@ -265,35 +305,56 @@ __global__ void __launch_bounds__(LANES) k_block_choose(SelectArgs a) {
     }
   }
   const bool some = equal && equal != ~0u;  // of equal scores the first ones
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
   uint32_t done = 0, level = 0;             // written; met on the border
-  for (uint32_t i0 = 0, turn = 0; i0 < many; i0 += LANES, turn ^= 1) {
-    const uint32_t i = i0 + threadIdx.x;
-    const bool choice = i >= lo && i < hi;
-    const uint64_t s = choice && equal ? score(i) : 0, below = ((uint64_t)1 << lane) - 1;
-    const bool on = choice && equal && s == border;
-    bool take = i < many && (!choice || (equal && (s > border || (on && !some))));
-    if (some) {
-      const uint64_t ons = __ballot(on);
-      if (lane == 0) before[turn][0][w] = (uint32_t)__popcll(ons);
-      __syncthreads();
-      uint32_t rank = level + (uint32_t)__popcll(ons & below);
-      for (uint32_t z = 0; z < LANES / 64; ++z) {
-        const uint32_t c = before[turn][0][z];
-        if (z < w) rank += c;
-        level += c;
+  // HELD runs of LANES blocks at a time: each wave's counts of all of them, and the sums of those before it
+  for (uint32_t i0 = 0, turn = 0; i0 < many; i0 += HELD * LANES, turn ^= 1) {
+    uint64_t s[HELD];
+    bool take[HELD];
+#pragma unroll
+    for (uint32_t k = 0; k < HELD; ++k) {
+      const uint32_t i = i0 + k * LANES + threadIdx.x;
+      const bool choice = i >= lo && i < hi;
+      s[k] = i0 == 0 ? held[k] : choice ? order_of(scores[i]) : 0;
+      const bool on = choice && equal && s[k] == border;
+      take[k] = i < many && (!choice || (equal && (s[k] > border || (on && !some))));
+      s[k] = on;  // from here on only that
+    }
+    auto counts = [&](uint32_t which, auto flag) {
+#pragma unroll
+      for (uint32_t k = 0; k < HELD; ++k) {
+        const uint64_t x = __ballot(flag(k));
+        if (lane == 0) before[turn][which][k * kWaves + w] = (uint32_t)__popcll(x);
       }
-      take = take || (on && rank < equal);
+      __syncthreads();
+      if (w == 0) {  // running sums over HELD * kWaves counts
+        uint32_t sum = 0;
+        for (uint32_t x = 0; x < HELD * kWaves; x += 64) {
+          const uint32_t c = x + lane < HELD * kWaves ? before[turn][which][x + lane] : 0;
+          const uint32_t upto = wave_scan(c, lane);
+          if (x + lane < HELD * kWaves) before[turn][which][x + lane] = sum + upto;
+          sum += uniform(__shfl(upto, 63));
+        }
+      }
+      __syncthreads();
+    };
+    auto start = [&](uint32_t which, uint32_t k) { return k * kWaves + w ? before[turn][which][k * kWaves + w - 1] : 0; };
+    if (some) {
+      counts(0, [&](uint32_t k) { return s[k] != 0; });
+#pragma unroll
+      for (uint32_t k = 0; k < HELD; ++k) {
+        const uint32_t rank = level + start(0, k) + (uint32_t)__popcll(__ballot(s[k] != 0) & below);
+        take[k] = take[k] || (s[k] && rank < equal);
+      }
+      level += before[turn][0][HELD * kWaves - 1];
     }
-    const uint64_t takes = __ballot(take);
-    if (lane == 0) before[turn][1][w] = (uint32_t)__popcll(takes);
-    __syncthreads();
-    uint32_t at = done + (uint32_t)__popcll(takes & below);
-    for (uint32_t z = 0; z < LANES / 64; ++z) {
-      const uint32_t c = before[turn][1][z];
-      if (z < w) at += c;
-      done += c;
+    counts(1, [&](uint32_t k) { return take[k]; });
+#pragma unroll
+    for (uint32_t k = 0; k < HELD; ++k) {
+      const uint32_t at = done + start(1, k) + (uint32_t)__popcll(__ballot(take[k]) & below);
+      if (take[k]) out[at] = (int32_t)(i0 + k * LANES + threadIdx.x);
     }
-    if (take) out[at] = (int32_t)i;
+    done += before[turn][1][HELD * kWaves - 1];
   }
 }
 
@@ -315,15 +376,14 @@ static int rows_of(const lr_layout* L, int64_t capacity, bool output, Rows* r) {
 
 template <int DT, int CT, int V>
 static int launch_keys(const BlockKeysArgs& a, dim3 grid, hipStream_t st) {
-  hipLaunchKernelGGL((k_block_keys<DT, CT, V>), grid, dim3(64), 0, st, a);
+  hipLaunchKernelGGL((k_block_keys<DT, CT, V>), grid, dim3(256), 0, st, a);
   return check_op_launch();
 }
 // In chunks of v elements, or one at a time.
 template <int DT, int CT>
 static int launch_keys_of(const BlockKeysArgs& a, int64_t v, dim3 grid, hipStream_t st) {
-  constexpr int kMost = CT == LR_F32 ? 4 : CT == LR_E4M3 || CT == LR_INT8 ? 16 : 8;
+  constexpr int kMost = CT == LR_F32 ? 4 : 8;
   if (v == kMost) return launch_keys<DT, CT, kMost>(a, grid, st);
-  if (v == kMost / 2 && v == 8) return launch_keys<DT, CT, 8>(a, grid, st);
   return launch_keys<DT, CT, 1>(a, grid, st);
 }
 
@@ -372,7 +432,7 @@ int lr_block_keys(const lr_cache* c, const int64_t* slots, int64_t n, void* keys
   const Mode kd = mode_of(c->k_layout, 0), kh = mode_of(c->k_layout, 1), ks = mode_of(c->k_layout, 2);
   const Mode kp = mode_of(c->k_layout, 3);
   if (o.dim != kd.size || o.heads != kh.size || o.items != kp.size) return LR_ERR_SIZE_MISMATCH;
-  if (kh.size > 65535 || n > kMaxCount) return LR_ERR_OVERFLOW;
+  if (kh.size > 4 * 65535 || n > kMaxCount) return LR_ERR_OVERFLOW;
   const int64_t e = dtype_bytes(dtype), ce = dtype_bytes(c->dtype);
   const Buffer in[] = {{slots, n * 8}, {c->k, c->k_capacity * ce}, {c->v, c->v_capacity * ce},
                        {c->k_scale, c->scale_capacity * 4}, {c->v_scale, c->scale_capacity * 4}};
@@ -400,13 +460,13 @@ int lr_block_keys(const lr_cache* c, const int64_t* slots, int64_t n, void* keys
   a.heads = (uint32_t)kh.size;
   a.n = (uint32_t)n;
   a.dim = (int32_t)kd.size;
-  // 64 entries a wave, fewer where that would leave part of the device without one: a step's entries are each the
-  // newest of their page, a prompt's one in page_size
-  const int64_t waves = 8192;
-  a.chunk = (uint32_t)std::min<int64_t>(64, std::max<int64_t>(1, n * kh.size / waves));
-  int64_t v = 16 / ce;
+  // 64 entries a workgroup, fewer where that would leave part of the device without one: a step's entries are each
+  // the newest of their page, a prompt's one in page_size
+  const int64_t heads4 = (kh.size + 3) / 4;
+  a.chunk = (uint32_t)std::min<int64_t>(64, std::max<int64_t>(1, n * heads4 / 2048));
+  int64_t v = ce == 4 ? 4 : 8;
   while (v > 1 && (a.dim % v || !rows_aligned(c->k_layout, c->k, ce, v))) v /= 2;
-  const dim3 grid((unsigned)((n + a.chunk - 1) / a.chunk), a.heads);
+  const dim3 grid((unsigned)((n + a.chunk - 1) / a.chunk), (unsigned)heads4);
   const hipStream_t st = (hipStream_t)stream;
   return with_model_type(dtype, [&](auto dt) {
     constexpr int D = decltype(dt)::value;
@@ -483,9 +543,9 @@ int lr_block_select(const void* q, const lr_layout* Lq, int64_t q_capacity, cons
     if (rc) return rc;
   }
   if (max_pages > 1024)
-    hipLaunchKernelGGL((k_block_choose<1024>), dim3((unsigned)rows), dim3(1024), 0, st, a);
+    hipLaunchKernelGGL((k_block_choose<1024, 8>), dim3((unsigned)rows), dim3(1024), 0, st, a);
   else
-    hipLaunchKernelGGL((k_block_choose<256>), dim3((unsigned)rows), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_block_choose<256, 4>), dim3((unsigned)rows), dim3(256), 0, st, a);
   return check_op_launch();
 }
 

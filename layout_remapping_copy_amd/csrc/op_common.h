@@ -239,19 +239,14 @@ struct AxesArg {
 };
 // A token's positions on all axes, read side by side: reading the one that a pair asks for would wait for its axis first.
 struct AxisPositions {
-  int64_t p[kMaxAxes];
+  int64_t p0, p1, p2, p3;  // no array: one that a lane's own axis indexes would be kept in shared memory
   __device__ __forceinline__ int64_t of(int32_t axis) const {  // the first one's for an axis that is none
-    int64_t x = p[0];
-#pragma unroll
-    for (int k = 1; k < kMaxAxes; ++k) x = axis == k ? p[k] : x;
-    return x;
+    return axis == 1 ? p1 : axis == 2 ? p2 : axis == 3 ? p3 : p0;
   }
 };
 __device__ __forceinline__ AxisPositions axis_positions(const int64_t* first, const AxesArg& x) {
-  AxisPositions r;
-#pragma unroll
-  for (int k = 0; k < kMaxAxes; ++k) r.p[k] = first[k < x.axes ? k * x.stride : 0];
-  return r;
+  return AxisPositions{first[0], first[x.axes > 1 ? x.stride : 0], first[x.axes > 2 ? 2 * x.stride : 0],
+                       first[x.axes > 3 ? 3 * x.stride : 0]};
 }
 
 // cos and sin of the angles of one unit's V pairs: pair k of a half layout is element k of both chunks, pairs

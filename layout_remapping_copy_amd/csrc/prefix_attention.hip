@@ -7,6 +7,258 @@
 
 namespace lr {
 
+// ------------------------------------------------------------------ many rows on one prefix
+
+typedef float F16x __attribute__((ext_vector_type(16)));
+typedef short S4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) S4 LdsS4;
+typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ F16x mfma32(B8 a, B8 b, F16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ F16x mfma32(H8 a, H8 b, F16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+
+constexpr uint32_t kTileRows = 128, kTileTokens = 64, kPitch = 256;  // of a workgroup; of a step; bytes of a row in shared memory
+
+// Where chunk c (16 bytes) of a row lies in its 256 bytes of shared memory: 16 rows' chunks of one number, and 16 rows'
+// pairs of chunks, then spread over all banks.
+__device__ __forceinline__ uint32_t place_in_row(uint32_t row, uint32_t c) { return row * kPitch + (c ^ (row & 15)) * 16; }
+
+// 128 rows (query heads of one cache head, of all sequences) share the keys and values of a run of tokens: a workgroup
+// brings 64 tokens at a time to shared memory, 8-bit codes as 16-bit numbers, while its four waves work on the 64
+// before, 32 rows each.  The scores of 32 tokens x 32 rows are a product of keys (first operand, from shared memory)
+// and queries (in registers), so that a lane has scores of one row alone: its maximum and sum need one exchange.  They
+// are also the second operand of the next product, values transposed x weights, when its inner index runs over the
+// tokens as they lie in the lane; the values' operand comes by transpose reads of shared memory.
+template <int DT, int CT, int DC>
+__global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
+  using T = typename ElemOf<DT>::T;
+  using M = typename MatrixOf<DT>::T;  // 8 numbers of the model's type
+  constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
+  constexpr int kElem = kQuant ? 1 : 2, kKeySteps = DC / 16, kValSteps = DC / 32;
+  // weights meet the values in the model's type, in bf16 where those are codes
+  using P = std::conditional_t<kQuant, B8, M>;
+  using PE = std::conditional_t<kQuant, __bf16, T>;
+  using CT8 = std::conditional_t<kQuant, U2, U4>;  // 8 elements of the cache
+  constexpr uint32_t kTile = kTileTokens * kPitch;
+  __shared__ __attribute__((aligned(16))) char keys[2 * kTile], values[2 * kTile];
+  __shared__ __attribute__((aligned(16))) int64_t offs_all[4][kTileTokens][2];
+  __shared__ __attribute__((aligned(16))) float scales_all[kQuant ? 4 : 1][2][2][kTileTokens];
+  const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64), r = lane & 31, half = lane >> 5;
+  auto offs = offs_all[w];
+  auto scales = scales_all[kQuant ? w : 0];
+  const uint32_t row0 = threadIdx.x / 16, chunk = threadIdx.x % 16;  // of the rows row0 + 16 x this lane brings one chunk
+  // Where this lane reads its operands: of the keys row r, of the values four columns of a token (below).  The other
+  // chunks of the row are at the same place but for bits 5 to 7, in which their numbers differ.
+  const uint32_t key_at = place_in_row(r, half), val_row = 4 * half + (lane & 15) / 4;
+  uint32_t val_at[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+    val_at[y] = place_in_row(val_row + 8 * y, 2 * (lane >> 4 & 1) + (lane & 3) / 2) + (lane & 1) * 8;
+  const bool key_chunk = chunk * 8 < (uint32_t)a.dk, val_chunk = chunk * 8 < (uint32_t)a.dv;
+
+  Run run;
+  if (!run_begin(a, &run)) return;
+  do {
+    const uint32_t g = run.u / a.tiles, tile0 = run.u % a.tiles * kTileRows + w * 32, row = tile0 + here(r);
+    const uint32_t lo = run.lo, hi = run.hi;
+    const bool idle = tile0 >= a.group;
+
+    M q[kKeySteps];
+    {
+      const uint32_t hq = here(half);
+      const T* x = (const T*)a.q + query_at(a, run.b, g, row < a.group ? row : 0);
+#pragma unroll
+      for (int kk = 0; kk < kKeySteps; ++kk) {
+        const uint32_t e0 = kk * 16 + hq * 8, e = e0 < (uint32_t)a.dk ? e0 : 0;
+        if (a.q_wide) {
+          q[kk] = *(const M*)(x + e);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[kk][i] = x[(int64_t)(e + i) * a.qd];
+        }
+        if (row >= a.group || e0 >= (uint32_t)a.dk) q[kk] = M{};
+      }
+    }
+
+    const char* kbase = (const char*)a.k + ((int64_t)g * a.kh + (key_chunk ? chunk * 8 : 0)) * kElem;
+    const char* vbase = (const char*)a.v + ((int64_t)g * a.vh + (val_chunk ? chunk * 8 : 0)) * kElem;
+    const uint32_t one = a.fd_page.m ? 0 : ~0u;  // pages of one slot: the quotient is the dividend
+    auto page_index = [&](uint32_t t) -> uint32_t { return (__umulhi(t, a.fd_page.m) >> a.fd_page.s) + (t & one); };
+    // Lane l's page of token t0 + l; loads past the end are of the last token's, and left out after.
+    auto page_of = [&](uint32_t t0) -> int32_t { return a.table[page_index(t0 + lane < hi ? t0 + lane : hi - 1)]; };
+    // Row offsets to shared memory (the cache's first row for what is not seen); returns the mask of the seen tokens.
+    auto place = [&](uint32_t t0, int32_t page, float* ks, float* vs) -> uint64_t {
+      const uint32_t t = t0 + lane;
+      const bool ok = (t < hi) & ((uint32_t)page < a.pages);
+      const uint32_t in = ok ? t - page_index(t) * a.page_size : 0, pg = ok ? page : 0;
+      wave_fence();
+      offs[lane][0] = (int64_t)(pg * (uint64_t)a.kp + in * (uint64_t)a.ksl) * kElem;
+      offs[lane][1] = (int64_t)(pg * (uint64_t)a.vp + in * (uint64_t)a.vsl) * kElem;
+      wave_fence();
+      if constexpr (kQuant) {
+        const uint64_t at = pg * (uint64_t)a.sp + in * (uint64_t)a.ssl + (uint64_t)g * a.sh;
+        *ks = ok ? a.ks[at] * a.scale2 : 0.f;
+        *vs = ok ? a.vs[at] : 0.f;
+      }
+      return __ballot(ok);
+    };
+    CT8 kr[4], vr[4];
+    uint32_t bad = 0;  // of this lane's rows, those not seen
+    auto load = [&](uint64_t seen) {
+      bad = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t t = row0 + 16 * x;
+        kr[x] = *(const CT8*)(kbase + offs[t][0]);
+        vr[x] = *(const CT8*)(vbase + offs[t][1]);
+        bad |= (uint32_t)(~(seen >> t) & 1) << x;
+      }
+    };
+    auto store = [&](uint32_t buf) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t at = place_in_row(row0 + 16 * x, chunk);
+        U4 k, v;
+        if constexpr (kQuant) {
+          k = __builtin_bit_cast(U4, decode<DT, CT>(kr[x]));
+          v = __builtin_bit_cast(U4, decode<LR_BF16, CT>(vr[x]));
+        } else {
+          k = kr[x];
+          v = vr[x];
+        }
+        if (!key_chunk) k = U4{};
+        if (bad >> x & 1) v = U4{};  // what is not seen may hold NaN
+        *(U4*)&keys[buf * kTile + at] = k;
+        *(U4*)&values[buf * kTile + at] = v;
+      }
+    };
+
+    F16x o[kValSteps];
+#pragma unroll
+    for (int d = 0; d < kValSteps; ++d) o[d] = F16x{};
+    // Scores are taken off `base`, at most 8 below the running maximum; weights in fp16 parts off a base 7 to 15 below
+    // it, so that one of 2^-32 of the largest still counts.
+    constexpr float kLow = std::is_same_v<PE, _Float16> ? 7.f : 0.f;
+    float base = -__FLT_MAX__, l = 0;
+    if (lo < hi) {
+      float ks[2] = {}, vs[2] = {};
+      uint64_t seen = place(lo, page_of(lo), &ks[0], &vs[0]);
+      load(seen);
+      int32_t page = page_of(lo + kTileTokens);
+      store(0);
+      if constexpr (kQuant) scales[0][0][lane] = ks[0], scales[0][1][lane] = vs[0];
+      uint64_t seen_next = place(lo + kTileTokens, page, &ks[1], &vs[1]);
+      load(seen_next);
+      page = page_of(lo + 2 * kTileTokens);
+      __syncthreads();
+      uint32_t buf = 0;
+      for (uint32_t t0 = lo; t0 < hi; t0 += kTileTokens, buf ^= 1) {
+        store(buf ^ 1);
+        if constexpr (kQuant) scales[buf ^ 1][0][lane] = ks[1], scales[buf ^ 1][1][lane] = vs[1];
+        const uint64_t seen_after = place(t0 + 2 * kTileTokens, page, &ks[1], &vs[1]);
+        load(seen_after);
+        page = page_of(t0 + 3 * kTileTokens);
+        if (!idle) {
+#pragma unroll 1
+          for (uint32_t tt = 0; tt < 2; ++tt) {
+            const uint32_t from = buf * kTile + tt * 32 * kPitch;
+            const uint32_t mask = (uint32_t)(seen >> (32 * tt));
+            F16x s = {};
+#pragma unroll
+            for (int kk = 0; kk < kKeySteps; ++kk) {
+              const U4 k = *(const U4*)&keys[from + (key_at ^ 32 * kk)];
+              s = mfma32(__builtin_bit_cast(M, k), q[kk], s);
+            }
+            // element i is token 8 (i / 4) + 4 half + i % 4 of the 32
+            F4 vsc[4];
+            if constexpr (kQuant) {
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const F4 ksc = *(const F4*)&scales[buf][0][32 * tt + 8 * z + 4 * half];
+                vsc[z] = *(const F4*)&scales[buf][1][32 * tt + 8 * z + 4 * half];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[4 * z + i] *= ksc[i];
+              }
+            } else {
+              s *= a.scale2;
+            }
+            if (mask != ~0u)
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                s[i] = mask >> (8 * (i / 4) + 4 * half + i % 4) & 1 ? s[i] : -__builtin_inff();
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i]);
+            if (__any(top > base + (8.f + kLow))) {
+              top = fmaxf(base, fmaxf(top, __shfl_xor(top, 32)) - kLow);
+              const float keep = __builtin_amdgcn_exp2f(base - top);
+              base = top;
+              l *= keep;
+#pragma unroll
+              for (int d = 0; d < kValSteps; ++d) o[d] *= keep;
+            }
+            // The weights in two 16-bit parts, 16 bits in bf16 and 22 in fp16.  A bf16 first part is the number's upper half,
+            // so that the second is not negative; where values may be infinite it is not zero either, as an infinite value
+            // times zero would be NaN.  fp16 parts are rounded, the first not to zero, and the second meets finite values.
+            P phi[2], plo[2];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x = __builtin_amdgcn_exp2f(s[i] - base);
+              l += x;
+              if constexpr (kQuant) x *= vsc[i / 4][i % 4];
+              if constexpr (std::is_same_v<PE, _Float16>) {
+                phi[i / 8][i % 8] = (PE)fmaxf(x, 0x1p-24f);
+                plo[i / 8][i % 8] = (PE)(x - (float)phi[i / 8][i % 8]);
+              } else {
+                const uint32_t up = __float_as_uint(x) & 0xffff0000u;
+                phi[i / 8][i % 8] = __builtin_bit_cast(PE, (uint16_t)(up >> 16));
+                const float rest = x - __uint_as_float(up);
+                plo[i / 8][i % 8] = (PE)(kQuant ? rest : fmaxf(rest, 0x1p-100f));
+              }
+            }
+#pragma unroll
+            for (int d = 0; d < kValSteps; ++d)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                // this lane's column 32 d + r of tokens 16 z + 4 half + (0 .. 3) and 8 further: it addresses four columns
+                // of one token, and receives its own column of the tokens that its group of 16 lanes addresses
+                U4 v;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const char* at = &values[from + 16 * z * kPitch + (val_at[y] ^ 64 * d)];
+                  const U2 x = __builtin_bit_cast(U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4*)const_cast<char*>(at)));
+                  v[2 * y] = x[0], v[2 * y + 1] = x[1];
+                }
+                o[d] = mfma32(__builtin_bit_cast(P, v), phi[z], o[d]);
+                if constexpr (std::is_same_v<PE, _Float16>)
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) v[y] = finite_pair<LR_F16>(v[y]);
+                o[d] = mfma32(__builtin_bit_cast(P, v), plo[z], o[d]);
+              }
+          }
+        }
+        seen = seen_next;
+        seen_next = seen_after;
+        __syncthreads();
+      }
+    }
+    const float total = l + __shfl_xor(l, 32);
+    if (row < a.group) {
+      const uint32_t he = here(half);
+      const uint64_t at = (uint64_t)(g * a.group + row) * a.splits + run.split;
+#pragma unroll
+      for (int d = 0; d < kValSteps; ++d)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const uint32_t e = 32 * d + 8 * z + 4 * he;
+          if (e < (uint32_t)a.dv)
+            *(F4*)&a.part_o[at * a.dv + e] = F4{o[d][4 * z], o[d][4 * z + 1], o[d][4 * z + 2], o[d][4 * z + 3]};
+        }
+      if (he == 0) leave_part(a, run, g * a.group + row, base == -__FLT_MAX__ ? -__builtin_inff() : base, total);
+    }
+  } while (run_next(a, &run));
+}
+
 struct PrefixJoin {
   const float *ml, *o;  // parts of the prefix, for row b * group + r of cache head g: (g, row, split)
   uint32_t splits, group, batch;
@@ -24,6 +276,33 @@ __global__ void __launch_bounds__(256) k_prefix_join(AttentionArgs a, PrefixJoin
   join_list(p.ml + 2 * pre, p.o + pre * a.dv, p.splits, a.dv, q4, false, &j);
   join_list(a.part_ml + 2 * own, a.part_o + own * a.dv, a.splits, a.dv, q4, false, &j);
   join_out<DT>(a, b, h, q4, j, a.lens[b] < 0, os);
+}
+
+// Rows of a cache head from which on k_prefix_rows is taken.
+constexpr uint32_t kManyRows = 64;
+
+// Whether k_prefix_rows takes such a call: 16-bit products, heads of up to 128.
+static bool rows_fit(const AttentionArgs& a, int32_t dtype) {
+  return a.path == LR_ATTENTION_MATRIX && dtype != LR_F32 && a.dk <= 128 && a.dv <= 128;
+}
+template <int DT, int CT> static int launch_rows_of(const AttentionArgs& a, hipStream_t st) {
+  const dim3 grid(a.splits == 1 ? a.units : a.grid);
+  const int32_t widest = std::max(a.dk, a.dv);
+  if (widest <= 64)
+    hipLaunchKernelGGL((k_prefix_rows<DT, CT, 64>), grid, dim3(256), 0, st, a);
+  else if (widest <= 96)
+    hipLaunchKernelGGL((k_prefix_rows<DT, CT, 96>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_prefix_rows<DT, CT, 128>), grid, dim3(256), 0, st, a);
+  return check_op_launch();
+}
+template <int DT> static int launch_rows_from(const AttentionArgs& a, int32_t ctype, hipStream_t st) {
+  if (ctype == LR_E4M3) return launch_rows_of<DT, LR_E4M3>(a, st);
+  if (ctype == LR_INT8) return launch_rows_of<DT, LR_INT8>(a, st);
+  return launch_rows_of<DT, DT>(a, st);
+}
+static int launch_rows(const AttentionArgs& a, int32_t dtype, int32_t ctype, hipStream_t st) {
+  return dtype == LR_F16 ? launch_rows_from<LR_F16>(a, ctype, st) : launch_rows_from<LR_BF16>(a, ctype, st);
 }
 
 // The arguments of both passes and what they leave.
@@ -123,7 +402,16 @@ int lr_prefix_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, 
   attention_buffers(c, Lq, q, dtype, p.p_own.path, &a);
   attention_buffers(c, Lq, q, dtype, p.p_pre.path, &x);
   const hipStream_t st = (hipStream_t)stream;
-  if (int rc = launch_attention_pass(x, dtype, c->dtype, st)) return rc;
+  // Many rows share what a workgroup brings to shared memory.
+  const bool many = rows_fit(x, dtype) && x.group >= kManyRows;
+  if (many) {
+    x.tiles = (x.group + kTileRows - 1) / kTileRows;
+    x.units = x.kv_heads * x.tiles;
+    x.wide_heads = 1;
+    x.block = kBlock;
+    x.grid = 2 * kRuns;
+  }
+  if (int rc = many ? launch_rows(x, dtype, c->dtype, st) : launch_attention_pass(x, dtype, c->dtype, st)) return rc;
   if (int rc = launch_attention_pass(a, dtype, c->dtype, st)) return rc;
   const PrefixJoin j{x.part_ml, x.part_o, x.splits, a.group, a.batch, make_fastdiv(a.group)};
   return with_model_type(dtype, [&](auto dt) {
