@@ -19,9 +19,12 @@ __device__ __forceinline__ F16x mfma32(H8 a, H8 b, F16x c) { return __builtin_am
 
 constexpr uint32_t kTileRows = 128, kTileTokens = 64, kPitch = 256;  // of a workgroup; of a step; bytes of a row in shared memory
 
-// Where chunk c (16 bytes) of a row lies in its 256 bytes of shared memory: 16 rows' chunks of one number, and 16 rows'
-// pairs of chunks, then spread over all banks.
-__device__ __forceinline__ uint32_t place_in_row(uint32_t row, uint32_t c) { return row * kPitch + (c ^ (row & 15)) * 16; }
+// Where chunk c (16 bytes) of a row lies in its 256 bytes of shared memory: 16 rows' chunks of one number spread over
+// all banks, for the keys' operand, and 4 rows' groups of four chunks, for the values' (4 cycles of a read for each;
+// the row's number itself in place of its halves swapped: 8 for the values').
+__device__ __forceinline__ uint32_t place_in_row(uint32_t row, uint32_t c) {
+  return row * kPitch + (c ^ ((row & 3) << 2 | (row >> 2 & 3))) * 16;
+}
 
 // 128 rows (query heads of one cache head, of all sequences) share the keys and values of a run of tokens: a workgroup
 // brings 64 tokens at a time to shared memory, 8-bit codes as 16-bit numbers, while its four waves work on the 64
@@ -56,6 +59,11 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
     val_at[y] = place_in_row(val_row + 8 * y, 2 * (lane >> 4 & 1) + (lane & 3) / 2) + (lane & 1) * 8;
   const bool key_chunk = chunk * 8 < (uint32_t)a.dk, val_chunk = chunk * 8 < (uint32_t)a.dv;
 
+  // Scores times `unit` are in base-2 units: the scale where tokens have none of their own, its sign in the queries so
+  // that the largest product is the largest score.
+  const float sign = a.scale2 < 0 ? -1.f : a.scale2 > 0 ? 1.f : 0.f;
+  const float unit = kQuant || a.scale2 == 0 ? 1.f : __builtin_fabsf(a.scale2);
+
   Run run;
   if (!run_begin(a, &run)) return;
   do {
@@ -77,6 +85,7 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
           for (int i = 0; i < 8; ++i) q[kk][i] = x[(int64_t)(e + i) * a.qd];
         }
         if (row >= a.group || e0 >= (uint32_t)a.dk) q[kk] = M{};
+        if constexpr (!kQuant) q[kk] *= (T)sign;
       }
     }
 
@@ -163,12 +172,31 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
           for (uint32_t tt = 0; tt < 2; ++tt) {
             const uint32_t from = buf * kTile + tt * 32 * kPitch;
             const uint32_t mask = (uint32_t)(seen >> (32 * tt));
+            // Operands are read ahead of the products that need them, by addresses made here: kept over the loop, they
+            // would take the registers for that.
+            const uint32_t kp = here(from + key_at), vp[2] = {here(from + val_at[0]), here(from + val_at[1])};
+            auto key = [&](int kk) -> M { return __builtin_bit_cast(M, *(const U4*)&keys[kp ^ 32 * kk]); };
+            // Column 32 d + r of this lane in the tokens 16 z + 4 half + (0 .. 3) and 8 further: a lane addresses four columns
+            // of one token, and receives its own column of the tokens that its group of 16 lanes addresses.
+            auto value = [&](int d, int z) -> U4 {
+              U4 v;
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const char* at = &values[(vp[y] ^ 64 * d) + 16 * z * kPitch];
+                const U2 x = __builtin_bit_cast(U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4*)const_cast<char*>(at)));
+                v[2 * y] = x[0], v[2 * y + 1] = x[1];
+              }
+              return v;
+            };
             F16x s = {};
+            M k0 = key(0), k1 = key(1);
 #pragma unroll
             for (int kk = 0; kk < kKeySteps; ++kk) {
-              const U4 k = *(const U4*)&keys[from + (key_at ^ 32 * kk)];
-              s = mfma32(__builtin_bit_cast(M, k), q[kk], s);
+              const M k2 = kk + 2 < kKeySteps ? key(kk + 2) : k1;
+              s = mfma32(k0, q[kk], s);
+              k0 = k1, k1 = k2;
             }
+            U4 v0 = value(0, 0), v1 = value(0, 1);
             // element i is token 8 (i / 4) + 4 half + i % 4 of the 32
             F4 vsc[4];
             if constexpr (kQuant) {
@@ -179,8 +207,6 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[4 * z + i] *= ksc[i];
               }
-            } else {
-              s *= a.scale2;
             }
             if (mask != ~0u)
 #pragma unroll
@@ -189,6 +215,7 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
             float top = -__builtin_inff();
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i]);
+            top *= unit;
             if (__any(top > base + (8.f + kLow))) {
               top = fmaxf(base, fmaxf(top, __shfl_xor(top, 32)) - kLow);
               const float keep = __builtin_amdgcn_exp2f(base - top);
@@ -203,7 +230,7 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
             P phi[2], plo[2];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              float x = __builtin_amdgcn_exp2f(s[i] - base);
+              float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], unit, -base));
               l += x;
               if constexpr (kQuant) x *= vsc[i / 4][i % 4];
               if constexpr (std::is_same_v<PE, _Float16>) {
@@ -217,24 +244,18 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
               }
             }
 #pragma unroll
-            for (int d = 0; d < kValSteps; ++d)
+            for (int d = 0; d < kValSteps; ++d) {
+              U4 n0 = v0, n1 = v1;
+              if (d + 1 < kValSteps) n0 = value(d + 1, 0), n1 = value(d + 1, 1);
+              o[d] = mfma32(__builtin_bit_cast(P, v0), phi[0], o[d]);
+              o[d] = mfma32(__builtin_bit_cast(P, v1), phi[1], o[d]);
+              if constexpr (std::is_same_v<PE, _Float16>)
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                // this lane's column 32 d + r of tokens 16 z + 4 half + (0 .. 3) and 8 further: it addresses four columns
-                // of one token, and receives its own column of the tokens that its group of 16 lanes addresses
-                U4 v;
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const char* at = &values[from + 16 * z * kPitch + (val_at[y] ^ 64 * d)];
-                  const U2 x = __builtin_bit_cast(U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4*)const_cast<char*>(at)));
-                  v[2 * y] = x[0], v[2 * y + 1] = x[1];
-                }
-                o[d] = mfma32(__builtin_bit_cast(P, v), phi[z], o[d]);
-                if constexpr (std::is_same_v<PE, _Float16>)
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) v[y] = finite_pair<LR_F16>(v[y]);
-                o[d] = mfma32(__builtin_bit_cast(P, v), plo[z], o[d]);
-              }
+                for (int y = 0; y < 4; ++y) v0[y] = finite_pair<LR_F16>(v0[y]), v1[y] = finite_pair<LR_F16>(v1[y]);
+              o[d] = mfma32(__builtin_bit_cast(P, v0), plo[0], o[d]);
+              o[d] = mfma32(__builtin_bit_cast(P, v1), plo[1], o[d]);
+              v0 = n0, v1 = n1;
+            }
           }
         }
         seen = seen_next;
