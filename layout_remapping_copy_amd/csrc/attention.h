@@ -135,11 +135,11 @@ __device__ __forceinline__ void run_unit(const AttentionArgs& a, uint32_t w, Run
   const uint64_t hi = (uint64_t)r->sp.base + (stop - r->start) * a.block;
   r->hi = hi < r->sp.n ? (uint32_t)hi : r->sp.n;
 }
-__device__ __forceinline__ bool run_begin(const AttentionArgs& a, Run* r) {
+__device__ __forceinline__ bool run_begin(const AttentionArgs& a, uint32_t block, Run* r) {
   const uint32_t lane = threadIdx.x & 63;
   if (a.splits == 1) {  // one unit a workgroup
-    r->b = blockIdx.x / a.units;
-    r->u = blockIdx.x % a.units;
+    r->b = block / a.units;
+    r->u = block % a.units;
     r->sp = span_of(a, a.lens[r->b]);
     r->deal = Deal{1, 1};
     r->w = 0;
@@ -157,11 +157,11 @@ __device__ __forceinline__ bool run_begin(const AttentionArgs& a, Run* r) {
       all += more;
     }
     r->deal = deal_of(a, all);
-    if (blockIdx.x >= r->deal.used) return false;
+    if (block >= r->deal.used) return false;
     // Workgroups go to the eight dies in turn; neighbouring runs, which are often heads of the same tokens, go
     // to one die, whose cache then holds the lines they share: a token's scales for all heads lie in one line
     // (64 x 16384 e4m3 tokens: 466 to 441 us; runs that share no lines are within 1 %).
-    r->w = r->deal.used % 8 ? blockIdx.x : blockIdx.x % 8 * (r->deal.used / 8) + blockIdx.x / 8;
+    r->w = r->deal.used % 8 ? block : block % 8 * (r->deal.used / 8) + block / 8;
     r->at = run_start(r->deal, r->w);
     r->end = run_start(r->deal, r->w + 1);
     uint64_t past = 0;  // blocks of the sequences before the 64 looked at
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(256) k_attention_element(AttentionArgs a) {
   __shared__ float ms[4], ls[4];
   const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
   Run run;
-  if (!run_begin(a, &run)) return;
+  if (!run_begin(a, blockIdx.x, &run)) return;
   do {
     const uint32_t b = run.b, h = run.u, g = h / a.group, bh = b * a.heads + h, split = run.split, hi = run.hi;
     const uint64_t lo = run.lo;
@@ -466,8 +466,18 @@ struct MatrixShape {
 // busy 19 % of the first, 37 % of the second, with the matrix units' part.
 // One workgroup a CU keeps enough loads under way; two and three a CU (512 and 768 runs) took 359 and 367 us against
 // 353, as more rows of memory are open at once.  Plain loads took 20 % longer than streaming ones.
+template <int DT, int CT, int DC, int HT, int WAVES> struct MatrixShared {
+  static constexpr int kRow = 16 * MatrixShape<DT, CT, DC, HT>::kValChunk + 4;  // floats; the 4 keep 16 heads' accesses off one bank
+  static constexpr int kJoin = WAVES == kOverHeads ? 1 : 16;                    // four heads are not joined
+  int64_t offs[4][64];
+  __attribute__((aligned(16))) float scales[4][64];
+  float ms[4][kJoin * HT], ls[4][kJoin * HT];
+  __attribute__((aligned(16))) float os[4][kJoin * kRow];
+};
+// The run of workgroup `block` of the pass.
 template <int DT, int CT, int DC, int HT, int WAVES>
-__global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves)) k_attention_matrix(AttentionArgs a) {
+__device__ __forceinline__ void attention_run(const AttentionArgs& a, uint32_t block,
+                                              MatrixShared<DT, CT, DC, HT, WAVES>& shared) {
   constexpr bool by_heads = WAVES == kOverHeads, listed = WAVES == kOverBlocks;
   using S = MatrixShape<DT, CT, DC, HT>;
   using T = typename ElemOf<DT>::T;
@@ -476,18 +486,16 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
   typedef typename Raw<8>::T KHalf;
   using VR = typename Raw<S::kValChunk * S::kElem>::T;
   constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
-  constexpr int kRow = 16 * S::kValChunk + 4;  // floats; the 4 keep 16 heads' accesses off one bank
-  __shared__ int64_t offs_all[4][64];
-  __shared__ __attribute__((aligned(16))) float scale_all[4][64];
-  constexpr int kJoin = by_heads ? 1 : 16;  // four heads are not joined
-  __shared__ float ms[4][kJoin * HT], ls[4][kJoin * HT];
-  __shared__ __attribute__((aligned(16))) float os[4][kJoin * kRow];
+  constexpr int kRow = MatrixShared<DT, CT, DC, HT, WAVES>::kRow;
+  auto& ms = shared.ms;
+  auto& ls = shared.ls;
+  auto& os = shared.os;
   const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64), r = lane & 15, j = lane >> 4;
-  int64_t* offs = offs_all[w];
-  float* scales = scale_all[w];
+  int64_t* offs = shared.offs[w];
+  float* scales = shared.scales[w];
 
   Run run;
-  if (!run_begin(a, &run)) return;
+  if (!run_begin(a, block, &run)) return;
   for (bool again = false;; again = true) {
     const uint32_t b = run.b, split = run.split, hi = run.hi;
     const uint32_t g = by_heads ? run.u / a.tiles * 4 + w : run.u / a.tiles;
@@ -883,6 +891,12 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
     }
     if (!run_next(a, &run)) break;
   }
+}
+
+template <int DT, int CT, int DC, int HT, int WAVES>
+__global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves)) k_attention_matrix(AttentionArgs a) {
+  __shared__ MatrixShared<DT, CT, DC, HT, WAVES> shared;
+  attention_run<DT, CT, DC, HT, WAVES>(a, blockIdx.x, shared);
 }
 
 // The parts of one query head, joined by a workgroup: a wave has the weights of 64 parts at a time, one a lane; 256

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
   const float unit = kQuant || a.scale2 == 0 ? 1.f : __builtin_fabsf(a.scale2);
 
   Run run;
-  if (!run_begin(a, &run)) return;
+  if (!run_begin(a, blockIdx.x, &run)) return;
   do {
     const uint32_t g = run.u / a.tiles, tile0 = run.u % a.tiles * kTileRows + w * 32, row = tile0 + here(r);
     const uint32_t lo = run.lo, hi = run.hi;
@@ -280,6 +280,18 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
   } while (run_next(a, &run));
 }
 
+// Both passes in one launch, for calls whose time is mostly that of launches: the first `first` workgroups have the
+// prefix, the others the sequences' own tokens.
+template <int DT, int CT, int DC>
+__global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, 1>::kMinWaves)) k_prefix_pair(AttentionArgs prefix, AttentionArgs own,
+                                                                                             uint32_t first) {
+  __shared__ MatrixShared<DT, CT, DC, 1, kOverTokens> shared;
+  if (blockIdx.x < first)
+    attention_run<DT, CT, DC, 1, kOverTokens>(prefix, blockIdx.x, shared);
+  else
+    attention_run<DT, CT, DC, 1, kOverTokens>(own, blockIdx.x - first, shared);
+}
+
 struct PrefixJoin {
   const float *ml, *o;  // parts of the prefix, for row b * group + r of cache head g: (g, row, split)
   uint32_t splits, group, batch;
@@ -299,8 +311,15 @@ __global__ void __launch_bounds__(256) k_prefix_join(AttentionArgs a, PrefixJoin
   join_out<DT>(a, b, h, q4, j, a.lens[b] < 0, os);
 }
 
-// Rows of a cache head from which on k_prefix_rows is taken.
+// From so many rows of a cache head on they share what a workgroup brings to shared memory, if there is work enough for
+// that to pay.  32 query heads on 8 of 128 bf16, in us with k_attention_matrix and with k_prefix_rows: 64 rows on 8191
+// tokens 30 and 33, on 65536 109 and 80; 96 on 8191 39 and 35; 128 on 1000 24 and 26; 192 on 1000 31 and 29, on 65536
+// 270 and 131; 32 rows on 65536 69 and 73.  Over e4m3 the lines cross at the same places.
 constexpr uint32_t kManyRows = 64;
+constexpr int64_t kEnoughWork = 600000, kEnoughCodes = 1 << 20;  // rows times tokens
+static bool much_work(const AttentionArgs& x, int32_t ctype) {
+  return (int64_t)x.group * x.max_pages * x.page_size >= (is_quantised(ctype) ? kEnoughCodes : kEnoughWork);
+}
 
 // Whether k_prefix_rows takes such a call: 16-bit products, heads of up to 128.
 static bool rows_fit(const AttentionArgs& a, int32_t dtype) {
@@ -324,6 +343,27 @@ template <int DT> static int launch_rows_from(const AttentionArgs& a, int32_t ct
 }
 static int launch_rows(const AttentionArgs& a, int32_t dtype, int32_t ctype, hipStream_t st) {
   return dtype == LR_F16 ? launch_rows_from<LR_F16>(a, ctype, st) : launch_rows_from<LR_BF16>(a, ctype, st);
+}
+
+template <int DT, int CT, int DC>
+static int launch_pair_wide(const AttentionArgs& x, const AttentionArgs& a, hipStream_t st) {
+  const unsigned first = x.splits == 1 ? x.units : x.grid, second = a.splits == 1 ? a.batch * a.units : a.grid;
+  hipLaunchKernelGGL((k_prefix_pair<DT, CT, DC>), dim3(first + second), dim3(256), 0, st, x, a, first);
+  return check_op_launch();
+}
+// In the widths of 64, 128 and 256: reading is not what such calls wait for.
+template <int DT, int CT> static int launch_pair_of(const AttentionArgs& x, const AttentionArgs& a, hipStream_t st) {
+  return a.wide <= 64    ? launch_pair_wide<DT, CT, 64>(x, a, st)
+         : a.wide <= 128 ? launch_pair_wide<DT, CT, 128>(x, a, st)
+                         : launch_pair_wide<DT, CT, 256>(x, a, st);
+}
+static int launch_pair(const AttentionArgs& x, const AttentionArgs& a, int32_t dtype, int32_t ctype, hipStream_t st) {
+  return with_model_type(dtype, [&](auto dt) {
+    constexpr int D = decltype(dt)::value;
+    if (ctype == LR_E4M3) return launch_pair_of<D, LR_E4M3>(x, a, st);
+    if (ctype == LR_INT8) return launch_pair_of<D, LR_INT8>(x, a, st);
+    return launch_pair_of<D, D>(x, a, st);
+  });
 }
 
 // The arguments of both passes and what they leave.
@@ -423,17 +463,29 @@ int lr_prefix_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, 
   attention_buffers(c, Lq, q, dtype, p.p_own.path, &a);
   attention_buffers(c, Lq, q, dtype, p.p_pre.path, &x);
   const hipStream_t st = (hipStream_t)stream;
-  // Many rows share what a workgroup brings to shared memory.
-  const bool many = rows_fit(x, dtype) && x.group >= kManyRows;
-  if (many) {
+  const bool matrix = x.path == LR_ATTENTION_MATRIX && a.path == LR_ATTENTION_MATRIX;
+  if (rows_fit(x, dtype) && x.group >= kManyRows && much_work(x, c->dtype)) {
     x.tiles = (x.group + kTileRows - 1) / kTileRows;
     x.units = x.kv_heads * x.tiles;
     x.wide_heads = 1;
     x.block = kBlock;
-    x.grid = 2 * kRuns;
+    // Two workgroups a CU, but one where that leaves runs of under two blocks of 128 tokens: 128 rows on 16000 tokens 46
+    // us with two and 43 with one, 192 rows 54 and 58.
+    const int64_t blocks = x.units * ((int64_t)x.max_pages * x.page_size / kBlock);
+    x.grid = (uint32_t)(blocks >= 4 * kRuns ? 2 * kRuns : kRuns);
+    if (int rc = launch_rows(x, dtype, c->dtype, st)) return rc;
+    if (int rc = launch_attention_pass(a, dtype, c->dtype, st)) return rc;
+  } else if (matrix && !much_work(x, c->dtype) && x.wide_heads == 1 && a.wide_heads == 1) {
+    for (AttentionArgs* y : {&x, &a}) {
+      y->unit_heads = 16;
+      y->tiles = (y->group + 15) / 16;
+      y->units = y->kv_heads * y->tiles;
+    }
+    if (int rc = launch_pair(x, a, dtype, c->dtype, st)) return rc;
+  } else {
+    if (int rc = launch_attention_pass(x, dtype, c->dtype, st)) return rc;
+    if (int rc = launch_attention_pass(a, dtype, c->dtype, st)) return rc;
   }
-  if (int rc = many ? launch_rows(x, dtype, c->dtype, st) : launch_attention_pass(x, dtype, c->dtype, st)) return rc;
-  if (int rc = launch_attention_pass(a, dtype, c->dtype, st)) return rc;
   const PrefixJoin j{x.part_ml, x.part_o, x.splits, a.group, a.batch, make_fastdiv(a.group)};
   return with_model_type(dtype, [&](auto dt) {
     hipLaunchKernelGGL((k_prefix_join<decltype(dt)::value>), dim3((unsigned)(batch * a.heads)), dim3(256), 0, st, a, j);
