@@ -14,9 +14,48 @@ struct BlockKeysArgs {
   int64_t kd, kh, ksl, kp, sh, ssl, sp, od, oh, op;
   int64_t cache_slots;
   FastDiv fd_page;
-  uint32_t page_size, heads, n, chunk;
+  uint32_t page_size, heads, n, chunk, heads_y;  // heads_y: of a workgroup
   int32_t dim;
 };
+
+// The upper half of the lanes' x exchanged with the lower half's y (of each 32 lanes, where not WIDE), in one instruction
+// for 32 bits: x + y is then what either half keeps of a sum by halves.
+template <bool WIDE> __device__ __forceinline__ void halves_swapped(double* x, double* y) {
+  uint64_t a = (uint64_t)__double_as_longlong(*x), b = (uint64_t)__double_as_longlong(*y), c[2], d[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const auto r = WIDE ? __builtin_amdgcn_permlane32_swap((uint32_t)(a >> (32 * h)), (uint32_t)(b >> (32 * h)), false, false)
+                        : __builtin_amdgcn_permlane16_swap((uint32_t)(a >> (32 * h)), (uint32_t)(b >> (32 * h)), false, false);
+    c[h] = r[0], d[h] = r[1];
+  }
+  *x = __longlong_as_double((long long)(c[1] << 32 | c[0]));
+  *y = __longlong_as_double((long long)(d[1] << 32 | d[0]));
+}
+
+// Adds the sums of lanes that are D, D / 2, ... `lanes` apart: of N columns each half of them keeps half, of one both.
+template <int D, int N>
+__device__ __forceinline__ void add_halves(double* sum, uint32_t lanes, uint32_t lane, uint32_t* first, uint32_t* left) {
+  if ((uint32_t)D < lanes) return;
+  const bool high = lane & D;
+  if constexpr (N > 1) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      double low = sum[i], up = sum[N / 2 + i];
+      if constexpr (D >= 16) {
+        halves_swapped<(D >= 32)>(&low, &up);
+        sum[i] = low + up;
+      } else {
+        asm("" : "+v"(low), "+v"(up));  // values: not one element of sum at an index of the lane's own
+        sum[i] = (high ? up : low) + __shfl_xor(high ? low : up, D);
+      }
+    }
+    *first += high ? N / 2 : 0;
+    *left = N / 2;
+  } else {
+    sum[0] += __shfl_xor(sum[0], D);
+  }
+  if constexpr (D > 1) add_halves<D / 2, (N > 1 ? N / 2 : 1)>(sum, lanes, lane, first, left);
+}
 
 // A workgroup has `chunk` entries of slots and makes the mean of every page whose newest slot is among them; its waves
 // take cache heads of one page side by side, which share lines of memory, their scales above all.  A row of a page is a
@@ -42,71 +81,89 @@ __global__ void __launch_bounds__(256) k_block_keys(BlockKeysArgs a) {
   uint32_t lanes = 1;  // of a row, a power of two
   while (lanes * V < (uint32_t)a.dim && lanes < 64) lanes *= 2;
   const uint32_t rows = 64 / lanes, row = lane / lanes, col = lane % lanes * V;
-  const uint32_t side = min(a.heads, 4u) == 3 ? 4 : min(a.heads, 4u), mates = 4 / side;  // heads, pages at a time
-  for (uint32_t rank = 0; todo; ++rank) {
-    const int f = __ffsll((unsigned long long)todo) - 1;
-    todo &= todo - 1;
-    if (rank % mates != w / side) continue;
-    const uint32_t p = uniform(__shfl(page, f)), count = uniform(__shfl(in, f)) + 1;
-    for (uint32_t h = blockIdx.y * 4 + w % side; h < min(a.heads, (blockIdx.y + 1) * 4); h += side) {
-      const C* k = (const C*)a.k + (int64_t)p * a.kp + (int64_t)h * a.kh;
-      const float* ks = kQuant ? a.ks + (int64_t)p * a.sp + (int64_t)h * a.sh : nullptr;
-      T* out = (T*)a.out + (int64_t)p * a.op + (int64_t)h * a.oh;
-      for (uint32_t e0 = 0; e0 < (uint32_t)a.dim; e0 += lanes * V) {
-        const bool ok = e0 + col < (uint32_t)a.dim;
-        double sum[V] = {};
-        for (uint32_t t0 = 0; t0 < count; t0 += 4 * rows) {
-          Vec x[4];
-          float s[4];
+  // This lane's row among those read at a time, as offsets; where it is past the newest slot, the first of them is read.
+  const int64_t k_row = (int64_t)row * a.ksl, s_row = (int64_t)row * a.ssl;
+  // Cache heads side by side, one a wave, as many as there are up to 4; the waves left over take other pages.
+  const uint32_t side = a.heads > 2 ? 2 : a.heads - 1;  // as a power of two
+  const uint32_t mine_h = w & ((1u << side) - 1), mine_p = w >> side, others = (4u >> side) - 1;
+  const uint32_t h_end = min(a.heads, (blockIdx.y + 1) * a.heads_y);
+  // A wave's work in order: its pages, the cache heads of each, the columns of each that the lanes cover at a time.
+  uint32_t p = 0, count = 0, h = h_end, e0 = 0, rank = 0;
+  auto next_work = [&]() -> bool {
+    e0 += lanes * V;
+    if (h < h_end && e0 < (uint32_t)a.dim) return true;
+    e0 = 0;
+    h += 1u << side;
+    if (h < h_end) return true;
+    while (todo) {
+      const int f = __ffsll((unsigned long long)todo) - 1;
+      todo &= todo - 1;
+      if ((rank++ & others) != mine_p) continue;
+      p = uniform(__shfl(page, f)), count = uniform(__shfl(in, f)) + 1;
+      h = blockIdx.y * a.heads_y + mine_h;
+      return h < h_end;  // the same for every page
+    }
+    return false;
+  };
+  // Rows t0 .. t0 + 4 rows - 1 of it, and their scales.
+  Vec x[4];
+  float sc[4];
+  auto load = [&](uint32_t t0) {
+    const C* k = (const C*)a.k + (int64_t)p * a.kp + (int64_t)h * a.kh;
+    const float* ks = kQuant ? a.ks + (int64_t)p * a.sp + (int64_t)h * a.sh : nullptr;
+    const int64_t at_col = e0 + col < (uint32_t)a.dim ? (int64_t)(e0 + col) * (V > 1 ? 1 : a.kd) : 0, at_row = k_row + at_col;
 #pragma unroll
-          for (uint32_t z = 0; z < 4; ++z) {
-            if (t0 + z * rows >= count) continue;  // the same for all lanes
-            const uint32_t t = min(t0 + z * rows + row, count - 1);
-            x[z] = *(const Vec*)(k + (int64_t)t * a.ksl + (ok ? (int64_t)(e0 + col) * a.kd : 0));
-            if constexpr (kQuant) s[z] = ks[(int64_t)t * a.ssl];
+    for (uint32_t z = 0; z < 4; ++z) {
+      const uint32_t t = t0 + z * rows;
+      if (t >= count) continue;  // the same for all lanes
+      int64_t at = at_row, at_s = s_row;
+      if (t + rows > count && t + row >= count) at = at_col, at_s = 0;
+      x[z] = __builtin_nontemporal_load((const Vec*)(k + (int64_t)t * a.ksl + at));
+      if constexpr (kQuant) sc[z] = (ks + (int64_t)t * a.ssl)[at_s];
+    }
+  };
+  bool more = next_work();
+  if (more) load(0);
+  while (more) {
+    const uint32_t n = count, at = e0 + col;
+    T* out = (T*)a.out + (int64_t)p * a.op + (int64_t)h * a.oh;
+    double sum[V] = {};
+    for (uint32_t t0 = 0; t0 < n; t0 += 4 * rows) {
+      Vec y[4];
+      float s[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) y[z] = x[z], s[z] = sc[z];
+      if (t0 + 4 * rows < n) {
+        load(t0 + 4 * rows);
+      } else {
+        more = next_work();
+        if (more) load(0);
+      }
+#pragma unroll
+      for (uint32_t z = 0; z < 4; ++z) {
+        const uint32_t t = t0 + z * rows;
+        if (t >= n || (t + rows > n && t + row >= n)) continue;
+        float v[V];
+        if constexpr (kQuant && V > 1) {
+#pragma unroll
+          for (int i = 0; i < V; i += 4) {
+            const F4 d = decode4<CT>(((const uint32_t*)&y[z])[i / 4]);
+            v[i] = d[0], v[i + 1] = d[1], v[i + 2] = d[2], v[i + 3] = d[3];
           }
+        } else {
 #pragma unroll
-          for (uint32_t z = 0; z < 4; ++z) {
-            if (t0 + z * rows + row >= count) continue;
-            float v[V];
-            if constexpr (kQuant && V > 1) {
-#pragma unroll
-              for (int i = 0; i < V; i += 4) {
-                const F4 d = decode4<CT>(((const uint32_t*)&x[z])[i / 4]);
-                v[i] = d[0], v[i + 1] = d[1], v[i + 2] = d[2], v[i + 3] = d[3];
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < V; ++i) v[i] = value_of<CT>(x[z][i]);
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = kQuant ? __builtin_fma((double)v[i], (double)s[z], sum[i]) : sum[i] + (double)v[i];
-          }
+          for (int i = 0; i < V; ++i) v[i] = value_of<CT>(y[z][i]);
         }
-        uint32_t first = 0, left = V;  // the columns that this lane is left with
 #pragma unroll
-        for (int d = 32, n = V; d; d >>= 1, n = n > 1 ? n / 2 : 1) {
-          if ((uint32_t)d < lanes) continue;
-          const bool high = lane & d;
-          if (n > 1) {
-#pragma unroll
-            for (int i = 0; i < n / 2; ++i) {
-              double low = sum[i], up = sum[n / 2 + i];
-              asm("" : "+v"(low), "+v"(up));  // values: not one element of sum at an index of the lane's own
-              sum[i] = (high ? up : low) + __shfl_xor(high ? low : up, d);
-            }
-            first += high ? n / 2 : 0;
-            left = n / 2;
-          } else {
-            sum[0] += __shfl_xor(sum[0], d);
-          }
-        }
-        const double part = 1.0 / (double)count;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if ((uint32_t)i < left && ok) out[(int64_t)(e0 + col + first + i) * a.od] = (T)(float)(sum[i] * part);
+        for (int i = 0; i < V; ++i) sum[i] = kQuant ? __builtin_fma((double)v[i], (double)s[z], sum[i]) : sum[i] + (double)v[i];
       }
     }
+    uint32_t first = 0, left = V;  // the columns that this lane is left with
+    add_halves<32, V>(sum, lanes, lane, &first, &left);
+    const double part = 1.0 / (double)n;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if ((uint32_t)i < left && at < (uint32_t)a.dim) out[(int64_t)(at + first + i) * a.od] = (T)(float)(sum[i] * part);
   }
 }
 
@@ -474,13 +531,14 @@ int lr_block_keys(const lr_cache* c, const int64_t* slots, int64_t n, void* keys
   a.heads = (uint32_t)kh.size;
   a.n = (uint32_t)n;
   a.dim = (int32_t)kd.size;
-  // 64 entries a workgroup, fewer where that would leave part of the device without one: a step's entries are each
-  // the newest of their page, a prompt's one in page_size
-  const int64_t heads4 = (kh.size + 3) / 4;
-  a.chunk = (uint32_t)std::min<int64_t>(64, std::max<int64_t>(1, n * heads4 / 2048));
+  // 64 entries and all heads a workgroup, fewer where that would leave part of the device without one: a step's
+  // entries are each the newest of their page, a prompt's one in page_size
+  a.chunk = (uint32_t)std::min<int64_t>(64, std::max<int64_t>(1, n / 2048));
+  a.heads_y = a.chunk < 64 ? 4 : std::max<uint32_t>(4, (a.heads + 65534) / 65535);
+  if (a.chunk == 64 && n >= 64 * 2048) a.heads_y = a.heads;
   int64_t v = ce == 4 ? 4 : 8;
   while (v > 1 && (a.dim % v || !rows_aligned(c->k_layout, c->k, ce, v))) v /= 2;
-  const dim3 grid((unsigned)((n + a.chunk - 1) / a.chunk), (unsigned)heads4);
+  const dim3 grid((unsigned)((n + a.chunk - 1) / a.chunk), (a.heads + a.heads_y - 1) / a.heads_y);
   const hipStream_t st = (hipStream_t)stream;
   return with_model_type(dtype, [&](auto dt) {
     constexpr int D = decltype(dt)::value;

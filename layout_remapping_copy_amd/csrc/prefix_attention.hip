@@ -17,7 +17,7 @@ typedef uint32_t U2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ F16x mfma32(B8 a, B8 b, F16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ F16x mfma32(H8 a, H8 b, F16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 
-constexpr uint32_t kTileRows = 128, kTileTokens = 64, kPitch = 256;  // of a workgroup; of a step; bytes of a row in shared memory
+constexpr uint32_t kTileTokens = 64, kPitch = 256;  // of a step; bytes of a row in shared memory
 
 // Where chunk c (16 bytes) of a row lies in its 256 bytes of shared memory: 16 rows' chunks of one number spread over
 // all banks, for the keys' operand, and 4 rows' groups of four chunks, for the values' (4 cycles of a read for each;
@@ -26,14 +26,20 @@ __device__ __forceinline__ uint32_t place_in_row(uint32_t row, uint32_t c) {
   return row * kPitch + (c ^ ((row & 3) << 2 | (row >> 2 & 3))) * 16;
 }
 
-// 128 rows (query heads of one cache head, of all sequences) share the keys and values of a run of tokens: a workgroup
-// brings 64 tokens at a time to shared memory, 8-bit codes as 16-bit numbers, while its four waves work on the 64
-// before, 32 rows each.  The scores of 32 tokens x 32 rows are a product of keys (first operand, from shared memory)
-// and queries (in registers), so that a lane has scores of one row alone: its maximum and sum need one exchange.  They
-// are also the second operand of the next product, values transposed x weights, when its inner index runs over the
-// tokens as they lie in the lane; the values' operand comes by transpose reads of shared memory.
-template <int DT, int CT, int DC>
-__global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
+// 128 or 256 rows (query heads of one cache head, of all sequences) share the keys and values of a run of tokens: a
+// workgroup of four or eight waves brings 64 tokens at a time to shared memory, 8-bit codes as 16-bit numbers, while
+// its waves work on the 64 before, 32 rows each.  The scores of 32 tokens x 32 rows are a product of keys (first operand,
+// from shared memory) and queries (in registers), so that a lane has scores of one row alone: its maximum and sum need
+// one exchange.  They are also the second operand of the next product, values transposed x weights, when its inner index
+// runs over the tokens as they lie in the lane; the values' operand comes by transpose reads of shared memory.
+//
+// What bounds it is the issue of the vector and the matrix instructions, which share each SIMD's time: 8192 rows on 32768
+// tokens (8 cache heads of 128 bf16, 137 GFLOP) 222 us, 620 TFLOP/s, the matrix units busy 45 % and the vector units 50 %
+// of the cycles; with the second part of the weights the matrix units do half as much again.  Without that part it would
+// take 47 us less, without the exponentials 15, without bringing tiles 38 (four waves).
+template <int DT, int CT, int DC, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 2) k_prefix_rows(AttentionArgs a) {
+  constexpr int kRows = 16 / WAVES, kApart = 4 * WAVES;  // rows of a tile that a lane brings a chunk of, and their distance
   using T = typename ElemOf<DT>::T;
   using M = typename MatrixOf<DT>::T;  // 8 numbers of the model's type
   constexpr bool kQuant = CT == LR_E4M3 || CT == LR_INT8;
@@ -44,12 +50,12 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
   using CT8 = std::conditional_t<kQuant, U2, U4>;  // 8 elements of the cache
   constexpr uint32_t kTile = kTileTokens * kPitch;
   __shared__ __attribute__((aligned(16))) char keys[2 * kTile], values[2 * kTile];
-  __shared__ __attribute__((aligned(16))) int64_t offs_all[4][kTileTokens][2];
-  __shared__ __attribute__((aligned(16))) float scales_all[kQuant ? 4 : 1][2][2][kTileTokens];
+  __shared__ __attribute__((aligned(16))) int64_t offs_all[WAVES][kTileTokens][2];
+  __shared__ __attribute__((aligned(16))) float scales_all[kQuant ? WAVES : 1][2][2][kTileTokens];
   const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64), r = lane & 31, half = lane >> 5;
   auto offs = offs_all[w];
   auto scales = scales_all[kQuant ? w : 0];
-  const uint32_t row0 = threadIdx.x / 16, chunk = threadIdx.x % 16;  // of the rows row0 + 16 x this lane brings one chunk
+  const uint32_t row0 = threadIdx.x / 16, chunk = threadIdx.x % 16;  // of the rows row0 + kApart x this lane brings one chunk
   // Where this lane reads its operands: of the keys row r, of the values four columns of a token (below).  The other
   // chunks of the row are at the same place but for bits 5 to 7, in which their numbers differ.
   const uint32_t key_at = place_in_row(r, half), val_row = 4 * half + (lane & 15) / 4;
@@ -67,7 +73,7 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
   Run run;
   if (!run_begin(a, blockIdx.x, &run)) return;
   do {
-    const uint32_t g = run.u / a.tiles, tile0 = run.u % a.tiles * kTileRows + w * 32, row = tile0 + here(r);
+    const uint32_t g = run.u / a.tiles, tile0 = run.u % a.tiles * (32 * WAVES) + w * 32, row = tile0 + here(r);
     const uint32_t lo = run.lo, hi = run.hi;
     const bool idle = tile0 >= a.group;
 
@@ -111,13 +117,13 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
       }
       return __ballot(ok);
     };
-    CT8 kr[4], vr[4];
+    CT8 kr[kRows], vr[kRows];
     uint32_t bad = 0;  // of this lane's rows, those not seen
     auto load = [&](uint64_t seen) {
       bad = 0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t t = row0 + 16 * x;
+      for (int x = 0; x < kRows; ++x) {
+        const uint32_t t = row0 + kApart * x;
         kr[x] = *(const CT8*)(kbase + offs[t][0]);
         vr[x] = *(const CT8*)(vbase + offs[t][1]);
         bad |= (uint32_t)(~(seen >> t) & 1) << x;
@@ -125,8 +131,8 @@ __global__ void __launch_bounds__(256, 2) k_prefix_rows(AttentionArgs a) {
     };
     auto store = [&](uint32_t buf) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t at = place_in_row(row0 + 16 * x, chunk);
+      for (int x = 0; x < kRows; ++x) {
+        const uint32_t at = place_in_row(row0 + kApart * x, chunk);
         U4 k, v;
         if constexpr (kQuant) {
           k = __builtin_bit_cast(U4, decode<DT, CT>(kr[x]));
@@ -325,24 +331,27 @@ static bool much_work(const AttentionArgs& x, int32_t ctype) {
 static bool rows_fit(const AttentionArgs& a, int32_t dtype) {
   return a.path == LR_ATTENTION_MATRIX && dtype != LR_F32 && a.dk <= 128 && a.dv <= 128;
 }
-template <int DT, int CT> static int launch_rows_of(const AttentionArgs& a, hipStream_t st) {
+template <int DT, int CT, int DC> static int launch_rows_wide(const AttentionArgs& a, uint32_t waves, hipStream_t st) {
   const dim3 grid(a.splits == 1 ? a.units : a.grid);
-  const int32_t widest = std::max(a.dk, a.dv);
-  if (widest <= 64)
-    hipLaunchKernelGGL((k_prefix_rows<DT, CT, 64>), grid, dim3(256), 0, st, a);
-  else if (widest <= 96)
-    hipLaunchKernelGGL((k_prefix_rows<DT, CT, 96>), grid, dim3(256), 0, st, a);
+  if (waves == 8)
+    hipLaunchKernelGGL((k_prefix_rows<DT, CT, DC, 8>), grid, dim3(512), 0, st, a);
   else
-    hipLaunchKernelGGL((k_prefix_rows<DT, CT, 128>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_prefix_rows<DT, CT, DC, 4>), grid, dim3(256), 0, st, a);
   return check_op_launch();
 }
-template <int DT> static int launch_rows_from(const AttentionArgs& a, int32_t ctype, hipStream_t st) {
-  if (ctype == LR_E4M3) return launch_rows_of<DT, LR_E4M3>(a, st);
-  if (ctype == LR_INT8) return launch_rows_of<DT, LR_INT8>(a, st);
-  return launch_rows_of<DT, DT>(a, st);
+template <int DT, int CT> static int launch_rows_of(const AttentionArgs& a, uint32_t waves, hipStream_t st) {
+  const int32_t widest = std::max(a.dk, a.dv);
+  return widest <= 64   ? launch_rows_wide<DT, CT, 64>(a, waves, st)
+         : widest <= 96 ? launch_rows_wide<DT, CT, 96>(a, waves, st)
+                        : launch_rows_wide<DT, CT, 128>(a, waves, st);
 }
-static int launch_rows(const AttentionArgs& a, int32_t dtype, int32_t ctype, hipStream_t st) {
-  return dtype == LR_F16 ? launch_rows_from<LR_F16>(a, ctype, st) : launch_rows_from<LR_BF16>(a, ctype, st);
+template <int DT> static int launch_rows_from(const AttentionArgs& a, uint32_t waves, int32_t ctype, hipStream_t st) {
+  if (ctype == LR_E4M3) return launch_rows_of<DT, LR_E4M3>(a, waves, st);
+  if (ctype == LR_INT8) return launch_rows_of<DT, LR_INT8>(a, waves, st);
+  return launch_rows_of<DT, DT>(a, waves, st);
+}
+static int launch_rows(const AttentionArgs& a, uint32_t waves, int32_t dtype, int32_t ctype, hipStream_t st) {
+  return dtype == LR_F16 ? launch_rows_from<LR_F16>(a, waves, ctype, st) : launch_rows_from<LR_BF16>(a, waves, ctype, st);
 }
 
 template <int DT, int CT, int DC>
@@ -465,15 +474,19 @@ int lr_prefix_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, 
   const hipStream_t st = (hipStream_t)stream;
   const bool matrix = x.path == LR_ATTENTION_MATRIX && a.path == LR_ATTENTION_MATRIX;
   if (rows_fit(x, dtype) && x.group >= kManyRows && much_work(x, c->dtype)) {
-    x.tiles = (x.group + kTileRows - 1) / kTileRows;
+    // Eight waves share a tile's staging (1024 rows on 32768 tokens 244 us with four, 222 with eight), but four where that
+    // spares codes, whose staging costs more, half a tile of rows that are none (384 rows on 65536: 218 and 236).
+    const uint32_t fours = (x.group + 127) / 128;
+    const uint32_t waves = fours > 1 && !(is_quantised(c->dtype) && fours % 2) ? 8 : 4;
+    x.tiles = waves == 8 ? (fours + 1) / 2 : fours;
     x.units = x.kv_heads * x.tiles;
     x.wide_heads = 1;
     x.block = kBlock;
     // Two workgroups a CU, but one where that leaves runs of under two blocks of 128 tokens: 128 rows on 16000 tokens 46
     // us with two and 43 with one, 192 rows 54 and 58.
     const int64_t blocks = x.units * ((int64_t)x.max_pages * x.page_size / kBlock);
-    x.grid = (uint32_t)(blocks >= 4 * kRuns ? 2 * kRuns : kRuns);
-    if (int rc = launch_rows(x, dtype, c->dtype, st)) return rc;
+    x.grid = (uint32_t)(waves == 4 && blocks >= 4 * kRuns ? 2 * kRuns : kRuns);
+    if (int rc = launch_rows(x, waves, dtype, c->dtype, st)) return rc;
     if (int rc = launch_attention_pass(a, dtype, c->dtype, st)) return rc;
   } else if (matrix && !much_work(x, c->dtype) && x.wide_heads == 1 && a.wide_heads == 1) {
     for (AttentionArgs* y : {&x, &a}) {
