@@ -164,3 +164,166 @@ def test_axes_binding_refusals():
     with pytest.raises(TypeError):
         B._axes_rotation(t, torch.arange(3, dtype=torch.int32), "half")
     assert ctypes.sizeof(B.lr_axes_rotation) == 40
+
+
+# -------------------------------------------------------------------------------- refusals: a shared prefix
+def prefix(c=None, plan=False, **kw):
+    a = dict(q=Y, Lq="(64,8,3):(1,64,512)", cq=1536, prefix=A, pp=4, plen=A + 0x1000, table=S, stride=4, pages=4, lens=S + 4096,
+             batch=3, out=Y + 0x100000, Lo="(64,8,3):(1,64,512)", co=1536, lse=None, dtype=B.BF16, scale=0.125, ws=Y + 0x200000,
+             wb=1 << 24)
+    a.update(kw)
+    c = c if c is not None else cache()
+    Lq, Lo = lr.Layout(a["Lq"]).c, lr.Layout(a["Lo"]).c
+    if plan:
+        return lr.lib().lr_prefix_attention_plan(Lq, c, Lo, a["pp"], a["pages"], a["dtype"], B.lr_prefix_plan())
+    return lr.lib().lr_prefix_attention(a["q"], Lq, a["cq"], c, a["prefix"], a["pp"], a["plen"], a["table"], a["stride"],
+                                        a["pages"], a["lens"], a["batch"], a["out"], Lo, a["co"], a["lse"], a["dtype"],
+                                        a["scale"], a["ws"], a["wb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), B.OK), (dict(batch=0, prefix=None, plen=None, table=None, lens=None), B.OK),
+    (dict(q=None), B.ERR_INVALID), (dict(out=None), B.ERR_INVALID), (dict(table=None), B.ERR_INVALID),
+    (dict(lens=None), B.ERR_INVALID), (dict(prefix=None), B.ERR_INVALID), (dict(plen=None), B.ERR_INVALID),
+    (dict(batch=-1), B.ERR_INVALID), (dict(batch=4), B.ERR_BOUNDS), (dict(scale=math.nan), B.ERR_INVALID),
+    (dict(scale=math.inf), B.ERR_INVALID), (dict(pages=0), B.ERR_INVALID), (dict(pp=0), B.ERR_INVALID),
+    (dict(pp=-1), B.ERR_INVALID), (dict(pages=1 << 40), B.ERR_OVERFLOW), (dict(pp=1 << 40), B.ERR_OVERFLOW),
+    (dict(stride=-1), B.ERR_INVALID), (dict(cq=1535), B.ERR_BOUNDS), (dict(co=1535), B.ERR_BOUNDS),
+    (dict(dtype=B.E4M3), B.ERR_TYPE), (dict(Lq="(32,8,3):(1,64,512)"), B.ERR_SIZE_MISMATCH),
+    (dict(Lo="(64,4,3):(1,64,512)"), B.ERR_SIZE_MISMATCH),
+    (dict(Lq="(64,7,3):(1,64,512)", Lo="(64,7,3):(1,64,512)"), B.ERR_SIZE_MISMATCH),
+    (dict(Lo="(64,8,3):(1,64,0)"), B.ERR_ALIAS), (dict(out=Y), B.ERR_OVERLAP), (dict(out=X), B.ERR_OVERLAP),
+    (dict(lse=Y), B.ERR_OVERLAP), (dict(out=S), B.ERR_OVERLAP), (dict(out=A - 8), B.ERR_OVERLAP), (dict(lse=A + 0x1000), B.ERR_OVERLAP),
+    (dict(lse=A - 92), B.ERR_OVERLAP), (dict(ws=Y, batch=0), B.ERR_OVERLAP), (dict(ws=A & ~15), B.ERR_OVERLAP),
+    (dict(ws=None), B.ERR_CAPACITY), (dict(wb=100), B.ERR_CAPACITY), (dict(ws=Y + 0x200004), B.ERR_INVALID),
+    (dict(Lq="(64,(2,4),3):(1,(512,64),2048)", cq=9999), B.ERR_INVALID)])
+def test_prefix_refusals(kw, code):
+    assert prefix(**kw) == code
+
+
+def test_prefix_pairs_and_plan():
+    assert prefix(c=cache(B.F16)) == B.ERR_TYPE
+    big = "(288,2,16,8):(1,288,576,9216)"
+    c = cache(B.BF16, Lk=big, Lv=big, ck=73728, cv=73728)
+    q = "(288,8,3):(1,288,2304)"
+    assert prefix(c=c, Lq=q, Lo=q, cq=6912, co=6912) == B.ERR_INVALID and prefix(plan=True, c=c, Lq=q, Lo=q) == B.ERR_INVALID
+    assert prefix(plan=True) == B.OK
+    assert lr.lib().lr_prefix_attention_plan(None, cache(), None, 1, 1, B.BF16, None) == B.ERR_INVALID
+    for heads, batch, pp, pages in ((8, 3, 1, 1), (8, 1, 4000, 1), (64, 128, 2048, 128), (2, 200, 20000, 3), (80, 7, 3, 5000)):
+        p = B.lr_prefix_plan()
+        L = lr.Layout(f"(64,{heads},{batch}):(1,64,{64 * heads})").c
+        assert lr.lib().lr_prefix_attention_plan(L, cache(), L, pp, pages, B.BF16, p) == B.OK
+        parts = batch * heads * (p.prefix_splits + p.own_splits)
+        assert p.prefix_splits >= 1 and p.own_splits >= 1
+        assert parts * 66 * 4 <= p.workspace_bytes <= parts * 66 * 4 + 64
+        n = 64 * heads * batch
+        args = dict(Lq=f"(64,{heads},{batch}):(1,64,{64 * heads})", Lo=f"(64,{heads},{batch}):(1,64,{64 * heads})", cq=n, co=n,
+                    pp=pp, pages=pages, stride=pages, batch=0, out=Y + (1 << 28), ws=Y + (1 << 29))
+        assert prefix(wb=p.workspace_bytes, **args) == B.OK and prefix(wb=p.workspace_bytes - 1, **args) == B.ERR_CAPACITY
+
+
+# -------------------------------------------------------------------------------- refusals: blocks
+def keys(c=None, **kw):
+    a = dict(slots=S, n=10, keys=Y, L="(64,2,8):(1,64,128)", cap=1024, dtype=B.BF16)
+    a.update(kw)
+    c = c if c is not None else cache()
+    return lr.lib().lr_block_keys(c, a["slots"], a["n"], a["keys"], lr.Layout(a["L"]).c if a["L"] else None, a["cap"], a["dtype"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=0), B.OK), (dict(n=0, slots=None), B.OK), (dict(n=-1), B.ERR_INVALID), (dict(slots=None), B.ERR_INVALID),
+    (dict(keys=None), B.ERR_INVALID), (dict(L=None), B.ERR_INVALID), (dict(dtype=B.INT8), B.ERR_TYPE), (dict(cap=1023), B.ERR_BOUNDS),
+    (dict(L="(32,2,8):(1,64,128)"), B.ERR_SIZE_MISMATCH), (dict(L="(64,1,8):(1,64,128)"), B.ERR_SIZE_MISMATCH),
+    (dict(L="(64,2,7):(1,64,128)"), B.ERR_SIZE_MISMATCH), (dict(L="(64,16):(1,64)"), B.ERR_INVALID),
+    (dict(L="(64,2,8):(1,64,0)"), B.ERR_ALIAS), (dict(L="(64,2,8):(1,32,128)"), B.ERR_ALIAS),
+    (dict(L="((8,8),2,8):((1,16),256,512)", cap=9999), B.ERR_INVALID), (dict(keys=S), B.ERR_OVERLAP), (dict(keys=X + 64), B.ERR_OVERLAP),
+    (dict(keys=V), B.ERR_OVERLAP), (dict(keys=W + 4096), B.ERR_OVERLAP), (dict(n=1 << 31), B.ERR_OVERFLOW)])
+def test_block_keys_refusals(kw, code):
+    assert keys(**kw) == code
+
+
+def test_block_keys_pairs():
+    assert keys(c=cache(B.F16), n=0) == B.ERR_TYPE and keys(c=cache(B.BF16), n=0) == B.OK
+    assert keys(c=cache(k=None)) == B.ERR_INVALID and keys(dtype=B.F32, n=0) == B.OK
+    assert keys(n=0, L="(64,2,8):(16,1024,2)", cap=4096) == B.OK        # any order of the head dimension, heads and pages
+
+
+def select(plan=False, **kw):
+    a = dict(q=Y, Lq="(64,8,3):(1,64,512)", cq=1536, keys=V, Lk="(64,2,9):(1,64,128)", ck=1152, dtype=B.BF16, table=S, stride=40,
+             pages=40, lens=S + 4096, page=16, batch=3, first=1, last=2, blocks=W, count=8, ws=Y + 0x200000, wb=3 * 2 * 40 * 8)
+    a.update(kw)
+    Lq, Lk = lr.Layout(a["Lq"]).c, lr.Layout(a["Lk"]).c
+    if plan:
+        n = ctypes.c_int64()
+        return lr.lib().lr_block_select_plan(Lq, Lk, a["pages"], n), n.value
+    return lr.lib().lr_block_select(a["q"], Lq, a["cq"], a["keys"], Lk, a["ck"], a["dtype"], a["table"], a["stride"], a["pages"],
+                                    a["lens"], a["page"], a["batch"], a["first"], a["last"], a["blocks"], a["count"], a["ws"],
+                                    a["wb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), B.OK), (dict(batch=0, table=None, lens=None), B.OK), (dict(q=None), B.ERR_INVALID), (dict(keys=None), B.ERR_INVALID),
+    (dict(blocks=None), B.ERR_INVALID), (dict(table=None), B.ERR_INVALID), (dict(lens=None), B.ERR_INVALID),
+    (dict(batch=-1), B.ERR_INVALID), (dict(batch=4), B.ERR_BOUNDS), (dict(stride=-1), B.ERR_INVALID), (dict(pages=0), B.ERR_INVALID),
+    (dict(page=0), B.ERR_INVALID), (dict(page=-1), B.ERR_INVALID), (dict(page=1 << 31), B.ERR_OVERFLOW), (dict(count=0), B.ERR_INVALID),
+    (dict(first=-1), B.ERR_INVALID), (dict(last=-1), B.ERR_INVALID), (dict(first=7), B.ERR_INVALID), (dict(first=9, last=0), B.ERR_INVALID),
+    (dict(first=(1 << 63) - 1, last=(1 << 63) - 1), B.ERR_INVALID), (dict(first=6, batch=0), B.OK), (dict(count=1 << 31, batch=0), B.ERR_OVERFLOW),
+    (dict(dtype=B.E4M3), B.ERR_TYPE), (dict(cq=1535), B.ERR_BOUNDS), (dict(ck=1151), B.ERR_BOUNDS),
+    (dict(Lk="(32,2,9):(1,64,128)"), B.ERR_SIZE_MISMATCH), (dict(Lk="(64,3,9):(1,64,128)"), B.ERR_BOUNDS),
+    (dict(Lk="(64,3,9):(1,64,192)", ck=1728), B.ERR_SIZE_MISMATCH),
+    (dict(Lk="(64,18):(1,64)"), B.ERR_INVALID), (dict(Lq="(288,8,3):(1,288,2304)", Lk="(288,2,9):(1,288,576)", cq=9999, ck=9999), B.ERR_INVALID),
+    (dict(ws=None), B.ERR_CAPACITY), (dict(wb=1919), B.ERR_CAPACITY), (dict(ws=Y + 0x200008), B.ERR_INVALID),
+    (dict(blocks=Y), B.ERR_OVERLAP), (dict(blocks=V + 2300), B.ERR_OVERLAP), (dict(blocks=S + 4), B.ERR_OVERLAP),
+    (dict(blocks=S + 4096), B.ERR_OVERLAP), (dict(ws=W), B.ERR_OVERLAP), (dict(ws=V), B.ERR_OVERLAP),
+    (dict(Lk="(64,2,9):(1,64,0)", batch=0), B.OK)])
+def test_block_select_refusals(kw, code):
+    assert select(**kw) == code
+
+
+def test_block_select_plan():
+    assert select(plan=True) == (B.OK, 3 * 2 * 40 * 8) and select(plan=True, pages=1) == (B.OK, 48)
+    assert select(plan=True, pages=0)[0] == B.ERR_INVALID and select(plan=True, pages=1 << 31)[0] == B.ERR_OVERFLOW
+    L = lr.Layout("(64,8,3):(1,64,512)").c
+    assert lr.lib().lr_block_select_plan(L, L, 4, None) == B.ERR_INVALID
+
+
+def attend_blocks(c=None, plan=False, **kw):
+    a = dict(q=Y, Lq="(64,8,3):(1,64,512)", cq=1536, blocks=A, count=5, table=S, stride=40, pages=40, lens=S + 4096, batch=3,
+             out=Y + 0x100000, Lo="(64,8,3):(1,64,512)", co=1536, lse=None, dtype=B.BF16, scale=0.125, ws=Y + 0x200000, wb=1 << 24)
+    a.update(kw)
+    c = c if c is not None else cache()
+    Lq, Lo = lr.Layout(a["Lq"]).c, lr.Layout(a["Lo"]).c
+    if plan:
+        p = B.lr_attention_plan()
+        return lr.lib().lr_block_attention_plan(Lq, c, Lo, a["count"], a["dtype"], p), p
+    return lr.lib().lr_block_attention(a["q"], Lq, a["cq"], c, a["blocks"], a["count"], a["table"], a["stride"], a["pages"],
+                                       a["lens"], a["batch"], a["out"], Lo, a["co"], a["lse"], a["dtype"], a["scale"], a["ws"],
+                                       a["wb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), B.OK), (dict(batch=0, blocks=None, table=None, lens=None), B.OK), (dict(q=None), B.ERR_INVALID),
+    (dict(out=None), B.ERR_INVALID), (dict(blocks=None), B.ERR_INVALID), (dict(table=None), B.ERR_INVALID),
+    (dict(lens=None), B.ERR_INVALID), (dict(batch=-1), B.ERR_INVALID), (dict(batch=4), B.ERR_BOUNDS),
+    (dict(scale=math.inf), B.ERR_INVALID), (dict(pages=0), B.ERR_INVALID), (dict(count=0), B.ERR_INVALID),
+    (dict(count=-1), B.ERR_INVALID), (dict(pages=1 << 40), B.ERR_OVERFLOW), (dict(count=1 << 40), B.ERR_OVERFLOW),
+    (dict(stride=-1), B.ERR_INVALID), (dict(cq=1535), B.ERR_BOUNDS), (dict(co=1535), B.ERR_BOUNDS), (dict(dtype=B.INT8), B.ERR_TYPE),
+    (dict(Lq="(32,8,3):(1,64,512)"), B.ERR_SIZE_MISMATCH), (dict(Lo="(64,8,3):(1,64,0)"), B.ERR_ALIAS), (dict(out=Y), B.ERR_OVERLAP),
+    (dict(out=A + 64), B.ERR_OVERLAP), (dict(out=S + 64), B.ERR_OVERLAP), (dict(lse=A - 92), B.ERR_OVERLAP), (dict(out=V), B.ERR_OVERLAP)])
+def test_block_attention_refusals(kw, code):
+    assert attend_blocks(**kw) == code
+
+
+def test_block_attention_plan():
+    rc, p = attend_blocks(plan=True, count=4000)
+    assert rc == B.OK and p.splits > 1 and p.workspace_bytes == 3 * 8 * p.splits * 66 * 4
+    assert attend_blocks(count=4000, wb=p.workspace_bytes - 1) == B.ERR_CAPACITY
+    assert attend_blocks(count=4000, ws=None) == B.ERR_CAPACITY and attend_blocks(count=4000, ws=Y + 0x200004) == B.ERR_INVALID
+    rc, p = attend_blocks(plan=True, count=4)
+    assert rc == B.OK and p.splits == 1 and p.workspace_bytes == 0
+    assert attend_blocks(c=cache(B.F16)) == B.ERR_TYPE
+    assert lr.lib().lr_block_attention_plan(None, cache(), None, 1, B.BF16, None) == B.ERR_INVALID
+
+
+def test_structs_match_the_header():
+    assert ctypes.sizeof(B.lr_prefix_plan) == 32

@@ -381,6 +381,117 @@ def test_prefix_attention_special_values(dev, dtype, heads):
     close(lse, wlse, tol.lse)
 
 
+# Calls of enough rows and tokens to share tiles in shared memory: from 64 rows of a cache head on, 600000 rows times
+# tokens (2^20 over 8-bit caches) that the prefix's pages have room for, 16-bit types, heads of up to 128.
+ROWS = [  # type, kind, heads, kv, dk, dv, page, order, prefix, sequences, pages of the prefix's table
+    ("bf16", "bf16", 16, 1, 128, 128, 16, "tokens", 3201, 12, 201), ("fp16", "fp16", 16, 1, 128, 128, 16, "heads", 4700, 8, 294),
+    ("bf16", "bf16", 8, 2, 64, 64, 8, "tokens", 777, 32, 700), ("fp16", "fp16", 8, 2, 96, 80, 32, "heads", 500, 40, 150),
+    ("bf16", "bf16", 5, 1, 72, 128, 5, "tokens", 333, 13, 2000), ("bf16", "bf16", 7, 1, 112, 40, 1, "heads", 130, 10, 9000),
+    ("bf16", "e4m3", 16, 1, 128, 128, 64, "heads", 3300, 21, 52), ("fp16", "int8", 16, 1, 96, 96, 16, "tokens", 2800, 24, 176),
+    ("bf16", "int8", 8, 1, 72, 64, 16, "heads", 1000, 24, 400), ("fp16", "e4m3", 8, 1, 128, 24, 16, "tokens", 90, 10, 900),
+    ("bf16", "e4m3", 4, 4, 80, 128, 8, "tokens", 300, 70, 2000), ("fp16", "fp16", 4, 4, 8, 8, 16, "tokens", 64, 129, 400),
+    ("bf16", "bf16", 16, 1, 32, 32, 16, "tokens", 40000, 4, 2500), ("bf16", "bf16", 1, 1, 128, 128, 16, "heads", 1, 64, 600),
+    ("bf16", "bf16", 4, 1, 64, 128, 16, "tokens", 400, 500, 26), ("fp16", "e4m3", 1, 1, 128, 128, 16, "heads", 5000, 257, 313),
+]
+
+
+def rows_case(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, b, width, **kw):
+    lens = [(37 * i) % 41 for i in range(b)]
+    cache, first, table, shared, slots, sides = prefix_case(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, lens, **kw)
+    wide = torch.full((max(width, -(-prefix // page)),), -1, dtype=torch.int32)
+    wide[:-(-prefix // page)] = first[:-(-prefix // page)]
+    return lens, cache, wide, table, shared, slots, sides
+
+
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,order,prefix,b,width", ROWS)
+def test_prefix_attention_rows(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, b, width):
+    t = T[dtype]
+    assert b * heads // kv >= 64 and b * heads // kv * width * page >= (1 << 20 if kind in TOP else 600000)
+    lens, cache, wide, table, shared, slots, (kn, vn) = rows_case(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, b, width)
+    q = rand((b, heads, dk), t, 11)
+    out, lse = torch.full((b, heads, dv), -7.0, dtype=t, device=dev), torch.full((b, heads), -7.0, device=dev)
+    Lq, Lo = f"({dk},{heads},{b}):(1,{dk},{heads * dk})", f"({dv},{heads},{b}):(1,{dv},{heads * dv})"
+    args = (q.to(dev), Lq, cache, wide.to(dev), int32([prefix], dev), table.to(dev), int32(lens, dev))
+    lr.prefix_attention(*args, out, Lo, lse=lse)
+    again = torch.empty_like(out)
+    lr.prefix_attention(*args, again, Lo)
+    assert torch.equal(out, again)
+    some = list(range(0, b, max(1, b // 12))) + [b - 1]                 # the 64-bit form takes a sequence at a time
+    seen = [torch.cat([shared, slots[i]]) for i in some]
+    want, wlse, tol = attention64(q[some], [kn[u] for u in seen], [vn[u] for u in seen], dk ** -0.5, t, kind)
+    close(out.cpu()[some], want, tol, "out")
+    close(lse.cpu()[some], wlse, tol.lse, "lse")
+
+
+@pytest.mark.parametrize("scale", [4.0, -0.7, 0.0])
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,order,prefix,b,width", [ROWS[2], ROWS[3], ROWS[8], ROWS[9]])
+def test_prefix_attention_rows_scales_and_pages(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, b, width, scale):
+    """Large, negative and no scales; pages that are none inside the prefix; rows without a sequence; strided queries;
+    a part of the batch, whose other rows stay."""
+    t = T[dtype]
+    lens, cache, wide, table, shared, slots, (kn, vn) = rows_case(dev, dtype, kind, heads, kv, dk, dv, page, order, prefix, b, width)
+    wide[1], wide[2] = -1, 1 << 30
+    kept = torch.cat([shared[:page], shared[3 * page:]])
+    lens[1], lens[b - 2] = -1, -7
+    row = dk + 3
+    q = rand((b + 2, heads, dk), t, 11)
+    flat = torch.full((heads * (b + 2) * row + 1,), float("nan"), dtype=t)
+    flat[1:].as_strided(q.shape, (row, (b + 2) * row, 1)).copy_(q)
+    out, lse = torch.full((b + 2, heads, dv), -7.0, dtype=t, device=dev), torch.full((b, heads), -7.0, device=dev)
+    lr.prefix_attention(flat.to(dev)[1:], f"({dk},{heads},{b + 2}):(1,{(b + 2) * row},{row})", cache, wide.to(dev), int32([prefix], dev),
+                        table.to(dev), int32(lens, dev), out, f"({dv},{heads},{b + 2}):(1,{dv},{heads * dv})", scale=scale, lse=lse)
+    some = [0, 1, 2, b // 2, b - 2, b - 1]
+    seen = [torch.cat([kept, slots[i]]) if lens[i] >= 0 else slots[i][:0] for i in some]
+    want, wlse, tol = attention64(q[some], [kn[u] for u in seen], [vn[u] for u in seen], scale, t, kind)
+    close(out.cpu()[some], want, tol, "out")
+    close(lse.cpu()[some], wlse, tol.lse, "lse")
+    assert (out[b:] == -7).all()
+
+
+@pytest.mark.parametrize("dtype,kind", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
+def test_prefix_attention_rows_special_values(dev, dtype, kind):
+    """Infinite values make their element infinite in every row, also where their weight has no second part; a NaN query
+    its own rows NaN; what the cache holds in other slots (NaN) does not matter."""
+    t, heads, kv, d, page, b, prefix = T[dtype], 8, 1, 64, 16, 20, 500
+    lens, cache, wide, table, shared, slots, (kn, vn) = rows_case(dev, dtype, kind, heads, kv, d, d, page, "tokens", prefix, b, 500)
+    q = rand((b, heads, d), t, 5)
+    q[2, 1, 5] = math.nan
+    if kind not in TOP:
+        rows = vn[shared[77:78]].clone()
+        rows[0, 0, 3], rows[0, 0, 40] = math.inf, -math.inf
+        put_rows(cache, "v", "tokens", page, kv, d, shared[77:78], rows.to(t))
+        put_rows(cache, "k", "tokens", page, kv, d, shared[77:78], torch.zeros(1, kv, d, dtype=t))
+        kn[shared[77]] = 0                                              # its score is 0: a weight of one part at some base
+    out, lse = torch.empty((b, heads, d), dtype=t, device=dev), torch.empty((b, heads), device=dev)
+    L = f"({d},{heads},{b}):(1,{d},{heads * d})"
+    lr.prefix_attention(q.to(dev), L, cache, wide.to(dev), int32([prefix], dev), table.to(dev), int32(lens, dev), out, L, lse=lse)
+    seen = [torch.cat([shared, u]) for u in slots]
+    clean = torch.where(q.isnan(), torch.zeros_like(q), q)
+    want, wlse, tol = attention64(clean, [kn[u] for u in seen], [vn[u] for u in seen], d ** -0.5, t, kind)
+    if kind not in TOP:
+        want[..., 3], want[..., 40] = math.inf, -math.inf
+    want[2, 1], wlse[2, 1] = math.nan, math.nan
+    close(out.cpu(), want, tol)
+    close(lse.cpu(), wlse, tol.lse)
+
+
+@pytest.mark.parametrize("dtype,kind,weight,floor", [("bf16", "bf16", 2.0 ** -15, 0.0), ("fp16", "fp16", 2.0 ** -22, 2.0 ** -30),
+                                                     ("fp16", "e4m3", 2.0 ** -15, 0.0)])
+def test_prefix_attention_rows_weights_in_two_parts(dev, dtype, kind, weight, floor):
+    """The weights have 16 bits (22 in fp16): values of one sign and size, whose sum one part of 8 bits would miss by more.
+    A first part that is cut off leaves the second half a step of 2^-8 of what is below 2^-7: 2^-15 of the weight; fp16
+    weights are kept from 0 by 2^-24 in the first part, which the second may not take off again, off a largest of 2^7."""
+    t, heads, kv, d, page, b, prefix = T[dtype], 8, 1, 64, 16, 20, 700
+    lens, cache, wide, table, shared, slots, (kn, vn) = rows_case(dev, dtype, kind, heads, kv, d, d, page, "heads", prefix, b, 500)
+    q = rand((b, heads, d), t, 5)
+    out = torch.empty((b, heads, d), dtype=t, device=dev)
+    L = f"({d},{heads},{b}):(1,{d},{heads * d})"
+    lr.prefix_attention(q.to(dev), L, cache, wide.to(dev), int32([prefix], dev), table.to(dev), int32([0] * b, dev), out, L)
+    some = [0, 7, 19]
+    want, tol = tight64(q[some], [kn[shared]] * 3, [vn[shared]] * 3, d ** -0.5, weight, floor)
+    close(out.cpu()[some], want, tol)
+
+
 # ------------------------------------------------------------------------------------ blocks: their keys
 KEYS = [  # type, kind, heads, d, page, order, lens
     ("bf16", "bf16", 8, 128, 16, "tokens", [100, 1, 16, 17]), ("bf16", "e4m3", 8, 128, 64, "heads", [300, 64, 1]),
