@@ -37,8 +37,13 @@ __device__ __forceinline__ uint32_t place_in_row(uint32_t row, uint32_t c) {
 // tokens (8 cache heads of 128 bf16, 137 GFLOP) 222 us, 620 TFLOP/s, the matrix units busy 45 % and the vector units 50 %
 // of the cycles; with the second part of the weights the matrix units do half as much again.  Without that part it would
 // take 47 us less, without the exponentials 15, without bringing tiles 38 (four waves).
+template <int CT, int WAVES> struct RowsShared {
+  __attribute__((aligned(16))) char keys[2 * kTileTokens * kPitch], values[2 * kTileTokens * kPitch];  // two tiles each
+  __attribute__((aligned(16))) int64_t offs[WAVES][kTileTokens][2];
+  __attribute__((aligned(16))) float scales[CT == LR_E4M3 || CT == LR_INT8 ? WAVES : 1][2][2][kTileTokens];
+};
 template <int DT, int CT, int DC, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, 2) k_prefix_rows(AttentionArgs a) {
+__device__ __forceinline__ void rows_run(const AttentionArgs& a, uint32_t block, RowsShared<CT, WAVES>& shared) {
   constexpr int kRows = 16 / WAVES, kApart = 4 * WAVES;  // rows of a tile that a lane brings a chunk of, and their distance
   using T = typename ElemOf<DT>::T;
   using M = typename MatrixOf<DT>::T;  // 8 numbers of the model's type
@@ -49,12 +54,10 @@ __global__ void __launch_bounds__(64 * WAVES, 2) k_prefix_rows(AttentionArgs a) 
   using PE = std::conditional_t<kQuant, __bf16, T>;
   using CT8 = std::conditional_t<kQuant, U2, U4>;  // 8 elements of the cache
   constexpr uint32_t kTile = kTileTokens * kPitch;
-  __shared__ __attribute__((aligned(16))) char keys[2 * kTile], values[2 * kTile];
-  __shared__ __attribute__((aligned(16))) int64_t offs_all[WAVES][kTileTokens][2];
-  __shared__ __attribute__((aligned(16))) float scales_all[kQuant ? WAVES : 1][2][2][kTileTokens];
+  char *keys = shared.keys, *values = shared.values;
   const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64), r = lane & 31, half = lane >> 5;
-  auto offs = offs_all[w];
-  auto scales = scales_all[kQuant ? w : 0];
+  auto offs = shared.offs[w];
+  auto scales = shared.scales[kQuant ? w : 0];
   const uint32_t row0 = threadIdx.x / 16, chunk = threadIdx.x % 16;  // of the rows row0 + kApart x this lane brings one chunk
   // Where this lane reads its operands: of the keys row r, of the values four columns of a token (below).  The other
   // chunks of the row are at the same place but for bits 5 to 7, in which their numbers differ.
@@ -71,7 +74,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) k_prefix_rows(AttentionArgs a) 
   const float unit = kQuant || a.scale2 == 0 ? 1.f : __builtin_fabsf(a.scale2);
 
   Run run;
-  if (!run_begin(a, blockIdx.x, &run)) return;
+  if (!run_begin(a, block, &run)) return;
   do {
     const uint32_t g = run.u / a.tiles, tile0 = run.u % a.tiles * (32 * WAVES) + w * 32, row = tile0 + here(r);
     const uint32_t lo = run.lo, hi = run.hi;
@@ -286,6 +289,28 @@ __global__ void __launch_bounds__(64 * WAVES, 2) k_prefix_rows(AttentionArgs a) 
   } while (run_next(a, &run));
 }
 
+template <int DT, int CT, int DC, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 2) k_prefix_rows(AttentionArgs a) {
+  __shared__ RowsShared<CT, WAVES> shared;
+  rows_run<DT, CT, DC, WAVES>(a, blockIdx.x, shared);
+}
+
+// Both passes in one launch where one workgroup a CU has the prefix: the first `first` workgroups.  The others have the
+// sequences' own tokens, whose bound is the reading of them, on the other half of each CU (32 sequences of up to 1024 tokens
+// behind 8191: 51 us with a launch for each pass, 40 this way).
+template <int DT, int CT, int DC, int OWN>
+__global__ void __launch_bounds__(256, 2) k_prefix_mixed(AttentionArgs prefix, AttentionArgs own, uint32_t first) {
+  constexpr int kOwn = DC == 96 && (CT == LR_E4M3 || CT == LR_INT8) ? 128 : DC;
+  __shared__ union {
+    RowsShared<CT, 4> rows;
+    MatrixShared<DT, CT, kOwn, 1, OWN> matrix;
+  } shared;
+  if (blockIdx.x < first)
+    rows_run<DT, CT, DC, 4>(prefix, blockIdx.x, shared.rows);
+  else
+    attention_run<DT, CT, kOwn, 1, OWN>(own, blockIdx.x - first, shared.matrix);
+}
+
 // Both passes in one launch, for calls whose time is mostly that of launches: the first `first` workgroups have the
 // prefix, the others the sequences' own tokens.
 template <int DT, int CT, int DC>
@@ -331,27 +356,36 @@ static bool much_work(const AttentionArgs& x, int32_t ctype) {
 static bool rows_fit(const AttentionArgs& a, int32_t dtype) {
   return a.path == LR_ATTENTION_MATRIX && dtype != LR_F32 && a.dk <= 128 && a.dv <= 128;
 }
-template <int DT, int CT, int DC> static int launch_rows_wide(const AttentionArgs& a, uint32_t waves, hipStream_t st) {
-  const dim3 grid(a.splits == 1 ? a.units : a.grid);
-  if (waves == 8)
-    hipLaunchKernelGGL((k_prefix_rows<DT, CT, DC, 8>), grid, dim3(512), 0, st, a);
+// How such a call runs: waves of a workgroup, and whether the sequences' own tokens go along in its launch.
+struct RowsLaunch {
+  uint32_t waves;
+  bool mixed;
+};
+template <int DT, int CT, int DC>
+static int launch_rows_wide(const AttentionArgs& x, const AttentionArgs& a, RowsLaunch how, hipStream_t st) {
+  const unsigned grid = x.splits == 1 ? x.units : x.grid, second = a.splits == 1 ? a.batch * a.units : a.grid;
+  if (how.mixed && a.wide_heads > 1)
+    hipLaunchKernelGGL((k_prefix_mixed<DT, CT, DC, kOverHeads>), dim3(grid + second), dim3(256), 0, st, x, a, grid);
+  else if (how.mixed)
+    hipLaunchKernelGGL((k_prefix_mixed<DT, CT, DC, kOverTokens>), dim3(grid + second), dim3(256), 0, st, x, a, grid);
+  else if (how.waves == 8)
+    hipLaunchKernelGGL((k_prefix_rows<DT, CT, DC, 8>), dim3(grid), dim3(512), 0, st, x);
   else
-    hipLaunchKernelGGL((k_prefix_rows<DT, CT, DC, 4>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_prefix_rows<DT, CT, DC, 4>), dim3(grid), dim3(256), 0, st, x);
   return check_op_launch();
 }
-template <int DT, int CT> static int launch_rows_of(const AttentionArgs& a, uint32_t waves, hipStream_t st) {
+template <int DT, int CT>
+static int launch_rows_of(const AttentionArgs& x, const AttentionArgs& a, RowsLaunch how, hipStream_t st) {
   const int32_t widest = std::max(a.dk, a.dv);
-  return widest <= 64   ? launch_rows_wide<DT, CT, 64>(a, waves, st)
-         : widest <= 96 ? launch_rows_wide<DT, CT, 96>(a, waves, st)
-                        : launch_rows_wide<DT, CT, 128>(a, waves, st);
+  return widest <= 64   ? launch_rows_wide<DT, CT, 64>(x, a, how, st)
+         : widest <= 96 ? launch_rows_wide<DT, CT, 96>(x, a, how, st)
+                        : launch_rows_wide<DT, CT, 128>(x, a, how, st);
 }
-template <int DT> static int launch_rows_from(const AttentionArgs& a, uint32_t waves, int32_t ctype, hipStream_t st) {
-  if (ctype == LR_E4M3) return launch_rows_of<DT, LR_E4M3>(a, waves, st);
-  if (ctype == LR_INT8) return launch_rows_of<DT, LR_INT8>(a, waves, st);
-  return launch_rows_of<DT, DT>(a, waves, st);
-}
-static int launch_rows(const AttentionArgs& a, uint32_t waves, int32_t dtype, int32_t ctype, hipStream_t st) {
-  return dtype == LR_F16 ? launch_rows_from<LR_F16>(a, waves, ctype, st) : launch_rows_from<LR_BF16>(a, waves, ctype, st);
+template <int DT>
+static int launch_rows_from(const AttentionArgs& x, const AttentionArgs& a, RowsLaunch how, int32_t ctype, hipStream_t st) {
+  if (ctype == LR_E4M3) return launch_rows_of<DT, LR_E4M3>(x, a, how, st);
+  if (ctype == LR_INT8) return launch_rows_of<DT, LR_INT8>(x, a, how, st);
+  return launch_rows_of<DT, DT>(x, a, how, st);
 }
 
 template <int DT, int CT, int DC>
@@ -475,19 +509,24 @@ int lr_prefix_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, 
   const bool matrix = x.path == LR_ATTENTION_MATRIX && a.path == LR_ATTENTION_MATRIX;
   if (rows_fit(x, dtype) && x.group >= kManyRows && much_work(x, c->dtype)) {
     // Eight waves share a tile's staging (1024 rows on 32768 tokens 244 us with four, 222 with eight), but four where that
-    // spares codes, whose staging costs more, half a tile of rows that are none (384 rows on 65536: 218 and 236).
+    // spares codes, whose staging costs more, half a tile of rows that are none (384 rows on 65536: 218 and 236).  Where
+    // one workgroup of four waves a CU has no more than 8 blocks of 128 tokens (5 of codes), the other half of the CU takes
+    // the sequences' own tokens in the same launch (up to 64 each: 128 rows on 8191 tokens 38 us without and 29 with, 512
+    // rows 65 and 58, 256 rows on 30000 82 and 84; over e4m3 256 rows on 8191 47 and 42, on 16000 60 and 63).
     const uint32_t fours = (x.group + 127) / 128;
-    const uint32_t waves = fours > 1 && !(is_quantised(c->dtype) && fours % 2) ? 8 : 4;
-    x.tiles = waves == 8 ? (fours + 1) / 2 : fours;
+    const int64_t blocks = (int64_t)x.kv_heads * fours * ((int64_t)x.max_pages * x.page_size / kBlock);
+    const bool mixed = blocks <= (is_quantised(c->dtype) ? 5 : 8) * kRuns && matrix && a.unit_heads == 16;
+    const RowsLaunch how{!mixed && fours > 1 && !(is_quantised(c->dtype) && fours % 2) ? 8u : 4u, mixed};
+    x.tiles = how.waves == 8 ? (fours + 1) / 2 : fours;
     x.units = x.kv_heads * x.tiles;
     x.wide_heads = 1;
     x.block = kBlock;
-    // Two workgroups a CU, but one where that leaves runs of under two blocks of 128 tokens: 128 rows on 16000 tokens 46
-    // us with two and 43 with one, 192 rows 54 and 58.
-    const int64_t blocks = x.units * ((int64_t)x.max_pages * x.page_size / kBlock);
-    x.grid = (uint32_t)(waves == 4 && blocks >= 4 * kRuns ? 2 * kRuns : kRuns);
-    if (int rc = launch_rows(x, waves, dtype, c->dtype, st)) return rc;
-    if (int rc = launch_attention_pass(a, dtype, c->dtype, st)) return rc;
+    x.grid = (uint32_t)(how.waves == 8 || mixed ? kRuns : 2 * kRuns);
+    const int rc = dtype == LR_F16 ? launch_rows_from<LR_F16>(x, a, how, c->dtype, st)
+                                   : launch_rows_from<LR_BF16>(x, a, how, c->dtype, st);
+    if (rc) return rc;
+    if (!how.mixed)
+      if (int rc2 = launch_attention_pass(a, dtype, c->dtype, st)) return rc2;
   } else if (matrix && !much_work(x, c->dtype) && x.wide_heads == 1 && a.wide_heads == 1) {
     for (AttentionArgs* y : {&x, &a}) {
       y->unit_heads = 16;
