@@ -35,6 +35,8 @@ Other modes (for rocprofv3 runs and their summaries under profiles/):
   --operators [NAMES]   the attention operators' listed cases (all, or some,
                         comma-separated): cold, and calls back to back on
                         rotating inputs, as a markdown table
+  --more-operators [NAMES]  the same of positions with several axes, attention over
+                        a shared prefix and over selected blocks
 """
 
 from __future__ import annotations
@@ -670,13 +672,12 @@ def batched_sweep(lr, torch, mode: str = "paths", steps: int = 20):
         torch.cuda.empty_cache()
 
 
-def operators_run(torch, names=None, reps: int = 20):
-    """Markdown table of the listed cases of perf/operators.py through the package's entry points.  Cold: 512 MiB
+def operators_run(torch, P, names=None, reps: int = 20):
+    """Markdown table of the listed cases of P, perf/operators.py or perf/more_operators.py, through the package's
+    entry points.  Cold: 512 MiB
     are filled before each timed call, which leaves the 256 MB cache full of lines that have to be written back.
     Back to back: 50 calls over two states, wall time with the device's work, the host's part of a call included."""
     import statistics
-
-    import perf.operators as P
 
     P.own = True
     flush = torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
@@ -857,6 +858,8 @@ def main():
                     help="with --launch: also time K back-to-back launches per spec")
     ap.add_argument("--operators", nargs="?", const="", metavar="NAMES",
                     help="the attention operators' listed cases, all or the comma-separated ones")
+    ap.add_argument("--more-operators", nargs="?", const="", metavar="NAMES",
+                    help="the listed cases of positions with several axes, shared prefixes and selected blocks")
     args = ap.parse_args()
 
     if args.summarize_counters:
@@ -884,7 +887,14 @@ def main():
         counters_run(lr, torch, W)
         return
     if args.operators is not None:
-        operators_run(torch, args.operators.split(",") if args.operators else None)
+        import perf.operators
+
+        operators_run(torch, perf.operators, args.operators.split(",") if args.operators else None)
+        return
+    if args.more_operators is not None:
+        import perf.more_operators
+
+        operators_run(torch, perf.more_operators, args.more_operators.split(",") if args.more_operators else None)
         return
     if args.launch:
         launch_run(lr, torch, W, args.launch, back_to_back=args.back_to_back)

@@ -903,13 +903,14 @@ def rope_axes_table(rot_dim: int, sections: Sequence[int], order: str = "blocks"
         raise ValueError(f"order {order!r} is neither 'blocks' nor 'cyclic'")
     p = lr_rope_params(rot_dim, ROPE_SCALING[scaling], base, factor, original_len, low, high)
     pairs = max(1, min(rot_dim, 1024) // 2)
-    turns, axis = (ctypes.c_int64 * pairs)(), (ctypes.c_int32 * pairs)()
+    both = (ctypes.c_int64 * (2 * pairs))()  # the frequencies, then the axes: one copy to the device
+    axis = (ctypes.c_int32 * (2 * pairs)).from_buffer(both, 8 * pairs)
     m = ctypes.c_double()
     axes = len(sections)
     _check(lib().lr_rope_axes_table(ctypes.byref(p), (ctypes.c_int32 * max(1, axes))(*sections), axes,
-                                    AXES_ORDER[order], int(own), turns, axis, ctypes.byref(m)), "rope_axes_table")
-    return RopeAxesTable(torch.tensor(list(turns), dtype=torch.int64).to(device),
-                         torch.tensor(list(axis), dtype=torch.int32).to(device), rot_dim, axes, m.value)
+                                    AXES_ORDER[order], int(own), both, axis, ctypes.byref(m)), "rope_axes_table")
+    held = torch.frombuffer(both, dtype=torch.int64).clone().to(device)
+    return RopeAxesTable(held[:pairs], held[pairs:].view(torch.int32)[:pairs], rot_dim, axes, m.value)
 
 
 def _axes_rotation(table: RopeAxesTable, positions, pairs: str) -> lr_axes_rotation:

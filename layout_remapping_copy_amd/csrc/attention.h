@@ -913,18 +913,22 @@ __device__ __forceinline__ Columns columns_of(int32_t dv) {
   const uint32_t wide = ((uint32_t)dv + 3) / 4;
   return Columns{wide, 256 / wide, threadIdx.x / wide, threadIdx.x % wide};
 }
-// Adds the parts of the list at ml and po; false for a unit that is whole, where that is asked for.
-__device__ __forceinline__ bool join_list(const float* part_ml, const float* part_o, uint32_t splits, int32_t dv,
+typedef float F2 __attribute__((ext_vector_type(2)));
+// Maximum and sum of this lane's part among the 64 from s on.
+__device__ __forceinline__ F2 part_at(const float* part_ml, uint32_t s, uint32_t splits) {
+  const uint32_t i = s + (threadIdx.x & 63);
+  return i < splits ? ((const F2*)part_ml)[i] : F2{-__builtin_inff(), 0.f};
+}
+// Adds the parts of the list at part_ml (the first 64 of which are `x`) and part_o; false for a unit that is whole, where
+// that is asked for.
+__device__ __forceinline__ bool join_list(F2 x, const float* part_ml, const float* part_o, uint32_t splits, int32_t dv,
                                           const Columns& q4, bool ask_whole, Joined* j) {
-  typedef float F2 __attribute__((ext_vector_type(2)));
   const uint32_t lane = threadIdx.x & 63, c = q4.c;
-  const F2* ml = (const F2*)part_ml;
   const float* po = part_o + 4 * c;
   float top = j->top, total = j->total;
   F4 acc = j->acc;
   for (uint32_t s = 0; s < splits; s += 64) {
-    F2 x = {-__builtin_inff(), 0.f};
-    if (s + lane < splits) x = ml[s + lane];
+    if (s) x = part_at(part_ml, s, splits);
     const uint64_t hit = __ballot(__float_as_uint(x[1]) >> 31);  // what is past the last part means nothing
     const uint32_t parts = hit ? __ffsll((unsigned long long)hit) : 64;
     if (ask_whole && s == 0 && parts == 1) return false;  // whole: written already
@@ -982,7 +986,8 @@ __global__ void __launch_bounds__(256) k_attention_join(AttentionArgs a) {
   const uint64_t at = (uint64_t)blockIdx.x * a.splits;
   const Columns q4 = columns_of(a.dv);
   Joined j{-__builtin_inff(), 0.f, F4{}};
-  if (!join_list(a.part_ml + 2 * at, a.part_o + at * a.dv, a.splits, a.dv, q4, true, &j)) return;
+  const float* ml = a.part_ml + 2 * at;
+  if (!join_list(part_at(ml, 0, a.splits), ml, a.part_o + at * a.dv, a.splits, a.dv, q4, true, &j)) return;
   join_out<DT>(a, blockIdx.x / a.heads, blockIdx.x % a.heads, q4, j, false, os);
 }
 

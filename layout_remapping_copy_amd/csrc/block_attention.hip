@@ -59,10 +59,15 @@ __device__ __forceinline__ void add_halves(double* sum, uint32_t lanes, uint32_t
 
 // A workgroup has `chunk` entries of slots and makes the mean of every page whose newest slot is among them; its waves
 // take cache heads of one page side by side, which share lines of memory, their scales above all.  A row of a page is a
-// group of lanes with V elements each, as many rows at a time as the wave has groups, their loads four ahead.  Sums are
-// held in 64 bits, in which those of a page of codes or 16-bit keys are exact but for extreme ranges: which blocks a
-// score selects does not hang on the order of a sum.  The groups' sums are added by halves, each half of the lanes
-// keeping half of the columns, so that a lane ends with few to divide and store.
+// group of lanes with V elements each, as many rows at a time as the wave has groups, four loads ahead, and the next
+// rows or page asked for before these are added.  Sums are held in 64 bits, in which those of a page of codes or 16-bit
+// keys are exact but for extreme ranges: which blocks a score selects does not hang on the order of a sum.  The groups'
+// sums are added by halves, each half of the lanes keeping half of the columns, so that a lane ends with few to divide
+// and store (all lanes with all columns: 254 us for the first size below).
+//
+// 262142 tokens of 8 heads of 128 e4m3 in pages of 16 (tokens first): 83 us, 3.4 TB/s, vector instructions busy 75 % of it:
+// adding in 32 bits would take 4 us less, adding nothing no less.  16 tokens, each the newest of its page of 64: 5 us,
+// slot, keys and store one after another.
 template <int DT, int CT, int V>
 __global__ void __launch_bounds__(256) k_block_keys(BlockKeysArgs a) {
   using T = typename ElemOf<DT>::T;
@@ -209,8 +214,9 @@ __device__ __forceinline__ double row_largest(double x) {
 // product of 64-bit matrix instructions, as fast as the vector units' 64 bits, with the sums over the lanes done; they
 // take 2048 cycles of a SIMD for 16 blocks of 128.  Keys and queries come from memory as the products' operands
 // themselves (16 rows, each lane a chunk of 16 bytes), so that waves share nothing; a wave takes every fourth tile of
-// its workgroup's, the next one's keys under way.  (Asking for the first tile's keys before the length is known: 12.7 us
-// for the 8 MB of 16 sequences' 8 heads, 11.3 this way.)
+// its workgroup's, the next one's keys under way.  2 sequences of 8192 blocks, 64 heads on 8 of 128 bf16 (34 MB): 17 us,
+// of which the products are 7; 16 sequences of up to 512 blocks, 32 heads (8 MB): 11 us, length, page, key and product
+// one after another (12.7 with the first tile's keys asked for before the length is known).
 template <int DT, int DC, bool WIDE>
 __global__ void __launch_bounds__(256) k_block_scores(SelectArgs a) {
   using T = typename ElemOf<DT>::T;
@@ -288,7 +294,8 @@ __device__ __forceinline__ uint64_t order_of(double x) {
 // The score at the border is found a digit of 8 bits at a time, from the highest bit in which any two scores differ,
 // until a digit's scores are all taken or all bits are known; the chosen blocks are then written in their order, of
 // equal scores at the border the first ones.  A lane keeps the first HELD scores of its own; those of longer rows are
-// read again for each digit.
+// read again for each digit.  16 rows of 8191 scores: 18 us, a chain of reading, four digits and three sums over the
+// workgroup; 128 rows of up to 512, by four waves each: 6 us.
 template <int LANES, int HELD>
 __global__ void __launch_bounds__(LANES) k_block_choose(SelectArgs a) {
   constexpr uint32_t kWaves = LANES / 64;
@@ -614,7 +621,7 @@ int lr_block_select(const void* q, const lr_layout* Lq, int64_t q_capacity, cons
     });
     if (rc) return rc;
   }
-  // a row of up to 1024 scores by four waves (6 us for 128 rows of up to 512), longer ones by sixteen
+  // a row of up to 1024 scores by four waves, longer ones by sixteen
   if (max_pages > 1024)
     hipLaunchKernelGGL((k_block_choose<1024, 8>), dim3((unsigned)rows), dim3(1024), 0, st, a);
   else

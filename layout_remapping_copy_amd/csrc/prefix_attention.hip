@@ -34,9 +34,9 @@ __device__ __forceinline__ uint32_t place_in_row(uint32_t row, uint32_t c) {
 // runs over the tokens as they lie in the lane; the values' operand comes by transpose reads of shared memory.
 //
 // What bounds it is the issue of the vector and the matrix instructions, which share each SIMD's time: 8192 rows on 32768
-// tokens (8 cache heads of 128 bf16, 137 GFLOP) 222 us, 620 TFLOP/s, the matrix units busy 45 % and the vector units 50 %
-// of the cycles; with the second part of the weights the matrix units do half as much again.  Without that part it would
-// take 47 us less, without the exponentials 15, without bringing tiles 38 (four waves).
+// tokens (8 cache heads of 128 bf16, 137 GFLOP) 206 us, 667 TFLOP/s, where a large library product reaches 1270; with
+// the second part of the weights the matrix units do half as much again.  With four waves (244 us: matrix units busy 44 %,
+// vector units 55 %) leaving out that part saved 47 us, the exponentials 15, bringing tiles 38.
 template <int CT, int WAVES> struct RowsShared {
   __attribute__((aligned(16))) char keys[2 * kTileTokens * kPitch], values[2 * kTileTokens * kPitch];  // two tiles each
   __attribute__((aligned(16))) int64_t offs[WAVES][kTileTokens][2];
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(256, 2) k_prefix_mixed(AttentionArgs prefix, A
 }
 
 // Both passes in one launch, for calls whose time is mostly that of launches: the first `first` workgroups have the
-// prefix, the others the sequences' own tokens.
+// prefix, the others the sequences' own tokens.  4 sequences of up to 60 tokens behind 1000, 32 heads on 8 of 128 bf16:
+// 8.7 us, 8.2 and 5.7 with a launch for each.
 template <int DT, int CT, int DC>
 __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, 1>::kMinWaves)) k_prefix_pair(AttentionArgs prefix, AttentionArgs own,
                                                                                              uint32_t first) {
@@ -329,6 +330,7 @@ struct PrefixJoin {
   FastDiv fd_group;
 };
 
+// A workgroup a query head, as k_attention_join.  8192 heads of some 10 parts, of 512 bytes each: 21 us, 2 TB/s; 128 heads: 4.7 us.
 template <int DT>
 __global__ void __launch_bounds__(256) k_prefix_join(AttentionArgs a, PrefixJoin p) {
   __shared__ __attribute__((aligned(16))) float os[256 * 4];
@@ -337,9 +339,12 @@ __global__ void __launch_bounds__(256) k_prefix_join(AttentionArgs a, PrefixJoin
   const uint64_t own = (uint64_t)blockIdx.x * a.splits;
   const uint64_t pre = ((uint64_t)(g * p.batch + b) * p.group + (h - g * p.group)) * p.splits;
   Joined j{-__builtin_inff(), 0.f, F4{}};
-  join_list(p.ml + 2 * pre, p.o + pre * a.dv, p.splits, a.dv, q4, false, &j);
-  join_list(a.part_ml + 2 * own, a.part_o + own * a.dv, a.splits, a.dv, q4, false, &j);
-  join_out<DT>(a, b, h, q4, j, a.lens[b] < 0, os);
+  const float *ml = p.ml + 2 * pre, *ml2 = a.part_ml + 2 * own;
+  const F2 x = part_at(ml, 0, p.splits), x2 = part_at(ml2, 0, a.splits);  // both lists' first, side by side
+  const bool blank = a.lens[b] < 0;
+  join_list(x, ml, p.o + pre * a.dv, p.splits, a.dv, q4, false, &j);
+  join_list(x2, ml2, a.part_o + own * a.dv, a.splits, a.dv, q4, false, &j);
+  join_out<DT>(a, b, h, q4, j, blank, os);
 }
 
 // From so many rows of a cache head on they share what a workgroup brings to shared memory, if there is work enough for
@@ -508,7 +513,7 @@ int lr_prefix_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, 
   const hipStream_t st = (hipStream_t)stream;
   const bool matrix = x.path == LR_ATTENTION_MATRIX && a.path == LR_ATTENTION_MATRIX;
   if (rows_fit(x, dtype) && x.group >= kManyRows && much_work(x, c->dtype)) {
-    // Eight waves share a tile's staging (1024 rows on 32768 tokens 244 us with four, 222 with eight), but four where that
+    // Eight waves share a tile's staging (1024 rows on 32768 tokens 244 us with four, 206 with eight), but four where that
     // spares codes, whose staging costs more, half a tile of rows that are none (384 rows on 65536: 218 and 236).  Where
     // one workgroup of four waves a CU has no more than 8 blocks of 128 tokens (5 of codes), the other half of the CU takes
     // the sequences' own tokens in the same launch (up to 64 each: 128 rows on 8191 tokens 38 us without and 29 with, 512

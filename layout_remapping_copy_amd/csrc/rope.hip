@@ -36,7 +36,8 @@ struct RopeChunkArgs {
 // instructions, a pair's turn 6: over 8 heads the arithmetic is 37 % of the vector units' time and memory the bound.
 // 16 x 4096 x 32 x 128 bf16, heads regrouped on the way (1 GiB moved): 179 us, 6.0 TB/s, against 157 for a plain
 // copy and 170 for the same regrouping without arithmetic.  Eight tokens of one step: 4.2 us, two dependent reads
-// of memory after the arguments'; a call is 6.9 us of the host.
+// of memory after the arguments'; a call is 6.9 us of the host.  With positions on three axes (AXES) the angles
+// wait for more reads, side by side: 8 x 8192 x 32 x 128 bf16, regrouped (1 GiB), 179 us too.
 template <int DT, int V, bool NT, bool AXES>
 __global__ void __launch_bounds__(256) k_rope_chunks(RopeChunkArgs a) {
   using T = typename ElemOf<DT>::T;
