@@ -712,7 +712,7 @@ int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, c
  * the same bits.  workspace: at least the plan's workspace_bytes, 16-byte aligned; never 0. */
 typedef struct {
   int32_t path;            /* lr_attention_path, for 16-byte aligned buffers */
-  int32_t row_tiles;       /* workgroups that share the prefix's keys of one cache head */
+  int32_t row_tiles;       /* workgroups that share the prefix's keys of one cache head, for all sequences */
   int64_t prefix_splits;   /* the most parts the prefix is cut into */
   int64_t own_splits;      /* the most parts a sequence's own tokens are cut into */
   int64_t workspace_bytes;

@@ -490,6 +490,7 @@ static int plan_blocks(const lr_layout* Lq, const lr_cache* c, const lr_layout* 
   if (int rc = attention_shapes(Lq, c, Lo, max_pages, dtype, a, out)) return rc;
   if (count < 1) return LR_ERR_INVALID;
   if (count > kMaxCount / a->page_size) return LR_ERR_OVERFLOW;
+  if ((double)mode_of(*Lq, 2).size * a->kv_heads * count > 0x1p60) return LR_ERR_OVERFLOW;
   a->count = (uint32_t)count;
   return attention_split(mode_of(*Lq, 2).size, count * a->page_size, true, a, out);
 }
@@ -565,14 +566,15 @@ int lr_block_select(const void* q, const lr_layout* Lq, int64_t q_capacity, cons
                     int64_t keys_capacity, int32_t dtype, const int32_t* table, int64_t table_stride, int64_t max_pages,
                     const int32_t* lens, int64_t page_size, int64_t batch, int64_t first, int64_t last, int32_t* blocks,
                     int64_t count, void* workspace, int64_t workspace_bytes, void* stream) {
-  if (!q || !keys || !blocks || batch < 0 || (batch > 0 && (!table || !lens)) || table_stride < 0) return LR_ERR_INVALID;
+  if (!q || !keys || batch < 0 || (batch > 0 && (!blocks || !table || !lens)) || table_stride < 0) return LR_ERR_INVALID;
   if (!is_model_type(dtype)) return LR_ERR_TYPE;
   Rows r, k;
   int64_t need;
   if (int rc = plan_select(Lq, q_capacity, Lkeys, keys_capacity, max_pages, &r, &k, &need)) return rc;
   if (batch > r.items) return LR_ERR_BOUNDS;
   if (page_size < 1 || first < 0 || last < 0 || count < 1 || first > count || last > count - first) return LR_ERR_INVALID;
-  if (max_pages > kMaxCount / page_size || count > kMaxCount) return LR_ERR_OVERFLOW;
+  if (max_pages > kMaxCount / page_size || count > kMaxCount || (double)batch * k.heads * count > 0x1p60)
+    return LR_ERR_OVERFLOW;
   if (!workspace || workspace_bytes < need) return LR_ERR_CAPACITY;
   if ((uintptr_t)workspace % 16) return LR_ERR_INVALID;
   const int64_t e = dtype_bytes(dtype);

@@ -361,13 +361,43 @@ static bool much_work(const AttentionArgs& x, int32_t ctype) {
 static bool rows_fit(const AttentionArgs& a, int32_t dtype) {
   return a.path == LR_ATTENTION_MATRIX && dtype != LR_F32 && a.dk <= 128 && a.dv <= 128;
 }
-// How such a call runs: waves of a workgroup, and whether the sequences' own tokens go along in its launch.
-struct RowsLaunch {
+// How the prefix's pass runs: by k_prefix_rows in workgroups of so many waves, by k_prefix_pair, or as that of a batch
+// of one sequence; and whether the sequences' own tokens go along in its launch.
+struct PrefixWay {
+  enum { kRows, kPair, kAlone } how;
   uint32_t waves;
   bool mixed;
 };
+// Chooses it, and sets the tiles and runs that go with it.
+static PrefixWay prefix_way(int32_t dtype, int32_t ctype, AttentionArgs* x, AttentionArgs* a) {
+  const bool matrix = x->path == LR_ATTENTION_MATRIX && a->path == LR_ATTENTION_MATRIX;
+  if (rows_fit(*x, dtype) && x->group >= kManyRows && much_work(*x, ctype)) {
+    // Eight waves share a tile's staging (1024 rows on 32768 tokens 244 us with four, 206 with eight), but four where that
+    // spares codes, whose staging costs more, half a tile of rows that are none (384 rows on 65536: 218 and 236).  Where
+    // one workgroup of four waves a CU has no more than 8 blocks of 128 tokens (5 of codes), the other half of the CU takes
+    // the sequences' own tokens in the same launch (up to 64 each: 128 rows on 8191 tokens 38 us without and 29 with, 512
+    // rows 65 and 58, 256 rows on 30000 82 and 84; over e4m3 256 rows on 8191 47 and 42, on 16000 60 and 63).
+    const uint32_t fours = (x->group + 127) / 128;
+    const int64_t blocks = (int64_t)x->kv_heads * fours * ((int64_t)x->max_pages * x->page_size / kBlock);
+    const bool mixed = blocks <= (is_quantised(ctype) ? 5 : 8) * kRuns && matrix && a->unit_heads == 16;
+    const uint32_t waves = !mixed && fours > 1 && !(is_quantised(ctype) && fours % 2) ? 8 : 4;
+    x->tiles = waves == 8 ? (fours + 1) / 2 : fours;
+    x->units = x->kv_heads * x->tiles;
+    x->wide_heads = 1;
+    x->block = kBlock;
+    x->grid = (uint32_t)(waves == 8 || mixed ? kRuns : 2 * kRuns);
+    return {PrefixWay::kRows, waves, mixed};
+  }
+  if (!matrix || much_work(*x, ctype) || x->wide_heads > 1 || a->wide_heads > 1) return {PrefixWay::kAlone, 4, false};
+  for (AttentionArgs* y : {x, a}) {
+    y->unit_heads = 16;
+    y->tiles = (y->group + 15) / 16;
+    y->units = y->kv_heads * y->tiles;
+  }
+  return {PrefixWay::kPair, 4, true};
+}
 template <int DT, int CT, int DC>
-static int launch_rows_wide(const AttentionArgs& x, const AttentionArgs& a, RowsLaunch how, hipStream_t st) {
+static int launch_rows_wide(const AttentionArgs& x, const AttentionArgs& a, PrefixWay how, hipStream_t st) {
   const unsigned grid = x.splits == 1 ? x.units : x.grid, second = a.splits == 1 ? a.batch * a.units : a.grid;
   if (how.mixed && a.wide_heads > 1)
     hipLaunchKernelGGL((k_prefix_mixed<DT, CT, DC, kOverHeads>), dim3(grid + second), dim3(256), 0, st, x, a, grid);
@@ -380,14 +410,14 @@ static int launch_rows_wide(const AttentionArgs& x, const AttentionArgs& a, Rows
   return check_op_launch();
 }
 template <int DT, int CT>
-static int launch_rows_of(const AttentionArgs& x, const AttentionArgs& a, RowsLaunch how, hipStream_t st) {
+static int launch_rows_of(const AttentionArgs& x, const AttentionArgs& a, PrefixWay how, hipStream_t st) {
   const int32_t widest = std::max(a.dk, a.dv);
   return widest <= 64   ? launch_rows_wide<DT, CT, 64>(x, a, how, st)
          : widest <= 96 ? launch_rows_wide<DT, CT, 96>(x, a, how, st)
                         : launch_rows_wide<DT, CT, 128>(x, a, how, st);
 }
 template <int DT>
-static int launch_rows_from(const AttentionArgs& x, const AttentionArgs& a, RowsLaunch how, int32_t ctype, hipStream_t st) {
+static int launch_rows_from(const AttentionArgs& x, const AttentionArgs& a, PrefixWay how, int32_t ctype, hipStream_t st) {
   if (ctype == LR_E4M3) return launch_rows_of<DT, LR_E4M3>(x, a, how, st);
   if (ctype == LR_INT8) return launch_rows_of<DT, LR_INT8>(x, a, how, st);
   return launch_rows_of<DT, DT>(x, a, how, st);
@@ -456,6 +486,9 @@ int lr_prefix_attention_plan(const lr_layout* Lq, const lr_cache* c, const lr_la
   if (!out) return LR_ERR_INVALID;
   PrefixPlan p;
   if (int rc = plan_prefix(Lq, c, Lo, prefix_pages, max_pages, dtype, &p)) return rc;
+  p.own.path = p.p_own.path;
+  p.pre.path = p.p_pre.path;
+  prefix_way(dtype, c->dtype, &p.pre, &p.own);
   out->path = p.p_own.path;
   out->row_tiles = (int32_t)p.pre.tiles;
   out->prefix_splits = p.p_pre.splits;
@@ -511,38 +544,18 @@ int lr_prefix_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, 
   attention_buffers(c, Lq, q, dtype, p.p_own.path, &a);
   attention_buffers(c, Lq, q, dtype, p.p_pre.path, &x);
   const hipStream_t st = (hipStream_t)stream;
-  const bool matrix = x.path == LR_ATTENTION_MATRIX && a.path == LR_ATTENTION_MATRIX;
-  if (rows_fit(x, dtype) && x.group >= kManyRows && much_work(x, c->dtype)) {
-    // Eight waves share a tile's staging (1024 rows on 32768 tokens 244 us with four, 206 with eight), but four where that
-    // spares codes, whose staging costs more, half a tile of rows that are none (384 rows on 65536: 218 and 236).  Where
-    // one workgroup of four waves a CU has no more than 8 blocks of 128 tokens (5 of codes), the other half of the CU takes
-    // the sequences' own tokens in the same launch (up to 64 each: 128 rows on 8191 tokens 38 us without and 29 with, 512
-    // rows 65 and 58, 256 rows on 30000 82 and 84; over e4m3 256 rows on 8191 47 and 42, on 16000 60 and 63).
-    const uint32_t fours = (x.group + 127) / 128;
-    const int64_t blocks = (int64_t)x.kv_heads * fours * ((int64_t)x.max_pages * x.page_size / kBlock);
-    const bool mixed = blocks <= (is_quantised(c->dtype) ? 5 : 8) * kRuns && matrix && a.unit_heads == 16;
-    const RowsLaunch how{!mixed && fours > 1 && !(is_quantised(c->dtype) && fours % 2) ? 8u : 4u, mixed};
-    x.tiles = how.waves == 8 ? (fours + 1) / 2 : fours;
-    x.units = x.kv_heads * x.tiles;
-    x.wide_heads = 1;
-    x.block = kBlock;
-    x.grid = (uint32_t)(how.waves == 8 || mixed ? kRuns : 2 * kRuns);
-    const int rc = dtype == LR_F16 ? launch_rows_from<LR_F16>(x, a, how, c->dtype, st)
-                                   : launch_rows_from<LR_BF16>(x, a, how, c->dtype, st);
+  const PrefixWay way = prefix_way(dtype, c->dtype, &x, &a);
+  if (way.how == PrefixWay::kRows) {
+    const int rc = dtype == LR_F16 ? launch_rows_from<LR_F16>(x, a, way, c->dtype, st)
+                                   : launch_rows_from<LR_BF16>(x, a, way, c->dtype, st);
     if (rc) return rc;
-    if (!how.mixed)
-      if (int rc2 = launch_attention_pass(a, dtype, c->dtype, st)) return rc2;
-  } else if (matrix && !much_work(x, c->dtype) && x.wide_heads == 1 && a.wide_heads == 1) {
-    for (AttentionArgs* y : {&x, &a}) {
-      y->unit_heads = 16;
-      y->tiles = (y->group + 15) / 16;
-      y->units = y->kv_heads * y->tiles;
-    }
+  } else if (way.how == PrefixWay::kPair) {
     if (int rc = launch_pair(x, a, dtype, c->dtype, st)) return rc;
   } else {
     if (int rc = launch_attention_pass(x, dtype, c->dtype, st)) return rc;
-    if (int rc = launch_attention_pass(a, dtype, c->dtype, st)) return rc;
   }
+  if (!way.mixed)
+    if (int rc = launch_attention_pass(a, dtype, c->dtype, st)) return rc;
   const PrefixJoin j{x.part_ml, x.part_o, x.splits, a.group, a.batch, make_fastdiv(a.group)};
   return with_model_type(dtype, [&](auto dt) {
     hipLaunchKernelGGL((k_prefix_join<decltype(dt)::value>), dim3((unsigned)(batch * a.heads)), dim3(256), 0, st, a, j);

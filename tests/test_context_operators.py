@@ -327,3 +327,23 @@ def test_block_attention_plan():
 
 def test_structs_match_the_header():
     assert ctypes.sizeof(B.lr_prefix_plan) == 32
+
+
+@pytest.mark.parametrize("heads,batch,pages,tiles", [
+    (8, 3, 1, 1), (8, 40, 10, 10), (80, 7, 3, 18),  # 12, 160 and 280 rows of a cache head: tiles of 16
+    (8, 40, 1000, 2), (8, 32, 8000, 1),             # 160 and 128 on 16000 and 128000 tokens: of 128
+    (64, 16, 300, 2), (64, 9, 2000, 3), (64, 128, 2048, 16)])  # 512 and 4096: of 256; 288 over codes: of 128
+def test_prefix_plan_tiles(heads, batch, pages, tiles):
+    """The plan says how many workgroups share the prefix's keys as the call will run, not as that of one sequence would."""
+    p = B.lr_prefix_plan()
+    L = lr.Layout(f"(64,{heads},{batch}):(1,64,{64 * heads})").c
+    assert lr.lib().lr_prefix_attention_plan(L, cache(), L, pages, 3, B.BF16, p) == B.OK
+    assert p.row_tiles == tiles
+
+
+def test_blocks_of_no_sequence():
+    assert select(batch=0, blocks=None, table=None, lens=None) == B.OK
+    assert select(batch=1, blocks=None) == B.ERR_INVALID
+    # as many entries as no memory holds, counted without a wrap
+    many = "(64,2,1000000000):(1,64,128)"
+    assert select(Lq=many, cq=1 << 62, batch=1000000000, count=(1 << 31) - 1, pages=1, ws=Y, wb=1 << 62) == B.ERR_OVERFLOW

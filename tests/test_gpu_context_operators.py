@@ -844,3 +844,70 @@ def test_steps_on_streams_and_in_a_graph(dev):
         torch.cuda.synchronize()
         assert all(torch.equal(a, w) for a, w in zip(out, want[i])), i
         torch.randn(1 << 20, device=dev).sum().item()                    # eager work between the replays
+
+
+def test_steps_of_no_sequence(dev):
+    """A step whose batch has become empty runs through all entry points and writes nothing."""
+    d, h, kv, page, pages, width = 64, 4, 2, 16, 6, 3
+    L, Lk, Lkeys = f"({d},{h},1):(1,{d},{h * d})", f"({d},{kv},1):(1,{d},{kv * d})", f"({d},{kv},{pages}):(1,{d},{kv * d})"
+    rt = lr.rope_axes_table(d, [16, 8, 8], device=dev)
+    cache, _ = make_cache(dev, "bf16", "tokens", pages, page, kv, d, d)
+    one = torch.ones((1, h, d), dtype=torch.bfloat16, device=dev)
+    k, keys = torch.ones((1, kv, d), dtype=torch.bfloat16, device=dev), torch.full((pages, kv, d), 3.0, dtype=torch.bfloat16, device=dev)
+    table, lens = torch.zeros((0, width), dtype=torch.int32, device=dev), int32([], dev)
+    slots, pos = torch.empty(0, dtype=torch.int64, device=dev), torch.empty((3, 0), dtype=torch.int64, device=dev)
+    outs = [torch.full_like(one, 7.0) for _ in range(3)]
+    blocks = torch.empty((0, kv, 4), dtype=torch.int32, device=dev)
+    before = cache.k.clone()
+    lr.rope_axes(one, L, outs[0], L, pos, rt)
+    lr.cache_write_axes(cache, k, Lk, k, Lk, slots, rt, pos)
+    lr.block_keys(cache, slots, keys, Lkeys)
+    lr.block_select(one, L, keys, Lkeys, table, lens, page, blocks)
+    lr.block_attention(one, L, cache, blocks, table, lens, outs[1], L)
+    lr.prefix_attention(one, L, cache, int32([0, 1], dev), int32([20], dev), table, lens, outs[2], L)
+    torch.cuda.synchronize()
+    assert all((x == 7.0).all() for x in outs) and (keys == 3.0).all() and torch.equal(cache.k, before)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(dev, kind):
+    """Pages 2^30 elements apart, the last one past 2^32: the same results as with pages next to each other."""
+    d, h, page, pages, b, step = 64, 4, 2048, 5, 32, 1 << 30
+    t = T[kind] if kind == "bf16" else torch.uint8
+    L, n = f"({d},{h},{b}):(1,{d},{h * d})", pages * page
+    Ls, Ln = f"(1,{page},{pages}):(1,1,{page})", f"({d},1,{n}):(1,{d},{d})"
+    rt = lr.rope_axes_table(d, [16, 8, 8], device=dev)
+    k, v = (rand((n, 1, d), torch.bfloat16, s).to(dev) for s in (1, 2))
+    q, pos = rand((b, h, d), torch.bfloat16, 3).to(dev), ints(0, 90, (3, n), 4).to(dev)
+    slots = torch.arange(n, device=dev)
+    table = torch.randperm(pages * b, generator=torch.Generator().manual_seed(5)).int().view(b, pages).to(dev) % pages
+    lens = int32([n - 37 * i for i in range(b)], dev)
+    prefix = int32([4, 1, 0, 3, 2], dev)
+
+    def run(stride):
+        size = (pages - 1) * stride + page * d
+        bufs = [torch.empty(size, dtype=t, device=dev) for _ in range(2)]
+        Lc = f"({d},1,{page},{pages}):(1,{d},{d},{stride})"
+        scales = [torch.empty(n, device=dev) for _ in range(2)] if kind != "bf16" else [None, None]
+        cache = lr.PagedCache(bufs[0], Lc, bufs[1], Lc, *scales, Ls if kind != "bf16" else None)
+        lr.cache_write_axes(cache, k, Ln, v, Ln, slots, rt, pos)
+        keys = torch.empty((pages - 1) * stride + d, dtype=torch.bfloat16, device=dev)
+        Lkeys = f"({d},1,{pages}):(1,{d},{stride})"
+        lr.block_keys(cache, slots, keys, Lkeys)
+        blocks = torch.empty((b, 1, 3), dtype=torch.int32, device=dev)
+        lr.block_select(q, L, keys, Lkeys, table, lens, page, blocks)
+        outs = [torch.empty_like(q) for _ in range(3)]
+        lr.block_attention(q, L, cache, blocks, table, lens, outs[0], L)
+        lr.prefix_attention(q, L, cache, prefix, int32([n - 5], dev), table, lens, outs[1], L)  # 128 rows share tiles
+        L4 = f"({d},{h},4):(1,{d},{h * d})"
+        lr.prefix_attention(q, L4, cache, prefix, int32([n - 5], dev), table, lens[:4], outs[2], L4)
+        outs[2][4:] = 0
+        last = keys.as_strided((pages, d), (stride, 1)).clone()
+        turned = torch.empty_like(last)
+        lr.rope_axes(keys, Lkeys, turned, f"({d},1,{pages}):(1,{d},{d})", pos[:, :pages].contiguous(), rt)
+        return [blocks, *outs, last, turned]
+
+    near = run(page * d)
+    for i, (x, y) in enumerate(zip(near, run(step))):
+        assert torch.equal(x, y), i
+    assert near[1].isfinite().all() and near[1].abs().max() > 0 and near[2].isfinite().all()
