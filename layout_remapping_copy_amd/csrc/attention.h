@@ -899,9 +899,9 @@ __global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, HT>::kMinWaves))
   attention_run<DT, CT, DC, HT, WAVES>(a, blockIdx.x, shared);
 }
 
-// The parts of one query head, joined by a workgroup: a wave has the weights of 64 parts at a time, one a lane; 256
-// lanes are groups of lanes with four columns each, a group takes every next part, and the groups' sums are added in
-// their order.
+// The parts of one query head, joined by a workgroup or a wave: a wave has the weights of 64 parts at a time, one a lane;
+// the LANES lanes are groups of lanes with four columns each, a group takes every next part, and the groups' sums are added
+// in their order.
 struct Joined {
   float top, total;
   F4 acc;
@@ -909,9 +909,9 @@ struct Joined {
 struct Columns {  // of this lane: four from 4 c on, for the parts grp, grp + groups, ...
   uint32_t wide, groups, grp, c;
 };
-__device__ __forceinline__ Columns columns_of(int32_t dv) {
-  const uint32_t wide = ((uint32_t)dv + 3) / 4;
-  return Columns{wide, 256 / wide, threadIdx.x / wide, threadIdx.x % wide};
+template <int LANES> __device__ __forceinline__ Columns columns_of(int32_t dv) {
+  const uint32_t wide = ((uint32_t)dv + 3) / 4, lane = threadIdx.x % LANES, grp = lane / wide;
+  return Columns{wide, LANES / wide, grp, lane - grp * wide};
 }
 typedef float F2 __attribute__((ext_vector_type(2)));
 // Maximum and sum of this lane's part among the 64 from s on.
@@ -960,14 +960,17 @@ __device__ __forceinline__ bool join_list(F2 x, const float* part_ml, const floa
   *j = Joined{top, total, acc};
   return true;
 }
-// The groups' sums added, and the head's output; `os`: 256 * 4 floats of the workgroup, `blank`: zeros instead.
-template <int DT>
+// The groups' sums added, and the head's output; `os`: LANES * 4 floats of these lanes, `blank`: zeros instead.
+template <int DT, int LANES>
 __device__ __forceinline__ void join_out(const AttentionArgs& a, uint32_t b, uint32_t h, const Columns& q4, Joined j, bool blank,
                                          float* os) {
   using T = typename ElemOf<DT>::T;
   F4 acc = j.acc;
-  *(F4*)&os[4 * threadIdx.x] = acc;
-  __syncthreads();
+  *(F4*)&os[4 * (threadIdx.x % LANES)] = acc;
+  if constexpr (LANES == 64)
+    wave_fence();
+  else
+    __syncthreads();
   if (q4.grp) return;
   for (uint32_t i = 1; i < q4.groups; ++i) acc += *(const F4*)&os[4 * (i * q4.wide + q4.c)];
   T* out = (T*)a.out + (int64_t)b * a.ob + (int64_t)h * a.oh;
@@ -984,11 +987,11 @@ template <int DT>
 __global__ void __launch_bounds__(256) k_attention_join(AttentionArgs a) {
   __shared__ __attribute__((aligned(16))) float os[256 * 4];
   const uint64_t at = (uint64_t)blockIdx.x * a.splits;
-  const Columns q4 = columns_of(a.dv);
+  const Columns q4 = columns_of<256>(a.dv);
   Joined j{-__builtin_inff(), 0.f, F4{}};
   const float* ml = a.part_ml + 2 * at;
   if (!join_list(part_at(ml, 0, a.splits), ml, a.part_o + at * a.dv, a.splits, a.dv, q4, true, &j)) return;
-  join_out<DT>(a, blockIdx.x / a.heads, blockIdx.x % a.heads, q4, j, false, os);
+  join_out<DT, 256>(a, blockIdx.x / a.heads, blockIdx.x % a.heads, q4, j, false, os);
 }
 
 // ------------------------------------------------------------------ host

@@ -330,13 +330,19 @@ struct PrefixJoin {
   FastDiv fd_group;
 };
 
-// A workgroup a query head, as k_attention_join.  8192 heads of some 10 parts, of 512 bytes each: 21 us, 2 TB/s; 128 heads: 4.7 us.
-template <int DT>
+// LANES lanes a query head: a workgroup, as k_attention_join, whose four waves go over the weights each; or a wave where
+// heads are many enough to keep the device busy so.  In us, by workgroups and by waves, of some 12 parts of 128 bf16 a
+// head: 1024 heads 7.2 and 11.2, 2048 10.6 and 11.6, 2560 11 and 10.7 (of 96, 34 parts; of 64 9 and 6.4), 4096 14 and 10.3,
+// 8192 21.7 and 12 (3.7 TB/s).
+constexpr uint32_t kManyHeads = 10 * kRuns;
+template <int DT, int LANES>
 __global__ void __launch_bounds__(256) k_prefix_join(AttentionArgs a, PrefixJoin p) {
   __shared__ __attribute__((aligned(16))) float os[256 * 4];
-  const uint32_t b = blockIdx.x / a.heads, h = blockIdx.x % a.heads, g = op_div(h, p.fd_group);
-  const Columns q4 = columns_of(a.dv);
-  const uint64_t own = (uint64_t)blockIdx.x * a.splits;
+  const uint32_t w = LANES == 64 ? uniform(threadIdx.x / 64) : 0, bh = blockIdx.x * (256 / LANES) + w;
+  if (bh >= a.batch * a.heads) return;
+  const uint32_t b = bh / a.heads, h = bh - b * a.heads, g = op_div(h, p.fd_group);
+  const Columns q4 = columns_of<LANES>(a.dv);
+  const uint64_t own = (uint64_t)bh * a.splits;
   const uint64_t pre = ((uint64_t)(g * p.batch + b) * p.group + (h - g * p.group)) * p.splits;
   Joined j{-__builtin_inff(), 0.f, F4{}};
   const float *ml = p.ml + 2 * pre, *ml2 = a.part_ml + 2 * own;
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(256) k_prefix_join(AttentionArgs a, PrefixJoin
   const bool blank = a.lens[b] < 0;
   join_list(x, ml, p.o + pre * a.dv, p.splits, a.dv, q4, false, &j);
   join_list(x2, ml2, a.part_o + own * a.dv, a.splits, a.dv, q4, false, &j);
-  join_out<DT>(a, b, h, q4, j, blank, os);
+  join_out<DT, LANES>(a, b, h, q4, j, blank, os + 4 * LANES * w);
 }
 
 // From so many rows of a cache head on they share what a workgroup brings to shared memory, if there is work enough for
@@ -557,8 +563,12 @@ int lr_prefix_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, 
   if (!way.mixed)
     if (int rc = launch_attention_pass(a, dtype, c->dtype, st)) return rc;
   const PrefixJoin j{x.part_ml, x.part_o, x.splits, a.group, a.batch, make_fastdiv(a.group)};
+  const unsigned rows = (unsigned)(batch * a.heads);
   return with_model_type(dtype, [&](auto dt) {
-    hipLaunchKernelGGL((k_prefix_join<decltype(dt)::value>), dim3((unsigned)(batch * a.heads)), dim3(256), 0, st, a, j);
+    if (rows >= kManyHeads)
+      hipLaunchKernelGGL((k_prefix_join<decltype(dt)::value, 64>), dim3((rows + 3) / 4), dim3(256), 0, st, a, j);
+    else
+      hipLaunchKernelGGL((k_prefix_join<decltype(dt)::value, 256>), dim3(rows), dim3(256), 0, st, a, j);
     return check_op_launch();
   });
 }

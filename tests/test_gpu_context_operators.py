@@ -911,3 +911,29 @@ def test_offsets_past_32_bits(dev, kind):
     for i, (x, y) in enumerate(zip(near, run(step))):
         assert torch.equal(x, y), i
     assert near[1].isfinite().all() and near[1].abs().max() > 0 and near[2].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,kind,heads,kv,dk,dv,page,b,prefix", [
+    ("bf16", "bf16", 8, 2, 128, 128, 16, 330, 700), ("fp16", "e4m3", 6, 2, 96, 96, 16, 431, 90), ("fp32", "fp32", 7, 7, 33, 33, 5, 367, 50),
+    ("bf16", "int8", 4, 1, 64, 256, 8, 643, 0), ("fp16", "fp16", 64, 8, 64, 4, 16, 41, 3000), ("fp32", "fp32", 5, 1, 8, 250, 4, 515, 61)])
+def test_prefix_attention_many_heads(dev, dtype, kind, heads, kv, dk, dv, page, b, prefix):
+    """So many heads that a wave joins each one's parts: widths that leave lanes without a column, heads that do not
+    fill the last workgroup, rows without a sequence, rows behind the batch."""
+    t = T[dtype]
+    assert b * heads >= 2560
+    lens = [(37 * i) % 53 if i % 101 else 900 for i in range(b)]
+    cache, first, table, shared, slots, (kn, vn) = prefix_case(dev, dtype, kind, heads, kv, dk, dv, page, "tokens", prefix, lens)
+    q = rand((b, heads, dk), t, 11)
+    none = [5, b - 2]
+    given = [-1 if i in none else n for i, n in enumerate(lens)]
+    out = torch.full((b + 1, heads, dv), -7.0, dtype=t, device=dev)
+    lse = torch.full((b + 1, heads), -7.0, device=dev)
+    lr.prefix_attention(q.to(dev), f"({dk},{heads},{b}):(1,{dk},{heads * dk})", cache, first.to(dev), int32([prefix], dev),
+                        table.to(dev), int32(given, dev), out, f"({dv},{heads},{b}):(1,{dv},{heads * dv})", lse=lse)
+    assert (out[b] == -7).all() and (lse[b] == -7).all()
+    assert (out[none] == 0).all() and (lse[none] == -math.inf).all()
+    some = [i for i in sorted({*range(0, b, max(1, b // 12)), 101, b - 1}) if i < b and i not in none]
+    seen = [torch.cat([shared, slots[i]]) for i in some]
+    want, wlse, tol = attention64(q[some], [kn[u] for u in seen], [vn[u] for u in seen], dk ** -0.5, t, kind)
+    close(out.cpu()[some], want, tol, "out")
+    close(lse.cpu()[some], wlse, tol.lse, "lse")
