@@ -674,9 +674,9 @@ def batched_sweep(lr, torch, mode: str = "paths", steps: int = 20):
 
 def operators_run(torch, P, names=None, reps: int = 20):
     """Markdown table of the listed cases of P, perf/operators.py or perf/more_operators.py, through the package's
-    entry points.  Cold: 512 MiB
-    are filled before each timed call, which leaves the 256 MB cache full of lines that have to be written back.
-    Back to back: 50 calls over two states, wall time with the device's work, the host's part of a call included."""
+    entry points.  Cold: 512 MiB are filled before each timed call, which leaves the 256 MB cache full of lines that
+    have to be written back.  Back to back: 50 calls over two states, wall time with the device's work, the host's
+    part of a call included."""
     import statistics
 
     P.own = True

@@ -65,7 +65,7 @@ __device__ __forceinline__ void add_halves(double* sum, uint32_t lanes, uint32_t
 // sums are added by halves, each half of the lanes keeping half of the columns, so that a lane ends with few to divide
 // and store (all lanes with all columns: 254 us for the first size below).
 //
-// 262142 tokens of 8 heads of 128 e4m3 in pages of 16 (tokens first): 83 us, 3.4 TB/s, vector instructions busy 75 % of it:
+// 262142 tokens of 8 heads of 128 e4m3 in pages of 16 (tokens first): 84 us, 3.3 TB/s, vector instructions busy 80 % of it:
 // adding in 32 bits would take 4 us less, adding nothing no less.  16 tokens, each the newest of its page of 64: 5 us,
 // slot, keys and store one after another.
 template <int DT, int CT, int V>

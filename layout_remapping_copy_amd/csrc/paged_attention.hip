@@ -74,8 +74,8 @@ int attention_split(int64_t sequences, int64_t span, bool listed, AttentionArgs*
   // Parts of a sequence: short ones stay whole, which saves the second launch; otherwise as many as there
   // are blocks, up to 8192 parts in all (their sums are some 66 MB for 16 heads of 128), or 8 a unit.
   const int64_t steps = (int64_t)((double)sequences * a->kv_heads / 4 * a->tiles * (double)((span + 31) / 32));
-  const bool by_heads = out->path == LR_ATTENTION_MATRIX && !listed && a->kv_heads % 4 == 0 && std::abs(a->kh) < ktok && std::abs(a->vh) < vtok &&
-                        span <= (int64_t(1) << 30) && steps >= 8 * kRuns;
+  const bool by_heads = out->path == LR_ATTENTION_MATRIX && !listed && a->kv_heads % 4 == 0 && std::abs(a->kh) < ktok &&
+                        std::abs(a->vh) < vtok && span <= (int64_t(1) << 30) && steps >= 8 * kRuns;
   a->wide_heads = by_heads ? 4 : 1;
   // Heads that end inside a line: their waves keep in step, so that the line is still near for the second of them
   // (as above: heads of 72 in bf16 153 to 144 us, of 112 201 to 185, of 160 265 to 254).  Heads of 64 would lose 6 %
@@ -95,7 +95,6 @@ int attention_split(int64_t sequences, int64_t span, bool listed, AttentionArgs*
   a->splits = (uint32_t)out->splits;
   return LR_OK;
 }
-
 
 void attention_buffers(const lr_cache* c, const lr_layout* Lq, const void* q, int32_t dtype, int32_t path, AttentionArgs* a) {
   const uintptr_t align = is_quantised(c->dtype) ? 8 : 16;

@@ -34,9 +34,9 @@ __device__ __forceinline__ uint32_t place_in_row(uint32_t row, uint32_t c) {
 // runs over the tokens as they lie in the lane; the values' operand comes by transpose reads of shared memory.
 //
 // What bounds it is the issue of the vector and the matrix instructions, which share each SIMD's time: 8192 rows on 32768
-// tokens (8 cache heads of 128 bf16, 137 GFLOP) 206 us, 667 TFLOP/s, where a large library product reaches 1270; with
-// the second part of the weights the matrix units do half as much again.  With four waves (244 us: matrix units busy 44 %,
-// vector units 55 %) leaving out that part saved 47 us, the exponentials 15, bringing tiles 38.
+// tokens (8 cache heads of 128 bf16, 137 GFLOP) 204 us, 674 TFLOP/s, where a large library product reaches 1270; with
+// the second part of the weights the matrix units do half as much again.  Matrix units are busy 49 % of it, vector units
+// 57 %.  With four waves (244 us, 44 % and 55 %) leaving out that part saved 47 us, the exponentials 15, bringing tiles 38.
 template <int CT, int WAVES> struct RowsShared {
   __attribute__((aligned(16))) char keys[2 * kTileTokens * kPitch], values[2 * kTileTokens * kPitch];  // two tiles each
   __attribute__((aligned(16))) int64_t offs[WAVES][kTileTokens][2];
@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(256, 2) k_prefix_mixed(AttentionArgs prefix, A
 // prefix, the others the sequences' own tokens.  4 sequences of up to 60 tokens behind 1000, 32 heads on 8 of 128 bf16:
 // 8.7 us, 8.2 and 5.7 with a launch for each.
 template <int DT, int CT, int DC>
-__global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, 1>::kMinWaves)) k_prefix_pair(AttentionArgs prefix, AttentionArgs own,
-                                                                                             uint32_t first) {
+__global__ void __launch_bounds__(256, (MatrixShape<DT, CT, DC, 1>::kMinWaves)) k_prefix_pair(
+    AttentionArgs prefix, AttentionArgs own, uint32_t first) {
   __shared__ MatrixShared<DT, CT, DC, 1, kOverTokens> shared;
   if (blockIdx.x < first)
     attention_run<DT, CT, DC, 1, kOverTokens>(prefix, blockIdx.x, shared);
@@ -378,7 +378,7 @@ struct PrefixWay {
 static PrefixWay prefix_way(int32_t dtype, int32_t ctype, AttentionArgs* x, AttentionArgs* a) {
   const bool matrix = x->path == LR_ATTENTION_MATRIX && a->path == LR_ATTENTION_MATRIX;
   if (rows_fit(*x, dtype) && x->group >= kManyRows && much_work(*x, ctype)) {
-    // Eight waves share a tile's staging (1024 rows on 32768 tokens 244 us with four, 206 with eight), but four where that
+    // Eight waves share a tile's staging (1024 rows on 32768 tokens 244 us with four, 204 with eight), but four where that
     // spares codes, whose staging costs more, half a tile of rows that are none (384 rows on 65536: 218 and 236).  Where
     // one workgroup of four waves a CU has no more than 8 blocks of 128 tokens (5 of codes), the other half of the CU takes
     // the sequences' own tokens in the same launch (up to 64 each: 128 rows on 8191 tokens 38 us without and 29 with, 512
