@@ -937,3 +937,26 @@ def test_prefix_attention_many_heads(dev, dtype, kind, heads, kv, dk, dv, page, 
     want, wlse, tol = attention64(q[some], [kn[u] for u in seen], [vn[u] for u in seen], dk ** -0.5, t, kind)
     close(out.cpu()[some], want, tol, "out")
     close(lse.cpu()[some], wlse, tol.lse, "lse")
+
+
+@pytest.mark.parametrize("dtype,kind,dim,page,width", [("bf16", "bf16", 128, 16, 512), ("fp16", "fp16", 64, 8, 600),
+                                                       ("bf16", "e4m3", 96, 32, 300), ("fp16", "int8", 128, 16, 513)])
+def test_prefix_attention_beside_long_sequences(dev, dtype, kind, dim, page, width):
+    """A prefix whose rows share tiles, in one launch with own tokens that four cache heads of a workgroup read."""
+    t, heads, kv, b, prefix = T[dtype], 32, 8, 32, 700
+    lens = [(97 * i) % 211 for i in range(b)]
+    lens[3], lens[20] = 1024, 777
+    assert b * heads // kv * width * page >= (1 << 20 if kind in TOP else 600000)
+    cache, first, table, shared, slots, (kn, vn) = prefix_case(dev, dtype, kind, heads, kv, dim, dim, page, "tokens", prefix, lens)
+    wide = torch.full((width,), -1, dtype=torch.int32)
+    wide[:-(-prefix // page)] = first[:-(-prefix // page)]
+    q, L = rand((b, heads, dim), t, 11), f"({dim},{heads},{b}):(1,{dim},{heads * dim})"
+    out, lse = torch.full((b, heads, dim), -7.0, dtype=t, device=dev), torch.full((b, heads), -7.0, device=dev)
+    given = [-1 if i == 7 else n for i, n in enumerate(lens)]
+    lr.prefix_attention(q.to(dev), L, cache, wide.to(dev), int32([prefix], dev), table.to(dev), int32(given, dev), out, L, lse=lse)
+    assert (out[7] == 0).all() and (lse[7] == -math.inf).all()
+    some = [0, 1, 3, 8, 20, 31]
+    seen = [torch.cat([shared, slots[i]]) for i in some]
+    want, wlse, tol = attention64(q[some], [kn[u] for u in seen], [vn[u] for u in seen], dim ** -0.5, t, kind)
+    close(out.cpu()[some], want, tol, "out")
+    close(lse.cpu()[some], wlse, tol.lse, "lse")
