@@ -167,8 +167,11 @@ __global__ void __launch_bounds__(256) k_block_keys(BlockKeysArgs a) {
     add_halves<32, V>(sum, lanes, lane, &first, &left);
     const double part = 1.0 / (double)n;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if ((uint32_t)i < left && at < (uint32_t)a.dim) out[(int64_t)(at + first + i) * a.od] = (T)(float)(sum[i] * part);
+    for (int i = 0; i < V; ++i) {
+      float mean = (float)(sum[i] * part);
+      asm("" : "+v"(mean));  // two roundings: the compiler makes one of them otherwise, with other bits next to a tie
+      if ((uint32_t)i < left && at < (uint32_t)a.dim) out[(int64_t)(at + first + i) * a.od] = (T)mean;
+    }
   }
 }
 

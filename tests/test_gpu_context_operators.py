@@ -547,6 +547,25 @@ def test_block_keys_layout(dev):
     assert int((keys == -7).sum()) == (pages - 3) * h * d
 
 
+@pytest.mark.parametrize("dtype,tiny", [("bf16", 2.0 ** -36), ("fp16", 2.0 ** -24)])
+@pytest.mark.parametrize("d", [24, 25])
+def test_block_keys_are_rounded_twice(dev, dtype, tiny, d):
+    """The mean is rounded to 32 bits and then to the type: a little off the middle of two numbers of the type, by what 32
+    bits do not hold, it becomes that middle, and then the even one of the two."""
+    t, page, eps = T[dtype], 16, torch.finfo(T[dtype]).eps
+    k = torch.zeros((2 * page, 1, d), dtype=F64)
+    k[0], k[page] = 16.0, -16.0
+    k[3, 0, ::2], k[5, 0, ::2] = 8 * eps, tiny                          # 1 + eps / 2, and a little more
+    k[page + 1, 0, ::2], k[page + 2, 0, ::2] = -24 * eps, tiny          # -1 - 3 eps / 2, and a little less
+    assert torch.equal(k.to(t).to(F64), k)
+    cache, _ = make_cache(dev, dtype, "tokens", 2, page, 1, d, d)
+    L, slots = f"({d},1,{2 * page}):(1,{d},{d})", torch.arange(2 * page, device=dev)
+    lr.cache_write(cache, k.to(t).to(dev), L, k.to(t).to(dev), L, slots)
+    keys = lr.block_keys(cache, slots, torch.empty((2, 1, d), dtype=t, device=dev), f"({d},1,2):(1,{d},{d})").cpu()
+    assert (keys[0] == 1).all() and (keys[1, 0, 1::2] == -1).all() and (keys[1, 0, ::2] == -1 - 2 * eps).all()
+    assert torch.equal(keys, k.view(2, page, 1, d).mean(1).float().to(t))
+
+
 # ------------------------------------------------------------------------------------ blocks: the choice
 def chosen64(q, keys, table, lens, page, count, first, last):
     """The choice by its definition: scores in 64 bits, sorted by (score, index)."""
