@@ -61,7 +61,10 @@ __device__ __forceinline__ void add_halves(double* sum, uint32_t lanes, uint32_t
 // take cache heads of one page side by side, which share lines of memory, their scales above all.  A row of a page is a
 // group of lanes with V elements each, as many rows at a time as the wave has groups, four loads ahead, and the next
 // rows or page asked for before these are added.  Sums are held in 64 bits, in which those of a page of codes or 16-bit
-// keys are exact but for extreme ranges: which blocks a score selects does not hang on the order of a sum.  The groups'
+// keys are exact but for extreme ranges: which blocks a score selects does not hang on the order of a sum.  Codes times
+// scales are rounded to the 32 bits that lr_cache_read gives where keys have 16, so that a caller who makes keys of those
+// numbers gets the same ones, and from them the same choice (whole products turn 640 of the 16.8 million elements of the
+// first size below); keys of 32 bits, in which that rounding would show, are made of the whole products.  The groups'
 // sums are added by halves, each half of the lanes keeping half of the columns, so that a lane ends with few to divide
 // and store (all lanes with all columns: 254 us for the first size below).
 //
@@ -160,7 +163,9 @@ __global__ void __launch_bounds__(256) k_block_keys(BlockKeysArgs a) {
           for (int i = 0; i < V; ++i) v[i] = value_of<CT>(y[z][i]);
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] = kQuant ? __builtin_fma((double)v[i], (double)s[z], sum[i]) : sum[i] + (double)v[i];
+        for (int i = 0; i < V; ++i)
+          sum[i] = kQuant && DT == LR_F32 ? __builtin_fma((double)v[i], (double)s[z], sum[i])
+                                          : sum[i] + (double)(kQuant ? v[i] * s[z] : v[i]);
       }
     }
     uint32_t first = 0, left = V;  // the columns that this lane is left with

@@ -618,6 +618,37 @@ def test_block_select(dev, dtype, heads, kv, d, page, lens, count, first, last, 
     assert torch.equal(out[:b].cpu(), want) and (out[b] == -7).all()
 
 
+@pytest.mark.parametrize("dtype,kind,kv,d,page,order,lens", [("bf16", "e4m3", 4, 128, 16, "tokens", [20000, 16 * 999 + 3]),
+                                                             ("fp16", "int8", 2, 80, 8, "heads", [8001, 8000]),
+                                                             ("fp32", "e4m3", 2, 64, 16, "tokens", [16000])])
+def test_block_keys_and_choice_bit_by_bit(dev, dtype, kind, kv, d, page, order, lens):
+    """Keys of an 8-bit cache of thousands of pages equal, bit by bit, the 64-bit mean of the numbers that the cache gives in
+    32 bits (of codes times scales for keys of 32 bits), rounded to 32 bits and then to the type; the choice is the one from
+    those keys."""
+    t, b, heads, count = T[dtype], len(lens), 4 * kv, 64
+    cache, table, slots, (kn, _) = attention_case(dev, dtype, kind, heads, kv, d, d, page, order, lens)
+    pages = cache.k.numel() // (page * kv * d)
+    Lk, Lq = f"({d},{kv},{pages}):(1,{d},{kv * d})", f"({d},{heads},{b}):(1,{d},{heads * d})"
+    every = torch.cat(slots)
+    read, rest = (torch.empty((every.numel(), kv, d), dtype=torch.float32, device=dev) for _ in range(2))
+    Lr = f"({d},{kv},{every.numel()}):(1,{d},{kv * d})"
+    lr.cache_read(cache, every.to(dev), read, Lr, rest, Lr)
+    assert torch.equal(read.cpu(), kn[every].float())                   # one rounding of code * scale
+    numbers = kn if dtype == "fp32" else kn.float().to(F64)
+    want = torch.zeros((pages, kv, d), dtype=t)
+    for i, n in enumerate(lens):
+        whole = n // page * page
+        want[table[i, :n // page].long()] = numbers[slots[i][:whole]].view(-1, page, kv, d).mean(1).float().to(t)
+        if n > whole:
+            want[int(table[i, n // page])] = numbers[slots[i][whole:n]].mean(0).float().to(t)
+    keys = lr.block_keys(cache, every.to(dev), torch.zeros((pages, kv, d), dtype=t, device=dev), Lk)
+    assert torch.equal(keys.cpu(), want)
+    q = rand((b, heads, d), t, 9)
+    out = torch.empty((b, kv, count), dtype=torch.int32, device=dev)
+    lr.block_select(q.to(dev), Lq, keys, Lk, table.to(dev), int32(lens, dev), page, out)
+    assert torch.equal(out.cpu(), chosen64(q, want, table, lens, page, count, 1, 1))
+
+
 def test_block_select_special_scores(dev):
     """Infinities, NaN, zeros of both signs, pages that are none, lengths past the table, strided and offset tensors."""
     b, heads, kv, d, page, width = 3, 4, 2, 32, 16, 40
