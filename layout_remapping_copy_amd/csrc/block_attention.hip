@@ -217,6 +217,9 @@ __device__ __forceinline__ double row_largest(double x) {
   return fmax(x, exchanged<0x140>(x));
 }
 
+// What comes in chunks of 16 bytes: nothing, the keys, or the queries too.
+enum ScoreChunks { kNoChunks, kKeyChunks, kAllChunks };
+
 // score(b, g, j) = max over the query heads h of cache head g of q[b, h] . key[table[b, j], g], in 64 bits: which blocks
 // are chosen hangs on scores that differ in their last bits, so these are as good as exact.  16 blocks x 16 heads are a
 // product of 64-bit matrix instructions, as fast as the vector units' 64 bits, with the sums over the lanes done; they
@@ -224,13 +227,16 @@ __device__ __forceinline__ double row_largest(double x) {
 // themselves (16 rows, each lane a chunk of 16 bytes), so that waves share nothing; a wave takes every fourth tile of
 // its workgroup's, the next one's keys under way.  2 sequences of 8192 blocks, 64 heads on 8 of 128 bf16 (34 MB): 17 us,
 // of which the products are 7; 16 sequences of up to 512 blocks, 32 heads (8 MB): 11 us, length, page, key and product
-// one after another (12.7 with the first tile's keys asked for before the length is known).
-template <int DT, int DC, bool WIDE>
+// one after another (12.7 with the first tile's keys asked for before the length is known).  Queries whose rows are not
+// made of chunks leave the keys' as they are, in a kernel of their own: a branch between both cost 2 us of each.
+template <int DT, int DC, int CHUNKS>
 __global__ void __launch_bounds__(256) k_block_scores(SelectArgs a) {
   using T = typename ElemOf<DT>::T;
   constexpr uint32_t E = DT == LR_F32 ? 4 : 8;  // elements of a chunk
   using Vec = typename Chunk<T, (int)E>::Vec;
   constexpr uint32_t kChunks = DC / (4 * E);
+  constexpr std::bool_constant<CHUNKS != kNoChunks> keys_wide{};
+  constexpr std::bool_constant<CHUNKS == kAllChunks> queries_wide{};
   const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64), r = lane & 15, j = lane >> 4;
   const uint32_t bg = op_div(blockIdx.x, a.fd_runs), b = op_div(bg, a.fd_heads), g = bg - b * a.kv_heads;
   const uint32_t begin = (blockIdx.x - bg * a.runs) * 64 * a.rounds + 16 * w;
@@ -238,11 +244,11 @@ __global__ void __launch_bounds__(256) k_block_scores(SelectArgs a) {
   if (begin >= end || many <= a.count) return;  // all are taken: nothing to compare
   const int32_t* table = a.table + (int64_t)b * a.table_stride;
   double* scores = a.scores + (uint64_t)bg * a.max_pages;
-  auto load = [&](const T* row, int64_t stride, bool there, Vec* x) {
+  auto load = [&](auto wide, const T* row, int64_t stride, bool there, Vec* x) {
 #pragma unroll
     for (uint32_t c = 0; c < kChunks; ++c) {
       const uint32_t e0 = (c * 4 + j) * E;
-      if constexpr (WIDE) {
+      if constexpr (decltype(wide)::value) {
         x[c] = *(const Vec*)(row + (e0 < (uint32_t)a.dim ? e0 : 0));
         if (!there || e0 >= (uint32_t)a.dim) x[c] = Vec{};
       } else {
@@ -260,8 +266,9 @@ __global__ void __launch_bounds__(256) k_block_scores(SelectArgs a) {
     Vec q[kChunks], next[kChunks];
     int32_t page = page_at(begin);
     const bool head = h0 + r < a.group;
-    load((const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group + (head ? h0 + r : 0)) * a.qh, a.qd, head, q);
-    load(key_of(page), a.kd, true, next);
+    const T* query = (const T*)a.q + (int64_t)b * a.qb + (int64_t)(g * a.group + (head ? h0 + r : 0)) * a.qh;
+    load(queries_wide, query, a.qd, head, q);
+    load(keys_wide, key_of(page), a.kd, true, next);
     for (uint32_t j0 = begin; j0 < end; j0 += 64) {
       Vec k[kChunks];
 #pragma unroll
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(256) k_block_scores(SelectArgs a) {
       const uint64_t seen = __ballot((uint32_t)page < a.pages);
       if (j0 + 64 < end) {
         page = page_at(j0 + 64);
-        load(key_of(page), a.kd, true, next);
+        load(keys_wide, key_of(page), a.kd, true, next);
       }
       D4 acc = {};
 #pragma unroll
@@ -473,11 +480,13 @@ static int launch_keys_of(const BlockKeysArgs& a, int64_t v, dim3 grid, hipStrea
   return launch_keys<DT, CT, 1>(a, grid, st);
 }
 
-template <int DT, int DC> static int launch_scores(const SelectArgs& a, bool wide, dim3 grid, hipStream_t st) {
-  if (wide)
-    hipLaunchKernelGGL((k_block_scores<DT, DC, true>), grid, dim3(256), 0, st, a);
+template <int DT, int DC> static int launch_scores(const SelectArgs& a, ScoreChunks chunks, dim3 grid, hipStream_t st) {
+  if (chunks == kAllChunks)
+    hipLaunchKernelGGL((k_block_scores<DT, DC, kAllChunks>), grid, dim3(256), 0, st, a);
+  else if (chunks == kKeyChunks)
+    hipLaunchKernelGGL((k_block_scores<DT, DC, kKeyChunks>), grid, dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((k_block_scores<DT, DC, false>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_block_scores<DT, DC, kNoChunks>), grid, dim3(256), 0, st, a);
   return check_op_launch();
 }
 
@@ -622,12 +631,13 @@ int lr_block_select(const void* q, const lr_layout* Lq, int64_t q_capacity, cons
     a.runs = (uint32_t)((tiles + a.rounds - 1) / a.rounds);
     a.fd_runs = make_fastdiv(a.runs);
     const bool wide = r.dim % (16 / e) == 0 && rows_aligned(*Lkeys, keys, e, 16 / e);
+    const ScoreChunks chunks = !wide ? kNoChunks : rows_aligned(*Lq, q, e, 16 / e) ? kAllChunks : kKeyChunks;
     const dim3 grid((unsigned)(rows * a.runs));
     const int rc = with_model_type(dtype, [&](auto dt) {
       constexpr int D = decltype(dt)::value;
-      if (a.dim <= 64) return launch_scores<D, 64>(a, wide, grid, st);
-      if (a.dim <= 128) return launch_scores<D, 128>(a, wide, grid, st);
-      return launch_scores<D, 256>(a, wide, grid, st);
+      if (a.dim <= 64) return launch_scores<D, 64>(a, chunks, grid, st);
+      if (a.dim <= 128) return launch_scores<D, 128>(a, chunks, grid, st);
+      return launch_scores<D, 256>(a, chunks, grid, st);
     });
     if (rc) return rc;
   }

@@ -677,6 +677,37 @@ def test_block_select_special_scores(dev):
         assert torch.equal(out.cpu(), want), ("strided", count, first, last)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("queries,keys_as", [("column", "dense"), ("padded", "dense"), ("one", "dense"), ("dense", "padded"),
+                                             ("dense", "column"), ("column", "padded"), ("wide", "wide")])
+def test_block_select_strides(dev, dtype, queries, keys_as):
+    """Queries and keys each with a layout of their own: dense, padded to whole chunks or by an odd count in an offset
+    buffer, head dimensions apart, one number for a whole row; the choice is the dense ones'."""
+    t, b, heads, kv, d, page, width = T[dtype], 3, 10, 2, 64, 16, 300
+    lens, count = [width * page, 1234, 17], 20
+    pages = b * width + 2
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(1)).int()[:b * width].view(b, width)
+    q, keys = rand((b, heads, d), t, 2), rand((pages, kv, d), t, 3)
+    if queries == "one":
+        q = q[..., :1].expand(b, heads, d).contiguous()
+
+    def laid(x, how):                                                   # (buffer, offset, strides of d, heads, items)
+        n, h, _ = x.shape
+        if how == "one":
+            return x[..., 0].contiguous(), 0, (0, 1, h)
+        off, st = {"dense": (0, (1, d, h * d)), "padded": (1, (1, n * (d + 3), d + 3)), "wide": (8, (1, n * (d + 8), d + 8)),
+                   "column": (0, (h, 1, h * d))}[how]
+        buf = torch.full((off + n * h * (d + 8),), math.nan, dtype=t)
+        buf[off:].as_strided((n, h, d), (st[2], st[1], st[0])).copy_(x)
+        return buf, off, st
+    qb, qo, qs = laid(q, queries)
+    kb, ko, ks = laid(keys, keys_as)
+    out = torch.full((b, kv, count), -7, dtype=torch.int32, device=dev)
+    lr.block_select(qb.to(dev).view(-1)[qo:], f"({d},{heads},{b}):({qs[0]},{qs[1]},{qs[2]})", kb.to(dev)[ko:],
+                    f"({d},{kv},{pages}):({ks[0]},{ks[1]},{ks[2]})", table.to(dev), int32(lens, dev), page, out)
+    assert torch.equal(out.cpu(), chosen64(q, keys, table, lens, page, count, 1, 1))
+
+
 def test_block_select_by_last_bits(dev):
     """Scores that differ in the 40th bit, and scores of every size: the border is found at any bit."""
     d, page, n = 32, 1, 3000
