@@ -733,8 +733,8 @@ int lr_prefix_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, 
 /* The keys of the blocks that the tokens in slots[0..n) (device, as lr_cache_write, after it) were written to:
  *   keys[., h, p] = mean of the keys of slots 0 .. s of page p,
  * s the place in the page of its newest slot.  A page's slots are filled in their order, and those of one page that are
- * given have to stand next to each other in ascending order.  A slot outside the cache is passed over; pages that no
- * slot lies in keep their keys.  keys: layout (head_dim, heads, pages) of the cache's
+ * given have to stand next to each other in ascending order.  A slot outside the cache is passed over, wherever it stands,
+ * between those of one page too; pages that no slot lies in keep their keys.  keys: layout (head_dim, heads, pages) of the cache's
  * extents, in the model's type dtype (the cache's own, or any for LR_E4M3 and LR_INT8).  The keys of an 8-bit cache are
  * the numbers that lr_cache_read gives in LR_F32, for keys in LR_F32 code * scale unrounded.  Summed in 64 bits, the mean
  * rounded to 32 bits and then to dtype. */

@@ -1191,7 +1191,7 @@ def prefix_attention(q, Lq, cache: PagedCache, prefix, prefix_len, page_table, l
 def block_keys(cache: PagedCache, slots, keys, Lkeys, stream=None):
     """lr_block_keys: the keys of the blocks (pages) that the tokens in the int64 ``slots`` were written to, the mean of
     their tokens' keys, into ``keys`` of layout (head_dim, heads, pages).  Called with the slots of a cache_write, after
-    it.  Returns keys."""
+    it, padding (-1) anywhere among them; those of one page next to each other but for padding, ascending.  Returns keys."""
     _device_tensors(cache.index, "slots keys", slots, keys)
     if slots.dtype != _torch().int64:
         raise TypeError("slots must be int64")

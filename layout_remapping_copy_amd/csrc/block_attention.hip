@@ -57,6 +57,42 @@ __device__ __forceinline__ void add_halves(double* sum, uint32_t lanes, uint32_t
   if constexpr (D > 1) add_halves<D / 2, (N > 1 ? N / 2 : 1)>(sum, lanes, lane, first, left);
 }
 
+// The first slot inside the cache among the entries from `from` on, or -1: each wave of the workgroup takes every fourth
+// 1024 entries, half of the next ones under way, until it meets one or is past one that another wave met.  Padding behind
+// the last token is looked through to its end, as fast as one CU reads (some 65 GB/s): 8 heads of 128 bf16, 131071 entries
+// the first 101 of which have a slot, 23 us (8 if only the next entry were looked at), 262144 and 100001 65 us (47).
+__device__ __forceinline__ int64_t first_inside(const BlockKeysArgs& a, uint32_t from, uint32_t lane, uint32_t w) {
+  __shared__ uint32_t met;
+  if (threadIdx.x == 0) met = ~0u;
+  __syncthreads();
+  const uint32_t most = a.n - 1;
+  int64_t x[2][8];
+  auto load = [&](int half, uint32_t i) {
+#pragma unroll
+    for (uint32_t z = 0; z < 8; ++z) x[half][z] = a.slots[min(i + 64 * z + lane, most)];
+  };
+  auto look = [&](int half, uint32_t i) {
+    uint32_t high = ~0u;  // 0 where one is no negative number: then they are looked at one by one
+#pragma unroll
+    for (int z = 0; z < 8; ++z) high = min(high, (uint32_t)((uint64_t)x[half][z] >> 32));
+    if (!__any(high == 0)) return;
+#pragma unroll
+    for (uint32_t z = 0; z < 8; ++z)
+      if ((uint64_t)x[half][z] < (uint64_t)a.cache_slots) atomicMin(&met, min(i + 64 * z + lane, most));
+  };
+  load(0, from + 1024 * w);
+  load(1, from + 1024 * w + 512);
+  for (uint32_t i = from + 1024 * w; i < a.n; i += 4096) {
+    look(0, i);
+    load(0, i + 4096);
+    look(1, i + 512);
+    load(1, i + 4608);
+    if (*(volatile uint32_t*)&met < i + 4096) break;
+  }
+  __syncthreads();
+  return met == ~0u ? -1 : a.slots[met];
+}
+
 // A workgroup has `chunk` entries of slots and makes the mean of every page whose newest slot is among them; its waves
 // take cache heads of one page side by side, which share lines of memory, their scales above all.  A row of a page is a
 // group of lanes with V elements each, as many rows at a time as the wave has groups, four loads ahead, and the next
@@ -80,10 +116,26 @@ __global__ void __launch_bounds__(256) k_block_keys(BlockKeysArgs a) {
   const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
   const uint64_t at = (uint64_t)blockIdx.x * a.chunk + lane;
   const bool mine = lane < a.chunk && at < a.n;
-  const int64_t slot = mine ? a.slots[at] : -1, next = mine && at + 1 < a.n ? a.slots[at + 1] : -1;
+  const int64_t slot = mine ? a.slots[at] : -1;
+  int64_t next = mine && at + 1 < a.n ? a.slots[at + 1] : -1;
   const bool held = (uint64_t)slot < (uint64_t)a.cache_slots;
   const uint32_t page = held ? op_div((uint32_t)slot, a.fd_page) : 0, in = held ? (uint32_t)slot - page * a.page_size : 0;
-  // the newest of its page, unless the next entry is a later slot of the same page
+  // The newest of its page, unless the next entry inside the cache is a later slot of the same page.  Where others stand
+  // between, that is looked for in the chunk, for the chunk's last in the 64 entries behind, and if its page has later
+  // slots at all in those behind them.
+  if (__builtin_expect(__any(held && (uint64_t)next >= (uint64_t)a.cache_slots), 0)) {
+    const uint64_t inside = __ballot(held), after = inside & ~(((uint64_t)2 << lane) - 1);
+    next = __shfl((long long)slot, after ? __ffsll((unsigned long long)after) - 1 : 0);
+    const uint64_t behind = (blockIdx.x + (uint64_t)1) * a.chunk;
+    int64_t first = behind + lane < a.n ? a.slots[behind + lane] : -1;
+    const uint64_t near = __ballot((uint64_t)first < (uint64_t)a.cache_slots);
+    first = __shfl((long long)first, near ? __ffsll((unsigned long long)near) - 1 : 0);
+    if (!near) {
+      const uint32_t newest = uniform(__shfl(in, 63 - __builtin_clzll(inside)));
+      first = newest + 1 < a.page_size && behind + 64 < a.n ? first_inside(a, (uint32_t)behind + 64, lane, w) : -1;
+    }
+    if (!after) next = first;
+  }
   const bool later = next > slot && next < (int64_t)(page + (uint64_t)1) * a.page_size;
   uint64_t todo = __ballot(held && !later);
   uint32_t lanes = 1;  // of a row, a power of two

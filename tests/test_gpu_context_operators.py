@@ -566,6 +566,40 @@ def test_block_keys_are_rounded_twice(dev, dtype, tiny, d):
     assert torch.equal(keys, k.view(2, page, 1, d).mean(1).float().to(t))
 
 
+@pytest.mark.parametrize("dtype,kind,h,d,page,lens,runs,total", [
+    ("bf16", "bf16", 1, 32, 16, [100, 33, 16, 1], (0, 1), 0),           # an entry or none outside the cache behind each
+    ("bf16", "e4m3", 2, 64, 16, [100, 60], (0, 70), 0),                 # more than a wave looks at
+    ("fp16", "fp16", 8, 32, 64, [130, 70], (0, 6000), 0),               # many steps of looking on
+    ("bf16", "bf16", 4, 32, 16, [9000], (0, 2), 0),                     # workgroups of several entries
+    ("fp32", "fp32", 5, 20, 5, [4000, 333], (0, 1), 30000),             # a long end of padding
+    ("bf16", "int8", 8, 32, 16, [60001, 20000], (0, 1), 140000),        # workgroups of 64 entries
+])
+def test_block_keys_of_padded_slots(dev, dtype, kind, h, d, page, lens, runs, total):
+    """Slots outside the cache anywhere, also between those of one page and across the ends of workgroups: passed over."""
+    t, g = T[dtype], torch.Generator().manual_seed(8)
+    cache, table, slots, (kn, _) = attention_case(dev, dtype, kind, h, h, d, d, page, "tokens", lens)
+    pages = cache.k.numel() // (page * h * d)
+    numbers = kn.float().to(F64) if dtype != "fp32" else kn
+    want = torch.full((pages, h, d), -7.0, dtype=t)
+    for i, n in enumerate(lens):
+        for j in range(-(-n // page)):
+            want[int(table[i, j])] = numbers[slots[i][j * page:min(n, (j + 1) * page)]].mean(0).float().to(t)
+    every = torch.cat(slots)
+    holes = torch.randint(runs[0], runs[1] + 1, (every.numel(),), generator=g)
+    if runs[1] > 100:                                                   # long runs here and there
+        holes *= (torch.rand(every.numel(), generator=g) < 0.05)
+    at = torch.arange(every.numel()) + holes.cumsum(0)
+    padded = torch.full((max(total, int(at[-1]) + 1),), -1)
+    padded[1::3], padded[2::7] = pages * page, -2 ** 63
+    padded[at] = every
+    keys = lr.block_keys(cache, padded.to(dev), torch.full((pages, h, d), -7.0, dtype=t, device=dev),
+                         f"({d},{h},{pages}):(1,{d},{h * d})")
+    assert torch.equal(keys.cpu(), want)
+    rest = torch.full((pages, h, d), -7.0, dtype=t, device=dev)         # none inside the cache
+    lr.block_keys(cache, torch.full((5000,), -1, device=dev), rest, f"({d},{h},{pages}):(1,{d},{h * d})")
+    assert (rest == -7).all()
+
+
 # ------------------------------------------------------------------------------------ blocks: the choice
 def chosen64(q, keys, table, lens, page, count, first, last):
     """The choice by its definition: scores in 64 bits, sorted by (score, index)."""
