@@ -611,8 +611,7 @@ int lr_block_keys(const lr_cache* c, const int64_t* slots, int64_t n, void* keys
   // 64 entries and all heads a workgroup, fewer where that would leave part of the device without one: a step's
   // entries are each the newest of their page, a prompt's one in page_size
   a.chunk = (uint32_t)std::min<int64_t>(64, std::max<int64_t>(1, n / 2048));
-  a.heads_y = a.chunk < 64 ? 4 : std::max<uint32_t>(4, (a.heads + 65534) / 65535);
-  if (a.chunk == 64 && n >= 64 * 2048) a.heads_y = a.heads;
+  a.heads_y = a.chunk < 64 ? 4 : a.heads;
   int64_t v = ce == 4 ? 4 : 8;
   while (v > 1 && (a.dim % v || !rows_aligned(c->k_layout, c->k, ce, v))) v /= 2;
   const dim3 grid((unsigned)((n + a.chunk - 1) / a.chunk), (a.heads + a.heads_y - 1) / a.heads_y);
