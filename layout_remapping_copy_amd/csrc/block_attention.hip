@@ -222,10 +222,19 @@ __global__ void __launch_bounds__(256) k_block_keys(BlockKeysArgs a) {
     }
     uint32_t first = 0, left = V;  // the columns that this lane is left with
     add_halves<32, V>(sum, lanes, lane, &first, &left);
-    const double part = 1.0 / (double)n;
+    // The quotient itself, as times 1 / n a mean between two numbers would be rounded to the wrong one; a full page of a
+    // power of two, the usual case, has it without a division (with one for all pages 3 % more of the first size above).
+    if (__builtin_expect(n & (n - 1), 0)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] /= (double)n;
+    } else {
+      const int down = -(31 - __builtin_clz(n));
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] = __builtin_ldexp(sum[i], down);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float mean = (float)(sum[i] * part);
+      float mean = (float)sum[i];
       asm("" : "+v"(mean));  // two roundings: the compiler makes one of them otherwise, with other bits next to a tie
       if ((uint32_t)i < left && at < (uint32_t)a.dim) out[(int64_t)(at + first + i) * a.od] = (T)mean;
     }

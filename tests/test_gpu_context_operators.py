@@ -566,6 +566,28 @@ def test_block_keys_are_rounded_twice(dev, dtype, tiny, d):
     assert torch.equal(keys, k.view(2, page, 1, d).mean(1).float().to(t))
 
 
+@pytest.mark.parametrize("n", [9, 49, 103, 123])
+@pytest.mark.parametrize("d", [64, 33])
+def test_block_keys_between_two_numbers(dev, n, d):
+    """Means just between two numbers of 32 bits become the even one: the sum is divided, as times 1 / n it would be off."""
+    g = torch.Generator().manual_seed(n)
+    q = torch.randint(1 << 24, 30 << 20, (d,), generator=g) | 1         # 25 bits, the last one set
+    rows = torch.empty((128, 1, d), dtype=torch.int64)
+    rows[n - 1] = (1 << 24) - 1                                         # the one odd number; the others even, of 24 bits
+    left = n * q - rows[n - 1, 0]
+    even = left // (2 * (n - 1)) * 2
+    rows[:n - 1, 0] = even
+    rows[:n - 1, 0] += 2 * (torch.arange(n - 1)[:, None] < ((left - (n - 1) * even) // 2)[None])
+    rows[n:] = 5
+    assert torch.equal(rows[:n, 0].sum(0), n * q) and torch.equal(rows.float().long(), rows)
+    cache, _ = make_cache(dev, "fp32", "tokens", 1, 128, 1, d, d)
+    L = f"({d},1,128):(1,{d},{d})"
+    x = rows.float().to(dev)
+    lr.cache_write(cache, x, L, x, L, torch.arange(128, device=dev))
+    keys = lr.block_keys(cache, torch.arange(n, device=dev), torch.empty((1, 1, d), device=dev), f"({d},1,1):(1,{d},{d})")
+    assert torch.equal(keys.cpu()[0, 0], q.to(F64).float())
+
+
 @pytest.mark.parametrize("dtype,kind,h,d,page,lens,runs,total", [
     ("bf16", "bf16", 1, 32, 16, [100, 33, 16, 1], (0, 1), 0),           # an entry or none outside the cache behind each
     ("bf16", "e4m3", 2, 64, 16, [100, 60], (0, 70), 0),                 # more than a wave looks at
