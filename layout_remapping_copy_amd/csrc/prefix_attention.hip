@@ -13,6 +13,7 @@ typedef float F16x __attribute__((ext_vector_type(16)));
 typedef short S4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) S4 LdsS4;
 typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+typedef unsigned short W2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ F16x mfma32(B8 a, B8 b, F16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ F16x mfma32(H8 a, H8 b, F16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
@@ -41,6 +42,8 @@ template <int CT, int WAVES> struct RowsShared {
   __attribute__((aligned(16))) char keys[2 * kTileTokens * kPitch], values[2 * kTileTokens * kPitch];  // two tiles each
   __attribute__((aligned(16))) int64_t offs[WAVES][kTileTokens][2];
   __attribute__((aligned(16))) float scales[CT == LR_E4M3 || CT == LR_INT8 ? WAVES : 1][2][2][kTileTokens];
+  // of each tile, whether the values that a wave brought hold an infinity or a NaN
+  __attribute__((aligned(16))) uint32_t odd[2][CT == LR_E4M3 || CT == LR_INT8 ? 1 : WAVES];
 };
 template <int DT, int CT, int DC, int WAVES>
 __device__ __forceinline__ void rows_run(const AttentionArgs& a, uint32_t block, RowsShared<CT, WAVES>& shared) {
@@ -133,6 +136,7 @@ __device__ __forceinline__ void rows_run(const AttentionArgs& a, uint32_t block,
       }
     };
     auto store = [&](uint32_t buf) {
+      W2 most = {};  // of the values' upper bits, without signs
 #pragma unroll
       for (int x = 0; x < kRows; ++x) {
         const uint32_t at = place_in_row(row0 + kApart * x, chunk);
@@ -148,6 +152,15 @@ __device__ __forceinline__ void rows_run(const AttentionArgs& a, uint32_t block,
         if (bad >> x & 1) v = U4{};  // what is not seen may hold NaN
         *(U4*)&keys[buf * kTile + at] = k;
         *(U4*)&values[buf * kTile + at] = v;
+        if constexpr (!kQuant)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            most = __builtin_elementwise_max(most, __builtin_bit_cast(W2, v[y] & 0x7fff7fffu));
+      }
+      if constexpr (!kQuant) {
+        constexpr unsigned short kInf = DT == LR_F16 ? 0x7c00 : 0x7f80;
+        const bool any = __any(most[0] >= kInf || most[1] >= kInf);
+        if (lane == 0) shared.odd[buf][w] = any;
       }
     };
 
@@ -177,6 +190,12 @@ __device__ __forceinline__ void rows_run(const AttentionArgs& a, uint32_t block,
         load(seen_after);
         page = page_of(t0 + 3 * kTileTokens);
         if (!idle) {
+          uint32_t odd = 0;
+          if constexpr (!kQuant) {
+            U4 any = *(const U4*)&shared.odd[buf][0];
+            if constexpr (WAVES == 8) any |= *(const U4*)&shared.odd[buf][4];
+            odd = uniform(any[0] | any[1] | any[2] | any[3]);
+          }
 #pragma unroll 1
           for (uint32_t tt = 0; tt < 2; ++tt) {
             const uint32_t from = buf * kTile + tt * 32 * kPitch;
@@ -233,36 +252,43 @@ __device__ __forceinline__ void rows_run(const AttentionArgs& a, uint32_t block,
 #pragma unroll
               for (int d = 0; d < kValSteps; ++d) o[d] *= keep;
             }
-            // The weights in two 16-bit parts, 16 bits in bf16 and 22 in fp16.  A bf16 first part is the number's upper half,
-            // so that the second is not negative; where values may be infinite it is not zero either, as an infinite value
-            // times zero would be NaN.  fp16 parts are rounded, the first not to zero, and the second meets finite values.
-            P phi[2], plo[2];
+            // The weights in two 16-bit parts as in k_attention_matrix: the number, rounded, and what that left.  The second
+            // may be zero or negative, and meets finite values; which tiles hold others is found as they are brought (first
+            // parts cut off, whose rests are never negative, need no finite values, but have a bit less; finite values
+            // made in every tile take 344 us where prefix large takes 321).
+            U4 phi[2], plo[2];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], unit, -base));
-              l += x;
-              if constexpr (kQuant) x *= vsc[i / 4][i % 4];
-              if constexpr (std::is_same_v<PE, _Float16>) {
-                phi[i / 8][i % 8] = (PE)fmaxf(x, 0x1p-24f);
-                plo[i / 8][i % 8] = (PE)(x - (float)phi[i / 8][i % 8]);
-              } else {
-                const uint32_t up = __float_as_uint(x) & 0xffff0000u;
-                phi[i / 8][i % 8] = __builtin_bit_cast(PE, (uint16_t)(up >> 16));
-                const float rest = x - __uint_as_float(up);
-                plo[i / 8][i % 8] = (PE)(kQuant ? rest : fmaxf(rest, 0x1p-100f));
+            for (int i = 0; i < 16; i += 2) {
+              float x[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                x[y] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + y], unit, -base));
+                l += x[y];
+                if constexpr (kQuant) x[y] *= vsc[i / 4][i % 4 + y];
               }
+              uint32_t up, rest;  // pairs, converted together
+              if constexpr (std::is_same_v<PE, _Float16>) {
+                const H2 z = {(PE)fmaxf(x[0], 0x1p-24f), (PE)fmaxf(x[1], 0x1p-24f)};
+                up = __builtin_bit_cast(uint32_t, z);
+                rest = __builtin_bit_cast(uint32_t, H2{(PE)(x[0] - (float)z[0]), (PE)(x[1] - (float)z[1])});
+              } else {
+                up = __builtin_bit_cast(uint32_t, __builtin_convertvector((F2{x[0], x[1]}), B2));
+                const F2 left = {x[0] - __uint_as_float(up << 16), x[1] - __uint_as_float(up & 0xffff0000u)};
+                rest = __builtin_bit_cast(uint32_t, __builtin_convertvector(left, B2));
+              }
+              phi[i / 8][i % 8 / 2] = up, plo[i / 8][i % 8 / 2] = rest;
             }
 #pragma unroll
             for (int d = 0; d < kValSteps; ++d) {
               U4 n0 = v0, n1 = v1;
               if (d + 1 < kValSteps) n0 = value(d + 1, 0), n1 = value(d + 1, 1);
-              o[d] = mfma32(__builtin_bit_cast(P, v0), phi[0], o[d]);
-              o[d] = mfma32(__builtin_bit_cast(P, v1), phi[1], o[d]);
-              if constexpr (std::is_same_v<PE, _Float16>)
+              o[d] = mfma32(__builtin_bit_cast(P, v0), __builtin_bit_cast(P, phi[0]), o[d]);
+              o[d] = mfma32(__builtin_bit_cast(P, v1), __builtin_bit_cast(P, phi[1]), o[d]);
+              if (!kQuant && odd)
 #pragma unroll
-                for (int y = 0; y < 4; ++y) v0[y] = finite_pair<LR_F16>(v0[y]), v1[y] = finite_pair<LR_F16>(v1[y]);
-              o[d] = mfma32(__builtin_bit_cast(P, v0), plo[0], o[d]);
-              o[d] = mfma32(__builtin_bit_cast(P, v1), plo[1], o[d]);
+                for (int y = 0; y < 4; ++y) v0[y] = finite_pair<DT>(v0[y]), v1[y] = finite_pair<DT>(v1[y]);
+              o[d] = mfma32(__builtin_bit_cast(P, v0), __builtin_bit_cast(P, plo[0]), o[d]);
+              o[d] = mfma32(__builtin_bit_cast(P, v1), __builtin_bit_cast(P, plo[1]), o[d]);
               v0 = n0, v1 = n1;
             }
           }

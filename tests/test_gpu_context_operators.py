@@ -492,6 +492,73 @@ def test_prefix_attention_rows_weights_in_two_parts(dev, dtype, kind, weight, fl
     close(out.cpu()[some], want, tol)
 
 
+@pytest.mark.parametrize("heads,kv,width", [(8, 1, 500), (32, 4, 2200)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_prefix_attention_rows_infinities(dev, dtype, heads, kv, width):
+    """Infinite values at the ends of tiles, in places that different waves bring: their elements are infinite whatever the
+    second part of their weights is, one of either sign and a NaN make NaN, and the others are as exact as ever."""
+    t, d, page, b, prefix = T[dtype], 64, 16, 20, 300
+    lens, cache, wide, table, shared, slots, (kn, vn) = rows_case(dev, dtype, dtype, heads, kv, d, d, page, "tokens", prefix, b, width)
+    put = {0: (1, math.inf), 63: (2, -math.inf), 64: (3, math.inf), 95: (4, -math.inf), 200: (5, math.inf), 201: (5, -math.inf),
+           256: (6, math.nan), 299: (63, math.inf)}
+    clean = vn.clone()
+    for at, (col, x) in put.items():
+        vn[shared[at], :, col], clean[shared[at], :, col] = x, 0.0
+    put_rows(cache, "v", "tokens", page, kv, d, shared, vn[shared].to(t))
+    q = rand((b, heads, d), t, 5)
+    out, lse = torch.empty((b, heads, d), dtype=t, device=dev), torch.empty((b, heads), device=dev)
+    L = f"({d},{heads},{b}):(1,{d},{heads * d})"
+    lr.prefix_attention(q.to(dev), L, cache, wide.to(dev), int32([prefix], dev), table.to(dev), int32(lens, dev), out, L, lse=lse)
+    some = [0, 3, 11, b - 1]
+    seen = [torch.cat([shared, slots[i]]) for i in some]
+    want, wlse, tol = attention64(q[some], [kn[u] for u in seen], [clean[u] for u in seen], d ** -0.5, t, dtype)
+    for col, x in ((1, math.inf), (2, -math.inf), (3, math.inf), (4, -math.inf), (5, math.nan), (6, math.nan), (63, math.inf)):
+        want[..., col] = x
+    close(out.cpu()[some], want, tol)
+    close(lse.cpu()[some], wlse, tol.lse)
+
+
+@pytest.mark.parametrize("heads,kv,width", [(8, 1, 500), (32, 4, 2200)])  # with the sequences' tokens in one launch, and alone
+@pytest.mark.parametrize("dtype,kind,part", [("bf16", "bf16", 2.0 ** -19), ("fp16", "fp16", 2.0 ** -24),
+                                             ("fp16", "e4m3", 2.0 ** -19), ("bf16", "int8", 2.0 ** -19)])
+def test_prefix_attention_rows_two_tokens(dev, dtype, kind, part, heads, kv, width):
+    """Two tokens of nearly equal weights and opposite values: what is left shows the weights' bits, which are the paged
+    attention's.  The larger weight w is a power of two, the other w (1 - u) with u < 2^-10.  Its first part is w in bf16,
+    and the second, below 2^-10 w, is off by half of its 2^-8: 2^-19 w; in fp16 the first is off by 2^-12 w and the second by
+    2^-12 of that.  The output is half of these, rounded once; exponentials and sums in 32 bits are off by 2^-21 in all."""
+    t, d, page, b = T[dtype], 64, 16, 20
+    _, cache, wide, table, shared, _, _ = rows_case(dev, dtype, kind, heads, kv, d, d, page, "heads", 2, b, width)
+    k = torch.zeros((2, kv, d), dtype=F64)
+    k[0, :, 0], k[1, :, 0] = 1.0, 1 - 2.0 ** -8
+    v = torch.ones((2, kv, d), dtype=F64)
+    v[1] = -1
+    if kind in TOP:                                                     # codes of 1 and -1, the difference in the scales
+        pages = cache.k_scale.numel() // (page * kv)
+        _, ss = cache_strides("heads", kv, page, d)
+        at = shared.to(dev)
+        for buf, sc, rows, scales in ((cache.k, cache.k_scale, (k != 0).float(), [1.0, 1 - 2.0 ** -8]),
+                                      (cache.v, cache.v_scale, v.float(), [1.0, 1.0])):
+            codes = rows.to(T[kind])
+            s, _ = cache_strides("heads", kv, page, d)
+            view = buf.as_strided((pages, page, kv, d), s)
+            view[at // page, at % page] = (codes.view(torch.uint8) if kind == "e4m3" else codes).to(dev)
+            sc.as_strided((pages, page, kv), ss)[at // page, at % page] = torch.tensor(scales, device=dev)[:, None].expand(2, kv)
+    else:
+        put_rows(cache, "k", "heads", page, kv, d, shared, k.to(t))
+        put_rows(cache, "v", "heads", page, kv, d, shared, v.to(t))
+    q = rand((b, heads, d), t, 11)
+    q[..., 0] = (q[..., 0].abs() % 0.9375 + 0.0625).to(t)
+    out, lse = torch.empty((b, heads, d), dtype=t, device=dev), torch.empty((b, heads), device=dev)
+    L = f"({d},{heads},{b}):(1,{d},{heads * d})"
+    lr.prefix_attention(q.to(dev), L, cache, wide.to(dev), int32([2], dev), table.to(dev), int32([0] * b, dev), out, L,
+                        scale=0.25, lse=lse)
+    u = q[..., 0].to(F64) * 0.25
+    w = torch.exp(-u * 2.0 ** -8)
+    want = ((1 - w) / (1 + w))[..., None].expand(b, heads, d)
+    close(out, want, HALF[t] * want + part / 2 + 2.0 ** -21)
+    close(lse, u + torch.log1p(w), 2.0 ** -21)
+
+
 # ------------------------------------------------------------------------------------ blocks: their keys
 KEYS = [  # type, kind, heads, d, page, order, lens
     ("bf16", "bf16", 8, 128, 16, "tokens", [100, 1, 16, 17]), ("bf16", "e4m3", 8, 128, 64, "heads", [300, 64, 1]),
