@@ -77,7 +77,7 @@ __device__ __forceinline__ void rows_run(const AttentionArgs& a, uint32_t block,
   const float unit = kQuant || a.scale2 == 0 ? 1.f : __builtin_fabsf(a.scale2);
 
   Run run;
-  if (!run_begin(a, block, &run)) return;
+  if (!run_begin<false>(a, block, &run)) return;
   do {
     const uint32_t g = run.u / a.tiles, tile0 = run.u % a.tiles * (32 * WAVES) + w * 32, row = tile0 + here(r);
     const uint32_t lo = run.lo, hi = run.hi;
@@ -312,7 +312,7 @@ __device__ __forceinline__ void rows_run(const AttentionArgs& a, uint32_t block,
         }
       if (he == 0) leave_part(a, run, g * a.group + row, base == -__FLT_MAX__ ? -__builtin_inff() : base, total);
     }
-  } while (run_next(a, &run));
+  } while (run_next<false>(a, &run));
 }
 
 template <int DT, int CT, int DC, int WAVES>
