@@ -703,7 +703,9 @@ int lr_paged_attention(const void* q, const lr_layout* Lq, int64_t q_capacity, c
                        int32_t dtype, float scale, int64_t window, void* workspace, int64_t workspace_bytes,
                        void* stream);
 
-/* Attention of one new token a sequence where the whole batch shares a prefix, which is read once for all:
+/* Attention of one new token a sequence where the whole batch shares a prefix, which is read for many
+ * query heads at once (up to 256 of a cache head in 16-bit types with heads of up to 128, where there is work for so
+ * many, 16 or 32 else, 1 in LR_ATTENTION_ELEMENT):
  *   out[b, h] = softmax over the prefix's tokens and then the sequence's own, as lr_paged_attention.
  * The prefix is tokens 0 .. P - 1 of the pages prefix[0..prefix_pages) (device), P = prefix_len[0] (device) limited to
  * [0, prefix_pages * page_size); sequence b's own lens[b] tokens lie in the pages table[b * table_stride + ...] as those

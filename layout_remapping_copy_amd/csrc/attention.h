@@ -57,7 +57,7 @@ struct AttentionArgs {
 // 1 + ceil((n - 1) / min_share) runs, as none is shorter than min_share.  That has to be at most `splits`, the
 // parts of a unit that the workspace has room for, so min_share grows with the longest unit that the page table
 // admits; where the lengths are far below it, fewer than all workgroups have a run (64 sequences of 1000 tokens, 32
-// heads on 8 of 128: 48 us under a table just wide enough, 127 with 63 runs under one for 131072 tokens).
+// heads on 8 of 128: 54 us under a table just wide enough, 129 with 63 runs under one for 131072 tokens).
 constexpr int64_t kRuns = 256;                     // one a CU
 constexpr uint32_t kBlock = 128, kWideBlock = 32;  // a step of four waves over tokens, or over heads
 
@@ -461,9 +461,9 @@ struct MatrixShape {
 // transposed within the lane by byte permutes; the output's column 8 r + m is then row r of product m.
 //
 // What bounds it is the reading of the cache: 64 sequences of up to 16384 bf16 tokens, 64 query heads on 8 of 128
-// (2.15 GB) take 352 us a call, 6.1 TB/s, and 2 of 131071 e4m3 tokens 97 us, 5.7 TB/s, where a bare streaming read
-// reaches 7.2 (299 and 77 us); as many fp16 tokens 352 us, 2.21 GB of fp32 (32 sequences, 32 heads) 363 us, 6.1 TB/s,
-// and fp32 queries over 0.57 GB of e4m3 234 us, 2.4 TB/s, where the fp32 products are the bound.  The vector units are
+// (2.15 GB) take 338 us a call, 6.4 TB/s, and 2 of 131071 e4m3 tokens 93 us, 6.0 TB/s, where a bare streaming read
+// reaches 7.2 (299 and 77 us); as many fp16 tokens 339 us, 2.21 GB of fp32 (32 sequences, 32 heads) 340 us, 6.5 TB/s,
+// and fp32 queries over 0.57 GB of e4m3 228 us, 2.5 TB/s, where the fp32 products are the bound.  The vector units are
 // busy 19 % of the first, 37 % of the second, with the matrix units' part.
 // One workgroup a CU keeps enough loads under way; two and three a CU (512 and 768 runs) took 359 and 367 us against
 // 353, as more rows of memory are open at once.  Plain loads took 20 % longer than streaming ones.

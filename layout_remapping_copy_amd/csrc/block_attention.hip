@@ -104,9 +104,10 @@ __device__ __forceinline__ int64_t first_inside(const BlockKeysArgs& a, uint32_t
 // sums are added by halves, each half of the lanes keeping half of the columns, so that a lane ends with few to divide
 // and store (all lanes with all columns: 254 us for the first size below).
 //
-// 262142 tokens of 8 heads of 128 e4m3 in pages of 16 (tokens first): 84 us, 3.3 TB/s, vector instructions busy 80 % of it:
-// adding in 32 bits would take 4 us less, adding nothing no less.  16 tokens, each the newest of its page of 64: 5 us,
-// slot, keys and store one after another.
+// 262142 tokens of 8 heads of 128 e4m3 in pages of 16 (tokens first): 85 us, 3.3 TB/s.  Vector instructions are busy 83 % of
+// it, but adding nothing took no less: what bounds it is the loads, 8 bytes a lane, that a wave has under way (bf16, 16
+// bytes a lane: 115 us, 5.0 TB/s).  16 tokens, each the newest of its page of 64: 5 us, slot, keys and store one after
+// another.
 template <int DT, int CT, int V>
 __global__ void __launch_bounds__(256) k_block_keys(BlockKeysArgs a) {
   using T = typename ElemOf<DT>::T;

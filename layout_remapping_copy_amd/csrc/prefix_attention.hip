@@ -34,10 +34,11 @@ __device__ __forceinline__ uint32_t place_in_row(uint32_t row, uint32_t c) {
 // one exchange.  They are also the second operand of the next product, values transposed x weights, when its inner index
 // runs over the tokens as they lie in the lane; the values' operand comes by transpose reads of shared memory.
 //
-// What bounds it is the issue of the vector and the matrix instructions, which share each SIMD's time: 8192 rows on 32768
-// tokens (8 cache heads of 128 bf16, 137 GFLOP) 204 us, 674 TFLOP/s, where a large library product reaches 1270; with
-// the second part of the weights the matrix units do half as much again.  Matrix units are busy 49 % of it, vector units
-// 57 %.  With four waves (244 us, 44 % and 55 %) leaving out that part saved 47 us, the exponentials 15, bringing tiles 38.
+// What bounds it is that vector and matrix instructions take turns: a SIMD's two waves go from barrier to barrier through
+// products, exponentials and products in step.  8192 rows on 32768 tokens (8 cache heads of 128 bf16, 137 GFLOP) 212 us,
+// 648 TFLOP/s, where a large library product reaches 1270; with the second part of the weights the matrix units do
+// half as much again.  They are busy 48 % of it, the vector units 56 %: all of it together, where both at once could be
+// less.  With four waves (244 us, 44 % and 55 %) leaving out that part saved 47 us, the exponentials 15, bringing tiles 38.
 template <int CT, int WAVES> struct RowsShared {
   __attribute__((aligned(16))) char keys[2 * kTileTokens * kPitch], values[2 * kTileTokens * kPitch];  // two tiles each
   __attribute__((aligned(16))) int64_t offs[WAVES][kTileTokens][2];
